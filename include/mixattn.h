@@ -3,10 +3,11 @@
  *
  * One launch serves chunked-prefill rows (a causal query slice at a position
  * offset) and decode rows (one query each) of the same batch, reading a paged
- * KV cache stored as 32-element blocks (fp16, Q8_0 or Q4_0) and dequantising
- * inside the attention.  A second entry point quantises new K/V into the
- * cache.  Everything runs on the caller's CUDA stream; there is no CPU
- * fallback.
+ * KV cache stored as 32-element blocks (fp16, Q8_0 or Q4_0) or as 8-bit codes
+ * with one scale per page and kv head, and dequantising inside the attention.
+ * A second entry point quantises new K/V into the cache; a third rotates
+ * queries and keys by their positions first and quantises in the same launch.
+ * Everything runs on the caller's CUDA stream; there is no CPU fallback.
  *
  * Sources (reference page "自研RDNA高併發推論引擎 以AI Max+ 395為範例",
  * lcz.me topic 2938):
@@ -31,8 +32,8 @@
  *     piece whose every page was skipped has no keys: its outputs are NaN.
  *   - Device checks surface at the next call: once a kernel has set an error
  *     bit on a device (a bad page id or slot, or a bounded wait that gave up),
- *     every later call of mixattn_kv_append_quant, mixattn_kv_export_blocks,
- *     mixattn_run and mixattn_mixed_attention on that device returns
+ *     every later call of mixattn_kv_append_quant, mixattn_rope_append,
+ *     mixattn_kv_export_blocks, mixattn_run and mixattn_mixed_attention on that device returns
  *     MIXATTN_ERR_DEVICE_CHECK and launches nothing, until
  *     mixattn_device_error(1) clears the word.  The host learns of it through
  *     a pinned, host-mapped flag that the kernels set beside the word, so the
@@ -61,9 +62,32 @@ extern "C" {
 typedef enum {
   MIXATTN_KV_F16 = 0,  /* plain fp16, no scale plane                          */
   MIXATTN_KV_Q8_0 = 1, /* fp16 d = amax/127, int8 q = round(x/d)  (34 B/block) */
-  MIXATTN_KV_Q4_0 = 2  /* fp16 d = m/-8, 4-bit q = min(15, trunc(x/d + 8.5)),
+  MIXATTN_KV_Q4_0 = 2, /* fp16 d = m/-8, 4-bit q = min(15, trunc(x/d + 8.5)),
                           value (q-8)*d; byte k = q_k | q_{k+16} << 4 (18 B)  */
+  /* One fp32 scale d per (page, kv head) over its 32 x head_dim codes; K and V
+   * hold the same format.  See "Page-scaled formats" below. */
+  MIXATTN_KV_I8_PAGE = 3,  /* d >= amax/127, int8 q = round-half-even(x/d)        */
+  MIXATTN_KV_E4M3_PAGE = 4 /* d a power of two, amax <= 448 d, 8-bit float e4m3(x/d) */
 } mixattn_kv_fmt;
+
+/* Pair layout of a rotated head (mixattn_rope_config). */
+typedef enum {
+  MIXATTN_ROPE_HALF = 0,       /* pair i = elements (i, i + rot_dim/2) */
+  MIXATTN_ROPE_INTERLEAVED = 1 /* pair i = elements (2i, 2i + 1)       */
+} mixattn_rope_layout;
+
+/* How the pair frequencies f_i = base^(-2i/rot_dim) are scaled for contexts
+ * longer than the trained one (mixattn_rope_config). */
+typedef enum {
+  MIXATTN_ROPE_SCALE_NONE = 0,
+  MIXATTN_ROPE_SCALE_LINEAR = 1, /* f / factor                                              */
+  MIXATTN_ROPE_SCALE_RAMP = 2,   /* by pair index: kept below the pair that turns `high`
+                                    times in original_ctx tokens, f / factor above the one
+                                    that turns `low` times, a linear ramp between; cosines
+                                    and sines multiplied by 0.1 ln(factor) + 1              */
+  MIXATTN_ROPE_SCALE_BANDS = 3   /* by turns t = original_ctx f / 2 pi: f / factor for
+                                    t <= low, kept for t >= high, linear in t between       */
+} mixattn_rope_scaling;
 
 /* Row kinds of one ForwardBatch (§1). */
 typedef enum {
@@ -96,11 +120,27 @@ typedef void* mixattn_stream;
  * plane, so every page plane is one contiguous, 16-byte aligned run:
  *
  *   quant plane  [num_pages][num_kv_heads][page_size][row_bytes]
- *                row_bytes = 2*head_dim (F16), head_dim (Q8_0), head_dim/2 (Q4_0)
+ *                row_bytes = 2*head_dim (F16), head_dim (Q8_0, I8_PAGE, E4M3_PAGE),
+ *                head_dim/2 (Q4_0)
  *                Q8_0 row: block b = int8 q of elements 32b..32b+31, in order
  *                Q4_0 row: block b = 16 bytes, byte k = q_k | q_{k+16} << 4
  *   scale plane  [num_pages][num_kv_heads][page_size][head_dim/32] fp16 d
- *                (NULL for F16)
+ *                (NULL for F16); I8_PAGE, E4M3_PAGE: [num_pages][num_kv_heads] fp32 d
+ *
+ * Page-scaled formats.  A page holds 32 consecutive positions of one sequence,
+ * and its scale covers all of them, so it can grow while the page fills:
+ *   - an append that writes a page's slot 0 starts the page afresh (its old
+ *     scale and codes count for nothing);
+ *   - otherwise d = max(d_old, the scale its new tokens need), and when d grows
+ *     the page's other codes are rounded again, q' = round(q * (d_old / d)).
+ *     E4M3_PAGE scales are powers of two, so that step is exact but for codes
+ *     that become subnormal; I8_PAGE rounds them by up to half a step more;
+ *   - tokens of one append that share a page (in any order) count together;
+ *   - values beyond +-65504 saturate there, NaN counts as 0 (one such value
+ *     would otherwise spoil the scale of 32 positions).
+ * d and the codes are fp32 arithmetic with IEEE division: amax/127, x * (1/d).
+ * Pages must hold one sequence's positions in order (as the page table does), and
+ * appends to one page must be ordered (same stream, or an event between them).
  *
  * A canonical GGUF-style block (34 / 18 bytes) is the scale followed by that
  * block's quant bytes; mixattn_kv_export_blocks gathers them.
@@ -112,7 +152,7 @@ typedef struct {
   int32_t num_kv_heads; /* > 0                                                   */
   int32_t head_dim;     /* 64 or 128                                             */
   int32_t k_fmt;        /* mixattn_kv_fmt of K                                   */
-  int32_t v_fmt;        /* mixattn_kv_fmt of V                                   */
+  int32_t v_fmt;        /* mixattn_kv_fmt of V (F16 and the page-scaled formats: == k_fmt) */
   void* k_quant;        /* device */
   void* k_scale;        /* device, NULL iff k_fmt == F16 */
   void* v_quant;        /* device */
@@ -125,7 +165,7 @@ typedef struct {
  * Returns the total, or 0 if the dimensions or formats are invalid.
  * Per token and kv head this is 2D (F16), D + D/16 (Q8_0) and D/2 + D/16
  * (Q4_0) bytes for each of K and V: the §2 occupancy table's 2 : 1.0625 :
- * 0.5625 ratio.
+ * 0.5625 ratio; D + 1/8 for the page-scaled formats.
  */
 size_t mixattn_kv_cache_bytes(const mixattn_kv_cache* cache, size_t plane_bytes_out[4]);
 
@@ -142,7 +182,11 @@ size_t mixattn_kv_cache_bytes(const mixattn_kv_cache* cache, size_t plane_bytes_
  *   slot_mapping   device int32 [n_new]; negative = skip (padding token);
  *                  >= num_pages*page_size sets MIXATTN_DEVERR_SLOT, skipped
  *   n_new          >= 0 (0 launches nothing)
- * Two new tokens mapping to one slot race (last writer unspecified).
+ * Two new tokens mapping to one slot race (last writer unspecified); in the
+ * page-scaled formats the later one is kept.  There every window of 8 to 32
+ * tokens looks through the whole slot list for tokens of its pages, so a call's
+ * time has a part that grows with n_new^2 (about a tenth of it at 32768 tokens):
+ * feed longer prompts in several calls.
  */
 int mixattn_kv_append_quant(const mixattn_kv_cache* cache, const void* k_new, const void* v_new,
                             const int32_t* slot_mapping, int32_t n_new, mixattn_stream stream);
@@ -152,10 +196,78 @@ int mixattn_kv_append_quant(const mixattn_kv_cache* cache, const void* k_new, co
  *   which   0 = K, 1 = V
  *   slots   device int32 [n] physical slots (each < num_pages*page_size)
  *   out     device uint8 [n][num_kv_heads][head_dim/32][block_bytes],
- *           block_bytes = 64 (F16), 34 (Q8_0), 18 (Q4_0); no alignment needed
+ *           block_bytes = 64 (F16), 34 (Q8_0), 18 (Q4_0), 36 (page-scaled: the
+ *           page's fp32 scale, then 32 codes); no alignment needed
  */
 int mixattn_kv_export_blocks(const mixattn_kv_cache* cache, int32_t which, const int32_t* slots,
                              int32_t n, void* out, mixattn_stream stream);
+
+/*
+ * Rotary positions.  The first rot_dim elements of a head are rot_dim/2 pairs;
+ * at position p
+ *   (a_i, b_i) -> m (a_i cos w - b_i sin w, b_i cos w + a_i sin w),  w = p f_i,
+ * with m the config's multiplier; the head's other elements are copied.  fp16 in
+ * and out (saturating at +-65504), fp32 products; the angle is taken modulo a
+ * turn in 64-bit fixed point, so far positions lose nothing (f_i is rounded to
+ * 2^-64 of a turn).  Positions may be any int32.
+ */
+typedef struct {
+  int32_t rot_dim;      /* rotated elements of a head: a multiple of 16, <= 128      */
+  int32_t layout;       /* mixattn_rope_layout                                       */
+  int32_t scaling;      /* mixattn_rope_scaling                                      */
+  int32_t original_ctx; /* RAMP, BANDS: tokens of the trained context, > 0           */
+  double base;          /* > 1 (10000 is usual)                                      */
+  double factor;        /* LINEAR, RAMP, BANDS: > 0 (RAMP: >= 1)                     */
+  double low;           /* RAMP, BANDS: turns, 0 < low < high                        */
+  double high;
+  double mscale;        /* multiplier of the cosines and sines; 0 = the scaling's own */
+} mixattn_rope_config;
+
+typedef struct mixattn_rope mixattn_rope;
+
+/* Host table of a config (no device memory; usable on every device and stream,
+ * by several host threads).  rot_dim not a multiple of 16 -> UNSUPPORTED. */
+int mixattn_rope_create(mixattn_rope** rope_out, const mixattn_rope_config* config);
+void mixattn_rope_destroy(mixattn_rope* rope);
+
+/* The scaled frequencies f_i (rot_dim/2 doubles, radians per position) and the
+ * multiplier m; any output may be NULL. */
+int mixattn_rope_info(const mixattn_rope* rope, int32_t* rot_dim, double* frequencies, double* mscale);
+
+/*
+ * Rotate the heads of n_tokens tokens.
+ *   x, out       device fp16, token t's heads at x + t * x_stride (elements),
+ *                [n_heads][head_dim] contiguous; 16-byte aligned, strides a multiple
+ *                of 8 and >= n_heads * head_dim.  out == x with the same stride
+ *                rotates in place; other overlaps are refused where the strides
+ *                are equal and are otherwise the caller's to avoid.
+ *   positions    device int32 [n_tokens]
+ *   head_dim     64 or 128, >= the table's rot_dim
+ */
+int mixattn_rope_apply(const mixattn_rope* rope, const void* x, int64_t x_stride, void* out, int64_t out_stride,
+                       const int32_t* positions, int32_t n_tokens, int32_t n_heads, int32_t head_dim,
+                       mixattn_stream stream);
+
+/*
+ * The same for a step's queries and keys, the rotated keys and the values going
+ * straight into the cache (every format), in one launch.
+ *   q, q_out     as x and out above with num_q_heads heads; num_q_heads == 0
+ *                (q and q_out then ignored) appends only
+ *   k_new, v_new device fp16, token t at k_new + t * k_stride, [num_kv_heads][head_dim]
+ *                contiguous; alignment and strides as above.  q, k_new and v_new may
+ *                be slices of one projection's output.
+ *   positions    device int32 [n_new]
+ *   slot_mapping as for mixattn_kv_append_quant (a skipped token's query is still
+ *                rotated)
+ * The rotated key stays in fp32 until its one rounding to the cache's code (or
+ * fp16), so its error is the format's own; the codes can differ in the last step
+ * from those of mixattn_rope_apply followed by mixattn_kv_append_quant, which
+ * round it to fp16 in between.  q_out must not overlap k_new or v_new.
+ */
+int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope, int32_t num_q_heads, const void* q,
+                        int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new, int64_t k_stride,
+                        const void* v_new, int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping,
+                        int32_t n_new, mixattn_stream stream);
 
 /*
  * Plan: the host-side tiling of one ForwardBatch, reused for every layer.
@@ -273,6 +385,7 @@ int mixattn_workspace_bytes(const mixattn_kv_cache* cache, int32_t num_q_heads, 
  * every GPU that loads the library holds until the process exits, and the tile
  * list is staged in a library-owned host array.  No cudaMalloc, cudaFree,
  * cudaHostAlloc or other allocating routine is called.
+ *   - The page-scaled formats are not built on this path: MIXATTN_ERR_UNSUPPORTED.
  *   - Chunk tiles are never cut into key-range pieces here (that would need
  *     room for their partial results).  A batch whose remaining workspace
  *     exceeds 16 MiB -- at head_dim 128 and 4 q heads per kv head, about 8000

@@ -17,6 +17,9 @@ from dataclasses import dataclass
 from typing import Optional, Sequence
 
 F16, Q8_0, Q4_0 = 0, 1, 2
+I8_PAGE, E4M3_PAGE = 3, 4  # 8-bit codes with one fp32 scale per (page, kv head)
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_RAMP, ROPE_SCALE_BANDS = 0, 1, 2, 3
 ROW_DECODE, ROW_CHUNK = 0, 1
 PAGE = 32
 
@@ -33,6 +36,7 @@ EXPORTED = [
     "mixattn_plan_destroy", "mixattn_mixed_attention", "mixattn_workspace_bytes",
     "mixattn_device_error", "mixattn_status_string", "mixattn_version",
     "mixattn_mixed_attention_noalloc",
+    "mixattn_rope_create", "mixattn_rope_destroy", "mixattn_rope_info", "mixattn_rope_apply", "mixattn_rope_append",
     "mixattn_sched_default_config", "mixattn_sched_create", "mixattn_sched_destroy", "mixattn_sched_submit",
     "mixattn_sched_next_batch", "mixattn_sched_complete", "mixattn_sched_request_info", "mixattn_sched_counts",
 ]
@@ -63,6 +67,15 @@ class KVCacheDesc(ctypes.Structure):
         ("k_fmt", ctypes.c_int32), ("v_fmt", ctypes.c_int32),
         ("k_quant", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
         ("v_quant", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("scaling", ctypes.c_int32), ("original_ctx", ctypes.c_int32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("low", ctypes.c_double), ("high", ctypes.c_double), ("mscale", ctypes.c_double),
     ]
 
 
@@ -115,6 +128,17 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mixattn_status_string.restype = ctypes.c_char_p
     lib.mixattn_version.argtypes = []
     lib.mixattn_version.restype = i32
+    dbl = ctypes.c_double
+    lib.mixattn_rope_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(RopeConfig)]
+    lib.mixattn_rope_create.restype = ctypes.c_int
+    lib.mixattn_rope_destroy.argtypes = [vp]
+    lib.mixattn_rope_destroy.restype = None
+    lib.mixattn_rope_info.argtypes = [vp, i32p, ctypes.POINTER(dbl), ctypes.POINTER(dbl)]
+    lib.mixattn_rope_info.restype = ctypes.c_int
+    lib.mixattn_rope_apply.argtypes = [vp, vp, i64, vp, i64, vp, i32, i32, i32, vp]
+    lib.mixattn_rope_apply.restype = ctypes.c_int
+    lib.mixattn_rope_append.argtypes = [cachep, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp]
+    lib.mixattn_rope_append.restype = ctypes.c_int
     cfgp = ctypes.POINTER(SchedConfig)
     i64p = ctypes.POINTER(ctypes.c_int64)
     lib.mixattn_sched_default_config.argtypes = [cfgp]
@@ -163,11 +187,11 @@ def _ptr(t) -> ctypes.c_void_p:
 
 
 def block_bytes(fmt: int) -> int:
-    return {F16: 64, Q8_0: 34, Q4_0: 18}[fmt]
+    return {F16: 64, Q8_0: 34, Q4_0: 18, I8_PAGE: 36, E4M3_PAGE: 36}[fmt]
 
 
 def row_bytes(fmt: int, head_dim: int) -> int:
-    return {F16: 2 * head_dim, Q8_0: head_dim, Q4_0: head_dim // 2}[fmt]
+    return {F16: 2 * head_dim, Q4_0: head_dim // 2}.get(fmt, head_dim)
 
 
 def cache_desc(num_pages: int, num_kv_heads: int, head_dim: int, k_fmt: int, v_fmt: int,
@@ -243,6 +267,108 @@ def kv_export_blocks(cache: KVCache, which: int, slots, stream=None):
                                          _ptr(out), _stream_handle(stream))
     _check(st, "mixattn_kv_export_blocks")
     return out
+
+
+class Rope:
+    """Rotary-position table: ``rot_dim`` elements of each head, ``layout`` ROPE_HALF
+    (pairs i, i + rot_dim/2) or ROPE_INTERLEAVED (2i, 2i + 1), frequencies
+    base^(-2i/rot_dim) scaled for long contexts (``scaling``, see
+    ``mixattn_rope_scaling``).  Host only: one object serves every stream and device."""
+
+    def __init__(self, rot_dim: int, layout: int = ROPE_HALF, base: float = 10000.0,
+                 scaling: int = ROPE_SCALE_NONE, factor: float = 1.0, original_ctx: int = 0, low: float = 0.0,
+                 high: float = 0.0, mscale: float = 0.0):
+        self._handle = ctypes.c_void_p(0)
+        self._lib = load()
+        cfg = RopeConfig(rot_dim, layout, scaling, original_ctx, base, factor, low, high, mscale)
+        _check(self._lib.mixattn_rope_create(ctypes.byref(self._handle), ctypes.byref(cfg)), "mixattn_rope_create")
+        self.rot_dim, self.layout = int(rot_dim), int(layout)
+
+    def info(self) -> dict:
+        """{"frequencies": radians per position of each pair, "mscale": multiplier}."""
+        f, m = (ctypes.c_double * (self.rot_dim // 2))(), ctypes.c_double()
+        _check(self._lib.mixattn_rope_info(self._handle, None, f, ctypes.byref(m)), "mixattn_rope_info")
+        return {"frequencies": list(f), "mscale": m.value}
+
+    def close(self) -> None:
+        if self._handle and self._handle.value:
+            self._lib.mixattn_rope_destroy(self._handle)
+            self._handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _heads(x, n: int, name: str, heads: Optional[int] = None, head_dim: Optional[int] = None) -> int:
+    """Token stride (elements) of fp16 ``[n, heads, head_dim]`` whose heads are contiguous."""
+    import torch
+    if x.dtype != torch.float16 or x.dim() != 3 or x.shape[0] != n:
+        raise ValueError(f"{name}: fp16 [{n}, heads, head_dim] expected, got {x.dtype} {tuple(x.shape)}")
+    if (heads is not None and x.shape[1] != heads) or (head_dim is not None and x.shape[2] != head_dim):
+        raise ValueError(f"{name}: [{n}, {heads}, {head_dim}] expected, got {tuple(x.shape)}")
+    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return int(x.stride(0)) if n > 1 else int(x.shape[1] * x.shape[2])
+
+
+def _int_list(x, n: int, name: str) -> None:
+    import torch
+    if x.dtype != torch.int32 or x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 [{n}] expected, got {x.dtype} {tuple(x.shape)}")
+
+
+def _same_device(*tensors) -> None:
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for x in tensors:
+        if x is not None and (not x.is_cuda or x.device.index != here):
+            raise ValueError(f"tensors must be on the current CUDA device, got {x.device}")
+
+
+def rope_apply(rope: Rope, x, positions, out=None, stream=None):
+    """Rotate fp16 ``[n, heads, head_dim]`` (token stride free) by int32 ``positions [n]``;
+    ``out`` may be ``x`` itself."""
+    import torch
+    n = int(positions.shape[0])
+    xs = _heads(x, n, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    os_ = _heads(out, n, "out", x.shape[1], x.shape[2])
+    _int_list(positions, n, "positions")
+    _same_device(x, out, positions)
+    st = load().mixattn_rope_apply(rope._handle, _ptr(x), xs, _ptr(out), os_, _ptr(positions), n, int(x.shape[1]),
+                                   int(x.shape[2]), _stream_handle(stream))
+    _check(st, "mixattn_rope_apply")
+    return out
+
+
+def rope_append(cache: KVCache, rope: Rope, q, k_new, v_new, positions, slot_mapping, q_out=None, stream=None):
+    """Rotate a step's queries ``q [n, Hq, D]`` (may be None) and keys ``k_new [n, Hkv, D]`` by
+    int32 ``positions [n]``; the rotated keys and ``v_new`` go into the cache slots
+    ``slot_mapping``.  One launch; returns the rotated queries."""
+    import torch
+    n = int(positions.shape[0])
+    hkv, d = cache.num_kv_heads, cache.head_dim
+    ks, vs = _heads(k_new, n, "k_new", hkv, d), _heads(v_new, n, "v_new", hkv, d)
+    hq = qs = os_ = 0
+    if q is not None:
+        hq, qs = int(q.shape[1]) if q.dim() == 3 else 0, _heads(q, n, "q", None, d)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        os_ = _heads(q_out, n, "q_out", hq, d)
+    else:
+        q_out = None
+    _int_list(positions, n, "positions")
+    _int_list(slot_mapping, n, "slot_mapping")
+    _same_device(q, q_out, k_new, v_new, positions, slot_mapping, cache.k_quant)
+    st = load().mixattn_rope_append(ctypes.byref(cache.desc()), rope._handle, hq, _ptr(q), qs, _ptr(q_out), os_,
+                                    _ptr(k_new), ks, _ptr(v_new), vs, _ptr(positions), _ptr(slot_mapping), n,
+                                    _stream_handle(stream))
+    _check(st, "mixattn_rope_append")
+    return q_out
 
 
 class Plan:

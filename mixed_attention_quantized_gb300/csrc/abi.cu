@@ -12,6 +12,7 @@
 #include <cmath>
 #include <functional>
 #include <mutex>
+#include <new>
 #include <queue>
 #include <vector>
 
@@ -98,7 +99,9 @@ int pending_device_check() {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-bool valid_fmt(int f) { return f == MIXATTN_KV_F16 || f == MIXATTN_KV_Q8_0 || f == MIXATTN_KV_Q4_0; }
+bool valid_fmt(int f) {
+  return f == MIXATTN_KV_F16 || f == MIXATTN_KV_Q8_0 || f == MIXATTN_KV_Q4_0 || page_scaled(f);
+}
 
 // Dimensions and formats only (no pointers).
 int check_cache_dims(const mixattn_kv_cache* c) {
@@ -110,6 +113,8 @@ int check_cache_dims(const mixattn_kv_cache* c) {
   if (!valid_fmt(c->k_fmt) || !valid_fmt(c->v_fmt)) return MIXATTN_ERR_INVALID_ARG;
   const bool kf = c->k_fmt == MIXATTN_KV_F16, vf = c->v_fmt == MIXATTN_KV_F16;
   if (kf != vf) return MIXATTN_ERR_UNSUPPORTED;  // fp16 pairs only with fp16
+  // a page-scaled format pairs only with itself
+  if ((page_scaled(c->k_fmt) || page_scaled(c->v_fmt)) && c->k_fmt != c->v_fmt) return MIXATTN_ERR_UNSUPPORTED;
   if ((int64_t)c->num_pages * kPage > INT32_MAX) return MIXATTN_ERR_INVALID_ARG;
   return MIXATTN_OK;
 }
@@ -126,6 +131,8 @@ int check_cache(const mixattn_kv_cache* c) {
 
 cudaError_t dispatch_attention(int k_fmt, int v_fmt, int head_dim, const AttnParams& p, unsigned int* err,
                                cudaStream_t s) {
+  if (k_fmt == MIXATTN_KV_I8_PAGE) return launch_attention_i8_page(head_dim, p, err, s);
+  if (k_fmt == MIXATTN_KV_E4M3_PAGE) return launch_attention_e4m3_page(head_dim, p, err, s);
   if (k_fmt == MIXATTN_KV_F16) return launch_attention_f16_f16(head_dim, p, err, s);
   if (k_fmt == MIXATTN_KV_Q8_0 && v_fmt == MIXATTN_KV_Q8_0) return launch_attention_q8_q8(head_dim, p, err, s);
   if (k_fmt == MIXATTN_KV_Q4_0 && v_fmt == MIXATTN_KV_Q4_0) return launch_attention_q4_q4(head_dim, p, err, s);
@@ -230,7 +237,7 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
     const int64_t nq = s - o;
     // a short chunk row (speculative verify: q_len * G <= kVerifyMaxRows) runs like decode
     // rows, on split-K tiles of up to 8 (query, head) rows
-    const bool verify = kinds[r] == MIXATTN_ROW_CHUNK && nq * G <= kVerifyMaxRows;
+    const bool verify = kinds[r] == MIXATTN_ROW_CHUNK && (nq * G <= kVerifyMaxRows || page_scaled(c.k_fmt));
     any_verify = any_verify || verify;
     if (kinds[r] == MIXATTN_ROW_CHUNK && !verify) {
       const size_t first_chunk = chunks.size();
@@ -355,7 +362,32 @@ struct mixattn_plan {
   bool copy_recorded = false;
 };
 
+struct mixattn_rope {
+  double freq[kMaxRotPairs] = {};
+  double mscale = 1.0;
+  RopeTable table{};
+};
+
 namespace {
+
+// Tokens' heads in device memory: 16-byte aligned rows of `width` elements every `stride`.
+bool check_token_rows(const void* x, int64_t stride, int64_t width) {
+  return x && aligned(x, 16) && stride >= width && stride % 8 == 0 && stride <= INT64_MAX / 4 / INT32_MAX;
+}
+
+// In place, or rows that share nothing (decided where both strides are equal; one
+// token has no stride).
+bool check_rotate_overlap(const void* x, int64_t xs, const void* out, int64_t os, int64_t width, int64_t n) {
+  if (x == out && (xs == os || n == 1)) return true;
+  if (x == out) return false;
+  if (xs != os && n > 1) return true;
+  const int64_t xa = (int64_t)reinterpret_cast<uintptr_t>(x), oa = (int64_t)reinterpret_cast<uintptr_t>(out);
+  const int64_t step = 2 * xs, w = 2 * width, span = (n - 1) * step + w;
+  if (oa >= xa + span || xa >= oa + span) return true;
+  if (n == 1) return false;
+  const int64_t m = ((oa - xa) % step + step) % step;  // where out's rows start between x's
+  return m >= w && m + w <= step;
+}
 
 int plan_fill(mixattn_plan* p, int32_t n_rows, const int32_t* kinds, const int32_t* seq, const int32_t* off,
               int32_t max_pages, size_t* ws_bytes) {
@@ -403,9 +435,10 @@ size_t mixattn_kv_cache_bytes(const mixattn_kv_cache* c, size_t plane_bytes_out[
   if (check_cache_dims(c) != MIXATTN_OK) return 0;
   const size_t rows = (size_t)c->num_pages * c->num_kv_heads * kPage;
   const size_t kq = rows * quant_row_bytes(c->k_fmt, c->head_dim);
-  const size_t ks = rows * scale_row_bytes(c->k_fmt, c->head_dim);
+  const size_t pages = (size_t)c->num_pages * c->num_kv_heads;
+  const size_t ks = pages * scale_page_bytes(c->k_fmt, c->head_dim);
   const size_t vq = rows * quant_row_bytes(c->v_fmt, c->head_dim);
-  const size_t vs = rows * scale_row_bytes(c->v_fmt, c->head_dim);
+  const size_t vs = pages * scale_page_bytes(c->v_fmt, c->head_dim);
   if (plane_bytes_out) {
     plane_bytes_out[0] = kq;
     plane_bytes_out[1] = ks;
@@ -426,8 +459,131 @@ int mixattn_kv_append_quant(const mixattn_kv_cache* cache, const void* k_new, co
   if ((st = pending_device_check()) != MIXATTN_OK) return st;
   unsigned int* err = error_word();
   if (!err) return MIXATTN_ERR_CUDA;
-  cudaError_t e = launch_kv_append(*cache, k_new, v_new, slot_mapping, n_new, err,
-                                   static_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (page_scaled(cache->k_fmt)) {
+    const int64_t stride = (int64_t)cache->num_kv_heads * cache->head_dim;
+    e = launch_page_append(*cache, nullptr, 0, TokenRows{nullptr, 0}, nullptr, 0,
+                           TokenRows{static_cast<const uint16_t*>(k_new), stride},
+                           TokenRows{static_cast<const uint16_t*>(v_new), stride}, nullptr, slot_mapping, n_new, err,
+                           static_cast<cudaStream_t>(stream));
+  } else {
+    e = launch_kv_append(*cache, k_new, v_new, slot_mapping, n_new, err, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
+}
+
+int mixattn_rope_create(mixattn_rope** rope_out, const mixattn_rope_config* cfg) {
+  if (!rope_out) return MIXATTN_ERR_INVALID_ARG;
+  *rope_out = nullptr;
+  if (!cfg || cfg->rot_dim <= 0 || cfg->rot_dim > 2 * kMaxRotPairs) return MIXATTN_ERR_INVALID_ARG;
+  if (cfg->rot_dim % 16 != 0) return MIXATTN_ERR_UNSUPPORTED;
+  if (cfg->layout != MIXATTN_ROPE_HALF && cfg->layout != MIXATTN_ROPE_INTERLEAVED) return MIXATTN_ERR_INVALID_ARG;
+  auto finite = [](double x) { return std::isfinite(x); };
+  if (!finite(cfg->base) || cfg->base <= 1.0) return MIXATTN_ERR_INVALID_ARG;
+  if (!finite(cfg->mscale) || cfg->mscale < 0.0 || cfg->mscale > 1e4) return MIXATTN_ERR_INVALID_ARG;
+  const int sc = cfg->scaling;
+  if (sc < MIXATTN_ROPE_SCALE_NONE || sc > MIXATTN_ROPE_SCALE_BANDS) return MIXATTN_ERR_INVALID_ARG;
+  if (sc != MIXATTN_ROPE_SCALE_NONE && (!finite(cfg->factor) || cfg->factor < 1e-6)) return MIXATTN_ERR_INVALID_ARG;
+  if (sc == MIXATTN_ROPE_SCALE_RAMP && cfg->factor < 1.0) return MIXATTN_ERR_INVALID_ARG;
+  if (sc == MIXATTN_ROPE_SCALE_RAMP || sc == MIXATTN_ROPE_SCALE_BANDS) {
+    if (cfg->original_ctx <= 0 || !finite(cfg->low) || !finite(cfg->high) || cfg->low <= 0.0 || cfg->high <= cfg->low)
+      return MIXATTN_ERR_INVALID_ARG;
+  }
+  mixattn_rope* r = new (std::nothrow) mixattn_rope();
+  if (!r) return MIXATTN_ERR_CUDA;
+  const int rot = cfg->rot_dim, pairs = rot / 2;
+  const double two_pi = 6.283185307179586476925;
+  double m = 1.0, lo = 0.0, hi = 0.0;
+  if (sc == MIXATTN_ROPE_SCALE_RAMP) {
+    // the pair whose wavelength fits `turns` times into the trained context
+    auto pair_of = [&](double turns) {
+      return rot * std::log(cfg->original_ctx / (turns * two_pi)) / (2.0 * std::log(cfg->base));
+    };
+    lo = std::max(std::floor(pair_of(cfg->high)), 0.0);
+    hi = std::min(std::ceil(pair_of(cfg->low)), (double)(rot - 1));
+    m = 0.1 * std::log(cfg->factor) + 1.0;
+  }
+  for (int i = 0; i < pairs; ++i) {
+    double f = std::pow(cfg->base, -2.0 * i / rot);
+    if (sc == MIXATTN_ROPE_SCALE_LINEAR) {
+      f /= cfg->factor;
+    } else if (sc == MIXATTN_ROPE_SCALE_RAMP) {
+      const double t = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 1e-3)));
+      f = f * (1.0 - t) + f / cfg->factor * t;
+    } else if (sc == MIXATTN_ROPE_SCALE_BANDS) {
+      const double turns = cfg->original_ctx * f / two_pi;
+      const double t = std::min(1.0, std::max(0.0, (turns - cfg->low) / (cfg->high - cfg->low)));
+      f = f * t + f / cfg->factor * (1.0 - t);
+    }
+    r->freq[i] = f;
+    const double turn = f / two_pi - std::floor(f / two_pi);  // [0, 1): whole turns change nothing
+    const double fixed = std::ldexp(turn, 64);  // < 2^64; an integer from 2^52 on
+    r->table.turn[i] = (uint64_t)(fixed < 4503599627370496.0 ? std::floor(fixed + 0.5) : fixed);
+  }
+  r->mscale = cfg->mscale > 0.0 ? cfg->mscale : m;
+  r->table.mscale = (float)r->mscale;
+  r->table.rot = rot;
+  r->table.layout = cfg->layout;
+  *rope_out = r;
+  return MIXATTN_OK;
+}
+
+void mixattn_rope_destroy(mixattn_rope* rope) { delete rope; }
+
+int mixattn_rope_info(const mixattn_rope* rope, int32_t* rot_dim, double* frequencies, double* mscale) {
+  if (!rope) return MIXATTN_ERR_INVALID_ARG;
+  if (rot_dim) *rot_dim = rope->table.rot;
+  if (frequencies) memcpy(frequencies, rope->freq, sizeof(double) * (rope->table.rot / 2));
+  if (mscale) *mscale = rope->mscale;
+  return MIXATTN_OK;
+}
+
+int mixattn_rope_apply(const mixattn_rope* rope, const void* x, int64_t x_stride, void* out, int64_t out_stride,
+                       const int32_t* positions, int32_t n_tokens, int32_t n_heads, int32_t head_dim,
+                       mixattn_stream stream) {
+  if (!rope || n_tokens < 0 || n_heads <= 0) return MIXATTN_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return MIXATTN_ERR_UNSUPPORTED;
+  if (rope->table.rot > head_dim) return MIXATTN_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MIXATTN_OK;
+  const int64_t width = (int64_t)n_heads * head_dim;
+  if (!positions || !aligned(positions, 4)) return MIXATTN_ERR_INVALID_ARG;
+  if (!check_token_rows(x, x_stride, width) || !check_token_rows(out, out_stride, width) ||
+      !check_rotate_overlap(x, x_stride, out, out_stride, width, n_tokens))
+    return MIXATTN_ERR_INVALID_ARG;
+  cudaError_t e = launch_rope(rope->table, TokenRows{static_cast<const uint16_t*>(x), x_stride},
+                              static_cast<uint16_t*>(out), out_stride, positions, n_tokens, n_heads, head_dim,
+                              static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
+}
+
+int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope, int32_t num_q_heads, const void* q,
+                        int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new, int64_t k_stride,
+                        const void* v_new, int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping,
+                        int32_t n_new, mixattn_stream stream) {
+  int st = check_cache(cache);
+  if (st != MIXATTN_OK) return st;
+  if (!rope || n_new < 0 || num_q_heads < 0) return MIXATTN_ERR_INVALID_ARG;
+  if (rope->table.rot > cache->head_dim) return MIXATTN_ERR_INVALID_ARG;
+  if (n_new == 0) return MIXATTN_OK;
+  const int64_t kw = (int64_t)cache->num_kv_heads * cache->head_dim, qw = (int64_t)num_q_heads * cache->head_dim;
+  if (!positions || !slot_mapping || !aligned(positions, 4) || !aligned(slot_mapping, 4))
+    return MIXATTN_ERR_INVALID_ARG;
+  if (!check_token_rows(k_new, k_stride, kw) || !check_token_rows(v_new, v_stride, kw)) return MIXATTN_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && (!check_token_rows(q, q_stride, qw) || !check_token_rows(q_out, q_out_stride, qw) ||
+                          !check_rotate_overlap(q, q_stride, q_out, q_out_stride, qw, n_new)))
+    return MIXATTN_ERR_INVALID_ARG;
+  if ((st = pending_device_check()) != MIXATTN_OK) return st;
+  unsigned int* err = error_word();
+  if (!err) return MIXATTN_ERR_CUDA;
+  const TokenRows qr{static_cast<const uint16_t*>(q), q_stride}, kr{static_cast<const uint16_t*>(k_new), k_stride},
+      vr{static_cast<const uint16_t*>(v_new), v_stride};
+  uint16_t* qo = static_cast<uint16_t*>(q_out);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = page_scaled(cache->k_fmt)
+                      ? launch_page_append(*cache, &rope->table, num_q_heads, qr, qo, q_out_stride, kr, vr, positions,
+                                           slot_mapping, n_new, err, s)
+                      : launch_rope_append(*cache, rope->table, num_q_heads, qr, qo, q_out_stride, kr, vr, positions,
+                                           slot_mapping, n_new, err, s);
   return e == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
 }
 

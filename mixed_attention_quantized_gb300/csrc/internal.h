@@ -80,12 +80,16 @@ MIXATTN_HD int decode_pages_per_warp(int n_pages) {
 
 MIXATTN_HD int decode_pages_per_split(int n_pages) { return kWarps * decode_pages_per_warp(n_pages); }
 
+// Formats with one fp32 scale per (page, kv head).
+MIXATTN_HD bool page_scaled(int fmt) { return fmt == MIXATTN_KV_I8_PAGE || fmt == MIXATTN_KV_E4M3_PAGE; }
+
 MIXATTN_HD int quant_row_bytes(int fmt, int head_dim) {
-  return fmt == MIXATTN_KV_F16 ? 2 * head_dim : (fmt == MIXATTN_KV_Q8_0 ? head_dim : head_dim / 2);
+  return fmt == MIXATTN_KV_F16 ? 2 * head_dim : (fmt == MIXATTN_KV_Q4_0 ? head_dim / 2 : head_dim);
 }
 
-MIXATTN_HD int scale_row_bytes(int fmt, int head_dim) {
-  return fmt == MIXATTN_KV_F16 ? 0 : 2 * (head_dim / kBlock);
+// Scale bytes of one page of one kv head.
+MIXATTN_HD int scale_page_bytes(int fmt, int head_dim) {
+  return fmt == MIXATTN_KV_F16 ? 0 : (page_scaled(fmt) ? 4 : kPage * 2 * (head_dim / kBlock));
 }
 
 // Workspace layout of one plan (byte offsets from the workspace base).
@@ -151,6 +155,22 @@ struct AttnParams {
   int32_t slot_rows = 0;      // rows of a decode partial slot (0: group)
 };
 
+// Rotary positions (rope.cuh): frequencies as 64-bit fractions of a turn, passed to
+// kernels by value.
+constexpr int kMaxRotPairs = 64;
+struct RopeTable {
+  uint64_t turn[kMaxRotPairs];  // round(2^64 f_i / 2 pi)
+  float mscale;
+  int32_t rot;                  // rotated elements of a head (0: none)
+  int32_t layout;               // mixattn_rope_layout
+};
+
+// New tokens of one tensor for the append kernels: token t's heads at x + t * stride.
+struct TokenRows {
+  const uint16_t* x;  // fp16
+  int64_t stride;     // elements
+};
+
 // First key a query at position `pos` sees (0 without a window).
 MIXATTN_HD int window_first_key(int pos, int window) {
   return (window > 0 && pos + 1 > window) ? pos + 1 - window : 0;
@@ -169,11 +189,25 @@ MIXATTN_DECLARE_LAUNCH(launch_attention_q8_q8)
 MIXATTN_DECLARE_LAUNCH(launch_attention_q4_q4)
 MIXATTN_DECLARE_LAUNCH(launch_attention_q8_q4)
 MIXATTN_DECLARE_LAUNCH(launch_attention_q4_q8)
+MIXATTN_DECLARE_LAUNCH(launch_attention_i8_page)
+MIXATTN_DECLARE_LAUNCH(launch_attention_e4m3_page)
 #undef MIXATTN_DECLARE_LAUNCH
 cudaError_t launch_kv_append(const mixattn_kv_cache& c, const void* k_new, const void* v_new,
                              const int32_t* slots, int32_t n_new, unsigned int* err, cudaStream_t s);
 cudaError_t launch_kv_export(const mixattn_kv_cache& c, int which, const int32_t* slots, int32_t n,
                              void* out, unsigned int* err, cudaStream_t s);
+cudaError_t launch_rope(const RopeTable& t, const TokenRows& x, uint16_t* out, int64_t out_stride,
+                        const int32_t* positions, int32_t n_tokens, int32_t n_heads, int32_t head_dim, cudaStream_t s);
+// The append of a step; hq == 0: no queries.  launch_page_append takes the page-scaled
+// formats (`rope` NULL: keys as they are), launch_rope_append the others.
+cudaError_t launch_rope_append(const mixattn_kv_cache& c, const RopeTable& t, int hq, const TokenRows& q,
+                               uint16_t* q_out, int64_t q_out_stride, const TokenRows& k, const TokenRows& v,
+                               const int32_t* positions, const int32_t* slots, int32_t n_new, unsigned int* err,
+                               cudaStream_t s);
+cudaError_t launch_page_append(const mixattn_kv_cache& c, const RopeTable* rope, int hq, const TokenRows& q,
+                               uint16_t* q_out, int64_t q_out_stride, const TokenRows& k, const TokenRows& v,
+                               const int32_t* positions, const int32_t* slots, int32_t n_new, unsigned int* err,
+                               cudaStream_t s);
 
 }  // namespace mixattn
 #endif  // __CUDACC__

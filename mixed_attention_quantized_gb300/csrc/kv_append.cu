@@ -15,6 +15,7 @@
 // quant store of a warp is one contiguous, coalesced run.
 #include <cuda_runtime.h>
 
+#include "block_encode.cuh"
 #include "device_utils.cuh"
 #include "internal.h"
 
@@ -33,8 +34,6 @@ struct AppendArgs {
   int32_t num_slots;     // num_pages * 32
   unsigned int* err;
 };
-
-__device__ __forceinline__ float h2f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 
 template <int FMT>
 __device__ __forceinline__ void encode_group(const AppendArgs& a, int64_t group, int lane) {
@@ -66,64 +65,8 @@ __device__ __forceinline__ void encode_group(const AppendArgs& a, int64_t group,
     if (slot >= 0) {
       *reinterpret_cast<uint2*>(a.quant + row * (int64_t)(a.nb * 64) + b * 64 + 8 * sub) = raw;
     }
-    return;
-  } else if constexpr (FMT == MIXATTN_KV_Q8_0) {
-    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const float d = __fdiv_rn(amax, 127.0f);
-    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
-    uint32_t packed = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = (int)roundf(__fmul_rn(v[i], id));
-      packed |= (uint32_t)(uint8_t)(int8_t)q << (8 * i);
-    }
-    if (slot >= 0) {
-      *reinterpret_cast<uint32_t*>(a.quant + row * (int64_t)(a.nb * 32) + b * 32 + 4 * sub) = packed;
-      if (sub == 0) a.scale[row * a.nb + b] = __half_as_ushort(__float2half_rn(d));
-    }
-  } else {  // Q4_0
-    // element of largest magnitude, lowest index on ties
-    float best_abs = -1.0f, best_val = 0.0f;
-    int best_idx = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float m = fabsf(v[i]);
-      if (m > best_abs) {
-        best_abs = m;
-        best_val = v[i];
-        best_idx = 4 * sub + i;
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      const float oa = __shfl_xor_sync(0xFFFFFFFFu, best_abs, o);
-      const float ov = __shfl_xor_sync(0xFFFFFFFFu, best_val, o);
-      const int oi = __shfl_xor_sync(0xFFFFFFFFu, best_idx, o);
-      if (oa > best_abs || (oa == best_abs && oi < best_idx)) {
-        best_abs = oa;
-        best_val = ov;
-        best_idx = oi;
-      }
-    }
-    const float m = best_abs > 0.0f ? best_val : 0.0f;  // an all-zero block keeps m = +0
-    const float d = __fdiv_rn(m, -8.0f);
-    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
-    uint32_t q4 = 0;  // four nibbles, one per byte
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float s = __fadd_rn(__fmul_rn(v[i], id), 8.5f);
-      int q = (int)truncf(s);
-      q = q > 15 ? 15 : q;
-      q4 |= (uint32_t)q << (8 * i);
-    }
-    // element k (lanes 0-3 of the 8) pairs with element k+16 (lanes 4-7)
-    const uint32_t hi = __shfl_down_sync(0xFFFFFFFFu, q4, 4);
-    if (slot >= 0 && sub < 4) {
-      *reinterpret_cast<uint32_t*>(a.quant + row * (int64_t)(a.nb * 16) + b * 16 + 4 * sub) = q4 | (hi << 4);
-    }
-    if (slot >= 0 && sub == 0) a.scale[row * a.nb + b] = __half_as_ushort(__float2half_rn(d));
+  } else {
+    encode_block<FMT>(a.quant, a.scale, v, row, b, a.nb, sub, slot >= 0);
   }
 }
 
@@ -155,7 +98,8 @@ __global__ void __launch_bounds__(256) kv_export_kernel(ExportArgs a) {
   const int64_t g = (i / a.nb) % a.hkv;
   const int64_t s = i / ((int64_t)a.nb * a.hkv);
   const int32_t slot = a.slots[s];
-  const int bb = a.fmt == MIXATTN_KV_F16 ? 64 : (a.fmt == MIXATTN_KV_Q8_0 ? 34 : 18);
+  const bool paged = page_scaled(a.fmt);
+  const int bb = a.fmt == MIXATTN_KV_F16 ? 64 : (paged ? 36 : (a.fmt == MIXATTN_KV_Q8_0 ? 34 : 18));
   uint8_t* dst = a.out + i * bb;
   if (slot < 0 || slot >= a.num_slots) {
     set_device_error(a.err, MIXATTN_DEVERR_SLOT);
@@ -166,6 +110,13 @@ __global__ void __launch_bounds__(256) kv_export_kernel(ExportArgs a) {
   if (a.fmt == MIXATTN_KV_F16) {
     const uint8_t* src = a.quant + row * (int64_t)(a.nb * 64) + b * 64;
     for (int j = 0; j < 64; ++j) dst[j] = src[j];
+    return;
+  }
+  if (paged) {  // the page's fp32 scale (row / 32 = page * hkv + head), then the 32 codes
+    const uint32_t d = reinterpret_cast<const uint32_t*>(a.scale)[row / kPage];
+    for (int j = 0; j < 4; ++j) dst[j] = (uint8_t)(d >> (8 * j));
+    const uint8_t* src = a.quant + row * (int64_t)(a.nb * 32) + b * 32;
+    for (int j = 0; j < 32; ++j) dst[4 + j] = src[j];
     return;
   }
   const uint16_t d = a.scale[row * a.nb + b];

@@ -71,6 +71,8 @@ int check_cache_noalloc(const mixattn_kv_cache* c) {
   if (c->head_dim % kBlock != 0) return MIXATTN_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return MIXATTN_ERR_UNSUPPORTED;
   auto ok_fmt = [](int f) { return f == MIXATTN_KV_F16 || f == MIXATTN_KV_Q8_0 || f == MIXATTN_KV_Q4_0; };
+  // the page-scaled formats' tiles are not built on this path
+  if (page_scaled(c->k_fmt) && page_scaled(c->v_fmt)) return MIXATTN_ERR_UNSUPPORTED;
   if (!ok_fmt(c->k_fmt) || !ok_fmt(c->v_fmt)) return MIXATTN_ERR_INVALID_ARG;
   if ((c->k_fmt == MIXATTN_KV_F16) != (c->v_fmt == MIXATTN_KV_F16)) return MIXATTN_ERR_UNSUPPORTED;
   if ((int64_t)c->num_pages * kPage > INT32_MAX) return MIXATTN_ERR_INVALID_ARG;
