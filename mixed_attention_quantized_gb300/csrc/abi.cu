@@ -204,7 +204,7 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   const int G = hq / c.num_kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return MIXATTN_ERR_UNSUPPORTED;
   const int hkv = c.num_kv_heads;
-  const int T = kChunkM / G;  // query tokens per chunk tile
+  const int T = chunk_rows(c.k_fmt) / G;  // query tokens per chunk tile
   const int QPG = kMaxGroup / G;  // queries per decode-style tile of a verify row
   bool any_verify = false;
 
@@ -237,7 +237,7 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
     const int64_t nq = s - o;
     // a short chunk row (speculative verify: q_len * G <= kVerifyMaxRows) runs like decode
     // rows, on split-K tiles of up to 8 (query, head) rows
-    const bool verify = kinds[r] == MIXATTN_ROW_CHUNK && (nq * G <= kVerifyMaxRows || page_scaled(c.k_fmt));
+    const bool verify = kinds[r] == MIXATTN_ROW_CHUNK && nq * G <= kVerifyMaxRows;
     any_verify = any_verify || verify;
     if (kinds[r] == MIXATTN_ROW_CHUNK && !verify) {
       const size_t first_chunk = chunks.size();
@@ -317,7 +317,8 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   T2.n_chunk = (int32_t)n_pieces;
   T2.n_decode = (int32_t)decodes.size();
   T2.slot_rows = any_verify ? kMaxGroup : G;
-  T2.L = workspace_layout(n_rows, (int)n_tiles, T2.n_decode, T2.slot_rows, c.head_dim, any_split);
+  T2.L = workspace_layout(n_rows, (int)n_tiles, T2.n_decode, T2.slot_rows, c.head_dim, any_split,
+                          chunk_rows(c.k_fmt));
   T2.image.assign(T2.L.upload_end - T2.L.rows, 0);
   memcpy(T2.image.data(), rows.data(), sizeof(RowInfo) * rows.size());
   TileDesc* td = reinterpret_cast<TileDesc*>(T2.image.data() + (T2.L.tiles - T2.L.rows));

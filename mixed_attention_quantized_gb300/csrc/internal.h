@@ -26,6 +26,7 @@ constexpr int kFusedThreads = 512; // threads of a fused-launch CTA: three worki
                                    // an MMA/producer group on a chunk tile; a decode tile uses
                                    // the first kThreads
 constexpr int kChunkM = 128;       // rows (query tokens x group heads) of a chunk tile
+constexpr int kPageChunkM = 256;   // the same for the page-scaled formats: two 128-row query tiles
 constexpr int kChunkN = 128;       // keys per KV tile of the chunk path (4 pages)
 constexpr int kPagesPerKvTile = kChunkN / kPage;
 constexpr int kMaxGroup = 8;       // q heads per kv head held in one mma N=8 tile
@@ -101,16 +102,19 @@ struct WorkspaceLayout {
                           // chunk-piece tickets
   size_t upload_end;      // end of the block copied from the plan's host buffer
   size_t partials;        // float[n_decode_tiles][slot_rows][head_dim + 2]
-  size_t chunk_partials;  // float[n_chunk_tiles][128][head_dim + 2] when any chunk tile is split
+  size_t chunk_partials;  // float[n_chunk_tiles][chunk rows][head_dim + 2] when any chunk tile is split
   size_t total;
 };
+
+// Rows of a chunk tile (query tokens x group heads).
+MIXATTN_HD int chunk_rows(int fmt) { return page_scaled(fmt) ? kPageChunkM : kChunkM; }
 
 MIXATTN_HD size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // slot_rows: rows of one decode partial slot, G (every decode-kind tile holds one
 // query) or 8 when the plan has verify groups
 MIXATTN_HD WorkspaceLayout workspace_layout(int n_rows, int n_tiles, int n_decode_tiles, int slot_rows,
-                                            int head_dim, bool chunk_split) {
+                                            int head_dim, bool chunk_split, int chunk_m = kChunkM) {
   const size_t n_chunk = (size_t)(n_tiles - n_decode_tiles);
   WorkspaceLayout L;
   L.rows = 256;
@@ -120,7 +124,7 @@ MIXATTN_HD WorkspaceLayout workspace_layout(int n_rows, int n_tiles, int n_decod
   L.partials = align_up(L.upload_end, 256);
   L.chunk_partials =
       align_up(L.partials + sizeof(float) * (size_t)n_decode_tiles * slot_rows * (head_dim + 2), 256);
-  L.total = align_up(L.chunk_partials + (chunk_split ? sizeof(float) * n_chunk * kChunkM * (head_dim + 2) : 0), 256);
+  L.total = align_up(L.chunk_partials + (chunk_split ? sizeof(float) * n_chunk * chunk_m * (head_dim + 2) : 0), 256);
   return L;
 }
 
@@ -137,8 +141,8 @@ struct AttnParams {
   const TileDesc* tiles;
   uint32_t* counters;         // [n_decode_tiles] split tickets, then one per chunk tile (piece tickets)
   float* partials;            // [n_decode_tiles][slot_rows][D + 2]
-  float* chunk_partials;      // O [n_chunk_tiles][128][D], then (m, l) [n_chunk_tiles][128] of the
-                              // pieces of cut chunk tiles
+  float* chunk_partials;      // O [n_chunk_tiles][M][D], then (m, l) [n_chunk_tiles][M] of the
+                              // pieces of cut chunk tiles, M = chunk_rows(format)
   uint32_t* chunk_counters;   // [n_chunk_tiles]: piece tickets, indexed by a tile's first piece
   int32_t max_pages;
   int32_t num_pages;

@@ -339,16 +339,534 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
   }
 }
 
+// ===========================================================================
+// Chunk tiles
+// ===========================================================================
+//
+// A tile is 256 rows (256/G query tokens x G heads of one kv head) as two 128-row query
+// tiles A and B that share every converted K and V tile of 128 keys.  Codes are exact in
+// fp16, so one MMA a step does (the block formats' chunk tiles need a high and a low one),
+// and a KV tile's four pages are the four 32-column chunks in which the softmax reads its
+// scores: each chunk takes one (factor, offset) pair.  Roles of the 16 warps:
+//   softmax A (warps 0-3) and B (4-7), thread = TMEM lane = query row: row maximum and
+//     P' of S as fp16 over the scores already read; O rescaled only when a row's
+//     maximum passed its reference by more than 2^8; then the output;
+//   conversion (8-11): K and V codes from the cache planes, one tile ahead in
+//     registers, as fp16 into 128-byte-swizzled operand tiles, two buffers each;
+//   MMA (one thread of warp 12): PV_A(j-1) QK_A(j) PV_B(j-1) QK_B(j), so each query
+//     tile's softmax runs beside the other's MMAs.
+// The MMAs of one thread run in issue order and a commit covers all that were issued
+// before it: S_A(j) complete therefore means that PV_A(j-1) is too (O may be rescaled),
+// and QK_B(j) complete that K(j) and V(j-1) have been read.
+// TMEM: S_A | S_B | O_A | O_B, 128 columns each, P' over the first half of its S.
+// No role waits at a CTA barrier inside its loop; every wait is on an mbarrier, bounded,
+// and a role that gives up leaves its loops, after which the others' waits run out.
+template <int D>
+struct PageChunkSmem {
+  static constexpr int kTile = 128 * D * 2;  // fp16 [D/64][128 rows][128 B], swizzled
+  static constexpr int kQ = 0;               // query tiles A, B
+  static constexpr int kK = 2 * kTile;       // K(j) in buffer j % 2
+  static constexpr int kV = 4 * kTile;
+  static constexpr int kBar = 6 * kTile;
+  static constexpr int kTotal = kBar + 256 + 1024;  // + slack for 1024-byte alignment
+};
+
+// Sixteen codes as two 16-byte chunks of fp16 values.
+template <int F>
+__device__ __forceinline__ void codes16_to_half(const uint4& c, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (F == MIXATTN_KV_I8_PAGE) {
+      s8x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
+    } else {
+      asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+          : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+          : "r"(w[i]));
+    }
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// mbar_wait for a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* err) {
+  const bool ok = mbar_wait(bar, parity, err);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// The score factor, log2 dv and 1/dv of the page `pid` for kv head g.  A page outside the
+// cache (or past the row's keys) gets the offset -inf: its keys weigh nothing.
+struct PageTerms {
+  float a, b, inv;
+};
+__device__ __forceinline__ PageTerms page_terms(const AttnParams& p, int pid, int g) {
+  PageTerms r{1e-30f, -CUDART_INF_F, 0.f};
+  if (pid >= 0 && pid < p.num_pages) {
+    const int64_t at = (int64_t)pid * p.hkv + g;
+    const float dk = reinterpret_cast<const float*>(p.k_scale)[at];
+    const float dv = reinterpret_cast<const float*>(p.v_scale)[at];
+    r.a = fmaxf(dk * p.scale_log2, 1e-30f);  // a page of zero keys: scores 0, and -inf stays -inf
+    r.b = dv > 0.f ? log2f(dv) : 0.f;
+    r.inv = dv > 0.f ? __fdiv_rn(1.f, dv) : 1.f;
+  }
+  return r;
+}
+
+template <int F, int D>
+__device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int n_ctas, uint8_t* smem_raw,
+                                               unsigned int* err) {
+  using L = PageChunkSmem<D>;
+  constexpr uint32_t kTmemCols = 512, kOCol = 256;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* q_ready = bars;       // [2] query tile A / B of the next tile written   (4 warps)
+  uint64_t* qk_done = bars + 2;   // [2] S of A / B complete                          (commit)
+  uint64_t* p_ready = bars + 4;   // [2] P' of A / B written, O rescaled              (4 warps)
+  uint64_t* o_done = bars + 6;    // [2] the tile's last PV of A / B complete         (commit)
+  uint64_t* k_ready = bars + 8;   // [2] K(jg) in buffer jg % 2                       (4 warps)
+  uint64_t* v_ready = bars + 10;  // [2] V(jg) in buffer jg % 2                       (4 warps)
+  uint64_t* kv_free = bars + 12;  // [2] K(jg) and V(jg-1) read                       (commit)
+  uint64_t* mma_fin = bars + 14;  // every MMA of the CTA complete                    (commit)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.group, lg = p.log2_group;
+  const int n_rounds = (p.n_chunk_tiles + n_ctas - 1) / n_ctas;
+  if (tid == 0) {
+    for (int i = 0; i < 15; ++i) {
+      const bool commits = (i >= 2 && i < 4) || (i >= 6 && i < 8) || i >= 12;
+      mbar_init(bars + i, commits ? 1 : 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 8) {
+    // ======================= softmax A / B =======================
+    const int gq = warp >> 2;
+    const int row = tid & 127;
+    const int tok = (gq * 128 + row) >> lg, head = row & (G - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + 128 * gq;
+    const uint32_t o_col = tmem + lane_base + kOCol + 128 * gq;
+    const uint32_t ninf = __float_as_uint(-CUDART_INF_F);
+    bool ok = true;
+    uint32_t n_qk = 0, n_tile = 0;  // S tiles and chunk tiles this group has taken (barrier phases)
+    // the CTA's next round >= k with a tile in which this query tile has rows
+    auto next_round = [&](int k) {
+      for (; k < n_rounds; ++k) {
+        const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
+        if (idx >= 0 && (gq == 0 || p.tiles[idx].count * G > 128)) break;
+      }
+      return k;
+    };
+    auto write_q = [&](int k) {
+      const TileDesc t = p.tiles[chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles)];
+      const RowInfo ri = p.rows[t.row];
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                            ((int64_t)(ri.q_start + t.begin + min(tok, t.count - 1)) * p.hq + (int64_t)t.kvh * G + head) * D;
+      uint8_t* dst = smem + L::kQ + gq * L::kTile;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 w = tok < t.count ? ldg_u128(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + sw128_off(row, c & 7)) = w;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready[gq]);
+    };
+    int k = next_round(0);
+    if (k < n_rounds) write_q(k);
+    while (ok && k < n_rounds) {
+      const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
+      const TileDesc t = p.tiles[idx];
+      const RowInfo ri = p.rows[t.row];
+      const bool row_valid = tok < t.count;
+      const int pos = ri.q_offset + t.begin + min(tok, t.count - 1);
+      const int lo = window_first_key(pos, p.window);
+      const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
+      const int n_pages = (min(ri.seq_len, ri.q_offset + t.begin + t.count) + kPage - 1) / kPage;
+      const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages;
+      // lane l holds the terms of page l % 4 of the tile: this one's, and the next one's page id
+      auto pid_of = [&](int j) {
+        const int pg = (kv0 + j) * kPagesPerKvTile + (lane & 3);
+        return ldg_s32_or(pt_row + pg, j < n_kv && pg < n_pages, -1);
+      };
+      PageTerms next = page_terms(p, pid_of(0), t.kvh);
+      int next_pid = pid_of(1);
+      float m_run = -CUDART_INF_F, l_run = 0.f;
+      for (int j = 0; j < n_kv; ++j) {
+        const PageTerms mine = next;
+        ok = warp_wait(&qk_done[gq], n_qk & 1, err);
+        if (!ok) break;
+        ++n_qk;
+        tc_fence_after();
+        if (j + 1 < n_kv) {
+          next = page_terms(p, next_pid, t.kvh);
+          next_pid = pid_of(j + 2);
+        }
+        const int kbase = (kv0 + j) * kChunkN;
+        const bool diag = __any_sync(0xFFFFFFFFu, kbase + kChunkN - 1 > pos || kbase < lo);
+        uint32_t a[32];
+        // pass 1: the row's largest x of the tile
+        float m_tile = -CUDART_INF_F;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(s_col + 32 * c, a);
+          const float ca = __shfl_sync(0xFFFFFFFFu, mine.a, c), cb = __shfl_sync(0xFFFFFFFFu, mine.b, c);
+          tmem_wait_ld();
+          if (diag) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) a[e] = ninf;
+          }
+          float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            mx0 = fmax3(mx0, __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+            mx1 = fmax3(mx1, __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
+          }
+          m_tile = fmaxf(m_tile, fmaf(fmaxf(mx0, mx1), ca, cb));
+        }
+        // the reference moves only when P' would pass 2^8: O is then rescaled (PV(j-1) is
+        // complete, see above; a tile's first PV overwrites O)
+        const bool grow = m_tile > m_run + 8.f;
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float alpha = grow ? ex2(m_run - m_tile) : 1.f;
+          m_run = grow ? m_tile : m_run;
+          l_run *= alpha;
+          if (j > 0) {
+            const uint64_t al2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              tmem_ld32(o_col + 32 * ch, a);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float y0, y1;
+                f2_unpack(fmul2(f2_pack(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), al2), y0, y1);
+                a[e] = __float_as_uint(y0);
+                a[e + 1] = __float_as_uint(y1);
+              }
+              tmem_st32(o_col + 32 * ch, a);
+            }
+          }
+        }
+        const float mref = m_run == -CUDART_INF_F ? 0.f : m_run;
+        // pass 2: P' = 2^(x - m) as fp16 over the scores already read; sums in fp32
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(s_col + 32 * c, a);
+          const float ca = __shfl_sync(0xFFFFFFFFu, mine.a, c);
+          const float cb = __shfl_sync(0xFFFFFFFFu, mine.b, c) - mref;
+          const float ci = __shfl_sync(0xFFFFFFFFu, mine.inv, c);
+          const uint64_t ca2 = f2_pack(ca, ca), cb2 = f2_pack(cb, cb);
+          tmem_wait_ld();
+          if (diag) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) a[e] = ninf;
+          }
+          uint64_t sum_a = f2_pack(0.f, 0.f), sum_b = sum_a;
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float x0, x1, x2, x3;
+            f2_unpack(ffma2(f2_pack(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), ca2, cb2), x0, x1);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])), ca2, cb2), x2, x3);
+            const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+            sum_a = fadd2(sum_a, f2_pack(p0, p1));
+            sum_b = fadd2(sum_b, f2_pack(p2, p3));
+            pk[e >> 1] = pack_f16x2(p0, p1);
+            pk[(e >> 1) + 1] = pack_f16x2(p2, p3);
+          }
+          tmem_st16(s_col + 16 * c, pk);
+          float s0, s1, s2, s3;
+          f2_unpack(sum_a, s0, s1);
+          f2_unpack(sum_b, s2, s3);
+          l_run = fmaf((s0 + s1) + (s2 + s3), ci, l_run);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[gq]);
+      }
+      if (!ok) break;
+      // the next tile's Q (this tile's last QK is complete), then this tile's output
+      const int kn = next_round(k + 1);
+      if (kn < n_rounds) write_q(kn);
+      ok = warp_wait(&o_done[gq], n_tile & 1, err);
+      ++n_tile;
+      if (!ok) break;
+      tc_fence_after();
+      uint16_t* dst = static_cast<uint16_t*>(p.o) +
+                      ((int64_t)(ri.q_start + t.begin + tok) * p.hq + (int64_t)t.kvh * G + head) * D;
+      if (t.nsplit == 1) {
+        const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t v[32];
+          tmem_ld32(o_col + 32 * ch, v);
+          tmem_wait_ld();
+          if (row_valid) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_f16x2_out(__uint_as_float(v[8 * q4 + 2 * e]) * inv_l, __uint_as_float(v[8 * q4 + 2 * e + 1]) * inv_l);
+              *reinterpret_cast<uint4*>(dst + 32 * ch + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      } else {
+        // a piece of a cut tile leaves (m, l, O) of its rows; each warp's rows are merged by
+        // the last piece's same warp to finish (a 4-bit ticket per warp, in the words of the
+        // tile's first piece)
+        const int64_t n_o = (int64_t)p.n_chunk_tiles * kPageChunkM * D;
+        const int prow = gq * 128 + row;
+        float* o_part = p.chunk_partials + ((int64_t)idx * kPageChunkM + prow) * D;
+        float* ml_part = p.chunk_partials + n_o + ((int64_t)idx * kPageChunkM + prow) * 2;
+        ml_part[0] = m_run;
+        ml_part[1] = l_run;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t v[32];
+          tmem_ld32(o_col + 32 * ch, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q4 = 0; q4 < 8; ++q4)
+            *reinterpret_cast<uint4*>(o_part + 32 * ch + 4 * q4) =
+                make_uint4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+        }
+        __threadfence();
+        __syncwarp();
+        const int first = idx - t.part;
+        unsigned ticket = 0;
+        if (lane == 0) ticket = (atomicAdd(&p.chunk_counters[first], 1u << (4 * warp)) >> (4 * warp)) & 15u;
+        ticket = __shfl_sync(0xFFFFFFFFu, ticket, 0);
+        if (ticket == (unsigned)(t.nsplit - 1)) {
+          __threadfence();
+          const float* ml0 = p.chunk_partials + n_o + ((int64_t)first * kPageChunkM + prow) * 2;
+          const float* o0 = p.chunk_partials + ((int64_t)first * kPageChunkM + prow) * D;
+          float m_all = -CUDART_INF_F;
+          for (int q = 0; q < t.nsplit; ++q) m_all = fmaxf(m_all, __ldcg(ml0 + (int64_t)q * kPageChunkM * 2));
+          float w[4], l_all = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            w[q] = 0.f;
+            if (q < t.nsplit) {
+              const float mq = __ldcg(ml0 + (int64_t)q * kPageChunkM * 2);
+              w[q] = mq == -CUDART_INF_F ? 0.f : ex2(mq - m_all);
+              l_all += w[q] * __ldcg(ml0 + (int64_t)q * kPageChunkM * 2 + 1);
+            }
+          }
+          const float inv_l = 1.f / l_all;
+          if (row_valid) {
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 8) {
+              float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (q >= t.nsplit || w[q] == 0.f) continue;  // (a piece without keys holds no O)
+                const float* op = o0 + (int64_t)q * kPageChunkM * D + d0;
+                const float4 x0 = __ldcg(reinterpret_cast<const float4*>(op));
+                const float4 x1 = __ldcg(reinterpret_cast<const float4*>(op + 4));
+                acc[0] += w[q] * x0.x; acc[1] += w[q] * x0.y; acc[2] += w[q] * x0.z; acc[3] += w[q] * x0.w;
+                acc[4] += w[q] * x1.x; acc[5] += w[q] * x1.y; acc[6] += w[q] * x1.z; acc[7] += w[q] * x1.w;
+              }
+              *reinterpret_cast<uint4*>(dst + d0) =
+                  make_uint4(pack_f16x2_out(acc[0] * inv_l, acc[1] * inv_l), pack_f16x2_out(acc[2] * inv_l, acc[3] * inv_l),
+                             pack_f16x2_out(acc[4] * inv_l, acc[5] * inv_l), pack_f16x2_out(acc[6] * inv_l, acc[7] * inv_l));
+            }
+          }
+        }
+      }
+      // O has been read: this warp's next p_ready lets the next tile's first PV overwrite it
+      tc_fence_before();
+      k = kn;
+    }
+  } else if (warp < 12) {
+    // ======================= conversion of K and V =======================
+    constexpr int CPR = D / 16;         // 16-byte code chunks of a key
+    constexpr int KPI = 128 / CPR;      // keys between a thread's keys (16 or 32)
+    constexpr int NI = kChunkN / KPI;   // keys of a thread per tile (8 or 4)
+    const int t0 = tid - 256;
+    const int cc = t0 % CPR, key0 = t0 / CPR;
+    // destination of key key0 + i KPI: KPI is a multiple of 8, so the swizzle is the thread's own
+    const uint32_t off0 = (uint32_t)((cc >> 2) * (128 * 128)) + sw128_off(key0, 2 * (cc & 3));
+    const uint32_t off1 = (uint32_t)((cc >> 2) * (128 * 128)) + sw128_off(key0, 2 * (cc & 3) + 1);
+    bool ok = true;
+    int jg = 0;
+    for (int k = 0; ok && k < n_rounds; ++k) {
+      const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
+      if (idx < 0) continue;
+      const TileDesc t = p.tiles[idx];
+      const RowInfo ri = p.rows[t.row];
+      const int key_end = min(ri.seq_len, ri.q_offset + t.begin + t.count);
+      const int n_kv = t.kv1 - t.kv0;
+      const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages;
+      int pid[4];
+      auto load_pids = [&](int j) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int pg = (t.kv0 + j) * kPagesPerKvTile + c;
+          pid[c] = ldg_s32_or(pt_row + pg, j < n_kv && pg * kPage < key_end, kNoPage);
+        }
+      };
+      auto load = [&](uint4(&raw)[NI], const uint8_t* plane, int j) {
+        const int base = (t.kv0 + j) * kChunkN;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int key = key0 + i * KPI, c = (i * KPI) / kPage;  // key0 < KPI <= 32: the page is the loop's
+          const int id = pid[c];
+          const bool in = id >= 0 && id < p.num_pages;
+          raw[i] = ldg_u128_pred(plane + (((int64_t)(in ? id : 0) * p.hkv + t.kvh) * kPage + (key & (kPage - 1))) * D + 16 * cc,
+                                 in && base + key < key_end);
+        }
+      };
+      auto store = [&](const uint4(&raw)[NI], uint8_t* dst) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          uint4 x, y;
+          codes16_to_half<F>(raw[i], x, y);
+          *reinterpret_cast<uint4*>(dst + off0 + i * (KPI * 128)) = x;
+          *reinterpret_cast<uint4*>(dst + off1 + i * (KPI * 128)) = y;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      uint4 kr[NI], vr[NI];
+      load_pids(0);
+      load(kr, p.k_quant, 0);
+      for (int j = 0; j < n_kv; ++j, ++jg) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (pid[c] != kNoPage && (pid[c] < 0 || pid[c] >= p.num_pages) && t0 == 0)
+            set_device_error(err, MIXATTN_DEVERR_PAGE_ID);
+        load(vr, p.v_quant, j);
+        if (jg > 1) ok = warp_wait(&kv_free[jg & 1], (uint32_t)(((jg - 2) >> 1) & 1), err);
+        if (!ok) break;
+        store(kr, smem + L::kK + (jg & 1) * L::kTile);
+        if (lane == 0) mbar_arrive(&k_ready[jg & 1]);
+        load_pids(j + 1);
+        if (j + 1 < n_kv) load(kr, p.k_quant, j + 1);
+        if (jg > 1) ok = warp_wait(&kv_free[(jg - 1) & 1], (uint32_t)(((jg - 1) >> 1) & 1), err);
+        if (!ok) break;
+        store(vr, smem + L::kV + (jg & 1) * L::kTile);
+        if (lane == 0) mbar_arrive(&v_ready[jg & 1]);
+      }
+    }
+  } else if (tid == 384) {
+    // ======================= MMA =======================
+    constexpr uint32_t kIdescQK = idesc_f16_f32(128, kChunkN, false, false);
+    constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, false, true);
+    const uint64_t dQ = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
+    const uint64_t dK = sw128_desc(smem_u32(smem + L::kK), 16, 1024);
+    const uint64_t dV = sw128_desc(smem_u32(smem + L::kV), kChunkN * 128, 1024);
+    const uint32_t dVlo = (uint32_t)dV, dVhi = (uint32_t)(dV >> 32);
+    bool ok = true;
+    uint32_t n_p[2] = {0, 0}, n_tile[2] = {0, 0};
+    int jg0 = 0;
+    for (int k = 0; ok && k < n_rounds; ++k) {
+      const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
+      if (idx < 0) continue;
+      const TileDesc t = p.tiles[idx];
+      const int n_kv = t.kv1 - t.kv0;
+      const int n_q = t.count * G > 128 ? 2 : 1;
+      for (int j = 0; ok && j <= n_kv; ++j) {
+        const int jg = jg0 + j, st = jg & 1;
+        for (int q = 0; ok && q < n_q; ++q) {
+          const uint32_t s = tmem + 128 * q, o = tmem + kOCol + 128 * q;
+          if (j > 0) {  // PV(j-1)
+            const int jp = jg - 1;
+            ok = mbar_wait(&p_ready[q], n_p[q] & 1, err) && mbar_wait(&v_ready[jp & 1], (uint32_t)((jp >> 1) & 1), err);
+            if (!ok) break;
+            ++n_p[q];
+            tc_fence_after();
+            const uint32_t vb = dVlo + (uint32_t)(((jp & 1) * L::kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t boff = (uint32_t)(kk * 16 * 128) >> 4;
+              if (kk == 0) tc_mma_ts_w(o, s, vb + boff, dVhi, kIdescPV, j > 1 ? 1u : 0u);
+              else tc_mma_ts_w<1>(o, s + 8 * kk, vb + boff, dVhi, kIdescPV);
+            }
+            if (j == n_kv) tc_commit(&o_done[q]);
+          }
+          if (j < n_kv) {  // QK(j)
+            if (j == 0) {
+              ok = mbar_wait(&q_ready[q], n_tile[q] & 1, err);
+              ++n_tile[q];
+            }
+            ok = ok && mbar_wait(&k_ready[st], (uint32_t)((jg >> 1) & 1), err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qa = dQ + (uint64_t)((q * L::kTile) >> 4), kb = dK + (uint64_t)((st * L::kTile) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint64_t off = (uint64_t)(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
+              tc_mma_ss(s, qa + off, kb + off, kIdescQK, ks > 0 ? 1u : 0u);
+            }
+            tc_commit(&qk_done[q]);
+          }
+        }
+        if (ok && j < n_kv) tc_commit(&kv_free[st]);
+      }
+      jg0 += n_kv;
+    }
+    // nothing this thread started may still run when TMEM is released
+    tc_commit(mma_fin);
+    mbar_wait(mma_fin, 0u, err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
 template <int F, int D>
 __global__ void __launch_bounds__(kThreads, 2) page_decode_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   page_decode_tile<F, D>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
 }
 
+// The fused launch: chunk CTAs, then decode CTAs of two tiles each.
+template <int D>
+struct PageFusedSmem {
+  static constexpr int kHalf = (PageDecodeSmem<D>::kTotal + 1023) / 1024 * 1024;
+  static constexpr int kBytes = PageChunkSmem<D>::kTotal > 2 * kHalf ? PageChunkSmem<D>::kTotal : 2 * kHalf;
+  static_assert(kBytes <= 227 * 1024, "fused CTA does not fit in shared memory");
+};
+
+template <int F, int D>
+__global__ void __launch_bounds__(kFusedThreads, 1) page_mixed_kernel(AttnParams p, unsigned int* err) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int cta = blockIdx.x;
+  if (cta < p.n_chunk_ctas) {
+    page_chunk_cta<F, D>(p, cta, p.n_chunk_ctas, smem, err);
+  } else {
+    const int half = threadIdx.x >= kThreads ? 1 : 0;
+    const int d = 2 * (cta - p.n_chunk_ctas) + half;
+    if (d >= p.n_decode_tiles) return;
+    page_decode_tile<F, D>(p, p.tiles[p.n_chunk_tiles + d], smem + half * PageFusedSmem<D>::kHalf, err, half);
+  }
+}
+
 template <int F, int D>
 cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cudaStream_t s) {
   if (p.n_chunk_tiles + p.n_decode_tiles == 0) return cudaSuccess;
-  constexpr int kDec = PageDecodeSmem<D>::kTotal;
+  constexpr int kDec = PageDecodeSmem<D>::kTotal, kFused = PageFusedSmem<D>::kBytes;
   {
     static std::mutex mu;
     static bool configured[kMaxDevices] = {};
@@ -359,11 +877,21 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev]) {
       e = cudaFuncSetAttribute(page_decode_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDec);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(page_mixed_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFused);
       if (e != cudaSuccess) return e;
       configured[dev] = true;
     }
   }
-  page_decode_kernel<F, D><<<p.n_decode_tiles, kThreads, kDec, s>>>(p, err);
+  if (p.n_chunk_tiles == 0) {
+    page_decode_kernel<F, D><<<p.n_decode_tiles, kThreads, kDec, s>>>(p, err);
+  } else {
+    AttnParams q = p;
+    const bool persist = p.chunk_kv_tiles < kPersistMaxKvTiles * p.n_chunk_tiles;
+    q.n_chunk_ctas = persist ? std::min(p.n_chunk_tiles, sm_count()) : p.n_chunk_tiles;
+    const int n_ctas = q.n_chunk_ctas + (p.n_decode_tiles + 1) / 2;
+    page_mixed_kernel<F, D><<<n_ctas, kFusedThreads, kFused, s>>>(q, err);
+  }
   return cudaGetLastError();
 }
 

@@ -223,6 +223,16 @@ def test_long_rows_split(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64)])
+def test_more_chunk_tiles_than_ctas(fmt, hq, hkv, d):
+    """Enough chunk tiles that a CTA walks several, of uneven lengths and half-empty ones."""
+    rows = [(1500, 0), (400, 399), (1300, 500), (200, 170)]
+    if hq == hkv:
+        rows = [(3000, 0), (2100, 100), (600, 599)]
+    _check(fmt, rows, [0 if s - o == 1 else 1 for s, o in rows], hq, hkv, d, seed=61)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("d", [64, 128])
 def test_page_scales_far_apart(fmt, d):
     """Pages of V 2^24 apart in size, and pages of zeros: each weighs in at its own scale."""
