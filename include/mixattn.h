@@ -346,6 +346,10 @@ int mixattn_plan_info(const mixattn_plan* plan, int32_t* total_q, int32_t* n_chu
  * copies on other streams) and the attention kernel.  Runs of the
  * same plan on different streams must not overlap (they share the buffer only
  * for reading; the workspace is the caller's).
+ * The call may be captured into a CUDA graph.  Replays read the plan's buffer and
+ * use the captured pointers, so plan, workspace and tensors must live as long as
+ * the graph, the plan keeps its batch (mixattn_plan_update then returns
+ * MIXATTN_ERR_UNSUPPORTED), and replays that share a workspace must not overlap.
  */
 int mixattn_run(const mixattn_plan* plan, const void* q, const int32_t* page_table, void* o,
                 void* workspace, size_t workspace_bytes, mixattn_stream stream);

@@ -175,15 +175,19 @@ def _i32_array(values: Sequence[int]):
     return arr
 
 
-def _stream_handle(stream) -> ctypes.c_void_p:
+def _stream_handle(stream) -> int:
+    """cudaStream_t of a torch stream (default: the current one) as an integer."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(int(stream.cuda_stream))
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without the Stream object around it
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
 
 
-def _ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(int(t.data_ptr())) if t is not None else ctypes.c_void_p(0)
+def _ptr(t) -> int:
+    return t.data_ptr() if t is not None else 0
 
 
 def block_bytes(fmt: int) -> int:
@@ -247,11 +251,20 @@ class KVCache:
         return cache_desc(self.num_pages, self.num_kv_heads, self.head_dim, self.k_fmt, self.v_fmt,
                           _ptr(self.k_quant), _ptr(self.k_scale), _ptr(self.v_quant), _ptr(self.v_scale))
 
+    def _ref(self):
+        """byref(desc()), the structure kept while nothing in it has changed."""
+        key = (self.num_pages, self.num_kv_heads, self.head_dim, self.k_fmt, self.v_fmt, _ptr(self.k_quant),
+               _ptr(self.k_scale), _ptr(self.v_quant), _ptr(self.v_scale))
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != key:
+            kept = self.__dict__["_kept"] = (key, self.desc())
+        return ctypes.byref(kept[1])
+
 
 def kv_append_quant(cache: KVCache, k_new, v_new, slot_mapping, stream=None) -> None:
     """Quantise fp16 K/V ``[n_new, Hkv, D]`` into the cache slots ``slot_mapping`` (int32)."""
     n = int(k_new.shape[0]) if k_new is not None else 0
-    st = load().mixattn_kv_append_quant(ctypes.byref(cache.desc()), _ptr(k_new), _ptr(v_new),
+    st = load().mixattn_kv_append_quant(cache._ref(), _ptr(k_new), _ptr(v_new),
                                         _ptr(slot_mapping), n, _stream_handle(stream))
     _check(st, "mixattn_kv_append_quant")
 
@@ -302,45 +315,56 @@ class Rope:
             pass
 
 
-def _heads(x, n: int, name: str, heads: Optional[int] = None, head_dim: Optional[int] = None) -> int:
-    """Token stride (elements) of fp16 ``[n, heads, head_dim]`` whose heads are contiguous."""
+def _heads(x, n: int, name: str, here: int, heads: int = 0, head_dim: int = 0):
+    """(heads, head_dim, token stride in elements) of fp16 ``[n, heads, head_dim]`` on the
+    current device, the heads of a token contiguous."""
     import torch
-    if x.dtype != torch.float16 or x.dim() != 3 or x.shape[0] != n:
-        raise ValueError(f"{name}: fp16 [{n}, heads, head_dim] expected, got {x.dtype} {tuple(x.shape)}")
-    if (heads is not None and x.shape[1] != heads) or (head_dim is not None and x.shape[2] != head_dim):
-        raise ValueError(f"{name}: [{n}, {heads}, {head_dim}] expected, got {tuple(x.shape)}")
-    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+    shape = x.shape
+    if x.dtype is not torch.float16 or len(shape) != 3 or shape[0] != n:
+        raise ValueError(f"{name}: fp16 [{n}, heads, head_dim] expected, got {x.dtype} {tuple(shape)}")
+    _, h, d = shape
+    if (heads and h != heads) or (head_dim and d != head_dim):
+        raise ValueError(f"{name}: [{n}, {heads or 'heads'}, {head_dim}] expected, got {tuple(shape)}")
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return int(x.stride(0)) if n > 1 else int(x.shape[1] * x.shape[2])
+    _on_device(x, name, here)
+    return h, d, s0 if n > 1 else h * d
 
 
-def _int_list(x, n: int, name: str) -> None:
+def _int_list(x, n: int, name: str, here: int) -> None:
     import torch
-    if x.dtype != torch.int32 or x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
+    if x.dtype is not torch.int32 or x.shape != (n,) or not x.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 [{n}] expected, got {x.dtype} {tuple(x.shape)}")
+    _on_device(x, name, here)
 
 
-def _same_device(*tensors) -> None:
+def _on_device(x, name: str, here: int) -> None:
+    if x.get_device() != here:  # -1: not on a GPU
+        raise ValueError(f"{name}: a tensor on the current CUDA device expected, got {x.device}")
+
+
+def _here(x, name: str) -> int:
+    """The current device's index, on which ``x`` has to be."""
     import torch
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for x in tensors:
-        if x is not None and (not x.is_cuda or x.device.index != here):
-            raise ValueError(f"tensors must be on the current CUDA device, got {x.device}")
+    here = torch.cuda.current_device() if x.is_cuda else -2
+    _on_device(x, name, here)
+    return here
 
 
 def rope_apply(rope: Rope, x, positions, out=None, stream=None):
     """Rotate fp16 ``[n, heads, head_dim]`` (token stride free) by int32 ``positions [n]``;
     ``out`` may be ``x`` itself."""
-    import torch
-    n = int(positions.shape[0])
-    xs = _heads(x, n, "x")
+    n = positions.shape[0]
+    here = _here(positions, "positions")
+    h, d, xs = _heads(x, n, "x", here)
     if out is None:
+        import torch
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    os_ = _heads(out, n, "out", x.shape[1], x.shape[2])
-    _int_list(positions, n, "positions")
-    _same_device(x, out, positions)
-    st = load().mixattn_rope_apply(rope._handle, _ptr(x), xs, _ptr(out), os_, _ptr(positions), n, int(x.shape[1]),
-                                   int(x.shape[2]), _stream_handle(stream))
+    os_ = xs if out is x else _heads(out, n, "out", here, h, d)[2]
+    _int_list(positions, n, "positions", here)
+    st = load().mixattn_rope_apply(rope._handle, x.data_ptr(), xs, out.data_ptr(), os_, positions.data_ptr(), n, h, d,
+                                   _stream_handle(stream))
     _check(st, "mixattn_rope_apply")
     return out
 
@@ -349,24 +373,25 @@ def rope_append(cache: KVCache, rope: Rope, q, k_new, v_new, positions, slot_map
     """Rotate a step's queries ``q [n, Hq, D]`` (may be None) and keys ``k_new [n, Hkv, D]`` by
     int32 ``positions [n]``; the rotated keys and ``v_new`` go into the cache slots
     ``slot_mapping``.  One launch; returns the rotated queries."""
-    import torch
-    n = int(positions.shape[0])
+    n = positions.shape[0]
     hkv, d = cache.num_kv_heads, cache.head_dim
-    ks, vs = _heads(k_new, n, "k_new", hkv, d), _heads(v_new, n, "v_new", hkv, d)
+    here = _here(positions, "positions")
+    ks, vs = _heads(k_new, n, "k_new", here, hkv, d)[2], _heads(v_new, n, "v_new", here, hkv, d)[2]
     hq = qs = os_ = 0
     if q is not None:
-        hq, qs = int(q.shape[1]) if q.dim() == 3 else 0, _heads(q, n, "q", None, d)
+        hq, _, qs = _heads(q, n, "q", here, 0, d)
         if q_out is None:
+            import torch
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        os_ = _heads(q_out, n, "q_out", hq, d)
+        os_ = qs if q_out is q else _heads(q_out, n, "q_out", here, hq, d)[2]
     else:
         q_out = None
-    _int_list(positions, n, "positions")
-    _int_list(slot_mapping, n, "slot_mapping")
-    _same_device(q, q_out, k_new, v_new, positions, slot_mapping, cache.k_quant)
-    st = load().mixattn_rope_append(ctypes.byref(cache.desc()), rope._handle, hq, _ptr(q), qs, _ptr(q_out), os_,
-                                    _ptr(k_new), ks, _ptr(v_new), vs, _ptr(positions), _ptr(slot_mapping), n,
-                                    _stream_handle(stream))
+    _int_list(positions, n, "positions", here)
+    _int_list(slot_mapping, n, "slot_mapping", here)
+    _on_device(cache.k_quant, "cache", here)
+    st = load().mixattn_rope_append(cache._ref(), rope._handle, hq, _ptr(q), qs, _ptr(q_out), os_,
+                                    k_new.data_ptr(), ks, v_new.data_ptr(), vs, positions.data_ptr(),
+                                    slot_mapping.data_ptr(), n, _stream_handle(stream))
     _check(st, "mixattn_rope_append")
     return q_out
 

@@ -361,6 +361,7 @@ struct mixattn_plan {
   size_t host_cap = 0;
   cudaEvent_t copied = nullptr;
   bool copy_recorded = false;
+  bool captured = false;        // some run was captured: replays read the pinned buffer at any time
 };
 
 struct mixattn_rope {
@@ -392,6 +393,7 @@ bool check_rotate_overlap(const void* x, int64_t xs, const void* out, int64_t os
 
 int plan_fill(mixattn_plan* p, int32_t n_rows, const int32_t* kinds, const int32_t* seq, const int32_t* off,
               int32_t max_pages, size_t* ws_bytes) {
+  if (p->captured) return MIXATTN_ERR_UNSUPPORTED;
   Tiling t;
   int st = build_tiling(p->cache, p->hq, n_rows, kinds, seq, off, max_pages, device_sm_count(), p->window, &t);
   if (st != MIXATTN_OK) return st;
@@ -682,8 +684,17 @@ int mixattn_run(const mixattn_plan* plan_c, const void* q, const int32_t* page_t
                                          reinterpret_cast<uint4*>(ws + L.rows), n16);
     if (cudaGetLastError() != cudaSuccess) return MIXATTN_ERR_CUDA;
   }
-  if (cudaEventRecord(plan->copied, s) != cudaSuccess) return MIXATTN_ERR_CUDA;
-  plan->copy_recorded = true;
+  // a captured run replays whenever its graph does, so no event can tell when the buffer
+  // is free: the plan then keeps its tile list (an event recorded into the graph would
+  // also fail every later wait for it)
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MIXATTN_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) {
+    plan->captured = true;
+  } else {
+    if (cudaEventRecord(plan->copied, s) != cudaSuccess) return MIXATTN_ERR_CUDA;
+    plan->copy_recorded = true;
+  }
 
   AttnParams p;
   const mixattn_kv_cache& c = plan->cache;

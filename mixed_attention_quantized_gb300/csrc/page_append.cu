@@ -3,18 +3,22 @@
 // step's queries rotated in the same launch.
 //
 // The scale of a page covers tokens that arrive in different calls, so the unit of
-// work is a (page, kv head, tensor): one warp holds every new row of that page in
-// registers (one read of each new element), takes their maximum with the page's old
-// scale, and writes their codes; when the scale grew it rounds the page's other codes
+// work is a (page, kv head, tensor): the four warps of a CTA hold every new row of it in
+// registers (one read of each new element), take their maximum with the page's old
+// scale, and write their codes; when the scale grew they round the page's other codes
 // again.  A page that gets its slot 0 is new and its old scale counts for nothing.
 //
-// Which warp owns a page has to come from the slot list alone (no scratch memory, so
-// the call can be captured, replayed and run on any stream): a CTA takes a window of
-// W consecutive tokens, enters their pages into a small hash table and looks through
-// the whole list for tokens of those pages.  It owns the pages of which no earlier
-// window has a token.  That search is n^2 / W list entries over the call, 8 KB per CTA
-// at 2048 tokens.
+// Which CTA owns a page has to come from the slot list alone (no scratch memory, so
+// the call can be captured, replayed and run on any stream): eight CTAs take a window
+// of W consecutive tokens, enter its pages into a small hash table and look through
+// the whole list for tokens of those pages; they own the pages of which no earlier
+// window has a token.  Four of the eight take the keys' heads, four the values'.  In long
+// calls the eight form a cluster that shares the search, each looking through an eighth
+// and entering what it finds into all eight tables; in short ones, where a cluster's two
+// barriers would cost more than the list, each looks through all of it.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
+#include <string.h>
 
 #include "device_utils.cuh"
 #include "internal.h"
@@ -24,10 +28,12 @@ namespace mixattn {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendWarps = kAppendThreads / 32;
-constexpr int kWindow = 32;  // most tokens of a window, so most pages of a CTA
-constexpr int kHash = 64;
+constexpr int kAppendThreads = 128;
+constexpr int kSlices = 8;       // CTAs of a window
+constexpr int kWindow = 64;      // most tokens of a window, so most pages of a CTA
+constexpr int kHash = 128;
+constexpr int kAppendCtas = 7;   // CTAs of an SM (registers)
+constexpr int kClusterFrom = 1024;  // new tokens from which the search is shared
 
 struct PageAppendArgs {
   TokenRows q, k, v;
@@ -37,7 +43,7 @@ struct PageAppendArgs {
   const int32_t* slots;
   uint8_t* codes[2];  // K, V [num_pages][hkv][32][D]
   float* scales[2];   // K, V [num_pages][hkv]
-  int32_t n_new, window, heads_per_cta, head_groups, n_windows;
+  int32_t n_new, window, n_windows;
   int32_t hq, hkv, num_slots;
   unsigned int* err;
 };
@@ -52,7 +58,9 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(((b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0)) << 23);
 }
 
-// Codes of eight values at 1/d.
+// Codes of eight values at 1/d.  I8: a sum with 1.5 * 2^23 rounds a magnitude below 2^22 to
+// the nearest integer (ties to even) and leaves it, in two's complement, in the low byte;
+// |x| <= 127 d (1 + 2^-23) keeps it within +-127.
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   uint32_t w[2];
@@ -62,13 +70,10 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = __fmul_rn(x[4 * h + k], inv);
     if (FMT == MIXATTN_KV_I8_PAGE) {
-      uint32_t r = 0;
+      uint32_t q[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int q = max(-127, min(127, __float2int_rn(y[k])));
-        r |= (uint32_t)(uint8_t)(int8_t)q << (8 * k);
-      }
-      w[h] = r;
+      for (int k = 0; k < 4; ++k) q[k] = __float_as_uint(__fadd_rn(y[k], 12582912.f));
+      w[h] = prmt(prmt(q[0], q[1], 0x0040u), prmt(q[2], q[3], 0x0040u), 0x5410u);
     } else {
       uint16_t lo, hi;
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
@@ -85,230 +90,311 @@ __device__ __forceinline__ void decode8(const uint2& c, float (&x)[8]) {
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    uint32_t f[2];
     if (FMT == MIXATTN_KV_I8_PAGE) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[4 * h + k] = (float)(int8_t)(w[h] >> (8 * k));
+      s8x4_to_f16x2x2(w[h], f[0], f[1]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t f2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f2) : "h"((uint16_t)(w[h] >> (16 * k))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
-        x[4 * h + 2 * k] = f.x;
-        x[4 * h + 2 * k + 1] = f.y;
-      }
+      for (int k = 0; k < 2; ++k)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[k]) : "h"((uint16_t)(w[h] >> (16 * k))));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[k]));
+      x[4 * h + 2 * k] = v.x;
+      x[4 * h + 2 * k + 1] = v.y;
     }
   }
 }
 
-// One (page, head, tensor), by one warp.  tok[32]: the new token of each of the page's
-// slots, or -1.  ROT: cs_row(slot) is the shared (cos, sin) row of a new token.
-template <int FMT, int D, bool ROT, typename CsRow>
-__device__ __forceinline__ void append_page(const RopeTable& t, const CsRow& cs_row, const int32_t* tok,
-                                            const TokenRows& x, uint8_t* codes, float* scale_p, int h) {
-  constexpr int LPR = D / 16;        // lanes per row, an item of 16 elements each
-  constexpr int RPS = 32 / LPR;      // rows per step
-  constexpr int STEPS = kPage / RPS;
-  const int lane = threadIdx.x & 31;
-  const int j = lane % LPR, r0 = lane / LPR;
+// max(|a|, |b|, |c|), NaN if any is.
+__device__ __forceinline__ float amax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The largest of a value >= 0 (or NaN, which wins) over the CTA.
+__device__ __forceinline__ float cta_max(float v, float* warp_max) {
+  // non-negative floats and a NaN of clear sign compare like their bits
+  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = __uint_as_float(m);
+  __syncthreads();
+  uint32_t r = 0;
+#pragma unroll
+  for (int w = 0; w < kAppendThreads / 32; ++w) r = max(r, __float_as_uint(warp_max[w]));
+  return __uint_as_float(r);
+}
+
+// One thread's share of a page: item j (16 elements, two chunks) of rows r0 + s RPS.
+template <int D>
+struct PageShare {
+  static constexpr int LPR = D / 16;                // threads per row
+  static constexpr int RPS = kAppendThreads / LPR;  // rows per step: 16 or 32
+  static constexpr int STEPS = kPage / RPS;
+};
+
+// The new rows of one (page, head) as loaded: zeros where a slot gets no new token.
+template <int D>
+struct PageRaw {
+  uint4 v[PageShare<D>::STEPS][2];
+  float d_old;
+};
+
+// tok[32]: the new token of each of the page's slots, or -1.
+template <int D, bool ROT>
+__device__ __forceinline__ void load_page(PageRaw<D>& raw, const RopeTable& t, const int32_t* tok, const TokenRows& x,
+                                          const float* scale_p, int h) {
+  using P = PageShare<D>;
+  const int j = threadIdx.x % P::LPR, r0 = threadIdx.x / P::LPR;
   int e0 = 16 * j, e1 = e0 + 8;
   if (ROT) rope_item(t, j, e0, e1);
-  uint4 raw[STEPS][2];
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int id = tok[s * RPS + r0];
-    raw[s][0] = raw[s][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (id >= 0) {
-      const uint16_t* src = x.x + (int64_t)id * x.stride + (int64_t)h * D;
-      raw[s][0] = *reinterpret_cast<const uint4*>(src + e0);
-      raw[s][1] = *reinterpret_cast<const uint4*>(src + e1);
-    }
+  for (int s = 0; s < P::STEPS; ++s) {
+    const int id = tok[s * P::RPS + r0];
+    const uint16_t* src = x.x + (int64_t)max(id, 0) * x.stride + (int64_t)h * D;
+    raw.v[s][0] = ldg_u128_pred(src + e0, id >= 0);
+    raw.v[s][1] = ldg_u128_pred(src + e1, id >= 0);
   }
-  const bool fresh = tok[0] >= 0;
-  float d_old = fresh ? 0.f : *scale_p;
-  if (!(d_old >= 0.f && d_old < 1e30f)) d_old = 0.f;  // never written
-  auto values = [&](int s, float(&x0)[8], float(&x1)[8]) {
-    half8_to_float(raw[s][0], x0);
-    half8_to_float(raw[s][1], x1);
-    if (ROT) rope_rotate(t, cs_row(s * RPS + r0), j, x0, x1);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x0[k] = saturate_f16_range(x0[k]);
-      x1[k] = saturate_f16_range(x1[k]);
-    }
-  };
+  raw.d_old = tok[0] >= 0 ? 0.f : *scale_p;
+}
+
+// One (page, head, tensor) by the CTA.  ROT: cs[(4 s + i) kAppendThreads] are the (cos, sin) of
+// pairs 2i, 2i + 1 of this thread's item of step s.  warp_max: [2][warps].
+template <int FMT, int D, bool ROT>
+__device__ __forceinline__ void store_page(const PageRaw<D>& raw, const RopeTable& t, const float4* cs, const int32_t* tok,
+                                           uint8_t* codes, float* scale_p, float* warp_max) {
+  using P = PageShare<D>;
+  const int j = threadIdx.x % P::LPR, r0 = threadIdx.x / P::LPR;
+  int e0 = 16 * j, e1 = e0 + 8;
+  if (ROT) rope_item(t, j, e0, e1);
+  float x0[P::STEPS][8], x1[P::STEPS][8];
   float amax = 0.f;
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    if (tok[s * RPS + r0] >= 0) {
-      float x0[8], x1[8];
-      values(s, x0, x1);
+  for (int s = 0; s < P::STEPS; ++s) {
+    half8_to_float(raw.v[s][0], x0[s]);
+    half8_to_float(raw.v[s][1], x1[s]);
+    if (ROT) {
+      float2 c[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(x0[k]), fabsf(x1[k])));
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = cs[(4 * s + i) * kAppendThreads];
+        c[2 * i] = make_float2(v.x, v.y);
+        c[2 * i + 1] = make_float2(v.z, v.w);
+      }
+      rope_rotate(t, c, j, x0[s], x1[s]);
     }
-  }
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    for (int k = 0; k < 8; ++k) amax = amax3_nan(amax, x0[s][k], x1[s][k]);
+  }
+  amax = cta_max(amax, warp_max);  // (every thread holds the old scale before any writes the new one)
+  if (!(amax <= 65504.f)) {        // NaN, infinities or rotated values past the fp16 range: for all threads
+    amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < P::STEPS; ++s)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x0[s][k] = saturate_f16_range(x0[s][k]);
+        x1[s][k] = saturate_f16_range(x1[s][k]);
+        amax = amax3_nan(amax, x0[s][k], x1[s][k]);
+      }
+    amax = cta_max(amax, warp_max + kAppendThreads / 32);
+  }
+  const bool fresh = tok[0] >= 0;
+  const float d_old = raw.d_old >= 0.f && raw.d_old < 1e30f ? raw.d_old : 0.f;  // (never written: anything)
   const float d = fmaxf(d_old, scale_for<FMT>(amax));
   const float inv = d > 0.f ? __fdiv_rn(1.f, d) : 0.f;
   const bool grown = !fresh && d > d_old;
   const float ratio = grown ? __fdiv_rn(d_old, d) : 1.f;
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int slot = s * RPS + r0;
+  for (int s = 0; s < P::STEPS; ++s) {
+    const int slot = s * P::RPS + r0;
     uint8_t* row = codes + slot * D;
+    uint2* p0 = reinterpret_cast<uint2*>(row + e0);
+    uint2* p1 = reinterpret_cast<uint2*>(row + e1);
     if (tok[slot] >= 0) {
-      float x0[8], x1[8];
-      values(s, x0, x1);
-      *reinterpret_cast<uint2*>(row + e0) = encode8<FMT>(x0, inv);
-      *reinterpret_cast<uint2*>(row + e1) = encode8<FMT>(x1, inv);
+      *p0 = encode8<FMT>(x0[s], inv);
+      *p1 = encode8<FMT>(x1[s], inv);
     } else if (grown) {
-      float x0[8];
-      uint2* p0 = reinterpret_cast<uint2*>(row + e0);
-      decode8<FMT>(*p0, x0);
-      *p0 = encode8<FMT>(x0, ratio);
-      uint2* p1 = reinterpret_cast<uint2*>(row + e1);
-      decode8<FMT>(*p1, x0);
-      *p1 = encode8<FMT>(x0, ratio);
+      decode8<FMT>(*p0, x0[s]);
+      decode8<FMT>(*p1, x1[s]);
+      *p0 = encode8<FMT>(x0[s], ratio);
+      *p1 = encode8<FMT>(x1[s], ratio);
     }
   }
-  if (lane == 0 && (fresh || d != d_old)) *scale_p = d;
+  if (threadIdx.x == 0 && (fresh || d != raw.d_old)) *scale_p = d;
 }
 
-// Grid: first the append CTAs, [window][tensor][head group], then one CTA per token
-// that rotates its queries.
+// The jobs of one CTA: heads h0, h0 + 4, ... of every owned page.
 template <int FMT, int D, bool ROT>
-__global__ void __launch_bounds__(kAppendThreads) page_append_kernel(const __grid_constant__ RopeTable t,
+__device__ __forceinline__ void run_pages(const RopeTable& t, const PageAppendArgs& a, const TokenRows& x, int tensor,
+                                          int h0, int np, const int32_t (*tbl)[kPage], const int32_t* page_id,
+                                          const int32_t* not_mine, float* warp_max, float4* cs) {
+  using P = PageShare<D>;
+  auto next_page = [&](int p) {
+    while (p < np && not_mine[p]) ++p;
+    return p;
+  };
+  auto scale_of = [&](int p, int h) { return a.scales[tensor] + (int64_t)page_id[p] * a.hkv + h; };
+  int p = next_page(0), h = h0;
+  if (p >= np || h0 >= a.hkv) return;
+  PageRaw<D> raw;
+  load_page<D, ROT>(raw, t, tbl[p], x, scale_of(p, h), h);
+  int cs_page = -1;
+  for (int n = 0; p < np; ++n) {
+    const int32_t* tok = tbl[p];
+    if (ROT && cs_page != p) {  // this thread's pairs of its rows, shared by the heads (its own: no barrier)
+      cs_page = p;
+      const int j = threadIdx.x % P::LPR, r0 = threadIdx.x / P::LPR;
+#pragma unroll
+      for (int s = 0; s < P::STEPS; ++s) {
+        const int id = tok[s * P::RPS + r0];
+        if (id >= 0 && 16 * j < t.rot) {
+          const int32_t pos = a.positions[id];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 u = rope_cos_sin(t, pos, 8 * j + 2 * i), v = rope_cos_sin(t, pos, 8 * j + 2 * i + 1);
+            cs[(4 * s + i) * kAppendThreads] = make_float4(u.x, u.y, v.x, v.y);
+          }
+        }
+      }
+    }
+    int pn = p, hn = h + 4;
+    if (hn >= a.hkv) {
+      hn = h0;
+      pn = next_page(p + 1);
+    }
+    const PageRaw<D> now = raw;
+    if (pn < np) load_page<D, ROT>(raw, t, tbl[pn], x, scale_of(pn, hn), hn);
+    uint8_t* codes = a.codes[tensor] + ((int64_t)page_id[p] * a.hkv + h) * (kPage * D);
+    // two areas of maxima in turn: a job's are read before the barrier of the next
+    store_page<FMT, D, ROT>(now, t, cs, tok, codes, scale_of(p, h), warp_max + (n & 1) * (2 * kAppendThreads / 32));
+    p = pn;
+    h = hn;
+  }
+}
+
+// Grid: the append CTAs, [window][slice], then one CTA per token that rotates its queries.
+template <int FMT, int D, bool ROT, bool CLUSTER>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) page_append_kernel(const __grid_constant__ RopeTable t,
                                                                      PageAppendArgs a) {
+  using P = PageShare<D>;
   __shared__ int32_t tbl[kWindow][kPage];  // new token of each slot of each page, -1: none
   __shared__ int32_t hash_key[kHash], hash_val[kHash];
   __shared__ int32_t page_id[kWindow];
   __shared__ int32_t not_mine[kWindow];
-  __shared__ uint32_t rows[kWindow];       // mask of the page's new slots
+  __shared__ uint32_t filter[2];           // bit (page mod 64) of every page of the window
   __shared__ int32_t n_pages;
-  __shared__ int32_t row_tok[kPage];       // ROT: the batch's new tokens
-  extern __shared__ __align__(16) float2 cs[];  // ROT: [rows of a batch][rot/2]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n_append = a.n_windows * 2 * a.head_groups;
+  __shared__ float warp_max[4][kAppendThreads / 32];
+  __shared__ __align__(16) float4 cs[ROT ? P::STEPS * 4 * kAppendThreads : 1];  // keys: [step][i][thread]; queries: [pair]
+  const int tid = threadIdx.x;
+  const int n_append = a.n_windows * kSlices;
   if (ROT && (int)blockIdx.x >= n_append) {
     const int64_t tok = blockIdx.x - n_append;
-    rope_fill(t, a.positions[tok], cs);
+    if (tok >= a.n_new) return;  // (the grid is padded to whole clusters)
+    float2* cs_q = reinterpret_cast<float2*>(cs);
+    rope_fill(t, a.positions[tok], cs_q);
     __syncthreads();
-    rope_row<D>(t, cs, a.q.x + tok * a.q.stride, a.q_out + tok * a.q_out_stride, a.hq);
+    rope_row<D>(t, cs_q, a.q.x + tok * a.q.stride, a.q_out + tok * a.q_out_stride, a.hq);
     return;
   }
-  const int win = blockIdx.x / (2 * a.head_groups);
-  const int unit = blockIdx.x - win * 2 * a.head_groups;
-  const int tensor = unit & 1;
-  const int h0 = (unit >> 1) * a.heads_per_cta, nh = min(a.heads_per_cta, a.hkv - h0);
+  const int win = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
+  const int tensor = slice >> 2, h0 = slice & 3;  // heads h0, h0 + 4, ...
+  if (!CLUSTER && h0 >= a.hkv) return;
   const int w0 = win * a.window, wn = min(a.window, a.n_new - w0);
 
   // ---- the window's pages ----
-  for (int i = tid; i < kWindow * kPage; i += kAppendThreads) (&tbl[0][0])[i] = -1;
+  for (int i = tid; i < a.window * kPage; i += kAppendThreads) (&tbl[0][0])[i] = -1;
   if (tid < kHash) hash_key[tid] = -1;
-  if (tid < kWindow) {
-    not_mine[tid] = 0;
-    rows[tid] = 0u;
-  }
+  if (tid < kWindow) not_mine[tid] = 0;
+  if (tid < 2) filter[tid] = 0u;
+  if (tid == 0) n_pages = 0;
   __syncthreads();
-  if (warp == 0) {
-    int32_t slot = lane < wn ? a.slots[w0 + lane] : -1;
+  if (tid < wn) {
+    const int32_t slot = a.slots[w0 + tid];
     if (slot >= a.num_slots) {
       set_device_error(a.err, MIXATTN_DEVERR_SLOT);
-      slot = -1;
+    } else if (slot >= 0) {
+      const int page = slot / kPage;
+      for (int h = page % kHash;; h = (h + 1) % kHash) {  // at most kWindow keys in twice as many places
+        const int key = atomicCAS(&hash_key[h], -1, page);
+        if (key == page) break;
+        if (key == -1) {
+          const int idx = atomicAdd(&n_pages, 1);  // (their order changes nothing)
+          page_id[idx] = page;
+          hash_val[h] = idx;
+          atomicOr(&filter[(page >> 5) & 1], 1u << (page & 31));
+          break;
+        }
+      }
     }
-    const int page = slot >= 0 ? slot / kPage : -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, page);
-    const bool first = page >= 0 && (__ffs(same) - 1) == lane;
-    const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
-    if (first) {
-      const int idx = __popc(firsts & ((1u << lane) - 1u));
-      page_id[idx] = page;
-      int h = page % kHash;
-      while (atomicCAS(&hash_key[h], -1, page) != -1) h = (h + 1) % kHash;  // at most 32 keys in 64 places
-      hash_val[h] = idx;
-    }
-    if (lane == 0) n_pages = __popc(firsts);
   }
-  __syncthreads();
+  if (CLUSTER) cooperative_groups::this_cluster().sync();
+  else __syncthreads();
   const int np = n_pages;
-  if (np == 0) return;
+  if (!CLUSTER && np == 0) return;
   // ---- their tokens, anywhere in the call; the last of several for one slot counts ----
-  for (int i = tid; i < a.n_new; i += kAppendThreads) {
-    const int32_t slot = a.slots[i];
-    if (slot < 0 || slot >= a.num_slots) continue;
-    const int page = slot / kPage;
-    int h = page % kHash, key;
-    while ((key = hash_key[h]) != -1 && key != page) h = (h + 1) % kHash;
-    if (key == page) {
-      const int idx = hash_val[h];
-      atomicMax(&tbl[idx][slot % kPage], i);
-      atomicOr(&rows[idx], 1u << (slot % kPage));
-      if (i < w0) not_mine[idx] = 1;
-    }
-  }
-  __syncthreads();
-  // ---- the owned pages, in batches of at most 32 rows when cosines are shared ----
-  const TokenRows& x = tensor == 0 ? a.k : a.v;
-  const bool rot = ROT && tensor == 0;
-  const int half = t.rot / 2;
-  for (int p0 = 0; p0 < np;) {
-    int p1 = p0, n_rows = 0;
-    for (; p1 < np; ++p1) {
-      const int r = not_mine[p1] ? 0 : __popc(rows[p1]);
-      if (rot && p1 > p0 && n_rows + r > kPage) break;
-      n_rows += r;
-    }
-    if (rot) {
-      __syncthreads();  // the previous batch is done with cs
-      int base = 0;
-      for (int p = p0; p < p1; ++p) {
-        if (not_mine[p]) continue;
-        const uint32_t m = rows[p];
-        if ((p & (kAppendWarps - 1)) == warp && ((m >> lane) & 1u))
-          row_tok[base + __popc(m & ((1u << lane) - 1u))] = tbl[p][lane];
-        base += __popc(m);
-      }
-      __syncthreads();
-      for (int i = tid; i < n_rows * half; i += kAppendThreads) {
-        const int r = i / half;
-        cs[i] = rope_cos_sin(t, a.positions[row_tok[r]], i - r * half);
-      }
-      __syncthreads();
-    }
-    const int jobs = (p1 - p0) * nh;
-    for (int job = warp; job < jobs; job += kAppendWarps) {
-      const int pi = job / nh, p = p0 + pi, h = h0 + job - pi * nh;
-      if (not_mine[p]) continue;
-      const int64_t at = (int64_t)page_id[p] * a.hkv + h;
-      uint8_t* codes = a.codes[tensor] + at * (kPage * D);
-      float* scale = a.scales[tensor] + at;
-      if (rot) {
-        int base = 0;
-        for (int b = p0; b < p; ++b) base += not_mine[b] ? 0 : __popc(rows[b]);
-        const uint32_t m = rows[p];
-        auto cs_row = [&](int slot) { return cs + (base + __popc(m & ((1u << slot) - 1u))) * half; };
-        append_page<FMT, D, ROT>(t, cs_row, tbl[p], x, codes, scale, h);
+  const uint64_t filt = (uint64_t)filter[0] | ((uint64_t)filter[1] << 32);
+  constexpr int kLoads = 8;  // list entries in flight per thread
+  const int stride = CLUSTER ? kSlices * kAppendThreads : kAppendThreads;
+  for (int i0 = (CLUSTER ? slice * kAppendThreads : 0) + tid; i0 < a.n_new; i0 += kLoads * stride) {
+    int32_t slot[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) slot[u] = i0 + u * stride < a.n_new ? a.slots[i0 + u * stride] : -1;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int page = slot[u] >> 5;  // kPage == 32
+      if (slot[u] < 0 || slot[u] >= a.num_slots || !((filt >> (page & 63)) & 1ull)) continue;
+      int h = page % kHash, key;
+      while ((key = hash_key[h]) != -1 && key != page) h = (h + 1) % kHash;
+      if (key != page) continue;
+      const int idx = hash_val[h], i = i0 + u * stride;
+      int32_t* place = &tbl[idx][slot[u] % kPage];
+      if (CLUSTER) {
+        auto cl = cooperative_groups::this_cluster();
+        for (int r = 0; r < kSlices; ++r) {
+          atomicMax(cl.map_shared_rank(place, r), i);
+          if (i < w0) atomicOr(cl.map_shared_rank(&not_mine[idx], r), 1);
+        }
       } else {
-        auto no_row = [&](int) { return static_cast<const float2*>(nullptr); };
-        append_page<FMT, D, false>(t, no_row, tbl[p], x, codes, scale, h);
+        atomicMax(place, i);
+        if (i < w0) not_mine[idx] = 1;
       }
     }
-    p0 = p1;
   }
+  if (CLUSTER) cooperative_groups::this_cluster().sync();
+  else __syncthreads();
+  // ---- the owned pages: each job's rows are loaded before the job before it is done ----
+  const TokenRows& x = tensor == 0 ? a.k : a.v;
+  if (ROT && tensor == 0) run_pages<FMT, D, true>(t, a, x, tensor, h0, np, tbl, page_id, not_mine, &warp_max[0][0], cs + tid);
+  else run_pages<FMT, D, false>(t, a, x, tensor, h0, np, tbl, page_id, not_mine, &warp_max[0][0], nullptr);
+}
+
+template <int FMT, int D, bool ROT>
+cudaError_t launch_rot(const RopeTable& t, const PageAppendArgs& a, int64_t n_ctas, cudaStream_t s) {
+  if (a.n_new < kClusterFrom) {
+    page_append_kernel<FMT, D, ROT, false><<<(unsigned)n_ctas, kAppendThreads, 0, s>>>(t, a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n_ctas + kSlices - 1) / kSlices * kSlices));
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kSlices;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, page_append_kernel<FMT, D, ROT, true>, t, a);
 }
 
 template <int FMT, int D>
 cudaError_t launch_d(const RopeTable* rope, const PageAppendArgs& a, int64_t n_ctas, cudaStream_t s) {
-  if (rope) {
-    const int smem = kPage * (rope->rot / 2) * (int)sizeof(float2);  // at most 16 KB
-    page_append_kernel<FMT, D, true><<<(unsigned)n_ctas, kAppendThreads, smem, s>>>(*rope, a);
-  } else {
-    RopeTable none;
-    none.rot = 0;
-    page_append_kernel<FMT, D, false><<<(unsigned)n_ctas, kAppendThreads, 0, s>>>(none, a);
-  }
-  return cudaGetLastError();
+  if (rope) return launch_rot<FMT, D, true>(*rope, a, n_ctas, s);
+  RopeTable none;
+  memset(&none, 0, sizeof(none));
+  return launch_rot<FMT, D, false>(none, a, n_ctas, s);
 }
 
 }  // namespace
@@ -330,19 +416,16 @@ cudaError_t launch_page_append(const mixattn_kv_cache& c, const RopeTable* rope,
   a.scales[0] = static_cast<float*>(c.k_scale);
   a.scales[1] = static_cast<float*>(c.v_scale);
   a.n_new = n_new;
-  a.window = n_new >= 1024 ? 32 : 8;
+  // a decode step's tokens each have a page of their own: small windows spread them over
+  // the SMs; a prompt fills a page with 32 tokens
+  a.window = n_new >= 4096 ? 64 : (n_new >= kClusterFrom ? 32 : (n_new > 256 ? 8 : 1));
   a.hq = hq;
   a.hkv = c.num_kv_heads;
   a.num_slots = c.num_pages * kPage;
   a.err = err;
   a.n_windows = (n_new + a.window - 1) / a.window;
-  // heads per CTA: one warp each, fewer while the launch would leave SMs without work
-  a.heads_per_cta = kAppendWarps;
-  auto ctas = [&](int hpc) { return (int64_t)a.n_windows * 2 * ((a.hkv + hpc - 1) / hpc); };
-  while (a.heads_per_cta > 1 && ctas(a.heads_per_cta) < 2 * 152) a.heads_per_cta /= 2;
-  a.head_groups = (a.hkv + a.heads_per_cta - 1) / a.heads_per_cta;
-  const int64_t n_ctas = ctas(a.heads_per_cta) + (rope && hq > 0 ? n_new : 0);
-  if (n_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t n_ctas = (int64_t)a.n_windows * kSlices + (rope && hq > 0 ? n_new : 0);
+  if (n_ctas > INT32_MAX - kSlices) return cudaErrorInvalidConfiguration;
   const bool d64 = c.head_dim == 64;
   if (c.k_fmt == MIXATTN_KV_I8_PAGE)
     return d64 ? launch_d<MIXATTN_KV_I8_PAGE, 64>(rope, a, n_ctas, s) : launch_d<MIXATTN_KV_I8_PAGE, 128>(rope, a, n_ctas, s);

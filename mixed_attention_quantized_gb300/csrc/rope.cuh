@@ -10,9 +10,7 @@
 // 262144), so the table holds each frequency as a fraction of a turn in 64-bit
 // fixed point, T_i = round(2^64 f_i / 2 pi), and p T_i mod 2^64 is the angle's
 // fractional turn with an error of |p| 2^-65 turns -- one wrapping integer
-// multiply, no table of cosines to read and no range reduction.  Its top 32
-// bits become an fp32 number of half turns in [-1, 1) for sincospif; that
-// rounding is 2^-25 of a half turn, 1e-7 radians.
+// multiply, no table of cosines to read.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -25,13 +23,26 @@ namespace mixattn {
 
 #ifdef __CUDACC__
 
-// Cosine and sine of pair i at position pos, times the attention multiplier.
+// Cosine and sine of pair i at position pos, times the attention multiplier: the turn's
+// nearest quarter gives the signs and which is which, the rest (an angle within +-pi/4) the
+// Taylor sums to the 9th and 8th power, whose next terms are below 2e-9 and 3e-8.
 __device__ __forceinline__ float2 rope_cos_sin(const RopeTable& t, int32_t pos, int i) {
-  const uint64_t turn = t.turn[i] * (uint64_t)(int64_t)pos;
-  const float half_turns = (float)(int32_t)(uint32_t)(turn >> 32) * 4.6566128730773926e-10f;  // 2^-31
-  float s, c;
-  sincospif(half_turns, &s, &c);
-  return make_float2(c * t.mscale, s * t.mscale);
+  const uint32_t turn = (uint32_t)((t.turn[i] * (uint64_t)(int64_t)pos) >> 32);
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(turn - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  const float x2 = x * x;
+  float s = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);
+  s = fmaf(x2, s, 8.3333333e-3f);
+  s = fmaf(x2, s, -1.6666667e-1f);
+  s = fmaf(x2 * x, s, x);
+  float c = fmaf(x2, 2.4801587e-5f, -1.3888889e-3f);
+  c = fmaf(x2, c, 4.1666667e-2f);
+  c = fmaf(x2, c, -0.5f);
+  c = fmaf(x2, c, 1.f);
+  float co = (quarter & 1u) ? s : c, si = (quarter & 1u) ? c : s;
+  co = ((quarter + 1u) & 2u) ? -co : co;
+  si = (quarter & 2u) ? -si : si;
+  return make_float2(co * t.mscale, si * t.mscale);
 }
 
 // First elements of the two 8-element chunks of item j (0 .. D/16 - 1) of a head:
@@ -47,15 +58,14 @@ __device__ __forceinline__ void rope_item(const RopeTable& t, int j, int& e0, in
 }
 
 // Item j's 16 values x0 (chunk e0), x1 (chunk e1) rotated in place; cs holds the
-// (cos, sin) of the token's pairs.  Pairs of the item: 8j .. 8j+7.
-__device__ __forceinline__ void rope_rotate(const RopeTable& t, const float2* __restrict__ cs, int j, float (&x0)[8],
+// (cos, sin) of its pairs 8j .. 8j+7.
+__device__ __forceinline__ void rope_rotate(const RopeTable& t, const float2 (&cs)[8], int j, float (&x0)[8],
                                             float (&x1)[8]) {
   if (16 * j >= t.rot) return;
-  const float4* c4 = reinterpret_cast<const float4*>(cs + 8 * j);  // two pairs a load
   if (t.layout == MIXATTN_ROPE_HALF) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 c = c4[k];
+      const float4 c = make_float4(cs[2 * k].x, cs[2 * k].y, cs[2 * k + 1].x, cs[2 * k + 1].y);
       const float a0 = x0[2 * k], b0 = x1[2 * k], a1 = x0[2 * k + 1], b1 = x1[2 * k + 1];
       x0[2 * k] = a0 * c.x - b0 * c.y;
       x1[2 * k] = b0 * c.x + a0 * c.y;
@@ -67,7 +77,7 @@ __device__ __forceinline__ void rope_rotate(const RopeTable& t, const float2* __
     for (int k = 0; k < 4; ++k) {
       float(&x)[8] = k < 2 ? x0 : x1;
       const int o = 4 * (k & 1);
-      const float4 c = c4[k];
+      const float4 c = make_float4(cs[2 * k].x, cs[2 * k].y, cs[2 * k + 1].x, cs[2 * k + 1].y);
       const float a0 = x[o], b0 = x[o + 1], a1 = x[o + 2], b1 = x[o + 3];
       x[o] = a0 * c.x - b0 * c.y;
       x[o + 1] = b0 * c.x + a0 * c.y;
@@ -116,10 +126,17 @@ __device__ __forceinline__ void rope_row(const RopeTable& t, const float2* cs, c
     uint16_t* dst = out + (int64_t)h * D;
     uint4 w0 = *reinterpret_cast<const uint4*>(src + e0), w1 = *reinterpret_cast<const uint4*>(src + e1);
     if (16 * j < t.rot) {
+      float2 c[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(cs + 8 * j)[k];
+        c[2 * k] = make_float2(v.x, v.y);
+        c[2 * k + 1] = make_float2(v.z, v.w);
+      }
       float x0[8], x1[8];
       half8_to_float(w0, x0);
       half8_to_float(w1, x1);
-      rope_rotate(t, cs, j, x0, x1);
+      rope_rotate(t, c, j, x0, x1);
       w0 = float8_to_half(x0);
       w1 = float8_to_half(x1);
     }

@@ -350,3 +350,47 @@ def test_steps_of_a_serving_loop(fmt):
     torch.cuda.synchronize()
     for a, b in zip(before, (out, cache.k_quant, cache.v_quant, cache.k_scale)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", [1, ref.I8, ref.E4M3])
+def test_run_captured_and_replayed(fmt):
+    """A captured run replays on new queries and keys; its plan refuses another batch, and what
+    is called afterwards still works."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    rows, hq = [(300, 299), (400, 200), (70, 66)], 8
+    cache, pt, _ = _filled(fmt, rows, 2, 128, 51)
+    n = sum(s - o for s, o in rows)
+    rng = np.random.default_rng(52)
+    q = torch.from_numpy(rng.standard_normal((n, hq, 128)).astype(np.float16)).cuda()
+    ptd = torch.from_numpy(pt).cuda()
+    seqs, offs = [r[0] for r in rows], [r[1] for r in rows]
+    plan = mq.Plan(cache, hq, [0, 1, 1], seqs, offs, pt.shape[1])
+    ws = mq.alloc_workspace(plan.workspace_bytes)
+    o = torch.empty_like(q)
+    plan.run(q, ptd, o, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.run(q, ptd, o, ws)
+    other = mq.Plan(cache, hq, [0, 1, 1], seqs, offs, pt.shape[1])
+    for _ in range(2):
+        q.copy_(torch.from_numpy(rng.standard_normal((n, hq, 128)).astype(np.float16)))
+        want = torch.empty_like(o)
+        other.run(q, ptd, want, mq.alloc_workspace(other.workspace_bytes))
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+    with pytest.raises(mq.MixattnError) as e:
+        plan.update([0], [100], [99], pt.shape[1])
+    assert e.value.status == mq.ERR_UNSUPPORTED
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+    del g
+    plan.close()
+    other.update([0], [300], [299], pt.shape[1])  # a plan that was not captured goes on
+    other.run(q, ptd, o, mq.alloc_workspace(other.workspace_bytes))
+    torch.cuda.synchronize()
+    other.close()

@@ -1,8 +1,8 @@
 """Rotary positions on the GPU against fp64: alone, and on the way into every cache format.
 
 An fp16 output is off by its own rounding (2^-11 of the value, 2^-25 among the smallest
-numbers) and by the fp32 cosines and products: sincospif is within 2 ulp (2^-22), its
-argument within 2^-25 half turns (2^-23 radians), each product and sum within 2^-24, so
+numbers) and by the fp32 cosines and products: those are within 2^-22, the angle they
+are taken of within 2^-24 radians, each product and sum within 2^-24, so
 under 2^-20 of m (|a| + |b|) for a pair (a, b)."""
 import numpy as np
 import pytest
