@@ -30,8 +30,9 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 constexpr int kSlices = 8;       // CTAs of a window
-constexpr int kWindow = 64;      // most tokens of a window, so most pages of a CTA
-constexpr int kHash = 128;
+constexpr int kWindow = 128;     // most tokens of a window, so most pages of a CTA
+constexpr int kHash = 256;
+static_assert(kWindow <= kAppendThreads && kHash >= 2 * kWindow, "a thread per token of a window");
 constexpr int kAppendCtas = 7;   // CTAs of an SM (registers)
 constexpr int kClusterFrom = 1024;  // new tokens from which the search is shared
 
@@ -284,7 +285,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) page_append_kerne
   __shared__ int32_t page_id[kWindow];
   __shared__ int32_t not_mine[kWindow];
   __shared__ uint32_t filter[2];           // bit (page mod 64) of every page of the window
-  __shared__ int32_t n_pages;
   __shared__ float warp_max[4][kAppendThreads / 32];
   __shared__ __align__(16) float4 cs[ROT ? P::STEPS * 4 * kAppendThreads : 1];  // keys: [step][i][thread]; queries: [pair]
   const int tid = threadIdx.x;
@@ -304,35 +304,38 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) page_append_kerne
   const int w0 = win * a.window, wn = min(a.window, a.n_new - w0);
 
   // ---- the window's pages ----
+  // a page's place in the tables is the window index of its first token there, the same in
+  // all CTAs of the window: a cluster's CTAs enter tokens into one another's tables
   for (int i = tid; i < a.window * kPage; i += kAppendThreads) (&tbl[0][0])[i] = -1;
-  if (tid < kHash) hash_key[tid] = -1;
-  if (tid < kWindow) not_mine[tid] = 0;
+  for (int i = tid; i < kHash; i += kAppendThreads) {
+    hash_key[i] = -1;
+    hash_val[i] = kWindow;
+  }
   if (tid < 2) filter[tid] = 0u;
-  if (tid == 0) n_pages = 0;
   __syncthreads();
+  int my_page = -1, my_hash = 0;
   if (tid < wn) {
     const int32_t slot = a.slots[w0 + tid];
     if (slot >= a.num_slots) {
       set_device_error(a.err, MIXATTN_DEVERR_SLOT);
     } else if (slot >= 0) {
-      const int page = slot / kPage;
-      for (int h = page % kHash;; h = (h + 1) % kHash) {  // at most kWindow keys in twice as many places
-        const int key = atomicCAS(&hash_key[h], -1, page);
-        if (key == page) break;
-        if (key == -1) {
-          const int idx = atomicAdd(&n_pages, 1);  // (their order changes nothing)
-          page_id[idx] = page;
-          hash_val[h] = idx;
-          atomicOr(&filter[(page >> 5) & 1], 1u << (page & 31));
-          break;
-        }
+      my_page = slot / kPage;
+      for (my_hash = my_page % kHash;; my_hash = (my_hash + 1) % kHash) {  // at most kWindow keys in twice as many places
+        const int key = atomicCAS(&hash_key[my_hash], -1, my_page);
+        if (key == -1 || key == my_page) break;
       }
+      atomicMin(&hash_val[my_hash], tid);
+      atomicOr(&filter[(my_page >> 5) & 1], 1u << (my_page & 31));
     }
+  }
+  const bool any = __syncthreads_or(my_page >= 0);
+  if (tid < kWindow) {
+    page_id[tid] = my_page;
+    not_mine[tid] = !(my_page >= 0 && hash_val[my_hash] == tid);
   }
   if (CLUSTER) cooperative_groups::this_cluster().sync();
   else __syncthreads();
-  const int np = n_pages;
-  if (!CLUSTER && np == 0) return;
+  if (!CLUSTER && !any) return;
   // ---- their tokens, anywhere in the call; the last of several for one slot counts ----
   const uint64_t filt = (uint64_t)filter[0] | ((uint64_t)filter[1] << 32);
   constexpr int kLoads = 8;  // list entries in flight per thread
@@ -366,8 +369,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) page_append_kerne
   else __syncthreads();
   // ---- the owned pages: each job's rows are loaded before the job before it is done ----
   const TokenRows& x = tensor == 0 ? a.k : a.v;
-  if (ROT && tensor == 0) run_pages<FMT, D, true>(t, a, x, tensor, h0, np, tbl, page_id, not_mine, &warp_max[0][0], cs + tid);
-  else run_pages<FMT, D, false>(t, a, x, tensor, h0, np, tbl, page_id, not_mine, &warp_max[0][0], nullptr);
+  if (ROT && tensor == 0) run_pages<FMT, D, true>(t, a, x, tensor, h0, wn, tbl, page_id, not_mine, &warp_max[0][0], cs + tid);
+  else run_pages<FMT, D, false>(t, a, x, tensor, h0, wn, tbl, page_id, not_mine, &warp_max[0][0], nullptr);
 }
 
 template <int FMT, int D, bool ROT>
@@ -418,7 +421,8 @@ cudaError_t launch_page_append(const mixattn_kv_cache& c, const RopeTable* rope,
   a.n_new = n_new;
   // a decode step's tokens each have a page of their own: small windows spread them over
   // the SMs; a prompt fills a page with 32 tokens
-  a.window = n_new >= 4096 ? 64 : (n_new >= kClusterFrom ? 32 : (n_new > 256 ? 8 : 1));
+  a.window = n_new > 256 ? 8 : 1;
+  if (n_new >= kClusterFrom) a.window = min(kWindow, max(32, ((n_new + 119) / 120 + 7) / 8 * 8));
   a.hq = hq;
   a.hkv = c.num_kv_heads;
   a.num_slots = c.num_pages * kPage;

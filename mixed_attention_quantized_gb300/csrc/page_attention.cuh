@@ -343,22 +343,31 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
 // Chunk tiles
 // ===========================================================================
 //
-// A tile is 256 rows (256/G query tokens x G heads of one kv head) as two 128-row query
-// tiles A and B that share every converted K and V tile of 128 keys.  Codes are exact in
+// A tile is up to 256 rows (256/G query tokens x G heads of one kv head).  Codes are exact in
 // fp16, so one MMA a step does (the block formats' chunk tiles need a high and a low one),
-// and a KV tile's four pages are the four 32-column chunks in which the softmax reads its
-// scores: each chunk takes one (factor, offset) pair.  Roles of the 16 warps:
-//   softmax A (warps 0-3) and B (4-7), thread = TMEM lane = query row: row maximum and
-//     P' of S as fp16 over the scores already read; O rescaled only when a row's
-//     maximum passed its reference by more than 2^8; then the output;
-//   conversion (8-11): K and V codes from the cache planes, one tile ahead in
-//     registers, as fp16 into 128-byte-swizzled operand tiles, two buffers each;
-//   MMA (one thread of warp 12): PV_A(j-1) QK_A(j) PV_B(j-1) QK_B(j), so each query
-//     tile's softmax runs beside the other's MMAs.
+// and a KV tile's four pages are the four 32-column chunks of its scores: each takes one
+// (factor, offset) pair.  Two softmax groups, 0 and 1, keep the tensor pipe busy in turn:
+//   more than 128 rows: group q takes rows 128 q .. of every KV tile of 128 keys, both
+//     reading each converted K and V tile;
+//   at most 128 rows (a verify row, the end of a chunk): both take the same rows, group q
+//     every second KV tile, and group 0 joins the two results at the end.
+// Roles of the 16 warps:
+//   softmax (warps 0-3 and 4-7), thread = TMEM lane = query row: one pass over its 128 scores,
+//     a page's 32 at a time, against the row's reference m; P' as fp16 over the first half of
+//     the page's own scores.  m is an integer, 3 to 4 above the largest x when it was set, so
+//     P' < 2 until a score passes it by 2^4 or more: seen in the exponent bits of the page's
+//     P' before they are stored, and then m moves, and O and the tile's P' so far are
+//     multiplied by a power of two;
+//   conversion (K 8-11, V 13-15): codes loaded one KV tile ahead into registers, as fp16 into
+//     128-byte-swizzled operand tiles, two buffers each of K and V; a K warp also writes its
+//     page's terms (below);
+//   MMA (one thread of warp 12): PV(j-1) and QK(j) of one group, then of the other.
 // The MMAs of one thread run in issue order and a commit covers all that were issued
-// before it: S_A(j) complete therefore means that PV_A(j-1) is too (O may be rescaled),
-// and QK_B(j) complete that K(j) and V(j-1) have been read.
-// TMEM: S_A | S_B | O_A | O_B, 128 columns each, P' over the first half of its S.
+// before it: a group's S complete therefore means that its PV before it is too (O may be
+// rescaled).  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each, P' of a page over its own scores.
+// Every K warp takes part in every K tile and every V warp in every V tile, so nobody waits
+// for a phase of a barrier that is not the next one.  (A parity says only which of two
+// neighbouring phases is over.)
 // No role waits at a CTA barrier inside its loop; every wait is on an mbarrier, bounded,
 // and a role that gives up leaves its loops, after which the others' waits run out.
 template <int D>
@@ -367,7 +376,9 @@ struct PageChunkSmem {
   static constexpr int kQ = 0;               // query tiles A, B
   static constexpr int kK = 2 * kTile;       // K(j) in buffer j % 2
   static constexpr int kV = 4 * kTile;
-  static constexpr int kBar = 6 * kTile;
+  static constexpr int kMl = 6 * kTile;      // (m, l) of group 1's rows
+  static constexpr int kTerms = kMl + 1024;  // [4][4] terms of the pages of KV tile jg in slot jg % 4
+  static constexpr int kBar = kTerms + 256;
   static constexpr int kTotal = kBar + 256 + 1024;  // + slack for 1024-byte alignment
 };
 
@@ -396,22 +407,85 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// The score factor, log2 dv and 1/dv of the page `pid` for kv head g.  A page outside the
-// cache (or past the row's keys) gets the offset -inf: its keys weigh nothing.
-struct PageTerms {
-  float a, b, inv;
-};
-__device__ __forceinline__ PageTerms page_terms(const AttnParams& p, int pid, int g) {
-  PageTerms r{1e-30f, -CUDART_INF_F, 0.f};
-  if (pid >= 0 && pid < p.num_pages) {
-    const int64_t at = (int64_t)pid * p.hkv + g;
-    const float dk = reinterpret_cast<const float*>(p.k_scale)[at];
-    const float dv = reinterpret_cast<const float*>(p.v_scale)[at];
-    r.a = fmaxf(dk * p.scale_log2, 1e-30f);  // a page of zero keys: scores 0, and -inf stays -inf
-    r.b = dv > 0.f ? log2f(dv) : 0.f;
-    r.inv = dv > 0.f ? __fdiv_rn(1.f, dv) : 1.f;
+// The terms of a page: score factor, log2 dv and 1/dv.  A missing page (outside the cache, or
+// past the row's keys) gets the offset -inf: its keys weigh nothing.
+__device__ __forceinline__ float4 page_terms(float dk, float dv, bool there, float scale_log2) {
+  return make_float4(fmaxf(dk * scale_log2, 1e-30f),  // a page of zero keys: scores 0, and -inf stays -inf
+                     there ? (dv > 0.f ? log2f(dv) : 0.f) : -CUDART_INF_F, dv > 0.f ? __fdiv_rn(1.f, dv) : 1.f, 0.f);
+}
+
+// The softmax's rare step, for page c (32 scores at s_col + 32 c) of a warp in which some row's
+// P' would reach 2, or which has rows without a reference: moves the references of the rows
+// that need it, multiplies O (if there is one yet: `scale_o`), l and the P' of the KV tile's
+// pages before c by the change, a power of two, and writes the page's P'.  Out of line, so
+// that the common path stays short.  Returns (m, l).
+template <int D>
+__device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_col, int c, float4 tm, int c_first,
+                                                   int c_last, float m_run, float l_run, bool scale_o) {
+  const uint32_t sc = s_col + 32 * c;
+  float mx = -CUDART_INF_F;
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    uint32_t o[16];
+    tmem_ld16(sc + 16 * b, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (16 * b + e >= c_first && 16 * b + e <= c_last) mx = fmaxf(mx, __uint_as_float(o[e]));
   }
-  return r;
+  mx = fmaf(mx, tm.x, tm.y);
+  const bool grow = mx > -CUDART_INF_F && (m_run == -CUDART_INF_F || mx >= m_run + 0.99f);
+  const float m_new = grow ? ceilf(mx) + 3.f : m_run;
+  const float alpha = grow ? ex2(m_run - m_new) : 1.f;  // a power of two, or 0
+  l_run *= alpha;
+  if (scale_o) {
+    const uint64_t al2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16; ++ch) {
+      uint32_t o[16];
+      tmem_ld16(o_col + 16 * ch, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float y0, y1;
+        f2_unpack(fmul2(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), y0, y1);
+        o[e] = __float_as_uint(y0);
+        o[e + 1] = __float_as_uint(y1);
+      }
+      tmem_st16(o_col + 16 * ch, o);
+    }
+  }
+  const uint32_t al_h = pack_f16x2(alpha, alpha);  // (below 2^-24: P' and its page are nothing next to mx)
+  tmem_wait_st();  // the P' of the pages before are in place
+#pragma unroll 1
+  for (int b = 0; b < c; ++b) {
+    uint32_t o[16];
+    tmem_ld16(s_col + 32 * b, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(o[e], al_h);
+    tmem_st16(s_col + 32 * b, o);
+  }
+  // the page's P', 16 scores at a time: their 8 words stay before the scores not yet read
+  const float cb = tm.y - (m_new == -CUDART_INF_F ? 0.f : m_new);
+  float l_page = 0.f;
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    uint32_t o[16], w[8];
+    tmem_ld16(sc + 16 * b, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const bool in0 = 16 * b + e >= c_first && 16 * b + e <= c_last;
+      const bool in1 = 16 * b + e + 1 >= c_first && 16 * b + e + 1 <= c_last;
+      const float p0 = in0 ? ex2(fmaf(__uint_as_float(o[e]), tm.x, cb)) : 0.f;
+      const float p1 = in1 ? ex2(fmaf(__uint_as_float(o[e + 1]), tm.x, cb)) : 0.f;
+      l_page += p0 + p1;
+      w[e >> 1] = pack_f16x2(p0, p1);
+    }
+    tmem_st8(sc + 8 * b, w);
+  }
+  return make_float2(m_new, fmaf(l_page, tm.z, l_run));
 }
 
 template <int F, int D>
@@ -421,24 +495,28 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
   constexpr uint32_t kTmemCols = 512, kOCol = 256;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* q_ready = bars;       // [2] query tile A / B of the next tile written   (4 warps)
-  uint64_t* qk_done = bars + 2;   // [2] S of A / B complete                          (commit)
-  uint64_t* p_ready = bars + 4;   // [2] P' of A / B written, O rescaled              (4 warps)
-  uint64_t* o_done = bars + 6;    // [2] the tile's last PV of A / B complete         (commit)
-  uint64_t* k_ready = bars + 8;   // [2] K(jg) in buffer jg % 2                       (4 warps)
-  uint64_t* v_ready = bars + 10;  // [2] V(jg) in buffer jg % 2                       (4 warps)
-  uint64_t* kv_free = bars + 12;  // [2] K(jg) and V(jg-1) read                       (commit)
-  uint64_t* mma_fin = bars + 14;  // every MMA of the CTA complete                    (commit)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  // by 4 warps each:
+  uint64_t* q_ready = bars;        // [2] a group's query rows of its next tile written
+  uint64_t* p_ready = bars + 2;    // [2] a group's P' written, O rescaled
+  uint64_t* ml_ready = bars + 4;   // group 1's (m, l) in shared memory, its O complete
+  uint64_t* joined = bars + 5;     // group 0 has read group 1's O
+  uint64_t* k_ready = bars + 6;    // [2] K(jg) in buffer jg % 2
+  // by 3 warps:
+  uint64_t* v_ready = bars + 8;    // [2] V(jg) in buffer jg % 2
+  // by a commit:
+  uint64_t* qk_done = bars + 10;   // [2] a group's S complete
+  uint64_t* o_done = bars + 12;    // [2] a group's last PV of the tile complete
+  uint64_t* k_free = bars + 14;    // [2] K(jg) read
+  uint64_t* v_free = bars + 16;    // [2] V(jg) read
+  uint64_t* mma_fin = bars + 18;   // every MMA of the CTA complete
+  constexpr int kNumBars = 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group, lg = p.log2_group;
   const int n_rounds = (p.n_chunk_tiles + n_ctas - 1) / n_ctas;
   if (tid == 0) {
-    for (int i = 0; i < 15; ++i) {
-      const bool commits = (i >= 2 && i < 4) || (i >= 6 && i < 8) || i >= 12;
-      mbar_init(bars + i, commits ? 1 : 4);
-    }
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, i < 8 ? 4 : (i < 10 ? 3 : 1));
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -451,27 +529,33 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 8) {
-    // ======================= softmax A / B =======================
+    // ======================= softmax groups =======================
     const int gq = warp >> 2;
-    const int row = tid & 127;
-    const int tok = (gq * 128 + row) >> lg, head = row & (G - 1);
+    const int row = tid & 127, head = row & (G - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + 128 * gq;
     const uint32_t o_col = tmem + lane_base + kOCol + 128 * gq;
-    const uint32_t ninf = __float_as_uint(-CUDART_INF_F);
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
     bool ok = true;
-    uint32_t n_qk = 0, n_tile = 0;  // S tiles and chunk tiles this group has taken (barrier phases)
-    // the CTA's next round >= k with a tile in which this query tile has rows
+    uint32_t n_qk = 0, n_tile = 0, n_join = 0;  // S tiles, chunk tiles, joined tiles so far (barrier phases)
+    int jg0 = 0;  // KV tiles before the chunk tile, over all the CTA's (also those without this group)
+    int jg_skip = 0;  // KV tiles of the tiles that next_round has passed over
+    // the CTA's next round >= k with a tile in which this group takes part
     auto next_round = [&](int k) {
       for (; k < n_rounds; ++k) {
         const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
-        if (idx >= 0 && (gq == 0 || p.tiles[idx].count * G > 128)) break;
+        if (idx < 0) continue;
+        if (gq == 0) break;
+        const TileDesc& t = p.tiles[idx];
+        if (t.count * G > 128 || t.kv1 - t.kv0 > 1) break;
+        jg_skip += t.kv1 - t.kv0;
       }
       return k;
     };
     auto write_q = [&](int k) {
       const TileDesc t = p.tiles[chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles)];
       const RowInfo ri = p.rows[t.row];
+      const int tok = ((t.count * G > 128 ? gq * 128 : 0) + row) >> lg;
       const uint16_t* src = static_cast<const uint16_t*>(p.q) +
                             ((int64_t)(ri.q_start + t.begin + min(tok, t.count - 1)) * p.hq + (int64_t)t.kvh * G + head) * D;
       uint8_t* dst = smem + L::kQ + gq * L::kTile;
@@ -487,113 +571,75 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
     int k = next_round(0);
     if (k < n_rounds) write_q(k);
     while (ok && k < n_rounds) {
+      jg0 += jg_skip;
+      jg_skip = 0;
       const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
       const TileDesc t = p.tiles[idx];
       const RowInfo ri = p.rows[t.row];
+      const bool two = t.count * G > 128;  // each group its own rows; else each its own KV tiles
+      const int prow = (two ? gq * 128 : 0) + row;
+      const int tok = prow >> lg;
       const bool row_valid = tok < t.count;
       const int pos = ri.q_offset + t.begin + min(tok, t.count - 1);
       const int lo = window_first_key(pos, p.window);
       const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
-      const int n_pages = (min(ri.seq_len, ri.q_offset + t.begin + t.count) + kPage - 1) / kPage;
-      const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages;
-      // lane l holds the terms of page l % 4 of the tile: this one's, and the next one's page id
-      auto pid_of = [&](int j) {
-        const int pg = (kv0 + j) * kPagesPerKvTile + (lane & 3);
-        return ldg_s32_or(pt_row + pg, j < n_kv && pg < n_pages, -1);
-      };
-      PageTerms next = page_terms(p, pid_of(0), t.kvh);
-      int next_pid = pid_of(1);
+      const int j0 = two ? 0 : gq, dj = two ? 1 : 2;
       float m_run = -CUDART_INF_F, l_run = 0.f;
-      for (int j = 0; j < n_kv; ++j) {
-        const PageTerms mine = next;
+      for (int j = j0; j < n_kv; j += dj) {
         ok = warp_wait(&qk_done[gq], n_qk & 1, err);
         if (!ok) break;
         ++n_qk;
         tc_fence_after();
-        if (j + 1 < n_kv) {
-          next = page_terms(p, next_pid, t.kvh);
-          next_pid = pid_of(j + 2);
-        }
+        const float4* terms = reinterpret_cast<const float4*>(smem + L::kTerms) + 4 * ((jg0 + j) & 3);
         const int kbase = (kv0 + j) * kChunkN;
-        const bool diag = __any_sync(0xFFFFFFFFu, kbase + kChunkN - 1 > pos || kbase < lo);
-        uint32_t a[32];
-        // pass 1: the row's largest x of the tile
-        float m_tile = -CUDART_INF_F;
+        // the first and last visible key of the row in this tile (usually 0 and 127)
+        const int first = lo - kbase, last = pos - kbase;
+        const bool diag = __any_sync(0xFFFFFFFFu, last < kChunkN - 1 || first > 0);
+        float4 tn = terms[0];  // (a page ahead: a shared-memory load is slow beside the MMAs' reads)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          tmem_ld32(s_col + 32 * c, a);
-          const float ca = __shfl_sync(0xFFFFFFFFu, mine.a, c), cb = __shfl_sync(0xFFFFFFFFu, mine.b, c);
+          const float4 tm = tn;
+          tn = terms[(c + 1) & 3];
+          const int c_first = first - 32 * c, c_last = last - 32 * c;
+          const uint32_t sc = s_col + 32 * c;
+          uint32_t x[32], pk[16];
+          tmem_ld32(sc, x);
+          const float cb = tm.y - (m_run == -CUDART_INF_F ? 0.f : m_run);
+          const uint64_t ca2 = f2_pack(tm.x, tm.x), cb2 = f2_pack(cb, cb);
           tmem_wait_ld();
           if (diag) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) a[e] = ninf;
-          }
-          float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            mx0 = fmax3(mx0, __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-            mx1 = fmax3(mx1, __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
-          }
-          m_tile = fmaxf(m_tile, fmaf(fmaxf(mx0, mx1), ca, cb));
-        }
-        // the reference moves only when P' would pass 2^8: O is then rescaled (PV(j-1) is
-        // complete, see above; a tile's first PV overwrites O)
-        const bool grow = m_tile > m_run + 8.f;
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float alpha = grow ? ex2(m_run - m_tile) : 1.f;
-          m_run = grow ? m_tile : m_run;
-          l_run *= alpha;
-          if (j > 0) {
-            const uint64_t al2 = f2_pack(alpha, alpha);
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-              tmem_ld32(o_col + 32 * ch, a);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float y0, y1;
-                f2_unpack(fmul2(f2_pack(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), al2), y0, y1);
-                a[e] = __float_as_uint(y0);
-                a[e + 1] = __float_as_uint(y1);
-              }
-              tmem_st32(o_col + 32 * ch, a);
-            }
-          }
-        }
-        const float mref = m_run == -CUDART_INF_F ? 0.f : m_run;
-        // pass 2: P' = 2^(x - m) as fp16 over the scores already read; sums in fp32
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(s_col + 32 * c, a);
-          const float ca = __shfl_sync(0xFFFFFFFFu, mine.a, c);
-          const float cb = __shfl_sync(0xFFFFFFFFu, mine.b, c) - mref;
-          const float ci = __shfl_sync(0xFFFFFFFFu, mine.inv, c);
-          const uint64_t ca2 = f2_pack(ca, ca), cb2 = f2_pack(cb, cb);
-          tmem_wait_ld();
-          if (diag) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) a[e] = ninf;
+              if (e < c_first || e > c_last) x[e] = __float_as_uint(-CUDART_INF_F);
           }
           uint64_t sum_a = f2_pack(0.f, 0.f), sum_b = sum_a;
-          uint32_t pk[16];
+          uint32_t bits = 0;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float x0, x1, x2, x3;
-            f2_unpack(ffma2(f2_pack(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), ca2, cb2), x0, x1);
-            f2_unpack(ffma2(f2_pack(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])), ca2, cb2), x2, x3);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ca2, cb2), x0, x1);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), ca2, cb2), x2, x3);
             const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
             sum_a = fadd2(sum_a, f2_pack(p0, p1));
             sum_b = fadd2(sum_b, f2_pack(p2, p3));
             pk[e >> 1] = pack_f16x2(p0, p1);
             pk[(e >> 1) + 1] = pack_f16x2(p2, p3);
+            bits |= pk[e >> 1] | pk[(e >> 1) + 1];
           }
-          tmem_st16(s_col + 16 * c, pk);
-          float s0, s1, s2, s3;
-          f2_unpack(sum_a, s0, s1);
-          f2_unpack(sum_b, s2, s3);
-          l_run = fmaf((s0 + s1) + (s2 + s3), ci, l_run);
+          // a P' of 2 or more (infinity too) has the top exponent bit; a row without a reference
+          // takes one with its first key
+          const bool over = (bits & 0x40004000u) != 0u || m_run == -CUDART_INF_F;
+          if (!__any_sync(0xFFFFFFFFu, over)) {
+            tmem_st16(sc, pk);
+            float s0, s1, s2, s3;
+            f2_unpack(sum_a, s0, s1);
+            f2_unpack(sum_b, s2, s3);
+            l_run = fmaf((s0 + s1) + (s2 + s3), tm.z, l_run);
+            continue;
+          }
+          const float2 ml_new = page_move_reference<D>(s_col, o_col, c, tm, c_first, c_last, m_run, l_run, j > j0);
+          m_run = ml_new.x;
+          l_run = ml_new.y;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -601,51 +647,88 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         if (lane == 0) mbar_arrive(&p_ready[gq]);
       }
       if (!ok) break;
-      // the next tile's Q (this tile's last QK is complete), then this tile's output
+      // the next tile's Q (the group's last QK of this tile is complete), then this tile's output
+      jg0 += n_kv;
       const int kn = next_round(k + 1);
       if (kn < n_rounds) write_q(kn);
       ok = warp_wait(&o_done[gq], n_tile & 1, err);
       ++n_tile;
       if (!ok) break;
       tc_fence_after();
+      const bool join = !two && n_kv > 1;
+      if (join && gq == 1) {  // hand (m, l, O) to group 0 and wait until it has read them
+        ml[row] = make_float2(m_run, l_run);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_ready);
+        ok = warp_wait(joined, n_join & 1, err);
+        ++n_join;
+        tc_fence_after();
+        k = kn;
+        continue;
+      }
+      float w0 = 1.f, w1 = 0.f;  // weights of the two groups' O
+      if (join) {
+        ok = warp_wait(ml_ready, n_join & 1, err);
+        ++n_join;
+        if (!ok) break;
+        tc_fence_after();
+        const float2 other = ml[row];
+        const float m = fmaxf(m_run, other.x);
+        w0 = m_run == -CUDART_INF_F ? 0.f : ex2(m_run - m);
+        w1 = other.x == -CUDART_INF_F ? 0.f : ex2(other.x - m);
+        l_run = l_run * w0 + other.y * w1;
+        m_run = m;
+      }
+      // 16 columns of the tile's O, unnormalised
+      auto o_chunk = [&](int ch, uint32_t(&v)[16]) {
+        tmem_ld16(o_col + 16 * ch, v);
+        if (join) {
+          uint32_t u[16];
+          tmem_ld16(o_col + 128 + 16 * ch, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = __float_as_uint(__uint_as_float(v[e]) * w0 + __uint_as_float(u[e]) * w1);
+        } else {
+          tmem_wait_ld();
+        }
+      };
       uint16_t* dst = static_cast<uint16_t*>(p.o) +
                       ((int64_t)(ri.q_start + t.begin + tok) * p.hq + (int64_t)t.kvh * G + head) * D;
       if (t.nsplit == 1) {
         const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t v[32];
-          tmem_ld32(o_col + 32 * ch, v);
-          tmem_wait_ld();
+        for (int ch = 0; ch < D / 16; ++ch) {
+          uint32_t v[16];
+          o_chunk(ch, v);
           if (row_valid) {
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
+            for (int q4 = 0; q4 < 2; ++q4) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_f16x2_out(__uint_as_float(v[8 * q4 + 2 * e]) * inv_l, __uint_as_float(v[8 * q4 + 2 * e + 1]) * inv_l);
-              *reinterpret_cast<uint4*>(dst + 32 * ch + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(dst + 16 * ch + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
       } else {
         // a piece of a cut tile leaves (m, l, O) of its rows; each warp's rows are merged by
-        // the last piece's same warp to finish (a 4-bit ticket per warp, in the words of the
+        // the last piece's same warp to finish (a 4-bit ticket per warp, in the word of the
         // tile's first piece)
         const int64_t n_o = (int64_t)p.n_chunk_tiles * kPageChunkM * D;
-        const int prow = gq * 128 + row;
         float* o_part = p.chunk_partials + ((int64_t)idx * kPageChunkM + prow) * D;
         float* ml_part = p.chunk_partials + n_o + ((int64_t)idx * kPageChunkM + prow) * 2;
         ml_part[0] = m_run;
         ml_part[1] = l_run;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t v[32];
-          tmem_ld32(o_col + 32 * ch, v);
-          tmem_wait_ld();
+        for (int ch = 0; ch < D / 16; ++ch) {
+          uint32_t v[16];
+          o_chunk(ch, v);
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4)
-            *reinterpret_cast<uint4*>(o_part + 32 * ch + 4 * q4) =
+          for (int q4 = 0; q4 < 4; ++q4)
+            *reinterpret_cast<uint4*>(o_part + 16 * ch + 4 * q4) =
                 make_uint4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
         }
         __threadfence();
@@ -677,7 +760,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
               float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                if (q >= t.nsplit || w[q] == 0.f) continue;  // (a piece without keys holds no O)
+                if (q >= t.nsplit || w[q] == 0.f) continue;
                 const float* op = o0 + (int64_t)q * kPageChunkM * D + d0;
                 const float4 x0 = __ldcg(reinterpret_cast<const float4*>(op));
                 const float4 x1 = __ldcg(reinterpret_cast<const float4*>(op + 4));
@@ -691,83 +774,105 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
           }
         }
       }
-      // O has been read: this warp's next p_ready lets the next tile's first PV overwrite it
+      // O has been read: the groups' next p_ready lets the next tile's first PVs overwrite it
       tc_fence_before();
+      if (join) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(joined);
+      }
       k = kn;
     }
-  } else if (warp < 12) {
-    // ======================= conversion of K and V =======================
-    constexpr int CPR = D / 16;         // 16-byte code chunks of a key
-    constexpr int KPI = 128 / CPR;      // keys between a thread's keys (16 or 32)
-    constexpr int NI = kChunkN / KPI;   // keys of a thread per tile (8 or 4)
-    const int t0 = tid - 256;
-    const int cc = t0 % CPR, key0 = t0 / CPR;
-    // destination of key key0 + i KPI: KPI is a multiple of 8, so the swizzle is the thread's own
+  } else if (warp != 12) {
+    // ======================= conversion: K warps 8-11, V warps 13-15 =======================
+    constexpr int CPR = D / 16;           // 16-byte code chunks of a key
+    constexpr int KPL = 32 / CPR;         // keys of a load (4 or 8)
+    constexpr int NL = 48 / KPL;          // most loads of a warp and tile
+    const bool is_v = warp >= 12;
+    // the warp's keys of a tile: 32 each of K; 48, 40, 40 of V.  They lie in one or two pages,
+    // the second's from load `turn` on.
+    const int w = is_v ? warp - 13 : warp - 8;
+    const int r0 = is_v ? (w == 0 ? 0 : 8 + 40 * w) : 32 * w;
+    const int n_load = (is_v ? (w == 0 ? 48 : 40) : 32) / KPL;
+    const int turn = (kPage - (r0 & (kPage - 1))) / KPL;
+    const int cc = lane % CPR, key0 = r0 + lane / CPR;
+    // the lane's two 16-byte places in row key0 of a tile; row key0 + 4 i flips chunk bit 2 for odd i
     const uint32_t off0 = (uint32_t)((cc >> 2) * (128 * 128)) + sw128_off(key0, 2 * (cc & 3));
     const uint32_t off1 = (uint32_t)((cc >> 2) * (128 * 128)) + sw128_off(key0, 2 * (cc & 3) + 1);
+    const uint8_t* plane = (is_v ? p.v_quant : p.k_quant) + (key0 & (kPage - 1)) * D + 16 * cc;
+    uint64_t* freed = is_v ? v_free : k_free;
+    uint64_t* ready = is_v ? v_ready : k_ready;
     bool ok = true;
-    int jg = 0;
+    int jg = 0;  // KV tiles so far, over the CTA's chunk tiles: buffers and barrier phases follow it
     for (int k = 0; ok && k < n_rounds; ++k) {
       const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
       if (idx < 0) continue;
       const TileDesc t = p.tiles[idx];
       const RowInfo ri = p.rows[t.row];
-      const int key_end = min(ri.seq_len, ri.q_offset + t.begin + t.count);
+      const int key_end = min(ri.seq_len, ri.q_offset + t.begin + t.count) - t.kv0 * kChunkN;  // keys of the KV range
       const int n_kv = t.kv1 - t.kv0;
-      const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages;
-      int pid[4];
-      auto load_pids = [&](int j) {
+      const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages + t.kv0 * kPagesPerKvTile;
+      // the ids of the warp's two pages of KV tile j
+      auto pids_of = [&](int j) {
+        const int pg = j * kPagesPerKvTile + r0 / kPage;
+        return make_int2(ldg_s32_or(pt_row + pg, j < n_kv && pg * kPage < key_end, kNoPage),
+                         ldg_s32_or(pt_row + pg + 1, j < n_kv && turn < n_load && (pg + 1) * kPage < key_end, kNoPage));
+      };
+      uint4 raw[NL];
+      float dk = 0.f, dv = 1.f;
+      bool there = false;
+      auto load = [&](int j, int2 pid) {
+        const bool in_a = pid.x >= 0 && pid.x < p.num_pages, in_b = pid.y >= 0 && pid.y < p.num_pages;
+        if (((pid.x != kNoPage && !in_a) || (pid.y != kNoPage && !in_b)) && lane == 0)
+          set_device_error(err, MIXATTN_DEVERR_PAGE_ID);
+        const int64_t at_a = (int64_t)(in_a ? pid.x : 0) * p.hkv + t.kvh, at_b = (int64_t)(in_b ? pid.y : 0) * p.hkv + t.kvh;
+        const uint8_t* src_a = plane + at_a * (kPage * D);
+        const uint8_t* src_b = plane + (at_b - 1) * (kPage * D);  // (the offset below passes the page's end)
+        const int valid = key_end - j * kChunkN - key0;            // the lane's keys that exist
+        if (in_a && (turn >= n_load || in_b) && (j + 1) * kChunkN <= key_end) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int pg = (t.kv0 + j) * kPagesPerKvTile + c;
-          pid[c] = ldg_s32_or(pt_row + pg, j < n_kv && pg * kPage < key_end, kNoPage);
+          for (int i = 0; i < NL; ++i)
+            if (i < n_load) raw[i] = ldg_u128((i < turn ? src_a : src_b) + i * (KPL * D));
+        } else {
+#pragma unroll
+          for (int i = 0; i < NL; ++i)
+            if (i < n_load)
+              raw[i] = ldg_u128_pred((i < turn ? src_a : src_b) + i * (KPL * D), (i < turn ? in_a : in_b) && i * KPL < valid);
+        }
+        if (!is_v) {
+          there = in_a;
+          dk = ldg_f32_or(p.k_scale, at_a, in_a, 0.f);
+          dv = ldg_f32_or(p.v_scale, at_a, in_a, 1.f);
         }
       };
-      auto load = [&](uint4(&raw)[NI], const uint8_t* plane, int j) {
-        const int base = (t.kv0 + j) * kChunkN;
+      load(0, pids_of(0));
+      int2 next_pid = pids_of(1);
+      for (int j = 0; j < n_kv; ++j, ++jg) {
+        if (jg > 1) ok = warp_wait(&freed[jg & 1], (uint32_t)(((jg - 2) >> 1) & 1), err);  // tile jg - 2 has been read
+        if (!ok) break;
+        uint8_t* dst = smem + (is_v ? L::kV : L::kK) + (jg & 1) * L::kTile;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int key = key0 + i * KPI, c = (i * KPI) / kPage;  // key0 < KPI <= 32: the page is the loop's
-          const int id = pid[c];
-          const bool in = id >= 0 && id < p.num_pages;
-          raw[i] = ldg_u128_pred(plane + (((int64_t)(in ? id : 0) * p.hkv + t.kvh) * kPage + (key & (kPage - 1))) * D + 16 * cc,
-                                 in && base + key < key_end);
+        for (int i = 0; i < NL; ++i) {
+          if (i < n_load) {
+            uint4 x, y;
+            codes16_to_half<F>(raw[i], x, y);
+            const uint32_t flip = (KPL == 4 && (i & 1)) ? 64u : 0u;
+            *reinterpret_cast<uint4*>(dst + (off0 ^ flip) + i * (KPL * 128)) = x;
+            *reinterpret_cast<uint4*>(dst + (off1 ^ flip) + i * (KPL * 128)) = y;
+          }
         }
-      };
-      auto store = [&](const uint4(&raw)[NI], uint8_t* dst) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          uint4 x, y;
-          codes16_to_half<F>(raw[i], x, y);
-          *reinterpret_cast<uint4*>(dst + off0 + i * (KPI * 128)) = x;
-          *reinterpret_cast<uint4*>(dst + off1 + i * (KPI * 128)) = y;
-        }
+        if (!is_v && lane == 0)
+          reinterpret_cast<float4*>(smem + L::kTerms)[4 * (jg & 3) + w] = page_terms(dk, dv, there, p.scale_log2);
         fence_proxy_async_smem();
         __syncwarp();
-      };
-      uint4 kr[NI], vr[NI];
-      load_pids(0);
-      load(kr, p.k_quant, 0);
-      for (int j = 0; j < n_kv; ++j, ++jg) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (pid[c] != kNoPage && (pid[c] < 0 || pid[c] >= p.num_pages) && t0 == 0)
-            set_device_error(err, MIXATTN_DEVERR_PAGE_ID);
-        load(vr, p.v_quant, j);
-        if (jg > 1) ok = warp_wait(&kv_free[jg & 1], (uint32_t)(((jg - 2) >> 1) & 1), err);
-        if (!ok) break;
-        store(kr, smem + L::kK + (jg & 1) * L::kTile);
-        if (lane == 0) mbar_arrive(&k_ready[jg & 1]);
-        load_pids(j + 1);
-        if (j + 1 < n_kv) load(kr, p.k_quant, j + 1);
-        if (jg > 1) ok = warp_wait(&kv_free[(jg - 1) & 1], (uint32_t)(((jg - 1) >> 1) & 1), err);
-        if (!ok) break;
-        store(vr, smem + L::kV + (jg & 1) * L::kTile);
-        if (lane == 0) mbar_arrive(&v_ready[jg & 1]);
+        if (lane == 0) mbar_arrive(&ready[jg & 1]);
+        if (j + 1 < n_kv) {
+          load(j + 1, next_pid);
+          next_pid = pids_of(j + 2);
+        }
       }
     }
-  } else if (tid == 384) {
-    // ======================= MMA =======================
+  } else {
+    // ======================= MMA (lane 0; the other lanes help to wait) =======================
     constexpr uint32_t kIdescQK = idesc_f16_f32(128, kChunkN, false, false);
     constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, false, true);
     const uint64_t dQ = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
@@ -775,58 +880,86 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
     const uint64_t dV = sw128_desc(smem_u32(smem + L::kV), kChunkN * 128, 1024);
     const uint32_t dVlo = (uint32_t)dV, dVhi = (uint32_t)(dV >> 32);
     bool ok = true;
-    uint32_t n_p[2] = {0, 0}, n_tile[2] = {0, 0};
+    // Lane l waits for one of: K, V, P'_0, P'_1, Q_0, Q_1 (l = 0 .. 5); `seen` counts what it has
+    // waited for, which gives the barrier (K, V: two in turn) and its parity.  One poll takes
+    // as long for one barrier as for all of them, and a poll is ~170 cycles beside the MMAs.
+    const uint32_t my_bar = smem_u32(lane == 0 ? k_ready : (lane == 1 ? v_ready : (lane < 4 ? p_ready + (lane & 1) : q_ready + (lane & 1))));
+    const bool in_turn = lane < 2;
+    uint32_t seen = 0;
+    auto wait = [&](uint32_t mask) {
+      const bool need = (mask >> lane) & 1u;
+      const uint32_t bar = my_bar + (in_turn ? (seen & 1u) * 8u : 0u), parity = (in_turn ? seen >> 1 : seen) & 1u;
+      for (uint32_t i = 0; i < (1u << 21); ++i) {
+        const bool done = !need || mbar_try_wait_s(bar, parity);
+        if (__all_sync(0xFFFFFFFFu, done)) {
+          seen += need;
+          return true;
+        }
+      }
+      if (need) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
+      return false;
+    };
     int jg0 = 0;
     for (int k = 0; ok && k < n_rounds; ++k) {
       const int idx = chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles);
       if (idx < 0) continue;
       const TileDesc t = p.tiles[idx];
       const int n_kv = t.kv1 - t.kv0;
-      const int n_q = t.count * G > 128 ? 2 : 1;
-      for (int j = 0; ok && j <= n_kv; ++j) {
-        const int jg = jg0 + j, st = jg & 1;
-        for (int q = 0; ok && q < n_q; ++q) {
-          const uint32_t s = tmem + 128 * q, o = tmem + kOCol + 128 * q;
-          if (j > 0) {  // PV(j-1)
-            const int jp = jg - 1;
-            ok = mbar_wait(&p_ready[q], n_p[q] & 1, err) && mbar_wait(&v_ready[jp & 1], (uint32_t)((jp >> 1) & 1), err);
-            if (!ok) break;
-            ++n_p[q];
-            tc_fence_after();
-            const uint32_t vb = dVlo + (uint32_t)(((jp & 1) * L::kTile) >> 4);
+      const bool two = t.count * G > 128;
+      const int dj = two ? 1 : 2;
+      // two: PV_0(j-1) QK_0(j) PV_1(j-1) QK_1(j) for each j; else PV_q(j-2) QK_q(j), q = j % 2
+      int j = 0, q = 0;
+      const int n_steps = two ? 2 * (n_kv + 1) : n_kv + 2;
+#pragma unroll 1
+      for (int step = 0; step < n_steps; ++step) {
+        const bool has_k = j < n_kv, has_v = j >= dj && j - dj < n_kv;
+        const bool last_q = !two || q == 1, first_q = !two || q == 0;
+        const int jg = jg0 + j, jv = jg - dj;
+        uint32_t mask = (has_v ? 4u : 0u) << q;
+        if (has_k && j < dj) mask |= 16u << q;
+        if (first_q) mask |= (has_k ? 1u : 0u) | (has_v ? 2u : 0u);
+        ok = wait(mask);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t s_tm = tmem + 128 * q, o_tm = s_tm + kOCol;
+          if (has_v) {
+            const uint32_t vb = dVlo + (uint32_t)(((jv & 1) * L::kTile) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
+            for (int kk = 0; kk < 8; ++kk) {  // keys 16 kk ..: columns 32 (kk / 2) + 8 (kk % 2) of S
               const uint32_t boff = (uint32_t)(kk * 16 * 128) >> 4;
-              if (kk == 0) tc_mma_ts_w(o, s, vb + boff, dVhi, kIdescPV, j > 1 ? 1u : 0u);
-              else tc_mma_ts_w<1>(o, s + 8 * kk, vb + boff, dVhi, kIdescPV);
+              if (kk == 0) tc_mma_ts_w(o_tm, s_tm, vb + boff, dVhi, kIdescPV, j >= 2 * dj ? 1u : 0u);
+              else tc_mma_ts_w<1>(o_tm, s_tm + 32 * (kk >> 1) + 8 * (kk & 1), vb + boff, dVhi, kIdescPV);
             }
-            if (j == n_kv) tc_commit(&o_done[q]);
           }
-          if (j < n_kv) {  // QK(j)
-            if (j == 0) {
-              ok = mbar_wait(&q_ready[q], n_tile[q] & 1, err);
-              ++n_tile[q];
-            }
-            ok = ok && mbar_wait(&k_ready[st], (uint32_t)((jg >> 1) & 1), err);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t qa = dQ + (uint64_t)((q * L::kTile) >> 4), kb = dK + (uint64_t)((st * L::kTile) >> 4);
+          if (has_k) {
+            const uint64_t qa = dQ + (uint64_t)((q * L::kTile) >> 4), kb = dK + (uint64_t)(((jg & 1) * L::kTile) >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint64_t off = (uint64_t)(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
-              tc_mma_ss(s, qa + off, kb + off, kIdescQK, ks > 0 ? 1u : 0u);
+              tc_mma_ss(s_tm, qa + off, kb + off, kIdescQK, ks > 0 ? 1u : 0u);
             }
-            tc_commit(&qk_done[q]);
+          }
+          if (has_k) tc_commit(&qk_done[q]);
+          else if (has_v) tc_commit(&o_done[q]);
+          if (last_q) {
+            if (has_v) tc_commit(&v_free[jv & 1]);
+            if (has_k) tc_commit(&k_free[jg & 1]);
           }
         }
-        if (ok && j < n_kv) tc_commit(&kv_free[st]);
+        __syncwarp();
+        j += last_q;
+        q ^= 1;
       }
       jg0 += n_kv;
     }
     // nothing this thread started may still run when TMEM is released
-    tc_commit(mma_fin);
-    mbar_wait(mma_fin, 0u, err);
+    if (lane == 0) {
+      tc_commit(mma_fin);
+      mbar_wait(mma_fin, 0u, err);
+    }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {

@@ -145,7 +145,9 @@ def attention(q, kv, row_slots, rows, window=0):
 
 def attention_tolerance(fmt, q, o, size, k_scale, v_scale, n_keys):
     """Element-wise bound on the kernels' error, counted rounding by rounding:
-    p and o are rounded to fp16 (2^-11 each, p below 2^-14 by 2^-25 absolutely); I8 scores and
+    p and o are rounded to fp16 (2^-11 each, p below 2^-14 by 2^-25 absolutely, next to a largest
+    of 1 or more; chunk tiles keep the largest at 2^-4 or more, where n independent errors of
+    2^-21 / sqrt(3) have a root mean square below n 2^-25 from 86 keys on); I8 scores and
     values are sums of codes + 128 whose offset is taken out again, so their fp32 accumulation
     (one rounding of at most 2^-23 a step) counts against 255 rather than the code."""
     d = q.shape[2]

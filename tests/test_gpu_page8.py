@@ -44,7 +44,8 @@ def _same(cache, k_ref, v_ref, pages):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("n,order", [(1, "in"), (31, "in"), (33, "in"), (257, "in"), (700, "mixed"), (1500, "mixed")])
+@pytest.mark.parametrize("n,order", [(1, "in"), (31, "in"), (33, "in"), (257, "in"), (700, "mixed"), (1500, "mixed"),
+                                     (1030, "in"), (5003, "in"), (9000, "mixed"), (20001, "in")])
 def test_append_is_bit_exact(fmt, d, n, order):
     """One call of n tokens into fresh pages and into partly filled ones."""
     import mixed_attention_quantized_gb300 as mq
