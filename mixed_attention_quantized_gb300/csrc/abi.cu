@@ -657,6 +657,9 @@ int mixattn_plan_info(const mixattn_plan* plan, int32_t* total_q, int32_t* n_chu
 // Copies n16 16-byte words of a plan's tile list from its mapped pinned buffer
 // into the workspace.
 static __global__ void upload_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, size_t n16) {
+  // an attention kernel launched to overlap this one may start setting up (it waits for
+  // this grid's end before it reads the list)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x)
     dst[i] = src[i];
 }

@@ -488,6 +488,11 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
   return make_float2(m_new, fmaf(l_page, tm.z, l_run));
 }
 
+// The launches overlap the end of the kernel before them, which writes the tile list into the
+// workspace: nothing of the workspace (nor the tensors, which earlier kernels may be writing)
+// is touched before that grid is complete.
+__device__ __forceinline__ void wait_for_upload() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int F, int D>
 __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int n_ctas, uint8_t* smem_raw,
                                                unsigned int* err) {
@@ -527,6 +532,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_upload();
 
   if (warp < 8) {
     // ======================= softmax groups =======================
@@ -971,6 +977,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
 template <int F, int D>
 __global__ void __launch_bounds__(kThreads, 2) page_decode_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  wait_for_upload();
   page_decode_tile<F, D>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
 }
 
@@ -986,12 +993,13 @@ template <int F, int D>
 __global__ void __launch_bounds__(kFusedThreads, 1) page_mixed_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int cta = blockIdx.x;
-  if (cta < p.n_chunk_ctas) {
+  if (cta < p.n_chunk_ctas) {  // (waits for the upload when its barriers and TMEM are set up)
     page_chunk_cta<F, D>(p, cta, p.n_chunk_ctas, smem, err);
   } else {
     const int half = threadIdx.x >= kThreads ? 1 : 0;
     const int d = 2 * (cta - p.n_chunk_ctas) + half;
     if (d >= p.n_decode_tiles) return;
+    wait_for_upload();
     page_decode_tile<F, D>(p, p.tiles[p.n_chunk_tiles + d], smem + half * PageFusedSmem<D>::kHalf, err, half);
   }
 }
@@ -1016,16 +1024,26 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
       configured[dev] = true;
     }
   }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
   if (p.n_chunk_tiles == 0) {
-    page_decode_kernel<F, D><<<p.n_decode_tiles, kThreads, kDec, s>>>(p, err);
-  } else {
-    AttnParams q = p;
-    const bool persist = p.chunk_kv_tiles < kPersistMaxKvTiles * p.n_chunk_tiles;
-    q.n_chunk_ctas = persist ? std::min(p.n_chunk_tiles, sm_count()) : p.n_chunk_tiles;
-    const int n_ctas = q.n_chunk_ctas + (p.n_decode_tiles + 1) / 2;
-    page_mixed_kernel<F, D><<<n_ctas, kFusedThreads, kFused, s>>>(q, err);
+    cfg.gridDim = dim3(p.n_decode_tiles);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kDec;
+    return cudaLaunchKernelEx(&cfg, page_decode_kernel<F, D>, p, err);
   }
-  return cudaGetLastError();
+  AttnParams q = p;
+  const bool persist = p.chunk_kv_tiles < kPersistMaxKvTiles * p.n_chunk_tiles;
+  q.n_chunk_ctas = persist ? std::min(p.n_chunk_tiles, sm_count()) : p.n_chunk_tiles;
+  cfg.gridDim = dim3(q.n_chunk_ctas + (p.n_decode_tiles + 1) / 2);
+  cfg.blockDim = dim3(kFusedThreads);
+  cfg.dynamicSmemBytes = kFused;
+  return cudaLaunchKernelEx(&cfg, page_mixed_kernel<F, D>, q, err);
 }
 
 }  // namespace mixattn
