@@ -146,6 +146,7 @@ struct Tiling {
   int32_t total_q = 0, n_chunk = 0, n_decode = 0;
   int32_t slot_rows = 0;       // rows of a decode partial slot
   int32_t chunk_kv_tiles = 0;  // KV tiles over all chunk tiles (their mean decides persistence)
+  int32_t decode_pages = 0;    // pages over all decode tiles
   WorkspaceLayout L{};
 };
 
@@ -269,7 +270,8 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
       // window) to the last; the split size depends on the row alone
       const int64_t first_page = window_first_key((int)o, window) / kPage;
       const int64_t n_win = n_pages - first_page;
-      const int pps = decode_pages_per_split((int)n_win);
+      const int pps =
+          page_scaled(c.k_fmt) ? page_decode_pages_per_split((int)n_win) : decode_pages_per_split((int)n_win);
       const int ns = (int)((n_win + pps - 1) / pps);
       rows[r].n_splits = ns;
       // query groups innermost: the groups reading the same pages sit side by side in
@@ -338,6 +340,9 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   }
   for (size_t i = 0; i < decodes.size(); ++i) td[n_pieces + i] = decodes[i];
   T2.chunk_kv_tiles = (int32_t)std::min<int64_t>(kv_tiles, INT32_MAX);
+  int64_t decode_pages = 0;
+  for (const TileDesc& t : decodes) decode_pages += t.count;
+  T2.decode_pages = (int32_t)std::min<int64_t>(decode_pages, INT32_MAX);
   // counters stay zero: every run starts its split tickets from 0
   return MIXATTN_OK;
 }
@@ -719,6 +724,7 @@ int mixattn_run(const mixattn_plan* plan_c, const void* q, const int32_t* page_t
   p.n_chunk_tiles = plan->tiling.n_chunk;
   p.chunk_kv_tiles = plan->tiling.chunk_kv_tiles;
   p.n_decode_tiles = plan->tiling.n_decode;
+  p.decode_pages = plan->tiling.decode_pages;
   p.hq = plan->hq;
   p.hkv = c.num_kv_heads;
   p.group = plan->group;

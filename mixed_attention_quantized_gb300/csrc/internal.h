@@ -81,6 +81,13 @@ MIXATTN_HD int decode_pages_per_warp(int n_pages) {
 
 MIXATTN_HD int decode_pages_per_split(int n_pages) { return kWarps * decode_pages_per_warp(n_pages); }
 
+// The same for the page-scaled formats, whose decode tiles have 4 warps.
+constexpr int kPageWarps = 4;
+MIXATTN_HD int page_decode_pages_per_split(int n_pages) {
+  const int p = (n_pages + 31) / 32;
+  return kPageWarps * (p < 1 ? 1 : (p > 32 ? 32 : p));
+}
+
 // Formats with one fp32 scale per (page, kv head).
 MIXATTN_HD bool page_scaled(int fmt) { return fmt == MIXATTN_KV_I8_PAGE || fmt == MIXATTN_KV_E4M3_PAGE; }
 
@@ -150,6 +157,7 @@ struct AttnParams {
   int32_t n_chunk_ctas;       // CTAs walking the chunk tiles (set by the launcher)
   int32_t chunk_kv_tiles;     // KV tiles over all chunk tiles
   int32_t n_decode_tiles;
+  int32_t decode_pages = 0;   // pages over all decode tiles (set by a plan)
   int32_t hq;
   int32_t hkv;
   int32_t group;              // hq / hkv, 1..8

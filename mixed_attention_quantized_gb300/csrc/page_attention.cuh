@@ -9,13 +9,16 @@
 // cores exactly as they are, and P' is at most 1 (or 2^slack) whatever the range of V.
 // Partial results (m', O, l) of different key ranges merge as for a plain softmax.
 //
-// Decode tiles: a CTA of 8 warps takes a page range of one (row, kv head) for up to
+// Decode tiles: a CTA of 4 warps takes a page range of one (row, kv head) for up to
 // 8 (query, head) rows; each warp walks its pages 16 keys at a time through a cp.async
-// ring, QK^T and PV on mma.sync m16n8k16 with the codes as exact fp16 operands:
-//   I8_PAGE    u = q + 128 as the fp16 subnormal u 2^-24; the offset leaves the scores
-//              through the accumulators' start, the values through one more MMA;
-//   E4M3_PAGE  the code's exponent and mantissa shifted into fp16 places are its value
-//              times 2^-8, subnormals included.
+// ring, on mma.sync m16n8k16: S^T = c_k Q^T with the 16 keys in the M rows and the tile's
+// rows in N, P' turned by two movmatrix into the B operand of O^T += c_v^T P' (the page's
+// scale is in the exponent, so there is one P' for all of a row's 32-element blocks).  The
+// codes are exact fp16 operands:
+//   I8_PAGE    u = q + 128 as the fp16 subnormal u 2^-24 (one or two logic operations a pair);
+//              the offset leaves the scores through the accumulators' start, the values
+//              through one more MMA;
+//   E4M3_PAGE  cvt to fp16, two codes an instruction.
 #pragma once
 
 #include <mutex>
@@ -27,38 +30,75 @@ namespace mixattn {
 // Factor by which a code's fp16 operand is smaller than the code.
 template <int F>
 __device__ __forceinline__ constexpr float code_unit() {
-  return F == MIXATTN_KV_I8_PAGE ? 16777216.f : 256.f;
+  return F == MIXATTN_KV_I8_PAGE ? 16777216.f : 1.f;
 }
 
-// Bytes 0 and 2 (even) or 1 and 3 (odd) of a word of codes as fp16 operands.
-template <int F>
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-  if (F == MIXATTN_KV_I8_PAGE) return q8_even(w);
-  return ((w << 8) & 0x80008000u) | ((w << 7) & 0x3F803F80u);
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
+
+// Four codes of one key (bytes 0 .. 3 of w) as the two k-pairs of an operand: codes 0, 2 and
+// 1, 3 (I8_PAGE) or 0, 1 and 2, 3 (E4M3_PAGE).
 template <int F>
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
-  if (F == MIXATTN_KV_I8_PAGE) return q8_odd(w);
-  return (w & 0x80008000u) | ((w >> 1) & 0x3F803F80u);
+__device__ __forceinline__ void key_pairs(uint32_t w, uint32_t& a, uint32_t& b) {
+  if (F == MIXATTN_KV_I8_PAGE) {
+    a = q8_even(w);
+    b = q8_odd(w);
+  } else {
+    e4m3x4_to_f16x2x2(w, a, b);
+  }
 }
+
+// Two elements of two keys (bytes 0, 1 of the first, 2, 3 of the second) as the pairs (first,
+// second) of element 0 and of element 1.
+template <int F>
+__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t& e0, uint32_t& e1) {
+  if (F == MIXATTN_KV_I8_PAGE) {
+    e0 = q8_even(w);
+    e1 = q8_odd(w);
+  } else {
+    uint32_t x, y;
+    e4m3x4_to_f16x2x2(w, x, y);
+    e0 = prmt(x, y, 0x5410u);
+    e1 = prmt(x, y, 0x7632u);
+  }
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements, one row's neighbouring pair per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+constexpr int kPageThreads = 32 * kPageWarps;  // threads of a decode tile
 
 template <int D>
 struct PageDecodeSmem {
   static constexpr int kV = 16 * D;
   static constexpr int kStage = 32 * D;  // 16 keys of K, then of V
   static constexpr int kPerWarp = 16 + kMaxGroup * D;
-  static constexpr int kMerge = kWarps * kPerWarp * 4;
-  static constexpr int kStages = D == 128 ? 3 : 6;  // two CTAs per SM
-  static constexpr int kTotal = (kWarps * kStages * kStage > kMerge ? kWarps * kStages * kStage : kMerge) + 16;
-  static_assert(kTotal <= 113 * 1024, "two decode CTAs do not fit on an SM");
+  static constexpr int kMerge = kPageWarps * kPerWarp * 4;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kRings = kPageWarps * kStages * kStage;
+  static constexpr int kTotal = kRings > kMerge ? kRings : kMerge;
+  static constexpr int kCtas = 16 / kPageWarps;  // CTAs per SM: 16 warps of 128 registers
+  static_assert(kCtas * (kTotal + 1024) <= 227 * 1024, "the decode CTAs do not fit on an SM");
 };
+
+// Barrier over the warps of decode tile `part` of a CTA.
+__device__ __forceinline__ void page_decode_sync(int part) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + part), "n"(kPageThreads) : "memory");
+}
 
 // One decode tile (see decode_tile in attention_kernel.cuh for the roles of the
 // descriptor's fields): pages t.begin .. + t.count of kv head t.kvh for queries
 // t.kv1 .. + t.nsplit of row t.row, G heads each.
 template <int F, int D>
 __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const TileDesc& t, uint8_t* smem,
-                                                 unsigned int* err, int half) {
+                                                 unsigned int* err, int sub) {
   using S = PageDecodeSmem<D>;
   constexpr int KS = D / 16;
   constexpr int NS = S::kStages;
@@ -66,22 +106,24 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
   using PL = LdsmPlan<D>;
   static_assert(PL::kCh >= 4, "rows of four or more 16-byte chunks");
 
-  const int tid = threadIdx.x - half * kThreads, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x - sub * kPageThreads, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
   const int G = p.group;
   const int g = t.kvh;
   const RowInfo ri = p.rows[t.row];
   const int split = t.part;
   const int qg0 = t.kv1, nq = t.nsplit, R = nq * G;
-  const int my_q = qg0 + (r < R ? (r >> p.log2_group) : 0), my_h = r & (G - 1);
-  const int pos = ri.q_offset + my_q;
-  const int lo = window_first_key(pos, p.window);
+  const int my_q = qg0 + (r < R ? (r >> p.log2_group) : 0), my_h = r & (G - 1);  // tile row r, whose Q this lane holds
+  // the lane's scores are those of tile rows 2c and 2c + 1: their positions and window starts
+  auto pos_of = [&](int row) { return ri.q_offset + qg0 + (row < R ? (row >> p.log2_group) : 0); };
+  const int pos0 = pos_of(2 * c), pos1 = pos_of(2 * c + 1);
+  const int lo0 = window_first_key(pos0, p.window), lo1 = window_first_key(pos1, p.window);
   const int mask_hi = ri.q_offset + qg0 + 1;
   const int mask_lo = window_first_key(ri.q_offset + qg0 + nq - 1, p.window);
   // keys past the group's last query belong to no row of the tile
   const int last_page = (ri.q_offset + qg0 + nq - 1) / kPage;
   const int n_here = min(t.count, last_page + 1 - t.begin);
-  const int pg_base = n_here > 0 ? n_here / kWarps : 0, pg_rem = n_here > 0 ? n_here - pg_base * kWarps : 0;
+  const int pg_base = n_here > 0 ? n_here / kPageWarps : 0, pg_rem = n_here > 0 ? n_here - pg_base * kPageWarps : 0;
   const int wp0 = t.begin + warp * pg_base + min(warp, pg_rem);
   const int n_pg = pg_base + (warp < pg_rem ? 1 : 0);  // at most 32
   const int n_mt = 2 * n_pg;
@@ -90,7 +132,7 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
 #pragma unroll
   for (int i = 0; i < KS; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.f;
   float corr[4] = {0.f, 0.f, 0.f, 0.f};  // I8_PAGE: -128 2^-24 sum of P', every row the same
-  float m_run = -CUDART_INF_F, l_run = 0.f;
+  float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;  // rows 2c, 2c + 1
 
   const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages;
   const uint32_t ring_s = smem_u32(smem) + warp * (NS * S::kStage);
@@ -138,28 +180,32 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
     my_inv = dv > 0.f ? __fdiv_rn(1.f, dv) : 1.f;
   }
 
-  // Q as the A operand (tile row r; rows 8..15 zero): k-step 2b + j covers dims
-  // 32b + 16j + 4c + {0, 2} (a0) and {1, 3} (a2), the order of a word's even and odd codes
+  // Q as the B operand (column r: tile row r): k-step ks covers dims 16 ks + 4c .. + 3 in the
+  // order of key_pairs
   uint32_t qa[KS][2];
-  float cb = 0.f;  // I8_PAGE: start of the scores, -128 2^-24 sum of q
+  float cb0 = 0.f, cb1 = 0.f;  // I8_PAGE: start of the scores of rows 2c, 2c + 1: -128 2^-24 sum of q
   {
     const bool real = r < R;
     const uint16_t* qrow =
         static_cast<const uint16_t*>(p.q) + ((int64_t)(ri.q_start + my_q) * p.hq + (int64_t)g * G + my_h) * D;
+    float sum = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint2 v = ldg_u64(qrow + 16 * ks + 4 * c);
       if (!real) v = make_uint2(0u, 0u);
-      cb += (h2f_lo(v.x) + h2f_hi(v.x)) + (h2f_lo(v.y) + h2f_hi(v.y));
-      qa[ks][0] = prmt(v.x, v.y, 0x5410u);
-      qa[ks][1] = prmt(v.x, v.y, 0x7632u);
+      sum += (h2f_lo(v.x) + h2f_hi(v.x)) + (h2f_lo(v.y) + h2f_hi(v.y));
+      qa[ks][0] = kOff ? prmt(v.x, v.y, 0x5410u) : v.x;
+      qa[ks][1] = kOff ? prmt(v.x, v.y, 0x7632u) : v.y;
     }
-    cb += __shfl_xor_sync(0xFFFFFFFFu, cb, 1);
-    cb += __shfl_xor_sync(0xFFFFFFFFu, cb, 2);
-    cb = kOff ? cb * (-128.f * 5.9604644775390625e-8f) : 0.f;
+    if (kOff) {
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      sum *= -128.f * 5.9604644775390625e-8f;
+      cb0 = __shfl_sync(0xFFFFFFFFu, sum, 8 * c);
+      cb1 = __shfl_sync(0xFFFFFFFFu, sum, 8 * c + 4);
+    }
   }
 
-  const int kv0 = 2 * c;  // the lane's keys: kv0, kv0 + 1, kv0 + 8, kv0 + 9
   int st_cons = 0;
   for (int i = 0; i < n_mt; ++i) {
     issue(i + NS - 1);
@@ -174,67 +220,86 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
       const int key0 = (wp0 + (i >> 1)) * kPage + 16 * (i & 1);
       const bool partial = key0 + 16 > mask_hi || key0 < mask_lo;
 
-      // ---------------- S = Q c_k^T ----------------
-      float u0[4], u1[4];
-      u0[0] = u0[1] = u1[0] = u1[1] = cb;
-      u0[2] = u0[3] = u1[2] = u1[3] = 0.f;
+      // ---------------- S^T = c_k Q^T: keys r and r + 8, rows 2c and 2c + 1 ----------------
+      float u[4] = {cb0, cb1, cb0, cb1}, u2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int h = 0; h < PL::kGroups; ++h) {
         uint32_t w0[4], w1[4];
         ldsm_group<D, false>(st_s, off, h, w0, w1);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const uint32_t a[4] = {qa[4 * h + m][0], 0u, qa[4 * h + m][1], 0u};
-          const uint32_t b0[2] = {codes_even<F>(w0[m]), codes_odd<F>(w0[m])};
-          const uint32_t b1[2] = {codes_even<F>(w1[m]), codes_odd<F>(w1[m])};
-          mma_16816(u0, a, b0);
-          mma_16816(u1, a, b1);
+          uint32_t a[4];
+          key_pairs<F>(w0[m], a[0], a[2]);
+          key_pairs<F>(w1[m], a[1], a[3]);
+          mma_16816((m & 1) ? u2 : u, a, qa[4 * h + m]);
         }
       }
 
-      // ---------------- softmax over the 16 keys (tile row r) ----------------
-      float s[4] = {fmaf(u0[0], a_pg, b_pg), fmaf(u0[1], a_pg, b_pg), fmaf(u1[0], a_pg, b_pg), fmaf(u1[1], a_pg, b_pg)};
+      // ---------------- softmax over the 16 keys ----------------
+      const float mr0 = m0 == -CUDART_INF_F ? 0.f : m0, mr1 = m1 == -CUDART_INF_F ? 0.f : m1;
+      float x[4] = {fmaf(u[0] + u2[0], a_pg, b_pg - mr0), fmaf(u[1] + u2[1], a_pg, b_pg - mr1),
+                    fmaf(u[2] + u2[2], a_pg, b_pg - mr0), fmaf(u[3] + u2[3], a_pg, b_pg - mr1)};
       if (partial) {
-        auto seen = [&](int k) { return k <= pos && k >= lo; };
-        s[0] = seen(key0 + kv0) ? s[0] : -CUDART_INF_F;
-        s[1] = seen(key0 + kv0 + 1) ? s[1] : -CUDART_INF_F;
-        s[2] = seen(key0 + kv0 + 8) ? s[2] : -CUDART_INF_F;
-        s[3] = seen(key0 + kv0 + 9) ? s[3] : -CUDART_INF_F;
+        const int k0 = key0 + r, k1 = k0 + 8;
+        if (k0 > pos0 || k0 < lo0) x[0] = -CUDART_INF_F;
+        if (k0 > pos1 || k0 < lo1) x[1] = -CUDART_INF_F;
+        if (k1 > pos0 || k1 < lo0) x[2] = -CUDART_INF_F;
+        if (k1 > pos1 || k1 < lo1) x[3] = -CUDART_INF_F;
       }
-      // the reference follows the maximum lazily: P' stays <= 2^8, so the sums of 8-bit
+      // the references follow the maxima lazily: P' stays <= 2^8, so the sums of 8-bit
       // codes times P' stay far inside fp32 and P' inside fp16
       constexpr float kSlack = 8.f;
-      float pm = fmax3(s[0], s[1], fmaxf(s[2], s[3]));
-      if (__any_sync(0xFFFFFFFFu, pm > m_run + kSlack)) {
-        pm = fmaxf(pm, __shfl_xor_sync(0xFFFFFFFFu, pm, 1));
-        pm = fmaxf(pm, __shfl_xor_sync(0xFFFFFFFFu, pm, 2));
-        const bool grow = pm > m_run + kSlack;
-        const float alpha = grow ? ex2(m_run - pm) : 1.f;
-        m_run = grow ? pm : m_run;
-        l_run *= alpha;
-        const float a_even = __shfl_sync(0xFFFFFFFFu, alpha, 8 * c);
-        const float a_odd = __shfl_sync(0xFFFFFFFFu, alpha, 8 * c + 4);
+      float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
+      if (__any_sync(0xFFFFFFFFu, t0 > (m0 == -CUDART_INF_F ? m0 : kSlack) || t1 > (m1 == -CUDART_INF_F ? m1 : kSlack))) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, o));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, o));
+        }
+        const bool g0 = t0 > (m0 == -CUDART_INF_F ? m0 : kSlack), g1 = t1 > (m1 == -CUDART_INF_F ? m1 : kSlack);
+        const float n0 = g0 ? mr0 + t0 : m0, n1 = g1 ? mr1 + t1 : m1;
+        const float al0 = g0 ? ex2(m0 - n0) : 1.f, al1 = g1 ? ex2(m1 - n1) : 1.f;
+        if (g0) {
+          x[0] -= t0;
+          x[2] -= t0;
+        }
+        if (g1) {
+          x[1] -= t1;
+          x[3] -= t1;
+        }
+        m0 = n0;
+        m1 = n1;
+        l0 *= al0;
+        l1 *= al1;
 #pragma unroll
         for (int i2 = 0; i2 < KS; ++i2) {
-          o_acc[i2][0] *= a_even;
-          o_acc[i2][1] *= a_odd;
-          o_acc[i2][2] *= a_even;
-          o_acc[i2][3] *= a_odd;
+          o_acc[i2][0] *= al0;
+          o_acc[i2][1] *= al1;
+          o_acc[i2][2] *= al0;
+          o_acc[i2][3] *= al1;
         }
-        corr[0] *= a_even;
-        corr[1] *= a_odd;
+        corr[0] *= al0;
+        corr[1] *= al1;
       }
-      const float mref = m_run == -CUDART_INF_F ? 0.f : m_run;
-      const float p0 = ex2(s[0] - mref), p1 = ex2(s[1] - mref);
-      const float p8 = ex2(s[2] - mref), p9 = ex2(s[3] - mref);
-      l_run = fmaf((p0 + p1) + (p8 + p9), inv_pg, l_run);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+      l0 = fmaf(x[0] + x[2], inv_pg, l0);
+      l1 = fmaf(x[1] + x[3], inv_pg, l1);
 
       // ---------------- O^T += c_v^T P' ----------------
-      const uint32_t bq[2] = {pack_f16x2(p0, p1), pack_f16x2(p8, p9)};
+      const uint32_t bq[2] = {transpose8x8(pack_f16x2(x[0], x[1])), transpose8x8(pack_f16x2(x[2], x[3]))};
       if (kOff) {
         constexpr uint32_t o2 = 0x80808080u;  // (-128, -128) 2^-24
         const uint32_t ao[4] = {o2, o2, o2, o2};
         mma_16816(corr, ao, bq);
+      }
+      uint32_t mk0 = 0xFFFFFFFFu, mk1 = 0xFFFFFFFFu;
+      if (!kOff && partial) {  // codes of keys that no row sees may be NaN
+        const int lo_first = window_first_key(ri.q_offset + qg0, p.window), hi_last = ri.q_offset + qg0 + nq - 1;
+        auto any_row = [&](int k) { return k <= hi_last && k >= lo_first; };
+        const int k0 = key0 + 2 * c;
+        mk0 = (any_row(k0) ? 0x0000FFFFu : 0u) | (any_row(k0 + 1) ? 0xFFFF0000u : 0u);
+        mk1 = (any_row(k0 + 8) ? 0x0000FFFFu : 0u) | (any_row(k0 + 9) ? 0xFFFF0000u : 0u);
       }
 #pragma unroll
       for (int h = 0; h < PL::kGroups; ++h) {
@@ -242,7 +307,9 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
         ldsm_group<D, true>(st_s + S::kV, off, h, w0, w1);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const uint32_t a[4] = {codes_even<F>(w0[m]), codes_odd<F>(w0[m]), codes_even<F>(w1[m]), codes_odd<F>(w1[m])};
+          uint32_t a[4];
+          value_pairs<F>(kOff ? w0[m] : w0[m] & mk0, a[0], a[1]);
+          value_pairs<F>(kOff ? w1[m] : w1[m] & mk1, a[2], a[3]);
           mma_16816(o_acc[4 * h + m], a, bq);
         }
       }
@@ -252,15 +319,20 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
   cp_async_wait<0>();
 
   // ---------------- warp partial -> shared memory ----------------
-  l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
-  l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
-  decode_sync(half);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
+    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
+  }
+  page_decode_sync(sub);
   float* ws = reinterpret_cast<float*>(smem);
   float* wm = ws + warp * S::kPerWarp;  // m[8], l[8], O[8][D]
   const int h0 = 2 * c, h1 = 2 * c + 1;
-  if (c == 0 && r < R) {
-    wm[r] = m_run;
-    wm[8 + r] = l_run;
+  if (r == 0) {  // (rows past R are never read)
+    wm[h0] = m0;
+    wm[h1] = m1;
+    wm[8 + h0] = l0;
+    wm[8 + h1] = l1;
   }
 #pragma unroll
   for (int tt = 0; tt < KS; ++tt) {
@@ -274,68 +346,84 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
       wm[16 + h1 * D + d_hi] = (o_acc[tt][3] + corr[1]) * code_unit<F>();
     }
   }
-  decode_sync(half);
+  page_decode_sync(sub);
 
-  // ---------------- merge the 8 warps, then the splits ----------------
-  auto out_of = [&](int rr) {
-    return static_cast<uint16_t*>(p.o) +
-           ((int64_t)(ri.q_start + qg0 + (rr >> p.log2_group)) * p.hq + (int64_t)g * G + (rr & (G - 1))) * D;
-  };
-  const int n_out = R * D;
+  // ---------------- merge the warps, then the splits ----------------
+  // two neighbouring elements a thread: a warp's 64 belong to one row
+  const int n_items = R * D / 2;
   const bool single = ri.n_splits == 1;
   const int slot_rows = p.slot_rows > 0 ? p.slot_rows : G;
-  float* part = p.partials + (int64_t)(t.kv0 + split) * slot_rows * (D + 2);
-  for (int idx = tid; idx < n_out; idx += kThreads) {
-    const int h = idx / D, d = idx - h * D;
+  auto store = [&](int h, int d, float o0, float o1, float l) {
+    uint16_t* out = static_cast<uint16_t*>(p.o) +
+                    ((int64_t)(ri.q_start + qg0 + (h >> p.log2_group)) * p.hq + (int64_t)g * G + (h & (G - 1))) * D + d;
+    *reinterpret_cast<uint32_t*>(out) = pack_f16x2_out(o0 / l, o1 / l);
+  };
+  const int64_t stride = (int64_t)slot_rows * (D + 2);
+  float* part = p.partials + (int64_t)(t.kv0 + split) * stride;  // O [slot_rows][D], then (m, l) [slot_rows]
+  for (int idx = tid; idx < n_items; idx += kPageThreads) {
+    const int h = 2 * idx / D, d = 2 * idx - h * D;
     float mmax = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mmax = fmaxf(mmax, ws[w * S::kPerWarp + h]);
-    float lsum = 0.f, osum = 0.f;
+    for (int w = 0; w < kPageWarps; ++w) mmax = fmaxf(mmax, ws[w * S::kPerWarp + h]);
+    float l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {  // a warp without keys holds m = -inf and zeros
+    for (int w = 0; w < kPageWarps; ++w) {  // a warp without keys holds m = -inf and zeros
       const float* x = ws + w * S::kPerWarp;
       const float sc = x[h] == -CUDART_INF_F ? 0.f : ex2(x[h] - mmax);
-      lsum += sc * x[8 + h];
-      osum += sc * x[16 + h * D + d];
+      const float2 o = *reinterpret_cast<const float2*>(x + 16 + h * D + d);
+      l += sc * x[8 + h];
+      o0 += sc * o.x;
+      o1 += sc * o.y;
     }
     if (single) {
-      out_of(h)[d] = f16_out(osum / lsum);
+      store(h, d, o0, o1, l);
     } else {
-      part[h * D + d] = osum;
-      if (d == 0) {
-        part[slot_rows * D + 2 * h] = mmax;
-        part[slot_rows * D + 2 * h + 1] = lsum;
-      }
+      *reinterpret_cast<float2*>(part + h * D + d) = make_float2(o0, o1);
+      if (d == 0) *reinterpret_cast<float2*>(part + slot_rows * D + 2 * h) = make_float2(mmax, l);
     }
   }
   if (single) return;
   __threadfence();
-  decode_sync(half);
-  __shared__ int s_last_of[2];
-  int& s_last = s_last_of[half];
+  page_decode_sync(sub);
+  __shared__ int s_last_of[16 / kPageWarps];
+  int& s_last = s_last_of[sub];
   if (tid == 0) {
     const unsigned prev = atomicAdd(&p.counters[t.kv0], 1u);
     s_last = (prev == (unsigned)(ri.n_splits - 1));
   }
-  decode_sync(half);
+  page_decode_sync(sub);
   if (!s_last) return;
   __threadfence();
   const int ns = ri.n_splits;
-  const int64_t stride = (int64_t)slot_rows * (D + 2);
   const float* parts = p.partials + (int64_t)t.kv0 * stride;
-  for (int idx = tid; idx < n_out; idx += kThreads) {
-    const int h = idx / D, d = idx - h * D;
+  for (int idx = tid; idx < n_items; idx += kPageThreads) {  // (whole warps: n_items is a multiple of 32)
+    const int h = 2 * idx / D, d = 2 * idx - h * D;
+    const float* mlp = parts + slot_rows * D + 2 * h;  // the row's (m, l) of split s at mlp + s stride
     float mmax = -CUDART_INF_F;
-    for (int s2 = 0; s2 < ns; ++s2) mmax = fmaxf(mmax, __ldcg(parts + s2 * stride + slot_rows * D + 2 * h));
-    float lsum = 0.f, osum = 0.f;
-    for (int s2 = 0; s2 < ns; ++s2) {
-      const float* x = parts + s2 * stride;
-      const float mx = __ldcg(x + slot_rows * D + 2 * h);
-      const float sc = mx == -CUDART_INF_F ? 0.f : ex2(mx - mmax);
-      lsum += sc * __ldcg(x + slot_rows * D + 2 * h + 1);
-      osum += sc * __ldcg(x + h * D + d);
+    for (int s2 = lane; s2 < ns; s2 += 32) mmax = fmaxf(mmax, __ldcg(mlp + s2 * stride));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) mmax = fmaxf(mmax, __shfl_xor_sync(0xFFFFFFFFu, mmax, o));
+    float l = 0.f, o0 = 0.f, o1 = 0.f;
+    for (int b = 0; b < ns; b += 32) {  // lane s holds split b + s's weight
+      float sc = 0.f;
+      if (b + lane < ns) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(mlp + (b + lane) * stride));
+        sc = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - mmax);
+        l += sc * ml.y;
+      }
+      const int n = min(32, ns - b);
+      const float* op = parts + b * stride + h * D + d;
+#pragma unroll 8
+      for (int s2 = 0; s2 < n; ++s2) {
+        const float wgt = __shfl_sync(0xFFFFFFFFu, sc, s2);
+        const float2 o = __ldcg(reinterpret_cast<const float2*>(op + s2 * stride));
+        o0 += wgt * o.x;
+        o1 += wgt * o.y;
+      }
     }
-    out_of(h)[d] = f16_out(osum / lsum);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    store(h, d, o0, o1, l);
   }
 }
 
@@ -389,13 +477,8 @@ __device__ __forceinline__ void codes16_to_half(const uint4& c, uint4& lo, uint4
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (F == MIXATTN_KV_I8_PAGE) {
-      s8x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
-    } else {
-      asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-          : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
-          : "r"(w[i]));
-    }
+    if (F == MIXATTN_KV_I8_PAGE) s8x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
+    else e4m3x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
@@ -975,17 +1058,20 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
 }
 
 template <int F, int D>
-__global__ void __launch_bounds__(kThreads, 2) page_decode_kernel(AttnParams p, unsigned int* err) {
+__global__ void __launch_bounds__(kPageThreads, PageDecodeSmem<D>::kCtas) page_decode_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   wait_for_upload();
   page_decode_tile<F, D>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
 }
 
-// The fused launch: chunk CTAs, then decode CTAs of two tiles each.
+constexpr double kChunkShare = 1.15;
+
+// The fused launch: chunk CTAs, then decode CTAs of several tiles each.
 template <int D>
 struct PageFusedSmem {
-  static constexpr int kHalf = (PageDecodeSmem<D>::kTotal + 1023) / 1024 * 1024;
-  static constexpr int kBytes = PageChunkSmem<D>::kTotal > 2 * kHalf ? PageChunkSmem<D>::kTotal : 2 * kHalf;
+  static constexpr int kTiles = kFusedThreads / kPageThreads;
+  static constexpr int kPart = (PageDecodeSmem<D>::kTotal + 1023) / 1024 * 1024;
+  static constexpr int kBytes = PageChunkSmem<D>::kTotal > kTiles * kPart ? PageChunkSmem<D>::kTotal : kTiles * kPart;
   static_assert(kBytes <= 227 * 1024, "fused CTA does not fit in shared memory");
 };
 
@@ -996,11 +1082,12 @@ __global__ void __launch_bounds__(kFusedThreads, 1) page_mixed_kernel(AttnParams
   if (cta < p.n_chunk_ctas) {  // (waits for the upload when its barriers and TMEM are set up)
     page_chunk_cta<F, D>(p, cta, p.n_chunk_ctas, smem, err);
   } else {
-    const int half = threadIdx.x >= kThreads ? 1 : 0;
-    const int d = 2 * (cta - p.n_chunk_ctas) + half;
+    using FS = PageFusedSmem<D>;
+    const int sub = threadIdx.x / kPageThreads;
+    const int d = FS::kTiles * (cta - p.n_chunk_ctas) + sub;
     if (d >= p.n_decode_tiles) return;
     wait_for_upload();
-    page_decode_tile<F, D>(p, p.tiles[p.n_chunk_tiles + d], smem + half * PageFusedSmem<D>::kHalf, err, half);
+    page_decode_tile<F, D>(p, p.tiles[p.n_chunk_tiles + d], smem + sub * FS::kPart, err, sub);
   }
 }
 
@@ -1033,14 +1120,25 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
   cfg.stream = s;
   if (p.n_chunk_tiles == 0) {
     cfg.gridDim = dim3(p.n_decode_tiles);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kPageThreads);
     cfg.dynamicSmemBytes = kDec;
     return cudaLaunchKernelEx(&cfg, page_decode_kernel<F, D>, p, err);
   }
   AttnParams q = p;
   const bool persist = p.chunk_kv_tiles < kPersistMaxKvTiles * p.n_chunk_tiles;
   q.n_chunk_ctas = persist ? std::min(p.n_chunk_tiles, sm_count()) : p.n_chunk_tiles;
-  cfg.gridDim = dim3(q.n_chunk_ctas + (p.n_decode_tiles + 1) / 2);
+  if (persist && p.n_decode_tiles > 0 && sm_count() < (1 << 20)) {
+    // Chunk tiles are bound by the SM, decode tiles by HBM: side by side each takes about the
+    // time it needs anyway.  The chunk CTAs get the share of the SMs that lets both kinds end
+    // together, and a little more (decode CTAs take over the SMs that they leave, not the
+    // other way round).  Costs in SM cycles at head_dim 128, by timing each kind alone: a KV
+    // tile of 256 rows 5300, a page of decode 230.
+    const double tc = 5300.0 * p.chunk_kv_tiles, td = 230.0 * p.decode_pages;
+    const int share = (int)(kChunkShare * sm_count() * tc / (tc + td)) + 1;
+    q.n_chunk_ctas = std::min(q.n_chunk_ctas, share);
+  }
+  constexpr int kTiles = PageFusedSmem<D>::kTiles;
+  cfg.gridDim = dim3(q.n_chunk_ctas + (p.n_decode_tiles + kTiles - 1) / kTiles);
   cfg.blockDim = dim3(kFusedThreads);
   cfg.dynamicSmemBytes = kFused;
   return cudaLaunchKernelEx(&cfg, page_mixed_kernel<F, D>, q, err);
