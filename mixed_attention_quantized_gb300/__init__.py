@@ -175,15 +175,36 @@ def _i32_array(values: Sequence[int]):
     return arr
 
 
+class _Runtime:
+    """What every call needs of torch, looked up once (a call's own time is a few microseconds)."""
+
+    def __init__(self):
+        import torch
+        self.float16, self.int32 = torch.float16, torch.int32
+        c = torch._C
+        # the same as torch.cuda.current_device / current_stream without the objects around them
+        self.device = getattr(c, "_cuda_getDevice", torch.cuda.current_device)
+        self.raw_stream = getattr(c, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_rt = None
+
+
+def _runtime() -> _Runtime:
+    global _rt
+    if _rt is None:
+        _rt = _Runtime()
+    return _rt
+
+
 def _stream_handle(stream) -> int:
     """cudaStream_t of a torch stream (default: the current one) as an integer."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without the Stream object around it
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    rt = _rt or _runtime()
+    import torch
+    return rt.raw_stream(torch.cuda.current_device())
 
 
 def _ptr(t) -> int:
@@ -253,20 +274,24 @@ class KVCache:
 
     def _ref(self):
         """byref(desc()), the structure kept while nothing in it has changed."""
-        key = (self.num_pages, self.num_kv_heads, self.head_dim, self.k_fmt, self.v_fmt, _ptr(self.k_quant),
-               _ptr(self.k_scale), _ptr(self.v_quant), _ptr(self.v_scale))
+        kq, ks, vq, vs = self.k_quant, self.k_scale, self.v_quant, self.v_scale
+        key = (self.num_pages, self.num_kv_heads, self.head_dim, self.k_fmt, self.v_fmt,
+               kq.data_ptr() if kq is not None else 0, ks.data_ptr() if ks is not None else 0,
+               vq.data_ptr() if vq is not None else 0, vs.data_ptr() if vs is not None else 0)
         kept = self.__dict__.get("_kept")
         if kept is None or kept[0] != key:
-            kept = self.__dict__["_kept"] = (key, self.desc())
-        return ctypes.byref(kept[1])
+            desc = self.desc()
+            kept = self.__dict__["_kept"] = (key, desc, ctypes.byref(desc))
+        return kept[2]
 
 
 def kv_append_quant(cache: KVCache, k_new, v_new, slot_mapping, stream=None) -> None:
     """Quantise fp16 K/V ``[n_new, Hkv, D]`` into the cache slots ``slot_mapping`` (int32)."""
-    n = int(k_new.shape[0]) if k_new is not None else 0
-    st = load().mixattn_kv_append_quant(cache._ref(), _ptr(k_new), _ptr(v_new),
-                                        _ptr(slot_mapping), n, _stream_handle(stream))
-    _check(st, "mixattn_kv_append_quant")
+    n = k_new.shape[0] if k_new is not None else 0
+    st = (_lib or load()).mixattn_kv_append_quant(cache._ref(), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), n,
+                                                  _stream_handle(stream))
+    if st:
+        _check(st, "mixattn_kv_append_quant")
 
 
 def kv_export_blocks(cache: KVCache, which: int, slots, stream=None):
@@ -315,57 +340,59 @@ class Rope:
             pass
 
 
-def _heads(x, n: int, name: str, here: int, heads: int = 0, head_dim: int = 0):
-    """(heads, head_dim, token stride in elements) of fp16 ``[n, heads, head_dim]`` on the
-    current device, the heads of a token contiguous."""
-    import torch
+def _heads(rt: _Runtime, here: int, x, n: int, name: str, heads: int = 0, head_dim: int = 0):
+    """(heads, head_dim, token stride in elements) of fp16 ``[n, heads, head_dim]`` on device
+    ``here``, the heads of a token contiguous."""
     shape = x.shape
-    if x.dtype is not torch.float16 or len(shape) != 3 or shape[0] != n:
+    if x.dtype is not rt.float16 or len(shape) != 3 or shape[0] != n:
         raise ValueError(f"{name}: fp16 [{n}, heads, head_dim] expected, got {x.dtype} {tuple(shape)}")
     _, h, d = shape
     if (heads and h != heads) or (head_dim and d != head_dim):
         raise ValueError(f"{name}: [{n}, {heads or 'heads'}, {head_dim}] expected, got {tuple(shape)}")
     s0, s1, s2 = x.stride()
-    if s2 != 1 or (h > 1 and s1 != d):
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    _on_device(x, name, here)
+    if x.get_device() != here:
+        _wrong_device(x, name)
     return h, d, s0 if n > 1 else h * d
 
 
-def _int_list(x, n: int, name: str, here: int) -> None:
-    import torch
-    if x.dtype is not torch.int32 or x.shape != (n,) or not x.is_contiguous():
+def _int_list(rt: _Runtime, here: int, x, n: int, name: str) -> None:
+    if x.dtype is not rt.int32 or x.shape != (n,) or (n > 1 and x.stride(0) != 1):
         raise ValueError(f"{name}: contiguous int32 [{n}] expected, got {x.dtype} {tuple(x.shape)}")
-    _on_device(x, name, here)
+    if x.get_device() != here:
+        _wrong_device(x, name)
 
 
-def _on_device(x, name: str, here: int) -> None:
-    if x.get_device() != here:  # -1: not on a GPU
-        raise ValueError(f"{name}: a tensor on the current CUDA device expected, got {x.device}")
+def _wrong_device(x, name: str) -> None:
+    raise ValueError(f"{name}: a tensor on the current CUDA device expected, got {x.device}")
 
 
-def _here(x, name: str) -> int:
+def _call_device(rt: _Runtime, x, name: str) -> int:
     """The current device's index, on which ``x`` has to be."""
-    import torch
-    here = torch.cuda.current_device() if x.is_cuda else -2
-    _on_device(x, name, here)
+    here = rt.device() if x.is_cuda else -2
+    if x.get_device() != here:
+        _wrong_device(x, name)
     return here
 
 
 def rope_apply(rope: Rope, x, positions, out=None, stream=None):
     """Rotate fp16 ``[n, heads, head_dim]`` (token stride free) by int32 ``positions [n]``;
     ``out`` may be ``x`` itself."""
+    rt = _rt or _runtime()
     n = positions.shape[0]
-    here = _here(positions, "positions")
-    h, d, xs = _heads(x, n, "x", here)
+    here = _call_device(rt, positions, "positions")
+    h, d, xs = _heads(rt, here, x, n, "x")
     if out is None:
         import torch
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    os_ = xs if out is x else _heads(out, n, "out", here, h, d)[2]
-    _int_list(positions, n, "positions", here)
-    st = load().mixattn_rope_apply(rope._handle, x.data_ptr(), xs, out.data_ptr(), os_, positions.data_ptr(), n, h, d,
-                                   _stream_handle(stream))
-    _check(st, "mixattn_rope_apply")
+    os_ = xs if out is x else _heads(rt, here, out, n, "out", h, d)[2]
+    _int_list(rt, here, positions, n, "positions")
+    st = (_lib or load()).mixattn_rope_apply(
+        rope._handle, x.data_ptr(), xs, out.data_ptr(), os_, positions.data_ptr(), n, h, d,
+        stream.cuda_stream if stream is not None else rt.raw_stream(here))
+    if st:
+        _check(st, "mixattn_rope_apply")
     return out
 
 
@@ -373,26 +400,32 @@ def rope_append(cache: KVCache, rope: Rope, q, k_new, v_new, positions, slot_map
     """Rotate a step's queries ``q [n, Hq, D]`` (may be None) and keys ``k_new [n, Hkv, D]`` by
     int32 ``positions [n]``; the rotated keys and ``v_new`` go into the cache slots
     ``slot_mapping``.  One launch; returns the rotated queries."""
+    rt = _rt or _runtime()
     n = positions.shape[0]
+    here = _call_device(rt, positions, "positions")
     hkv, d = cache.num_kv_heads, cache.head_dim
-    here = _here(positions, "positions")
-    ks, vs = _heads(k_new, n, "k_new", here, hkv, d)[2], _heads(v_new, n, "v_new", here, hkv, d)[2]
-    hq = qs = os_ = 0
+    ks = _heads(rt, here, k_new, n, "k_new", hkv, d)[2]
+    vs = _heads(rt, here, v_new, n, "v_new", hkv, d)[2]
+    hq = qs = os_ = qp = op = 0
     if q is not None:
-        hq, _, qs = _heads(q, n, "q", here, 0, d)
+        hq, _, qs = _heads(rt, here, q, n, "q", 0, d)
         if q_out is None:
             import torch
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        os_ = qs if q_out is q else _heads(q_out, n, "q_out", here, hq, d)[2]
+        os_ = qs if q_out is q else _heads(rt, here, q_out, n, "q_out", hq, d)[2]
+        qp, op = q.data_ptr(), q_out.data_ptr()
     else:
         q_out = None
-    _int_list(positions, n, "positions", here)
-    _int_list(slot_mapping, n, "slot_mapping", here)
-    _on_device(cache.k_quant, "cache", here)
-    st = load().mixattn_rope_append(cache._ref(), rope._handle, hq, _ptr(q), qs, _ptr(q_out), os_,
-                                    k_new.data_ptr(), ks, v_new.data_ptr(), vs, positions.data_ptr(),
-                                    slot_mapping.data_ptr(), n, _stream_handle(stream))
-    _check(st, "mixattn_rope_append")
+    _int_list(rt, here, positions, n, "positions")
+    _int_list(rt, here, slot_mapping, n, "slot_mapping")
+    if cache.k_quant.get_device() != here:
+        _wrong_device(cache.k_quant, "cache")
+    st = (_lib or load()).mixattn_rope_append(
+        cache._ref(), rope._handle, hq, qp, qs, op, os_, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        positions.data_ptr(), slot_mapping.data_ptr(), n,
+        stream.cuda_stream if stream is not None else rt.raw_stream(here))
+    if st:
+        _check(st, "mixattn_rope_append")
     return q_out
 
 

@@ -395,3 +395,109 @@ def test_run_captured_and_replayed(fmt):
     other.run(q, ptd, o, mq.alloc_workspace(other.workspace_bytes))
     torch.cuda.synchronize()
     other.close()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_call_entry_point(fmt):
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    rows, kinds = [(300, 299), (400, 200), (70, 66)], [0, 1, 1]
+    cache, pt, _ = _filled(fmt, rows, 2, 64, 71)
+    q = np.random.default_rng(72).standard_normal((205, 8, 64)).astype(np.float16)
+    want = _attend(cache, pt, rows, kinds, 8, q)
+    got = mq.mixed_attention(cache, torch.from_numpy(q).cuda(), torch.from_numpy(pt).cuda(), [r[0] for r in rows],
+                             [r[1] for r in rows], kinds)
+    np.testing.assert_array_equal(got.cpu().numpy().astype(np.float64), want)
+    with pytest.raises(mq.MixattnError) as e:
+        mq.mixed_attention_noalloc(cache, torch.from_numpy(q).cuda(), torch.from_numpy(pt).cuda(),
+                                   [r[0] for r in rows], [r[1] for r in rows], kinds)
+    assert e.value.status == mq.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_planes_past_four_gigabytes(fmt):
+    """Pages whose offsets need more than 32 bits, at both ends of the pool."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    hkv, d, pages = 8, 128, 140_000  # 4.6 GB of codes for each of K and V
+    cache = _alloc(fmt, pages, hkv, d, fill=None)
+    ids = np.array([pages - 1, 0, pages - 7, 131_072, 131_071], dtype=np.int32)
+    seq, off, hq = 150, 100, 32
+    rng = np.random.default_rng(81)
+    k, v = rng.standard_normal((2, seq, hkv, d)).astype(np.float16)
+    t = np.arange(seq)
+    slots = ids[t // 32] * 32 + t % 32
+    _append(cache, k, v, slots)
+    q = rng.standard_normal((seq - off + 1, hq, d)).astype(np.float16)
+    pt = np.stack([ids, ids])
+    got = _attend(cache, pt, [(seq, off), (seq, seq - 1)], [1, 0], hq, q)
+    assert mq.device_error(clear=True) == 0
+    kv, scales = [], []
+    for x in (k, v):
+        r = ref.PageCache(fmt, 5, hkv, d)  # the same appends into a pool of five pages
+        r.append(x, t)
+        kv.append(r.values())
+        scales.append(r.scale.astype(np.float64))
+    want, size = ref.attention(q, kv, [t, t], [(seq, off), (seq, seq - 1)])
+    assert (np.abs(got - want) <= ref.attention_tolerance(fmt, q, want, size, *scales, seq)).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_append_captured_and_replayed(fmt):
+    """An append long enough for clusters, with rotary keys: captured, replayed on other inputs."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    n, hq, hkv, d, pages = 1500, 4, 3, 128, 60
+    rng = np.random.default_rng(91)
+    rope = mq.Rope(128)
+    slots = torch.from_numpy(rng.permutation(pages * 32)[:n].astype(np.int32)).cuda()
+    pos = torch.from_numpy(rng.integers(0, 100000, n).astype(np.int32)).cuda()
+    q, k, v = (torch.randn(n, h, d, device="cuda").half() for h in (hq, hkv, hkv))
+    a, b = _alloc(fmt, pages, hkv, d), _alloc(fmt, pages, hkv, d)
+    oa, ob = torch.empty_like(q), torch.empty_like(q)
+    mq.rope_append(a, rope, q, k, v, pos, slots, oa)
+    torch.cuda.synchronize()
+    for t in (a.k_quant, a.v_quant, a.k_scale, a.v_scale):
+        t.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mq.rope_append(a, rope, q, k, v, pos, slots, oa)
+    for _ in range(3):
+        for x in (q, k, v):
+            x.copy_(torch.randn_like(x))
+        g.replay()
+        mq.rope_append(b, rope, q, k, v, pos, slots, ob)
+        torch.cuda.synchronize()
+        for x, y in ((oa, ob), (a.k_quant, b.k_quant), (a.v_quant, b.v_quant), (a.k_scale, b.k_scale)):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_two_streams_at_once(fmt):
+    """Two batches side by side on two streams, each with its own plan and workspace."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    jobs = []
+    for seed, rows, kinds in ((1, [(3000, 2000), (5000, 4999), (900, 896)], [1, 0, 1]),
+                              (2, [(2500, 0), (7000, 6999)], [1, 0])):
+        cache, pt, _ = _filled(fmt, rows, 4, 128, seed)
+        n = sum(s - o for s, o in rows)
+        q = torch.from_numpy(np.random.default_rng(seed).standard_normal((n, 16, 128)).astype(np.float16)).cuda()
+        plan = mq.Plan(cache, 16, kinds, [r[0] for r in rows], [r[1] for r in rows], pt.shape[1])
+        jobs.append((plan, q, torch.from_numpy(pt).cuda(), torch.empty_like(q), mq.alloc_workspace(plan.workspace_bytes)))
+    want = []
+    for plan, q, pt, o, ws in jobs:
+        plan.run(q, pt, o, ws)
+        torch.cuda.synchronize()
+        want.append(o.clone())
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        for (plan, q, pt, o, ws), s in zip(jobs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                o.zero_()
+                plan.run(q, pt, o, ws)
+        torch.cuda.synchronize()
+        for (_, _, _, o, _), w in zip(jobs, want):
+            assert torch.equal(o, w)
+    assert mq.device_error(clear=True) == 0
