@@ -669,6 +669,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
       const int prow = (two ? gq * 128 : 0) + row;
       const int tok = prow >> lg;
       const bool row_valid = tok < t.count;
+      const bool idle = (prow & ~31) >= t.count * G;  // a warp whose rows are all past the tile's only keeps step
       const int pos = ri.q_offset + t.begin + min(tok, t.count - 1);
       const int lo = window_first_key(pos, p.window);
       const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
@@ -679,6 +680,11 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         if (!ok) break;
         ++n_qk;
         tc_fence_after();
+        if (idle) {  // (its P' rows are whatever was there: no other row's result reads them)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[gq]);
+          continue;
+        }
         const float4* terms = reinterpret_cast<const float4*>(smem + L::kTerms) + 4 * ((jg0 + j) & 3);
         const int kbase = (kv0 + j) * kChunkN;
         // the first and last visible key of the row in this tile (usually 0 and 127)
@@ -785,7 +791,8 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
       };
       uint16_t* dst = static_cast<uint16_t*>(p.o) +
                       ((int64_t)(ri.q_start + t.begin + tok) * p.hq + (int64_t)t.kvh * G + head) * D;
-      if (t.nsplit == 1) {
+      if (idle) {
+      } else if (t.nsplit == 1) {
         const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
 #pragma unroll 1
         for (int ch = 0; ch < D / 16; ++ch) {
