@@ -81,11 +81,17 @@ MIXATTN_HD int decode_pages_per_warp(int n_pages) {
 
 MIXATTN_HD int decode_pages_per_split(int n_pages) { return kWarps * decode_pages_per_warp(n_pages); }
 
-// The same for the page-scaled formats, whose decode tiles have 4 warps.
+// The same for the page-scaled formats, whose decode tiles have 4 warps, with
+// eight pages a warp at least: a second split costs a short row about 3 us (its
+// partial, the ticket, the merge).  Least pages a warp 1 / 2 / 4 / 8, in us: one
+// row of 300 tokens (32 query, 8 kv heads, D 128) 10.6 / 10.0 / 7.3 / 7.3, eight
+// rows of 1000 tokens 13.4 / 12.8 / 12.5 / 12.3, a 4-token verify row at 996
+// tokens 13.1 / 15.7 / 15.1 / 12.4; 16 rows of 8192 tokens 55.6 / 55.8 / 55.7 /
+// 55.5; the serving mix 158.8 / 158.7 / 158.8 / 160.5.
 constexpr int kPageWarps = 4;
 MIXATTN_HD int page_decode_pages_per_split(int n_pages) {
   const int p = (n_pages + 31) / 32;
-  return kPageWarps * (p < 1 ? 1 : (p > 32 ? 32 : p));
+  return kPageWarps * (p < 8 ? 8 : (p > 32 ? 32 : p));
 }
 
 // Formats with one fp32 scale per (page, kv head).
