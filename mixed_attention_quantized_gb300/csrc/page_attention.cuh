@@ -467,7 +467,8 @@ struct PageChunkSmem {
   static constexpr int kMl = 6 * kTile;      // (m, l) of group 1's rows
   static constexpr int kTerms = kMl + 1024;  // [4][4] terms of the pages of KV tile jg in slot jg % 4
   static constexpr int kBar = kTerms + 256;
-  static constexpr int kTotal = kBar + 256 + 1024;  // + slack for 1024-byte alignment
+  static constexpr int kOut = kBar + 256;    // 2 KB a softmax warp: 32 columns of its rows' output
+  static constexpr int kTotal = kOut + 8 * 2048 + 1024;  // + slack for 1024-byte alignment
 };
 
 // Sixteen codes as two 16-byte chunks of fp16 values.
@@ -620,7 +621,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
   if (warp < 8) {
     // ======================= softmax groups =======================
     const int gq = warp >> 2;
-    const int row = tid & 127, head = row & (G - 1);
+    const int row = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + 128 * gq;
     const uint32_t o_col = tmem + lane_base + kOCol + 128 * gq;
@@ -644,14 +645,19 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
     auto write_q = [&](int k) {
       const TileDesc t = p.tiles[chunk_tile_of(cta, k, n_ctas, p.n_chunk_tiles)];
       const RowInfo ri = p.rows[t.row];
-      const int tok = ((t.count * G > 128 ? gq * 128 : 0) + row) >> lg;
+      const int base = t.count * G > 128 ? gq * 128 : 0;
       const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                            ((int64_t)(ri.q_start + t.begin + min(tok, t.count - 1)) * p.hq + (int64_t)t.kvh * G + head) * D;
+                            ((int64_t)(ri.q_start + t.begin) * p.hq + (int64_t)t.kvh * G) * D;
       uint8_t* dst = smem + L::kQ + gq * L::kTile;
+      // a row's 16-byte chunks to neighbouring lanes, 2 or 4 rows a load (one row a lane is 32 lines
+      // a load: 7500 cycles for the tile, and the page ids and K codes wait behind them)
+      constexpr int CH = D / 8;
+      const int c = lane % CH;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = tok < t.count ? ldg_u128(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + sw128_off(row, c & 7)) = w;
+      for (int i = 0; i < CH; ++i) {
+        const int r = 32 * (warp & 3) + i * (32 / CH) + lane / CH, tok = (base + r) >> lg, h = (base + r) & (G - 1);
+        const uint4 w = tok < t.count ? ldg_u128(src + ((int64_t)tok * p.hq + h) * D + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + sw128_off(r, c & 7)) = w;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -789,42 +795,58 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
           tmem_wait_ld();
         }
       };
-      uint16_t* dst = static_cast<uint16_t*>(p.o) +
-                      ((int64_t)(ri.q_start + t.begin + tok) * p.hq + (int64_t)t.kvh * G + head) * D;
+      // 32 columns (from d0) of the warp's rows, packed, to the output: through shared memory, so that
+      // a store has four lanes to a row
+      const int row0 = prow & ~31, n_rows = t.count * G - row0;
+      uint16_t* dst = static_cast<uint16_t*>(p.o) + ((int64_t)(ri.q_start + t.begin) * p.hq + (int64_t)t.kvh * G) * D;
+      uint8_t* stage = smem + L::kOut + 2048 * warp;
+      auto put = [&](int d0, const uint32_t(&w)[16]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(stage + 64 * lane + 16 * (c ^ ((lane >> 1) & 3))) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2), c = lane & 3;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
+          if (r < n_rows)
+            *reinterpret_cast<uint4*>(dst + ((int64_t)((row0 + r) >> lg) * p.hq + ((row0 + r) & (G - 1))) * D + d0 + 8 * c) = x;
+        }
+        __syncwarp();
+      };
       if (idle) {
       } else if (t.nsplit == 1) {
         const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
 #pragma unroll 1
-        for (int ch = 0; ch < D / 16; ++ch) {
-          uint32_t v[16];
-          o_chunk(ch, v);
-          if (row_valid) {
+        for (int ch = 0; ch < D / 16; ch += 2) {
+          uint32_t w[16];
 #pragma unroll
-            for (int q4 = 0; q4 < 2; ++q4) {
-              uint32_t w[4];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[16];
+            o_chunk(ch + h, v);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_f16x2_out(__uint_as_float(v[8 * q4 + 2 * e]) * inv_l, __uint_as_float(v[8 * q4 + 2 * e + 1]) * inv_l);
-              *reinterpret_cast<uint4*>(dst + 16 * ch + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int e = 0; e < 8; ++e)
+              w[8 * h + e] = pack_f16x2_out(__uint_as_float(v[2 * e]) * inv_l, __uint_as_float(v[2 * e + 1]) * inv_l);
           }
+          put(16 * ch, w);
         }
       } else {
-        // a piece of a cut tile leaves (m, l, O) of its rows; each warp's rows are merged by
-        // the last piece's same warp to finish (a 4-bit ticket per warp, in the word of the
-        // tile's first piece)
+        // a piece of a cut tile leaves (m, l, O) of its rows (O as [32 rows][D / 4][row] of 4 columns);
+        // each warp's rows are merged by the last piece's same warp to finish (a 4-bit ticket per
+        // warp, in the word of the tile's first piece)
         const int64_t n_o = (int64_t)p.n_chunk_tiles * kPageChunkM * D;
-        float* o_part = p.chunk_partials + ((int64_t)idx * kPageChunkM + prow) * D;
-        float* ml_part = p.chunk_partials + n_o + ((int64_t)idx * kPageChunkM + prow) * 2;
-        ml_part[0] = m_run;
-        ml_part[1] = l_run;
+        auto o_at = [&](int tile) { return p.chunk_partials + ((int64_t)tile * kPageChunkM + row0) * D + 4 * lane; };
+        auto ml_at = [&](int tile) { return reinterpret_cast<float2*>(p.chunk_partials + n_o) + (int64_t)tile * kPageChunkM + prow; };
+        *ml_at(idx) = make_float2(m_run, l_run);
+        float* o_part = o_at(idx);
 #pragma unroll 1
         for (int ch = 0; ch < D / 16; ++ch) {
           uint32_t v[16];
           o_chunk(ch, v);
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4)
-            *reinterpret_cast<uint4*>(o_part + 16 * ch + 4 * q4) =
+            *reinterpret_cast<uint4*>(o_part + 128 * (4 * ch + q4)) =
                 make_uint4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
         }
         __threadfence();
@@ -835,38 +857,34 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         ticket = __shfl_sync(0xFFFFFFFFu, ticket, 0);
         if (ticket == (unsigned)(t.nsplit - 1)) {
           __threadfence();
-          const float* ml0 = p.chunk_partials + n_o + ((int64_t)first * kPageChunkM + prow) * 2;
-          const float* o0 = p.chunk_partials + ((int64_t)first * kPageChunkM + prow) * D;
-          float m_all = -CUDART_INF_F;
-          for (int q = 0; q < t.nsplit; ++q) m_all = fmaxf(m_all, __ldcg(ml0 + (int64_t)q * kPageChunkM * 2));
-          float w[4], l_all = 0.f;
+          float w[4], m_all = -CUDART_INF_F, l_all = 0.f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            w[q] = 0.f;
-            if (q < t.nsplit) {
-              const float mq = __ldcg(ml0 + (int64_t)q * kPageChunkM * 2);
-              w[q] = mq == -CUDART_INF_F ? 0.f : ex2(mq - m_all);
-              l_all += w[q] * __ldcg(ml0 + (int64_t)q * kPageChunkM * 2 + 1);
-            }
+            w[q] = q < t.nsplit ? __ldcg(ml_at(first + q)).x : -CUDART_INF_F;
+            m_all = fmaxf(m_all, w[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            w[q] = w[q] == -CUDART_INF_F ? 0.f : ex2(w[q] - m_all);
+            if (q < t.nsplit) l_all += w[q] * __ldcg(ml_at(first + q)).y;
           }
           const float inv_l = 1.f / l_all;
-          if (row_valid) {
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 8) {
-              float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int d0 = 0; d0 < D; d0 += 32) {
+            uint32_t out[16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (q >= t.nsplit || w[q] == 0.f) continue;
-                const float* op = o0 + (int64_t)q * kPageChunkM * D + d0;
-                const float4 x0 = __ldcg(reinterpret_cast<const float4*>(op));
-                const float4 x1 = __ldcg(reinterpret_cast<const float4*>(op + 4));
-                acc[0] += w[q] * x0.x; acc[1] += w[q] * x0.y; acc[2] += w[q] * x0.z; acc[3] += w[q] * x0.w;
-                acc[4] += w[q] * x1.x; acc[5] += w[q] * x1.y; acc[6] += w[q] * x1.z; acc[7] += w[q] * x1.w;
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(o_at(first + q) + 128 * (d0 / 4 + c)));
+                acc.x += w[q] * x.x; acc.y += w[q] * x.y; acc.z += w[q] * x.z; acc.w += w[q] * x.w;
               }
-              *reinterpret_cast<uint4*>(dst + d0) =
-                  make_uint4(pack_f16x2_out(acc[0] * inv_l, acc[1] * inv_l), pack_f16x2_out(acc[2] * inv_l, acc[3] * inv_l),
-                             pack_f16x2_out(acc[4] * inv_l, acc[5] * inv_l), pack_f16x2_out(acc[6] * inv_l, acc[7] * inv_l));
+              out[2 * c] = pack_f16x2_out(acc.x * inv_l, acc.y * inv_l);
+              out[2 * c + 1] = pack_f16x2_out(acc.z * inv_l, acc.w * inv_l);
             }
+            put(d0, out);
           }
         }
       }
