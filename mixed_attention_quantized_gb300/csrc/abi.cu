@@ -146,6 +146,7 @@ struct Tiling {
   int32_t total_q = 0, n_chunk = 0, n_decode = 0;
   int32_t slot_rows = 0;       // rows of a decode partial slot
   int32_t chunk_kv_tiles = 0;  // KV tiles over all chunk tiles (their mean decides persistence)
+  int64_t chunk_kv_halves = 0; // the same, a tile of more than 128 rows counted twice
   int32_t decode_pages = 0;    // pages over all decode tiles
   WorkspaceLayout L{};
 };
@@ -159,12 +160,12 @@ int device_sm_count() {
 }
 
 // Pieces per chunk tile of one chunk row: the key range of each of the row's
-// tiles is cut into s pieces (s = 1..4) when that shortens the row's share of
+// tiles is cut into s pieces (s = 1..most) when that shortens the row's share of
 // the launch, judged by placing the pieces heaviest first on the least-loaded
 // of n_sm SMs (one chunk CTA per SM).  A piece costs its KV tiles plus one for
 // its prologue and the merge; rows with a tile shorter than 8 KV tiles are
 // never cut.
-int chunk_split_factor(const std::vector<int64_t>& costs, int n_sm) {
+int chunk_split_factor(const std::vector<int64_t>& costs, int n_sm, int most) {
   if (n_sm <= 0 || costs.empty()) return 1;
   int64_t min_cost = costs[0];
   for (int64_t c : costs) min_cost = std::min(min_cost, c);
@@ -188,7 +189,7 @@ int chunk_split_factor(const std::vector<int64_t>& costs, int n_sm) {
   };
   int best = 1;
   int64_t best_span = makespan(1);
-  for (int s = 2; s <= 4; ++s) {
+  for (int s = 2; s <= most; ++s) {
     const int64_t sp = makespan(s);
     if (sp * 20 < best_span * 19) {  // at least 5% shorter
       best = s;
@@ -263,7 +264,7 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
       // a row's result does not depend on the rest of the batch
       std::vector<int64_t> costs;
       for (size_t i = first_chunk; i < chunks.size(); ++i) costs.push_back(chunks[i].cost);
-      const int split = chunk_split_factor(costs, n_sm);
+      const int split = chunk_split_factor(costs, n_sm, page_scaled(c.k_fmt) ? kPageMaxPieces : 4);
       for (size_t i = first_chunk; i < chunks.size(); ++i) chunks[i].split = split;
     } else {
       // pages from the one holding the first query's window start (page 0 without a
@@ -325,9 +326,11 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   memcpy(T2.image.data(), rows.data(), sizeof(RowInfo) * rows.size());
   TileDesc* td = reinterpret_cast<TileDesc*>(T2.image.data() + (T2.L.tiles - T2.L.rows));
   int64_t at = 0, kv_tiles = 0;
+  T2.chunk_kv_halves = 0;
   for (size_t i = 0; i < chunks.size(); ++i) {
     const int64_t n_kv = chunks[i].cost, kv_first = chunks[i].kv_first;
     kv_tiles += n_kv;
+    T2.chunk_kv_halves += n_kv * (chunks[i].t.count * G > 128 ? 2 : 1);
     const int split = chunks[i].split;
     for (int q = 0; q < split; ++q) {
       TileDesc t = chunks[i].t;
@@ -723,6 +726,7 @@ int mixattn_run(const mixattn_plan* plan_c, const void* q, const int32_t* page_t
   p.num_pages = c.num_pages;
   p.n_chunk_tiles = plan->tiling.n_chunk;
   p.chunk_kv_tiles = plan->tiling.chunk_kv_tiles;
+  p.chunk_kv_halves = (int32_t)std::min<int64_t>(plan->tiling.chunk_kv_halves, INT32_MAX);
   p.n_decode_tiles = plan->tiling.n_decode;
   p.decode_pages = plan->tiling.decode_pages;
   p.hq = plan->hq;

@@ -27,6 +27,7 @@ constexpr int kFusedThreads = 512; // threads of a fused-launch CTA: three worki
                                    // the first kThreads
 constexpr int kChunkM = 128;       // rows (query tokens x group heads) of a chunk tile
 constexpr int kPageChunkM = 256;   // the same for the page-scaled formats: two 128-row query tiles
+constexpr int kPageMaxPieces = 4;  // pieces of a chunk tile's key range, at most
 constexpr int kChunkN = 128;       // keys per KV tile of the chunk path (4 pages)
 constexpr int kPagesPerKvTile = kChunkN / kPage;
 constexpr int kMaxGroup = 8;       // q heads per kv head held in one mma N=8 tile
@@ -162,6 +163,7 @@ struct AttnParams {
   int32_t n_chunk_tiles;
   int32_t n_chunk_ctas;       // CTAs walking the chunk tiles (set by the launcher)
   int32_t chunk_kv_tiles;     // KV tiles over all chunk tiles
+  int32_t chunk_kv_halves;    // (page-scaled formats) the same, a tile of more than 128 rows counted twice
   int32_t n_decode_tiles;
   int32_t decode_pages = 0;   // pages over all decode tiles (set by a plan)
   int32_t hq;

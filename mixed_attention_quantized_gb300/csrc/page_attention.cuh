@@ -572,6 +572,84 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
   return make_float2(m_new, fmaf(l_page, tm.z, l_run));
 }
 
+// A chunk tile's output rows, D elements each, heads first, then tokens; written by a warp through
+// its 2 KB of shared memory, so that a store has four lanes to a row.
+struct PageRowsOut {
+  uint8_t* stage;
+  uint16_t* dst;  // row 0
+  int n_rows, lg, hq;
+
+  // columns d0 .. d0 + 31 of row row0 + lane, packed
+  template <int D>
+  __device__ __forceinline__ void put(int row0, int d0, const uint32_t (&w)[16]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint4*>(stage + 64 * lane + 16 * (c ^ ((lane >> 1) & 3))) =
+          make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), c = lane & 3, row = row0 + r;
+      const uint4 x = *reinterpret_cast<const uint4*>(stage + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
+      if (row < n_rows)
+        *reinterpret_cast<uint4*>(dst + ((int64_t)(row >> lg) * hq + (row & ((1 << lg) - 1))) * D + d0 + 8 * c) = x;
+    }
+    __syncwarp();
+  }
+};
+
+// Joins the pieces of a cut chunk tile for units u, u + u_step, .. below u_end; unit i is 32 rows
+// (block i / (D / 32)) by 32 columns.  o and ml: the first piece's partials.  Out of line, so that
+// it takes no registers from the common path.
+template <int D>
+__device__ __noinline__ void page_merge_pieces(PageRowsOut out, const float* o, const float2* ml, int nsplit, int u,
+                                               int u_end, int u_step) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; u < u_end; u += u_step) {
+    const int row0 = 32 * (u / (D / 32)), d0 = 32 * (u % (D / 32));
+    const float* o_unit = o + (int64_t)row0 * D + 32 * d0 + 4 * lane;
+    float2 s[kPageMaxPieces];
+    float m_all = -CUDART_INF_F, l_all = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPageMaxPieces; ++q) s[q] = __ldcg(ml + min(q, nsplit - 1) * kPageChunkM + row0 + lane);
+#pragma unroll
+    for (int q = 0; q < kPageMaxPieces; ++q) {
+      if (q >= nsplit) s[q].x = -CUDART_INF_F;
+      m_all = fmaxf(m_all, s[q].x);
+    }
+#pragma unroll
+    for (int q = 0; q < kPageMaxPieces; ++q) {
+      s[q].x = s[q].x == -CUDART_INF_F ? 0.f : ex2(s[q].x - m_all);
+      if (s[q].x != 0.f) l_all += s[q].x * s[q].y;
+    }
+    const float inv_l = 1.f / l_all;
+    uint32_t x[16];
+#pragma unroll
+    for (int c0 = 0; c0 < 8; c0 += 4) {  // the loads of 16 columns together
+      float4 y[kPageMaxPieces][4];
+#pragma unroll
+      for (int q = 0; q < kPageMaxPieces; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          y[q][c] = __ldcg(reinterpret_cast<const float4*>(o_unit + min(q, nsplit - 1) * (kPageChunkM * D) + 128 * (c0 + c)));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < kPageMaxPieces; ++q) {
+          if (s[q].x == 0.f) continue;  // (no key of the row in this piece, or no such piece: any value may stand there)
+          acc.x += s[q].x * y[q][c].x; acc.y += s[q].x * y[q][c].y; acc.z += s[q].x * y[q][c].z; acc.w += s[q].x * y[q][c].w;
+        }
+        x[2 * (c0 + c)] = pack_f16x2_out(acc.x * inv_l, acc.y * inv_l);
+        x[2 * (c0 + c) + 1] = pack_f16x2_out(acc.z * inv_l, acc.w * inv_l);
+      }
+    }
+    out.put<D>(row0, d0, x);
+  }
+}
+
 // The launches overlap the end of the kernel before them, which writes the tile list into the
 // workspace: nothing of the workspace (nor the tensors, which earlier kernels may be writing)
 // is touched before that grid is complete.
@@ -757,6 +835,13 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
       if (!ok) break;
       tc_fence_after();
       const bool join = !two && n_kv > 1;
+      const int row0 = prow & ~31;
+      const PageRowsOut out{smem + L::kOut + 2048 * warp,
+                            static_cast<uint16_t*>(p.o) + ((int64_t)(ri.q_start + t.begin) * p.hq + (int64_t)t.kvh * G) * D,
+                            t.count * G, lg, p.hq};
+      float* part = p.chunk_partials + (int64_t)idx * kPageChunkM * D;  // [32-row block][D / 4][row] of 4 columns
+      float2* ml_part = reinterpret_cast<float2*>(p.chunk_partials + (int64_t)p.n_chunk_tiles * kPageChunkM * D) +
+                        (int64_t)idx * kPageChunkM;
       if (join && gq == 1) {  // hand (m, l, O) to group 0 and wait until it has read them
         ml[row] = make_float2(m_run, l_run);
         tc_fence_before();
@@ -764,135 +849,90 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         if (lane == 0) mbar_arrive(ml_ready);
         ok = warp_wait(joined, n_join & 1, err);
         ++n_join;
-        tc_fence_after();
-        k = kn;
-        continue;
-      }
-      float w0 = 1.f, w1 = 0.f;  // weights of the two groups' O
-      if (join) {
-        ok = warp_wait(ml_ready, n_join & 1, err);
-        ++n_join;
         if (!ok) break;
         tc_fence_after();
-        const float2 other = ml[row];
-        const float m = fmaxf(m_run, other.x);
-        w0 = m_run == -CUDART_INF_F ? 0.f : ex2(m_run - m);
-        w1 = other.x == -CUDART_INF_F ? 0.f : ex2(other.x - m);
-        l_run = l_run * w0 + other.y * w1;
-        m_run = m;
-      }
-      // 16 columns of the tile's O, unnormalised
-      auto o_chunk = [&](int ch, uint32_t(&v)[16]) {
-        tmem_ld16(o_col + 16 * ch, v);
-        if (join) {
-          uint32_t u[16];
-          tmem_ld16(o_col + 128 + 16 * ch, u);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = __float_as_uint(__uint_as_float(v[e]) * w0 + __uint_as_float(u[e]) * w1);
-        } else {
-          tmem_wait_ld();
-        }
-      };
-      // 32 columns (from d0) of the warp's rows, packed, to the output: through shared memory, so that
-      // a store has four lanes to a row
-      const int row0 = prow & ~31, n_rows = t.count * G - row0;
-      uint16_t* dst = static_cast<uint16_t*>(p.o) + ((int64_t)(ri.q_start + t.begin) * p.hq + (int64_t)t.kvh * G) * D;
-      uint8_t* stage = smem + L::kOut + 2048 * warp;
-      auto put = [&](int d0, const uint32_t(&w)[16]) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(stage + 64 * lane + 16 * (c ^ ((lane >> 1) & 3))) =
-              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 2), c = lane & 3;
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
-          if (r < n_rows)
-            *reinterpret_cast<uint4*>(dst + ((int64_t)((row0 + r) >> lg) * p.hq + ((row0 + r) & (G - 1))) * D + d0 + 8 * c) = x;
-        }
-        __syncwarp();
-      };
-      if (idle) {
-      } else if (t.nsplit == 1) {
-        const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
-#pragma unroll 1
-        for (int ch = 0; ch < D / 16; ch += 2) {
-          uint32_t w[16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[16];
-            o_chunk(ch + h, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[8 * h + e] = pack_f16x2_out(__uint_as_float(v[2 * e]) * inv_l, __uint_as_float(v[2 * e + 1]) * inv_l);
-          }
-          put(16 * ch, w);
-        }
       } else {
-        // a piece of a cut tile leaves (m, l, O) of its rows (O as [32 rows][D / 4][row] of 4 columns);
-        // each warp's rows are merged by the last piece's same warp to finish (a 4-bit ticket per
-        // warp, in the word of the tile's first piece)
-        const int64_t n_o = (int64_t)p.n_chunk_tiles * kPageChunkM * D;
-        auto o_at = [&](int tile) { return p.chunk_partials + ((int64_t)tile * kPageChunkM + row0) * D + 4 * lane; };
-        auto ml_at = [&](int tile) { return reinterpret_cast<float2*>(p.chunk_partials + n_o) + (int64_t)tile * kPageChunkM + prow; };
-        *ml_at(idx) = make_float2(m_run, l_run);
-        float* o_part = o_at(idx);
-#pragma unroll 1
-        for (int ch = 0; ch < D / 16; ++ch) {
-          uint32_t v[16];
-          o_chunk(ch, v);
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
-            *reinterpret_cast<uint4*>(o_part + 128 * (4 * ch + q4)) =
-                make_uint4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+        float w0 = 1.f, w1 = 0.f;  // weights of the two groups' O
+        if (join) {
+          ok = warp_wait(ml_ready, n_join & 1, err);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 other = ml[row];
+          const float m = fmaxf(m_run, other.x);
+          w0 = m_run == -CUDART_INF_F ? 0.f : ex2(m_run - m);
+          w1 = other.x == -CUDART_INF_F ? 0.f : ex2(other.x - m);
+          l_run = l_run * w0 + other.y * w1;
+          m_run = m;
         }
+        // 16 columns of the tile's O, unnormalised
+        auto o_chunk = [&](int ch, uint32_t(&v)[16]) {
+          tmem_ld16(o_col + 16 * ch, v);
+          if (join) {
+            uint32_t u[16];
+            tmem_ld16(o_col + 128 + 16 * ch, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[e] = __float_as_uint(__uint_as_float(v[e]) * w0 + __uint_as_float(u[e]) * w1);
+          } else {
+            tmem_wait_ld();
+          }
+        };
+        if (idle) {
+        } else if (t.nsplit == 1) {
+          const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ch += 2) {
+            uint32_t w[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[16];
+              o_chunk(ch + h, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[8 * h + e] = pack_f16x2_out(__uint_as_float(v[2 * e]) * inv_l, __uint_as_float(v[2 * e + 1]) * inv_l);
+            }
+            out.put<D>(row0, 16 * ch, w);
+          }
+        } else {  // a piece of a cut tile leaves (m, l, O) of its rows
+          ml_part[prow] = make_float2(m_run, l_run);
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint32_t v[16];
+            o_chunk(ch, v);
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              *reinterpret_cast<uint4*>(part + (int64_t)row0 * D + 128 * (4 * ch + q4) + 4 * lane) =
+                  make_uint4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+          }
+        }
+        // O has been read: the groups' next p_ready lets the next tile's first PVs overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (join) {
+          if (lane == 0) mbar_arrive(joined);
+          if (t.nsplit > 1) ok = warp_wait(joined, n_join & 1, err);  // (below, this warp speaks for the others)
+          ++n_join;
+          if (!ok) break;
+        }
+      }
+      // The last piece to finish joins all: of a tile with rows in both groups each warp its own
+      // rows, else all eight warps a share (every piece has two KV tiles or more, so both groups
+      // are here for each).  A 4-bit ticket per warp, in the word of the tile's first piece; joined
+      // in the pieces' order, whichever was last.
+      if (t.nsplit > 1 && !(two && idle)) {
         __threadfence();
         __syncwarp();
-        const int first = idx - t.part;
         unsigned ticket = 0;
-        if (lane == 0) ticket = (atomicAdd(&p.chunk_counters[first], 1u << (4 * warp)) >> (4 * warp)) & 15u;
+        if (lane == 0) ticket = (atomicAdd(&p.chunk_counters[idx - t.part], 1u << (4 * warp)) >> (4 * warp)) & 15u;
         ticket = __shfl_sync(0xFFFFFFFFu, ticket, 0);
         if (ticket == (unsigned)(t.nsplit - 1)) {
           __threadfence();
-          float w[4], m_all = -CUDART_INF_F, l_all = 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            w[q] = q < t.nsplit ? __ldcg(ml_at(first + q)).x : -CUDART_INF_F;
-            m_all = fmaxf(m_all, w[q]);
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            w[q] = w[q] == -CUDART_INF_F ? 0.f : ex2(w[q] - m_all);
-            if (q < t.nsplit) l_all += w[q] * __ldcg(ml_at(first + q)).y;
-          }
-          const float inv_l = 1.f / l_all;
-#pragma unroll 1
-          for (int d0 = 0; d0 < D; d0 += 32) {
-            uint32_t out[16];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (q >= t.nsplit || w[q] == 0.f) continue;
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(o_at(first + q) + 128 * (d0 / 4 + c)));
-                acc.x += w[q] * x.x; acc.y += w[q] * x.y; acc.z += w[q] * x.z; acc.w += w[q] * x.w;
-              }
-              out[2 * c] = pack_f16x2_out(acc.x * inv_l, acc.y * inv_l);
-              out[2 * c + 1] = pack_f16x2_out(acc.z * inv_l, acc.w * inv_l);
-            }
-            put(d0, out);
-          }
+          constexpr int U = D / 32;
+          const int u0 = two ? (row0 / 32) * U : warp, u_end = two ? u0 + U : ((t.count * G + 31) / 32) * U;
+          page_merge_pieces<D>(out, part - (int64_t)t.part * kPageChunkM * D, ml_part - (int64_t)t.part * kPageChunkM, t.nsplit,
+                               u0, u_end, two ? 1 : 8);
         }
-      }
-      // O has been read: the groups' next p_ready lets the next tile's first PVs overwrite it
-      tc_fence_before();
-      if (join) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(joined);
       }
       k = kn;
     }
@@ -958,8 +998,29 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
           dv = ldg_f32_or(p.v_scale, at_a, in_a, 1.f);
         }
       };
+      // The loads reach one tile ahead, less than HBM's latency; each K warp's page of the tiles up
+      // to kAhead ahead, its V and its scales are on their way to L2 before.
+      constexpr int kAhead = 4;
+      auto ahead_id = [&](int j) {
+        const int pg = j * kPagesPerKvTile + w;
+        return ldg_s32_or(pt_row + pg, !is_v && j < n_kv && pg * kPage < key_end, kNoPage);
+      };
+      auto to_l2 = [&](int pid) {
+        if (pid < 0 || pid >= p.num_pages) return;
+        const int64_t at = (int64_t)pid * p.hkv + t.kvh;
+        if (D == 128 || lane < 16) prefetch_l2(p.k_quant + at * (kPage * D) + 128 * (lane % (D / 4)));
+        if (D == 128 || lane >= 16) prefetch_l2(p.v_quant + at * (kPage * D) + 128 * (lane % (D / 4)));
+        if (lane < 2) prefetch_l2((lane ? p.v_scale : p.k_scale) + at);
+      };
       load(0, pids_of(0));
       int2 next_pid = pids_of(1);
+      int ahead = kNoPage;
+      if (!is_v) {
+        const int id = ahead_id(1 + lane % kAhead);
+#pragma unroll 1
+        for (int i = 0; i < kAhead - 1; ++i) to_l2(__shfl_sync(0xFFFFFFFFu, id, i));
+        ahead = __shfl_sync(0xFFFFFFFFu, id, kAhead - 1);
+      }
       for (int j = 0; j < n_kv; ++j, ++jg) {
         if (jg > 1) ok = warp_wait(&freed[jg & 1], (uint32_t)(((jg - 2) >> 1) & 1), err);  // tile jg - 2 has been read
         if (!ok) break;
@@ -982,6 +1043,10 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         if (j + 1 < n_kv) {
           load(j + 1, next_pid);
           next_pid = pids_of(j + 2);
+          if (!is_v) {
+            to_l2(ahead);
+            ahead = ahead_id(j + 1 + kAhead);
+          }
         }
       }
     }
@@ -1089,7 +1154,7 @@ __global__ void __launch_bounds__(kPageThreads, PageDecodeSmem<D>::kCtas) page_d
   page_decode_tile<F, D>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
 }
 
-constexpr double kChunkShare = 1.15;
+constexpr double kChunkShare = 1.15, kHalf = 2650.0;
 
 // The fused launch: chunk CTAs, then decode CTAs of several tiles each.
 template <int D>
@@ -1158,7 +1223,7 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
     // together, and a little more (decode CTAs take over the SMs that they leave, not the
     // other way round).  Costs in SM cycles at head_dim 128, by timing each kind alone: a KV
     // tile of 256 rows 5300, a page of decode 230.
-    const double tc = 5300.0 * p.chunk_kv_tiles, td = 230.0 * p.decode_pages;
+    const double tc = kHalf * p.chunk_kv_halves, td = 230.0 * p.decode_pages;
     const int share = (int)(kChunkShare * sm_count() * tc / (tc + td)) + 1;
     q.n_chunk_ctas = std::min(q.n_chunk_ctas, share);
   }
