@@ -1154,7 +1154,7 @@ __global__ void __launch_bounds__(kPageThreads, PageDecodeSmem<D>::kCtas) page_d
   page_decode_tile<F, D>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
 }
 
-constexpr double kChunkShare = 1.15, kHalf = 2650.0;
+constexpr double kChunkShare = 1.15, kHalf = 2000.0;
 
 // The fused launch: chunk CTAs, then decode CTAs of several tiles each.
 template <int D>
@@ -1222,7 +1222,9 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
     // time it needs anyway.  The chunk CTAs get the share of the SMs that lets both kinds end
     // together, and a little more (decode CTAs take over the SMs that they leave, not the
     // other way round).  Costs in SM cycles at head_dim 128, by timing each kind alone: a KV
-    // tile of 256 rows 5300, a page of decode 230.
+    // tile of 128 rows 2000, a page of decode 230.  A cost of 1500 / 2000 / 2650 / 3300: the
+    // serving mix 171 / 148 / 152 / 153 us, the verify batch 272 / 232 / 234 / 234 us; a share
+    // of 1.3 for 1.15: 154 and 234 us; all SMs to the chunk CTAs: 171.7 us for the mix.
     const double tc = kHalf * p.chunk_kv_halves, td = 230.0 * p.decode_pages;
     const int share = (int)(kChunkShare * sm_count() * tc / (tc + td)) + 1;
     q.n_chunk_ctas = std::min(q.n_chunk_ctas, share);
