@@ -203,8 +203,7 @@ def _stream_handle(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
     rt = _rt or _runtime()
-    import torch
-    return rt.raw_stream(torch.cuda.current_device())
+    return rt.raw_stream(rt.device())
 
 
 def _ptr(t) -> int:
@@ -466,9 +465,9 @@ class Plan:
 
     def run(self, q, page_table, o, workspace, stream=None) -> None:
         st = self._lib.mixattn_run(self._handle, _ptr(q), _ptr(page_table), _ptr(o), _ptr(workspace),
-                                   int(workspace.numel() * workspace.element_size()),
-                                   _stream_handle(stream))
-        _check(st, "mixattn_run")
+                                   workspace.nbytes, _stream_handle(stream))
+        if st:
+            _check(st, "mixattn_run")
 
     def close(self) -> None:
         if self._handle and self._handle.value:
