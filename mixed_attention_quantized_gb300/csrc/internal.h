@@ -27,7 +27,8 @@ constexpr int kFusedThreads = 512; // threads of a fused-launch CTA: three worki
                                    // the first kThreads
 constexpr int kChunkM = 128;       // rows (query tokens x group heads) of a chunk tile
 constexpr int kPageChunkM = 256;   // the same for the page-scaled formats: two 128-row query tiles
-constexpr int kPageMaxPieces = 4;  // pieces of a chunk tile's key range, at most
+constexpr int kPageMaxPieces = 4;  // pieces of a page-scaled tile's key range, at most (six: the verify
+                                   // batch 234 -> 240 us, a piece costs about six KV tiles' time)
 constexpr int kChunkN = 128;       // keys per KV tile of the chunk path (4 pages)
 constexpr int kPagesPerKvTile = kChunkN / kPage;
 constexpr int kMaxGroup = 8;       // q heads per kv head held in one mma N=8 tile
@@ -35,7 +36,8 @@ constexpr int kMaxDevices = 64;    // per-device caches of the host side (device
 constexpr int kVerifyMaxRows = 24; // a chunk row with q_len * G <= this (speculative verify) runs on
                                    // decode-style split-K tiles of up to 8 (query, head) rows: each
                                    // such group costs about a third of a 128-row tensor-core tile
-                                   // per key, so up to three groups are cheaper than one tile
+                                   // per key, so up to three groups are cheaper than one tile (page-
+                                   // scaled, the verify batch at 16 / 24 / 32: 250 / 232 / 246 us)
 
 // Per-row data the kernel needs (copied with the tile list).
 struct RowInfo {
@@ -46,7 +48,7 @@ struct RowInfo {
 };
 
 // One tile of work for one CTA.
-//   chunk:  queries begin .. begin+count-1 of `row` (count <= 128 / G), kv head kvh,
+//   chunk:  queries begin .. begin+count-1 of `row` (count <= chunk_rows / G), kv head kvh,
 //           against 128-key KV tiles kv0 .. kv1-1; a tile whose key range is cut
 //           into nsplit pieces (part = 0 .. nsplit-1, consecutive in the tile
 //           list) leaves partial results that the last piece to finish merges

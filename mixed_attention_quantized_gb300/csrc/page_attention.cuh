@@ -19,6 +19,12 @@
 //              the offset leaves the scores through the accumulators' start, the values
 //              through one more MMA;
 //   E4M3_PAGE  cvt to fp16, two codes an instruction.
+// Bound: HBM once the rows are long (16 rows of 30000 tokens, 8 kv heads of 128: 152 us, 6.5 TB/s;
+// one session of 262144 tokens beside 15 short ones: 115 us, 97 at the copy rate), else the
+// prologue and the merge (one row of 300 tokens 7.1 us, 16 rows of 8192 tokens 56 us; the loads
+// alone take 49).  Keys in the M rows because eight query rows fill N exactly, where as M rows
+// half of an m16 would be padding; four warps because a CTA's splits then end together
+// sooner than with eight (55.6 against 65.8 us for 16 rows of 8192 tokens).
 #pragma once
 
 #include <mutex>
@@ -456,6 +462,13 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
 // Every K warp takes part in every K tile and every V warp in every V tile, so nobody waits
 // for a phase of a barrier that is not the next one.  (A parity says only which of two
 // neighbouring phases is over.)
+// A tile is cut into key ranges when its row alone cannot fill the SMs: a piece leaves (m, l, O) of
+// its rows, and the last to finish joins them.
+// Measured (8 kv heads of 128, four query heads each): the 2048-token chunk at 32768 keys beside
+// four decode rows 1.15 ms, 51% of the dense rate, where a 256 x 128 unit takes ~4000 SM cycles for
+// 2048 of MMAs.  What bounds it: a group's scores take it ~1300 cycles and the two hand-overs
+// ~500, more than the ~1550 of the other group's MMAs beside them (16 MMAs of 64 cycles, each
+// held up by operand reads and operand writes that share the 128 bytes a cycle of shared memory).
 // No role waits at a CTA barrier inside its loop; every wait is on an mbarrier, bounded,
 // and a role that gives up leaves its loops, after which the others' waits run out.
 template <int D>
@@ -948,7 +961,8 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
     const int r0 = is_v ? (w == 0 ? 0 : 8 + 40 * w) : 32 * w;
     const int n_load = (is_v ? (w == 0 ? 48 : 40) : 32) / KPL;
     const int turn = (kPage - (r0 & (kPage - 1))) / KPL;
-    const int cc = lane % CPR, key0 = r0 + lane / CPR;
+    // eight lanes write neighbouring chunks of two keys (of one, at D = 128, they would meet in banks)
+    const int cc = (lane & 3) | (D == 128 ? lane >> 4 << 2 : 0), key0 = r0 + (D == 128 ? (lane >> 2) & 3 : lane >> 2);
     // the lane's two 16-byte places in row key0 of a tile; row key0 + 4 i flips chunk bit 2 for odd i
     const uint32_t off0 = (uint32_t)((cc >> 2) * (128 * 128)) + sw128_off(key0, 2 * (cc & 3));
     const uint32_t off1 = (uint32_t)((cc >> 2) * (128 * 128)) + sw128_off(key0, 2 * (cc & 3) + 1);
@@ -999,7 +1013,8 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         }
       };
       // The loads reach one tile ahead, less than HBM's latency; each K warp's page of the tiles up
-      // to kAhead ahead, its V and its scales are on their way to L2 before.
+      // to kAhead ahead, its V and its scales are on their way to L2 before (16 rows of 16 tokens at
+      // 30000 keys 394 -> 363 us; a long chunk, whose tiles share their keys, is as fast without).
       constexpr int kAhead = 4;
       auto ahead_id = [&](int j) {
         const int pg = j * kPagesPerKvTile + w;
