@@ -23,8 +23,8 @@
 // one session of 262144 tokens beside 15 short ones: 115 us, 97 at the copy rate), else the
 // prologue and the merge (one row of 300 tokens 7.1 us, 16 rows of 8192 tokens 56 us; the loads
 // alone take 49).  Keys in the M rows because eight query rows fill N exactly, where as M rows
-// half of an m16 would be padding; four warps because a CTA's splits then end together
-// sooner than with eight (55.6 against 65.8 us for 16 rows of 8192 tokens).
+// half of an m16 would be padding (with the rows in M and eight warps a tile: 16 rows of 8192
+// tokens 66 us).
 #pragma once
 
 #include <mutex>
@@ -612,6 +612,8 @@ struct PageRowsOut {
   }
 };
 
+static_assert(kPageMaxPieces <= 4, "a tile is cut from eight KV tiles on: its pieces have two or more");
+
 // Joins the pieces of a cut chunk tile for units u, u + u_step, .. below u_end; unit i is 32 rows
 // (block i / (D / 32)) by 32 columns.  o and ml: the first piece's partials.  Out of line, so that
 // it takes no registers from the common path.
@@ -1013,7 +1015,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         }
       };
       // The loads reach one tile ahead, less than HBM's latency; each K warp's page of the tiles up
-      // to kAhead ahead, its V and its scales are on their way to L2 before (16 rows of 16 tokens at
+      // to kAhead ahead and its V are on their way to L2 before (16 rows of 16 tokens at
       // 30000 keys 394 -> 363 us; a long chunk, whose tiles share their keys, is as fast without).
       constexpr int kAhead = 4;
       auto ahead_id = [&](int j) {
@@ -1025,7 +1027,6 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         const int64_t at = (int64_t)pid * p.hkv + t.kvh;
         if (D == 128 || lane < 16) prefetch_l2(p.k_quant + at * (kPage * D) + 128 * (lane % (D / 4)));
         if (D == 128 || lane >= 16) prefetch_l2(p.v_quant + at * (kPage * D) + 128 * (lane % (D / 4)));
-        if (lane < 2) prefetch_l2((lane ? p.v_scale : p.k_scale) + at);
       };
       load(0, pids_of(0));
       int2 next_pid = pids_of(1);
@@ -1239,7 +1240,7 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
     // other way round).  Costs in SM cycles at head_dim 128, by timing each kind alone: a KV
     // tile of 128 rows 2000, a page of decode 230.  A cost of 1500 / 2000 / 2650 / 3300: the
     // serving mix 171 / 148 / 152 / 153 us, the verify batch 272 / 232 / 234 / 234 us; a share
-    // of 1.3 for 1.15: 154 and 234 us; all SMs to the chunk CTAs: 171.7 us for the mix.
+    // of 1.3 for 1.15: 154 and 234 us.
     const double tc = kHalf * p.chunk_kv_halves, td = 230.0 * p.decode_pages;
     const int share = (int)(kChunkShare * sm_count() * tc / (tc + td)) + 1;
     q.n_chunk_ctas = std::min(q.n_chunk_ctas, share);
