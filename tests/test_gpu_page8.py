@@ -158,7 +158,7 @@ def _filled(fmt, rows, hkv, d, seed, gains=None, spare=2, fill=0xFF):
     return cache, pt, row_slots
 
 
-def _attend(cache, pt, rows, kinds, hq, q, window=0, update_from=None):
+def _attend(cache, pt, rows, kinds, hq, q, window=0):
     import torch
     import mixed_attention_quantized_gb300 as mq
     seqs, offs = [r[0] for r in rows], [r[1] for r in rows]
@@ -221,6 +221,22 @@ def test_windows(fmt, window):
 def test_long_rows_split(fmt):
     rows = [(40000, 39999), (20011, 19900), (9000, 8997)]
     _check(fmt, rows, [0, 1, 1], 4, 1, 128, seed=77)
+
+
+CUT = [(7, 1030), (13, 1500), (16, 2309), (25, 1111), (32, 2000), (33, 3001), (50, 1400), (64, 1290), (65, 1025), (130, 4000)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq,hkv,d,window", [(4, 1, 128, 0), (4, 1, 64, 0), (8, 1, 128, 0), (2, 2, 128, 0), (16, 2, 64, 1100)])
+def test_cut_tiles_of_every_row_count(fmt, hq, hkv, d, window):
+    """Key ranges of few long tiles are cut into pieces that the last to finish joins: tiles of one to
+    eight 32-row blocks, the last ones partly filled, and the same bits from every run."""
+    rows = [(c + n, c) for n, c in CUT]
+    got = _check(fmt, rows, [1] * len(rows), hq, hkv, d, seed=13 + hq, window=window)
+    cache, pt, _ = _filled(fmt, rows, hkv, d, 13 + hq)
+    q = np.random.default_rng(14 + hq).standard_normal((got.shape[0], hq, d)).astype(np.float16)
+    for _ in range(3):
+        np.testing.assert_array_equal(_attend(cache, pt, rows, [1] * len(rows), hq, q, window), got)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
