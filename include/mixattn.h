@@ -186,7 +186,7 @@ size_t mixattn_kv_cache_bytes(const mixattn_kv_cache* cache, size_t plane_bytes_
  * page-scaled formats the later one is kept.  There every window of up to 128
  * tokens looks through the whole slot list for tokens of its pages, so a call's
  * time has a part that grows with n_new^2: feed prompts far beyond 32768 tokens
- * (66 us with 8 heads of 128) in several calls.
+ * (65 us with 8 heads of 128) in several calls.
  */
 int mixattn_kv_append_quant(const mixattn_kv_cache* cache, const void* k_new, const void* v_new,
                             const int32_t* slot_mapping, int32_t n_new, mixattn_stream stream);
