@@ -1,0 +1,54 @@
+"""Attention over the page-scaled formats against the tight bound of ``_page8_rows.py``, under
+which no lost page, split or piece of any row passes."""
+import numpy as np
+import pytest
+
+import _page8 as ref
+import _page8_rows as bound
+import test_gpu_page8 as base
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [ref.I8, ref.E4M3]
+
+
+def _planes(cache, row_slots):
+    """((K, V) codes, (K, V) scales), zeros in the pages that no row uses."""
+    kq, ks, vq, vs = base._planes(cache)
+    used = np.isin(np.arange(cache.num_pages), np.unique(np.concatenate(row_slots) // 32))
+    return tuple(np.where(used[:, None, None, None], x, 0) for x in (kq, vq)), tuple(
+        np.where(used[:, None], x, 0) for x in (ks, vs))
+
+
+def _kinds(rows):
+    return [0 if s - o == 1 else 1 for s, o in rows]
+
+
+def _queries(rows, hq, d, seed):
+    return np.random.default_rng(seed).standard_normal((sum(s - o for s, o in rows), hq, d)).astype(np.float16)
+
+
+def _check(fmt, cache, pt, row_slots, rows, q, window=0, **kw):
+    import mixed_attention_quantized_gb300 as mq
+    got = base._attend(cache, pt, rows, _kinds(rows), q.shape[1], q, window)
+    assert mq.device_error(clear=True) == 0
+    codes, scales = _planes(cache, row_slots)
+    want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows, window, **kw)
+    assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_rows(fmt, d):
+    """Decode splits, verify groups and cut chunk tiles: each row at its own bound."""
+    rows = [(40000, 39999), (9000, 8997), (20011, 19900), (4200, 4190), (2500, 2499), (1, 0), (33, 32)]
+    cache, pt, row_slots = base._filled(fmt, rows, 1, d, 177)
+    _check(fmt, cache, pt, row_slots, rows, _queries(rows, 4, d, 178))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window", [33, 1100])
+def test_windows(fmt, window):
+    rows = [(6000, 5999), (3000, 2996), (5000, 4800), (700, 0)]
+    cache, pt, row_slots = base._filled(fmt, rows, 2, 128, window)
+    _check(fmt, cache, pt, row_slots, rows, _queries(rows, 8, 128, window + 1), window)
