@@ -45,6 +45,15 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint
       : "r"(w));
 }
 
+// log2 dv and 1/dv of a page's V.  A page of zeros has no scale: its codes add nothing to O
+// whatever stands in for it, and in l any pair (b, 2^-b) counts its keys rightly.  But b is part of
+// the x that the reference m' follows, so it lies below that of every page with a value in it (fp16
+// values: dv >= 2^-32): a zero page takes no bits of the others' P', and 2^60 times the sum of
+// 2^31 P' below 2^15 is far inside fp32.
+__device__ __forceinline__ float2 value_scale_terms(float dv) {
+  return dv > 0.f ? make_float2(log2f(dv), __fdiv_rn(1.f, dv)) : make_float2(-60.f, 1152921504606846976.f);
+}
+
 // Four codes of one key (bytes 0 .. 3 of w) as the two k-pairs of an operand: codes 0, 2 and
 // 1, 3 (I8_PAGE) or 0, 1 and 2, 3 (E4M3_PAGE).
 template <int F>
@@ -182,8 +191,9 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
     const float dk = reinterpret_cast<const float*>(p.k_scale)[at];
     const float dv = reinterpret_cast<const float*>(p.v_scale)[at];
     my_a = dk * p.scale_log2 * code_unit<F>();
-    my_b = dv > 0.f ? log2f(dv) : 0.f;  // a page of zeros: its codes are 0, any scale does
-    my_inv = dv > 0.f ? __fdiv_rn(1.f, dv) : 1.f;
+    const float2 tv = value_scale_terms(dv);
+    my_b = tv.x;
+    my_inv = tv.y;
   }
 
   // Q as the B operand (column r: tile row r): k-step ks covers dims 16 ks + 4c .. + 3 in the
@@ -507,8 +517,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
 // The terms of a page: score factor, log2 dv and 1/dv.  A missing page (outside the cache, or
 // past the row's keys) gets the offset -inf: its keys weigh nothing.
 __device__ __forceinline__ float4 page_terms(float dk, float dv, bool there, float scale_log2) {
+  const float2 tv = value_scale_terms(dv);
   return make_float4(fmaxf(dk * scale_log2, 1e-30f),  // a page of zero keys: scores 0, and -inf stays -inf
-                     there ? (dv > 0.f ? log2f(dv) : 0.f) : -CUDART_INF_F, dv > 0.f ? __fdiv_rn(1.f, dv) : 1.f, 0.f);
+                     there ? tv.x : -CUDART_INF_F, tv.y, 0.f);
 }
 
 // The softmax's rare step, for page c (32 scores at s_col + 32 c) of a warp in which some row's

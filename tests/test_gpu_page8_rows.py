@@ -52,3 +52,31 @@ def test_windows(fmt, window):
     rows = [(6000, 5999), (3000, 2996), (5000, 4800), (700, 0)]
     cache, pt, row_slots = base._filled(fmt, rows, 2, 128, window)
     _check(fmt, cache, pt, row_slots, rows, _queries(rows, 8, 128, window + 1), window)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("gain", [2.0 ** -10, 2.0 ** -13])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_values_beside_pages_of_zeros(fmt, gain, d):
+    """A page whose V is all zero counts in the softmax's sum and takes no bits from the others."""
+    def gains(rng, n):
+        g = np.full(-(-n // 32), gain)
+        g[rng.random(len(g)) < 0.3] = 0
+        g[0] = 0
+        return g.repeat(32)[:n]
+    rows = [(500, 499), (1500, 1499), (6000, 5999), (200, 100), (700, 694), (4000, 3960), (600, 0)]
+    cache, pt, row_slots = base._filled(fmt, rows, 2, d, 203, gains)
+    assert any((s == 0).any() for s in _planes(cache, row_slots)[1])
+    _check(fmt, cache, pt, row_slots, rows, _queries(rows, 4, d, 204))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_of_zeros_only(fmt):
+    """No value but zeros: zeros out, in every kind of row and a batch with other rows."""
+    rows = [(300, 299), (9000, 8999), (70, 66), (400, 200), (500, 499)]
+    def gains(rng, n):
+        return np.zeros(n) if n != 500 else np.ones(n)
+    cache, pt, row_slots = base._filled(fmt, rows, 1, 128, 207, gains)
+    q = _queries(rows, 4, 128, 208)
+    got = base._attend(cache, pt, rows, _kinds(rows), 4, q)
+    assert (got[:-1] == 0).all() and np.abs(got[-1]).max() > 0
