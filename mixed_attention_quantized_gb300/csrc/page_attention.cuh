@@ -5,8 +5,13 @@
 //     x_j = log2(e)/sqrt(D) dk (q . c_k) + log2 dv,    P'_j = 2^(x_j - m'),
 //     O = sum_j P'_j c_v,   l = sum over pages (sum_j P'_j) / dv,   o = O / l,
 // m' a running reference of the x_j.  The scale of V rides in the exponent, so a page
-// costs one multiply-add per score whatever its scales are, the codes go to the tensor
-// cores exactly as they are, and P' is at most 1 (or 2^slack) whatever the range of V.
+// costs one multiply-add per score whatever its scales are, and the codes go to the tensor
+// cores exactly as they are.  P' is rounded to fp16 there (2^-11 at most, as the probabilities of the
+// block formats; for values of either sign 2e-4 of the output's size, beside 2e-4 of the output's own
+// rounding -- exact ones would take a high and a low operand, twice the MMAs); l sums them in fp32.  The
+// reference keeps the largest P' between 2^6 and 2^16, so that weights down to 2^-20 of it
+// still have all 11 bits and those to 2^-30 some: a long tail under one dominant key counts in O
+// as it does in l.
 // Partial results (m', O, l) of different key ranges merge as for a plain softmax.
 //
 // Decode tiles: a CTA of 4 warps takes a page range of one (row, kv head) for up to
@@ -49,7 +54,7 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint
 // whatever stands in for it, and in l any pair (b, 2^-b) counts its keys rightly.  But b is part of
 // the x that the reference m' follows, so it lies below that of every page with a value in it (fp16
 // values: dv >= 2^-32): a zero page takes no bits of the others' P', and 2^60 times the sum of
-// 2^31 P' below 2^15 is far inside fp32.
+// 2^31 P' below 2^16 is far inside fp32.
 __device__ __forceinline__ float2 value_scale_terms(float dv) {
   return dv > 0.f ? make_float2(log2f(dv), __fdiv_rn(1.f, dv)) : make_float2(-60.f, 1152921504606846976.f);
 }
@@ -262,17 +267,19 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
         if (k1 > pos0 || k1 < lo0) x[2] = -CUDART_INF_F;
         if (k1 > pos1 || k1 < lo1) x[3] = -CUDART_INF_F;
       }
-      // the references follow the maxima lazily: P' stays <= 2^8, so the sums of 8-bit
-      // codes times P' stay far inside fp32 and P' inside fp16
-      constexpr float kSlack = 8.f;
+      // a reference is set 7 below the largest x and follows it lazily: P' stays <= 2^15, inside
+      // fp16, and the sums of 8-bit codes times P' far inside fp32
+      constexpr float kTop = 15.f, kSet = 7.f;
       float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
-      if (__any_sync(0xFFFFFFFFu, t0 > (m0 == -CUDART_INF_F ? m0 : kSlack) || t1 > (m1 == -CUDART_INF_F ? m1 : kSlack))) {
+      if (__any_sync(0xFFFFFFFFu, t0 > (m0 == -CUDART_INF_F ? m0 : kTop) || t1 > (m1 == -CUDART_INF_F ? m1 : kTop))) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, o));
           t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, o));
         }
-        const bool g0 = t0 > (m0 == -CUDART_INF_F ? m0 : kSlack), g1 = t1 > (m1 == -CUDART_INF_F ? m1 : kSlack);
+        const bool g0 = t0 > (m0 == -CUDART_INF_F ? m0 : kTop), g1 = t1 > (m1 == -CUDART_INF_F ? m1 : kTop);
+        t0 -= kSet;
+        t1 -= kSet;
         const float n0 = g0 ? mr0 + t0 : m0, n1 = g1 ? mr1 + t1 : m1;
         const float al0 = g0 ? ex2(m0 - n0) : 1.f, al1 = g1 ? ex2(m1 - n1) : 1.f;
         if (g0) {
@@ -458,10 +465,10 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
 // Roles of the 16 warps:
 //   softmax (warps 0-3 and 4-7), thread = TMEM lane = query row: one pass over its 128 scores,
 //     a page's 32 at a time, against the row's reference m; P' as fp16 over the first half of
-//     the page's own scores.  m is an integer, 3 to 4 above the largest x when it was set, so
-//     P' < 2 until a score passes it by 2^4 or more: seen in the exponent bits of the page's
-//     P' before they are stored, and then m moves, and O and the tile's P' so far are
-//     multiplied by a power of two;
+//     the page's own scores.  m is an integer, 6 to 7 below the largest x when it was set, so the
+//     sum of a page's P', which l needs anyway, is below the fp16 range unless one of its x passes
+//     that one by 4 or more; where it is not, m moves before the P' are stored, and O and the
+//     tile's P' so far are multiplied by a power of two;
 //   conversion (K 8-11, V 13-15): codes loaded one KV tile ahead into registers, as fp16 into
 //     128-byte-swizzled operand tiles, two buffers each of K and V; a K warp also writes its
 //     page's terms (below);
@@ -522,8 +529,14 @@ __device__ __forceinline__ float4 page_terms(float dk, float dv, bool there, flo
                      there ? tv.x : -CUDART_INF_F, tv.y, 0.f);
 }
 
+// A chunk row's reference: kChunkSet below the (rounded up) largest x when it is set, and moved
+// when the 32 P' of a page sum to kChunkTop (so one is 2^10.98 or more; none above 65504
+// passes).  The page's largest fp16 P' as the test, by packed integer maxima, with 11 and 2^15: the
+// chunk of 2048 tokens at 32768 keys 1160 -> 1200 us.
+constexpr float kChunkSet = 7.f, kChunkTop = 65000.f, kChunkMoved = 10.9f;
+
 // The softmax's rare step, for page c (32 scores at s_col + 32 c) of a warp in which some row's
-// P' would reach 2, or which has rows without a reference: moves the references of the rows
+// P' sum to kChunkTop, or which has rows without a reference: moves the references of the rows
 // that need it, multiplies O (if there is one yet: `scale_o`), l and the P' of the KV tile's
 // pages before c by the change, a power of two, and writes the page's P'.  Out of line, so
 // that the common path stays short.  Returns (m, l).
@@ -542,8 +555,8 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
       if (16 * b + e >= c_first && 16 * b + e <= c_last) mx = fmaxf(mx, __uint_as_float(o[e]));
   }
   mx = fmaf(mx, tm.x, tm.y);
-  const bool grow = mx > -CUDART_INF_F && (m_run == -CUDART_INF_F || mx >= m_run + 0.99f);
-  const float m_new = grow ? ceilf(mx) + 3.f : m_run;
+  const bool grow = mx > -CUDART_INF_F && (m_run == -CUDART_INF_F || mx >= m_run + kChunkMoved);
+  const float m_new = grow ? ceilf(mx) - kChunkSet : m_run;
   const float alpha = grow ? ex2(m_run - m_new) : 1.f;  // a power of two, or 0
   l_run *= alpha;
   if (scale_o) {
@@ -563,7 +576,10 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
       tmem_st16(o_col + 16 * ch, o);
     }
   }
-  const uint32_t al_h = pack_f16x2(alpha, alpha);  // (below 2^-24: P' and its page are nothing next to mx)
+  // alpha as two fp16 powers of two, down to 2^-48: below 2^-40 no P' is left of it
+  const float e_all = grow ? fmaxf(m_run - m_new, -48.f) : 0.f, e_half = ceilf(0.5f * e_all);
+  const float al_1 = ex2(e_half), al_2 = ex2(e_all - e_half);
+  const uint32_t al_h = pack_f16x2(al_1, al_1), al_l = pack_f16x2(al_2, al_2);
   tmem_wait_st();  // the P' of the pages before are in place
 #pragma unroll 1
   for (int b = 0; b < c; ++b) {
@@ -571,7 +587,7 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
     tmem_ld16(s_col + 32 * b, o);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(o[e], al_h);
+    for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(hmul2_u32(o[e], al_h), al_l);
     tmem_st16(s_col + 32 * b, o);
   }
   // the page's P', 16 scores at a time: their 8 words stay before the scores not yet read
@@ -818,7 +834,6 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
               if (e < c_first || e > c_last) x[e] = __float_as_uint(-CUDART_INF_F);
           }
           uint64_t sum_a = f2_pack(0.f, 0.f), sum_b = sum_a;
-          uint32_t bits = 0;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float x0, x1, x2, x3;
@@ -829,17 +844,15 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
             sum_b = fadd2(sum_b, f2_pack(p2, p3));
             pk[e >> 1] = pack_f16x2(p0, p1);
             pk[(e >> 1) + 1] = pack_f16x2(p2, p3);
-            bits |= pk[e >> 1] | pk[(e >> 1) + 1];
           }
-          // a P' of 2 or more (infinity too) has the top exponent bit; a row without a reference
-          // takes one with its first key
-          const bool over = (bits & 0x40004000u) != 0u || m_run == -CUDART_INF_F;
+          float s0, s1;
+          f2_unpack(fadd2(sum_a, sum_b), s0, s1);
+          const float l_page = s0 + s1;
+          // (infinity and NaN too; a row without a reference takes one with its first key)
+          const bool over = !(l_page < kChunkTop) || m_run == -CUDART_INF_F;
           if (!__any_sync(0xFFFFFFFFu, over)) {
             tmem_st16(sc, pk);
-            float s0, s1, s2, s3;
-            f2_unpack(sum_a, s0, s1);
-            f2_unpack(sum_b, s2, s3);
-            l_run = fmaf((s0 + s1) + (s2 + s3), tm.z, l_run);
+            l_run = fmaf(l_page, tm.z, l_run);
             continue;
           }
           const float2 ml_new = page_move_reference<D>(s_col, o_col, c, tm, c_first, c_last, m_run, l_run, j > j0);

@@ -24,7 +24,7 @@ import numpy as np
 
 import _page8 as ref
 
-TOP_DECODE, TOP_CHUNK = 0, -4  # log2 of the least largest P'
+TOP_DECODE, TOP_CHUNK = 7, 6  # log2 of the least largest P'
 
 
 def attention(fmt, q, codes, scales, row_slots, rows, window=0, missing=(), coherent=False, tops=None, group_rows=24):

@@ -80,3 +80,41 @@ def test_rows_of_zeros_only(fmt):
     q = _queries(rows, 4, 128, 208)
     got = base._attend(cache, pt, rows, _kinds(rows), 4, q)
     assert (got[:-1] == 0).all() and np.abs(got[-1]).max() > 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sink", [0, 1])
+def test_long_tail_under_one_dominant_key(fmt, d, sink):
+    """One key (the row's first, or one in the middle) 8 to 22 bits above all others, its own value
+    zero: the output is the tail's, whose weights are far below the largest.  Values of one sign."""
+    import mixed_attention_quantized_gb300 as mq
+    rows = [(9000, 8999), (9000, 8994), (9000, 8960), (9000, 8800), (3000, 2999)]
+    rng = np.random.default_rng(301)
+    need = [-(-s // 32) for s, _ in rows]
+    pt = np.full((len(rows), max(need)), -1, dtype=np.int32)
+    perm, at, row_slots = rng.permutation(sum(need)).astype(np.int32), 0, []
+    cache = base._alloc(fmt, sum(need), 1, d)
+    for r, (seq, _) in enumerate(rows):
+        pt[r, :need[r]] = perm[at:at + need[r]]
+        at += need[r]
+        t = np.arange(seq)
+        slots = pt[r, t // 32] * 32 + t % 32
+        k = 0.1 * rng.standard_normal((seq, 1, d))
+        k[:, :, 0] = 0
+        v = rng.uniform(0.5, 1.5, (seq, 1, d))
+        dominant = seq // 2 * sink
+        k[dominant], v[dominant] = 0, 0
+        k[dominant, 0, 0] = 16
+        base._append(cache, k.astype(np.float16), v.astype(np.float16), slots)
+        row_slots.append(slots)
+    q = _queries(rows, 4, d, 302)
+    bits = rng.uniform(8, 22, q.shape[:2])
+    bits[0] = [8, 14, 18, 22]
+    q[:, :, 0] = bits * np.log(2) * np.sqrt(d) / 16
+    got = base._attend(cache, pt, rows, _kinds(rows), 4, q)
+    assert mq.device_error(clear=True) == 0
+    codes, scales = _planes(cache, row_slots)
+    want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows, coherent=True)
+    assert (tol < 0.02 * want + 2.0 ** -24).all()  # the bound means something for every element
+    assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
