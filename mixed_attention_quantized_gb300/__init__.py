@@ -283,6 +283,10 @@ class KVCache:
             kept = self.__dict__["_kept"] = (key, desc, ctypes.byref(desc))
         return kept[2]
 
+    def __getstate__(self):
+        """Everything but the kept descriptor, which holds addresses and cannot be copied or pickled."""
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
+
 
 def kv_append_quant(cache: KVCache, k_new, v_new, slot_mapping, stream=None) -> None:
     """Quantise fp16 K/V ``[n_new, Hkv, D]`` into the cache slots ``slot_mapping`` (int32)."""
