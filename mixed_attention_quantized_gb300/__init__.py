@@ -6,6 +6,11 @@ current CUDA stream) into the C ABI declared in ``include/mixattn.h``; every
 step of the path runs in the library's CUDA kernels.  There is no CPU
 fallback: if the library is missing or fails to load, every call raises.
 
+``stream`` of a call is the torch stream to launch on (default: the current one).
+What the call itself allocates then belongs to that stream, as if it were the
+current one; the tensors given to it are the caller's to order before it and to keep
+alive (or ``record_stream``) until it is done.
+
 Reference: page "自研RDNA高併發推論引擎 以AI Max+ 395為範例" (§1 mixed batch,
 §2 blocked Q8 / 4-bit KV modes).
 """
@@ -206,6 +211,16 @@ def _stream_handle(stream) -> int:
     return rt.raw_stream(rt.device())
 
 
+def _empty(like, stream, shape=None, dtype=None):
+    """An uninitialised tensor beside ``like`` (its shape and type unless given) that a launch on
+    ``stream`` writes: of that stream's memory, so that no other stream's work can still be using it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape or like.shape, dtype=dtype or like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape or like.shape, dtype=dtype or like.dtype, device=like.device)
+
+
 def _ptr(t) -> int:
     return t.data_ptr() if t is not None else 0
 
@@ -302,8 +317,7 @@ def kv_export_blocks(cache: KVCache, which: int, slots, stream=None):
     import torch
     fmt = cache.k_fmt if which == 0 else cache.v_fmt
     n = int(slots.shape[0])
-    out = torch.empty((n, cache.num_kv_heads, cache.head_dim // 32, block_bytes(fmt)),
-                      dtype=torch.uint8, device=slots.device)
+    out = _empty(slots, stream, (n, cache.num_kv_heads, cache.head_dim // 32, block_bytes(fmt)), torch.uint8)
     st = load().mixattn_kv_export_blocks(ctypes.byref(cache.desc()), int(which), _ptr(slots), n,
                                          _ptr(out), _stream_handle(stream))
     _check(st, "mixattn_kv_export_blocks")
@@ -387,8 +401,7 @@ def rope_apply(rope: Rope, x, positions, out=None, stream=None):
     here = _call_device(rt, positions, "positions")
     h, d, xs = _heads(rt, here, x, n, "x")
     if out is None:
-        import torch
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(x, stream)
     os_ = xs if out is x else _heads(rt, here, out, n, "out", h, d)[2]
     _int_list(rt, here, positions, n, "positions")
     st = (_lib or load()).mixattn_rope_apply(
@@ -413,8 +426,7 @@ def rope_append(cache: KVCache, rope: Rope, q, k_new, v_new, positions, slot_map
     if q is not None:
         hq, _, qs = _heads(rt, here, q, n, "q", 0, d)
         if q_out is None:
-            import torch
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _empty(q, stream)
         os_ = qs if q_out is q else _heads(rt, here, q_out, n, "q_out", hq, d)[2]
         qp, op = q.data_ptr(), q_out.data_ptr()
     else:
@@ -495,10 +507,11 @@ def workspace_bytes(cache: KVCache, num_q_heads: int, row_kinds, seq_lens, q_off
     return int(ws.value)
 
 
-def alloc_workspace(nbytes: int, device="cuda"):
-    """A 256-byte aligned uint8 device buffer of nbytes (torch-owned)."""
+def alloc_workspace(nbytes: int, device="cuda", stream=None):
+    """A 256-byte aligned uint8 device buffer of nbytes (torch-owned), of ``stream``'s memory."""
     import torch
-    t = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):  # (None: the current stream)
+        t = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-t.data_ptr()) % 256
     return t[off:off + nbytes]
 
@@ -506,14 +519,13 @@ def alloc_workspace(nbytes: int, device="cuda"):
 def mixed_attention(cache: KVCache, q, page_table, seq_lens, q_offsets, row_kinds, o=None,
                     workspace=None, stream=None):
     """o = mixed_attention(q, page_table, seq_lens, q_offsets, row_kinds) in one call."""
-    import torch
     max_pages = int(page_table.shape[1])
     hq = int(q.shape[1])
     need = workspace_bytes(cache, hq, row_kinds, seq_lens, q_offsets, max_pages)
     if workspace is None:
-        workspace = alloc_workspace(need, q.device)
+        workspace = alloc_workspace(need, q.device, stream)
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q, stream)
     st = load().mixattn_mixed_attention(
         ctypes.byref(cache.desc()), hq, _ptr(q), _ptr(page_table), max_pages, len(seq_lens),
         _i32_array(seq_lens), _i32_array(q_offsets), _i32_array(row_kinds), _ptr(o), _ptr(workspace),
@@ -528,9 +540,8 @@ def mixed_attention_noalloc(cache: KVCache, q, page_table, seq_lens, q_offsets, 
     by the call): for callers that cannot provide device scratch memory.
     Batches needing more than the library's 16 MiB of scratch raise
     MixattnError(ERR_WORKSPACE); overlapping calls on different streams race."""
-    import torch
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q, stream)
     st = load().mixattn_mixed_attention_noalloc(
         ctypes.byref(cache.desc()), int(q.shape[1]), _ptr(q), _ptr(page_table), int(page_table.shape[1]),
         len(seq_lens), _i32_array(seq_lens), _i32_array(q_offsets), _i32_array(row_kinds), _ptr(o),
