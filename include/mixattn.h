@@ -364,6 +364,8 @@ void mixattn_plan_destroy(mixattn_plan* plan);
  * launch has finished.  A serving loop should keep a plan and call
  * mixattn_plan_update + mixattn_run instead, which never wait.  workspace as
  * for mixattn_run; query its size with mixattn_workspace_bytes.
+ * On a stream that is being captured it returns MIXATTN_ERR_UNSUPPORTED (a replay
+ * would read the freed plan): capture mixattn_run.
  */
 int mixattn_mixed_attention(const mixattn_kv_cache* cache, int32_t num_q_heads, const void* q,
                             const int32_t* page_table, int32_t max_pages, int32_t n_rows,

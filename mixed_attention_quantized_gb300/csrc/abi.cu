@@ -766,6 +766,12 @@ int mixattn_mixed_attention(const mixattn_kv_cache* cache, int32_t num_q_heads, 
                             const int32_t* page_table, int32_t max_pages, int32_t n_rows, const int32_t* seq_lens,
                             const int32_t* q_offsets, const int32_t* row_kinds, void* o, void* workspace,
                             size_t workspace_bytes, mixattn_stream stream) {
+  // a replay would read the tile list of the plan that this call frees
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capture) != cudaSuccess)
+    cudaGetLastError();  // (the launch below reports what is wrong)
+  else if (capture != cudaStreamCaptureStatusNone)
+    return MIXATTN_ERR_UNSUPPORTED;
   mixattn_plan* plan = nullptr;
   int st = mixattn_plan_create(&plan, cache, num_q_heads, n_rows, row_kinds, seq_lens, q_offsets, max_pages,
                                nullptr);

@@ -96,3 +96,30 @@ def test_a_step_on_a_side_stream(fmt):
             assert torch.equal(a, b)
     plan.close()
     assert mq.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("fmt", [1, ref.I8])
+@pytest.mark.parametrize("mode", ["relaxed", "thread_local"])
+def test_the_one_call_entry_point_is_not_captured(fmt, mode):
+    """It frees the plan whose tile list a replay would read: refused on a capturing stream, which goes
+    on capturing what it may."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    cache, pt, rows, kinds, q, _ = _case(fmt)
+    seqs, offs = [r[0] for r in rows], [r[1] for r in rows]
+    ws = mq.alloc_workspace(mq.workspace_bytes(cache, 8, kinds, seqs, offs, pt.shape[1]))
+    want = mq.mixed_attention(cache, q, pt, seqs, offs, kinds, workspace=ws)
+    o, rope = torch.zeros_like(q), mq.Rope(128)
+    pos = torch.arange(q.shape[0], dtype=torch.int32, device="cuda")
+    turned, kept = mq.rope_apply(rope, q, pos), torch.empty_like(q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode=mode):
+        with pytest.raises(mq.MixattnError) as e:
+            mq.mixed_attention(cache, q, pt, seqs, offs, kinds, o=o, workspace=ws)
+        mq.rope_apply(rope, q, pos, kept)
+    assert e.value.status == mq.ERR_UNSUPPORTED
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(kept, turned) and not o.any()
+    assert torch.equal(mq.mixed_attention(cache, q, pt, seqs, offs, kinds, workspace=ws), want)
