@@ -118,3 +118,30 @@ def test_long_tail_under_one_dominant_key(fmt, d, sink):
     want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows, coherent=True)
     assert (tol < 0.02 * want + 2.0 ** -24).all()  # the bound means something for every element
     assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
+
+
+# (row, page numbers without a page): first, last and whole KV tiles of four pages, both pages of a
+# conversion warp's pair and either one, in every kind of tile
+LOST = [((1000, 999), {0, 31}), ((3000, 2995), {1, 50, 92}), ((700, 500), {0, 5, 7, 12, 13, 14, 15}), ((700, 460), {21}),
+        ((2325, 2309), {8, 9, 10, 11, 40, 72}), ((4100, 4000), {1, 66, 127}), ((130, 0), {2})]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 900])
+def test_rows_without_some_pages(fmt, d, window):
+    """A page id outside the cache is flagged, and the row is attention over its other keys."""
+    import mixed_attention_quantized_gb300 as mq
+    mq.device_error(clear=True)
+    rows, lost = [r for r, _ in LOST], [p for _, p in LOST]
+    cache, pt, row_slots = base._filled(fmt, rows, 2, d, 501)
+    bad = [cache.num_pages, -1, -5, 2 ** 31 - 1, -2 ** 31]
+    for r, pages in enumerate(lost):
+        for i, p in enumerate(sorted(pages)):
+            pt[r, p] = bad[(r + i) % len(bad)]
+    q = _queries(rows, 8, d, 502)
+    got = base._attend(cache, pt, rows, _kinds(rows), 8, q, window)
+    assert mq.device_error(clear=True) == mq.DEVERR_PAGE_ID
+    codes, scales = _planes(cache, row_slots)
+    want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows, window, missing=lost)
+    assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
