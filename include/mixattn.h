@@ -263,6 +263,11 @@ int mixattn_rope_apply(const mixattn_rope* rope, const void* x, int64_t x_stride
  * fp16), so its error is the format's own; the codes can differ in the last step
  * from those of mixattn_rope_apply followed by mixattn_kv_append_quant, which
  * round it to fp16 in between.  q_out must not overlap k_new or v_new.
+ * Elements that are not finite: the page-scaled formats take K and V as described above.
+ * In Q8_0 and Q4_0 a key's infinities and rotated values beyond +-65504 saturate there and
+ * its NaN count as 0; values (V) are encoded as mixattn_kv_append_quant does, which does not
+ * look for them (an infinity or NaN spoils its block).  F16 keeps NaN; of rotated elements
+ * infinities saturate.
  */
 int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope, int32_t num_q_heads, const void* q,
                         int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new, int64_t k_stride,
