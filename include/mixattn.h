@@ -207,9 +207,11 @@ int mixattn_kv_export_blocks(const mixattn_kv_cache* cache, int32_t which, const
  * at position p
  *   (a_i, b_i) -> m (a_i cos w - b_i sin w, b_i cos w + a_i sin w),  w = p f_i,
  * with m the config's multiplier; the head's other elements are copied.  fp16 in
- * and out (saturating at +-65504), fp32 products; the angle is taken modulo a
- * turn in 64-bit fixed point, so far positions lose nothing (f_i is rounded to
- * 2^-64 of a turn).  Positions may be any int32.
+ * and out (saturating at +-65504, NaN stays NaN), fp32 products, cosines and sines
+ * within 2^-23 of their angle's.  The angle is p times f_i / 2 pi, a double
+ * (within 2^-55 of a turn for f_i <= 1), modulo a turn in 64-bit fixed point and cut to 2^-32
+ * of one: off by |p| 2^-55 + 2^-32 turns at most, 2^-32 up to position 2^22 and 2^-24 at the
+ * last.  Positions may be any int32.
  */
 typedef struct {
   int32_t rot_dim;      /* rotated elements of a head: a multiple of 16, <= 128      */
@@ -284,8 +286,8 @@ int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope,
  * and ceil(seq_len / page_size) <= max_pages.  seq_len counts the new tokens,
  * whose K/V must already be in the cache (append first, then attend).
  *
- * Tiles: chunk rows are cut into (kv head, 128/G query tokens x G heads)
- * tensor-core tiles, heaviest first; when a chunk row has too few tiles to keep
+ * Tiles: chunk rows are cut into (kv head, 128/G query tokens x G heads; 256/G for the
+ * page-scaled formats) tensor-core tiles, heaviest first; when a chunk row has too few tiles to keep
  * every SM of the current device busy to the end, the key range of each of its
  * tiles is cut into 2-4 pieces whose partial results merge by log-sum-exp
  * (a choice made from the row itself and the device's SM count).  Decode rows
