@@ -27,8 +27,9 @@ constexpr int kFusedThreads = 512; // threads of a fused-launch CTA: three worki
                                    // the first kThreads
 constexpr int kChunkM = 128;       // rows (query tokens x group heads) of a chunk tile
 constexpr int kPageChunkM = 256;   // the same for the page-scaled formats: two 128-row query tiles
-constexpr int kPageMaxPieces = 4;  // pieces of a page-scaled tile's key range, at most (six: the verify
-                                   // batch 234 -> 240 us, a piece costs about six KV tiles' time)
+constexpr int kPageMaxPieces = 4;  // pieces of a page-scaled tile's key range, at most (three: the chunk
+                                   // at 32768 keys 917 -> 952 us, the verify batch 221 -> 223; six, of
+                                   // an earlier form: 234 -> 240, a piece costs about six KV tiles' time)
 constexpr int kChunkN = 128;       // keys per KV tile of the chunk path (4 pages)
 constexpr int kPagesPerKvTile = kChunkN / kPage;
 constexpr int kMaxGroup = 8;       // q heads per kv head held in one mma N=8 tile
@@ -37,7 +38,7 @@ constexpr int kVerifyMaxRows = 24; // a chunk row with q_len * G <= this (specul
                                    // decode-style split-K tiles of up to 8 (query, head) rows: each
                                    // such group costs about a third of a 128-row tensor-core tile
                                    // per key, so up to three groups are cheaper than one tile (page-
-                                   // scaled, the verify batch at 16 / 24 / 32: 250 / 232 / 246 us)
+                                   // scaled, the verify batch at 16 / 24 / 32: 235 / 221 / 243 us)
 
 // Per-row data the kernel needs (copied with the tile list).
 struct RowInfo {

@@ -18,8 +18,10 @@
 // barriers would cost more than the list, each looks through all of it.
 //
 // Bound: bytes (2 read and 1 written per new element), behind a launch and the search, which
-// take about 4 us of each call.  Measured, 8 heads of 128: 64 tokens in pages of their own 4.1 us,
-// 2048 in a row 7.4, 8201 15.4 (50 MB, 3.3 TB/s), 32768 65 (3.1 TB/s).
+// take about 4 us of each call (8201 tokens: 8500 of 27000 cycles pass before the first key or
+// value is loaded).  Measured, 8 heads of 128: 64 tokens in pages of their own 4.1 us,
+// 2048 in a row 7.4, 8201 15.4 (50 MB, 3.3 TB/s), 32768 65 (3.1 TB/s).  With rotated keys and 32 query
+// heads, 2048 tokens 13.1, 8201 49.7; without queries 10.9 and 27.6.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <string.h>
@@ -37,7 +39,8 @@ constexpr int kSlices = 8;       // CTAs of a window
 constexpr int kWindow = 128;     // most tokens of a window, so most pages of a CTA
 constexpr int kHash = 256;
 static_assert(kWindow <= kAppendThreads && kHash >= 2 * kWindow, "a thread per token of a window");
-constexpr int kAppendCtas = 7;   // CTAs of an SM (registers)
+constexpr int kAppendCtas = 7;   // CTAs of an SM by registers; the rotary form at D = 128 holds
+                                 // 35.9 KB of shared memory (tbl and cs 16 KB each), which lets 6 be
 // New tokens from which the search is shared: at 1023 tokens in a row 5.5 us alone and 7.6 shared, at
 // 2048 10.2 and 7.6.
 constexpr int kClusterFrom = 1024;
@@ -440,10 +443,13 @@ cudaError_t launch_page_append(const mixattn_kv_cache& c, const RopeTable* rope,
   a.scales[1] = static_cast<float*>(c.v_scale);
   a.n_new = n_new;
   // A decode step's tokens each have a page of their own: windows of one token spread them over
-  // the SMs (64 tokens in 64 pages 4.1 us, with windows of eight 10.7; 200 8.0 and 11.7).  A prompt
-  // fills a page with 32 tokens (512 in a row 9.4 us in windows of one, 4.7 of eight).  From
-  // kClusterFrom on a window is as long as keeps the grid in one wave (2048 in a row 7.6 us with
-  // windows of 24, 9.6 with 64).
+  // the SMs (64 tokens in 64 pages 4.1 us, with windows of eight 10.7; 200 7.8 and 11.8).  A prompt
+  // fills a page with 32 tokens (512 in a row 9.1 us in windows of one, 4.8 of eight).  The count
+  // alone does not tell one from the other: 300 tokens in 300 pages take 11.9 us in windows of eight
+  // and 11.0 of one, from 512 on eight is faster for them too (15.4 and 16.8; 1000: 23.4 and 32.3).
+  // From kClusterFrom on there are at most 120 windows, 960 CTAs, which seven an SM hold at once
+  // (148 SMs or more; 2048 in a row 7.6 us with windows of 24, 9.6 with 64).  Not so the rotary
+  // form at D = 128: six an SM are 912 of 152 SMs, and its queries' CTAs come on top.
   a.window = n_new > 256 ? 8 : 1;
   if (n_new >= kClusterFrom) a.window = min(kWindow, ((n_new + 119) / 120 + 7) / 8 * 8);
   a.hq = hq;

@@ -482,10 +482,10 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
 // A tile is cut into key ranges when its row alone cannot fill the SMs: a piece leaves (m, l, O) of
 // its rows, and the last to finish joins them.
 // Measured (8 kv heads of 128, four query heads each): the 2048-token chunk at 32768 keys beside
-// four decode rows 1.15 ms, 51% of the dense rate, where a 256 x 128 unit takes ~4000 SM cycles for
-// 2048 of MMAs.  What bounds it: a group's scores take it ~1300 cycles and the two hand-overs
-// ~500, more than the ~1550 of the other group's MMAs beside them (16 MMAs of 64 cycles, each
-// held up by operand reads and operand writes that share the 128 bytes a cycle of shared memory).
+// four decode rows 0.92 ms, 64% of the dense rate, where a 256 x 128 unit takes ~3200 SM cycles for
+// 2048 of MMAs.  What bounds it: two groups' MMAs take ~1550 cycles each where they are issued alone
+// (16 of 64 cycles, each held up by operand reads and operand writes that share the 128 bytes a
+// cycle of shared memory), and a group's scores and two hand-overs have to fit beside the other's.
 // No role waits at a CTA barrier inside its loop; every wait is on an mbarrier, bounded,
 // and a role that gives up leaves its loops, after which the others' waits run out.
 template <int D>
@@ -1257,14 +1257,15 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
   AttnParams q = p;
   const bool persist = p.chunk_kv_tiles < kPersistMaxKvTiles * p.n_chunk_tiles;
   q.n_chunk_ctas = persist ? std::min(p.n_chunk_tiles, sm_count()) : p.n_chunk_tiles;
-  if (persist && p.n_decode_tiles > 0 && sm_count() < (1 << 20)) {
+  if (persist && p.n_decode_tiles > 0 && sm_count() < (1 << 20)) {  // (1 << 30: the device does not say)
     // Chunk tiles are bound by the SM, decode tiles by HBM: side by side each takes about the
     // time it needs anyway.  The chunk CTAs get the share of the SMs that lets both kinds end
     // together, and a little more (decode CTAs take over the SMs that they leave, not the
-    // other way round).  Costs in SM cycles at head_dim 128, by timing each kind alone: a KV
-    // tile of 128 rows 2000, a page of decode 230.  A cost of 1500 / 2000 / 2650 / 3300: the
-    // serving mix 171 / 148 / 152 / 153 us, the verify batch 272 / 232 / 234 / 234 us; a share
-    // of 1.3 for 1.15: 154 and 234 us.
+    // other way round).  Costs in SM cycles: a KV tile of 128 rows 2000, a page of decode 230.
+    // A cost of 1300 / 1600 / 2000 / 2650: the serving mix 151 / 146 / 144 / 149 us, the verify
+    // batch 246 / 239 / 221 / 222 us; a share of 1.3 for 1.15: 146 and 222 us.  The same at
+    // head_dim 64, where 1400 to 4000 differ by 2% (16 rows of 8192 tokens beside a 2048-token chunk
+    // 155 to 157 us, 48 beside one without history 126 to 128) and 1000 loses up to 40%.
     const double tc = kHalf * p.chunk_kv_halves, td = 230.0 * p.decode_pages;
     const int share = (int)(kChunkShare * sm_count() * tc / (tc + td)) + 1;
     q.n_chunk_ctas = std::min(q.n_chunk_ctas, share);
