@@ -145,3 +145,37 @@ def test_rows_without_some_pages(fmt, d, window):
     codes, scales = _planes(cache, row_slots)
     want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows, window, missing=lost)
     assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", ["ramp", "steps", "pairs"])
+def test_scores_that_keep_moving_the_reference(fmt, d, shape):
+    """Scores that rise or fall along the keys, by page or from key to key, up to 200 bits in all: the
+    references move at every page or once, by a little or past all that came before."""
+    import mixed_attention_quantized_gb300 as mq
+    rows = [(3000, 2999), (2600, 2595), (2500, 2470), (1000, 700), (9000, 8980)]
+    rng = np.random.default_rng(601)
+    need = [-(-s // 32) for s, _ in rows]
+    pt = np.full((len(rows), max(need)), -1, dtype=np.int32)
+    perm, at, row_slots = rng.permutation(sum(need)).astype(np.int32), 0, []
+    cache = base._alloc(fmt, sum(need), 1, d)
+    for r, (seq, _) in enumerate(rows):
+        pt[r, :need[r]] = perm[at:at + need[r]]
+        at += need[r]
+        t = np.arange(seq)
+        slots = pt[r, t // 32] * 32 + t % 32
+        k, v = rng.standard_normal((2, seq, 1, d))
+        height = {"ramp": t / seq, "steps": rng.random(need[r])[t // 32], "pairs": ((t // 2) % 48) / 48}[shape]
+        k[:, 0, 0] = 16 * height
+        v *= np.exp2(rng.integers(-6, 7, need[r]))[t // 32, None, None]
+        base._append(cache, k.astype(np.float16), v.astype(np.float16), slots)
+        row_slots.append(slots)
+    q = _queries(rows, 8, d, 602)
+    bits = np.array([3, 12, 40, 200, -3, -12, -40, -200])
+    q[:, :, 0] = bits * np.log(2) * np.sqrt(d) / 16
+    got = base._attend(cache, pt, rows, _kinds(rows), 8, q)
+    assert mq.device_error(clear=True) == 0
+    codes, scales = _planes(cache, row_slots)
+    want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows)
+    assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
