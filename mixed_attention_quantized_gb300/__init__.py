@@ -446,7 +446,9 @@ def rope_append(cache: KVCache, rope: Rope, q, k_new, v_new, positions, slot_map
 
 class Plan:
     """Host tiling of one ForwardBatch; reusable across layers and re-tileable.
-    ``window`` > 0 makes every run sliding-window attention (keys p-window+1..p)."""
+    ``window`` > 0 makes every run sliding-window attention (keys p-window+1..p).
+    A run captured into a CUDA graph reads the plan when it is replayed: keep the plan (and its
+    workspace) as long as the graph."""
 
     def __init__(self, cache: KVCache, num_q_heads: int, row_kinds, seq_lens, q_offsets,
                  max_pages: int, window: int = 0):
