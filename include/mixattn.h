@@ -208,10 +208,10 @@ int mixattn_kv_export_blocks(const mixattn_kv_cache* cache, int32_t which, const
  *   (a_i, b_i) -> m (a_i cos w - b_i sin w, b_i cos w + a_i sin w),  w = p f_i,
  * with m the config's multiplier; the head's other elements are copied.  fp16 in
  * and out (saturating at +-65504, NaN stays NaN), fp32 products, cosines and sines
- * within 2^-23 of their angle's.  The angle is p times f_i / 2 pi, a double
- * (within 2^-55 of a turn for f_i <= 1), modulo a turn in 64-bit fixed point and cut to 2^-32
- * of one: off by |p| 2^-55 + 2^-32 turns at most, 2^-32 up to position 2^22 and 2^-24 at the
- * last.  Positions may be any int32.
+ * of the angle rounded to fp32 (times m, within 1.5 half ulps).  The angle is p times
+ * f_i / 2 pi, a double (within 2^-55 of a turn for f_i <= 1), modulo a turn in 64-bit fixed
+ * point: off by |p| 2^-55 turns at most, 2^-31 at position 2^24 and 2^-24 at the last.
+ * Positions may be any int32.
  */
 typedef struct {
   int32_t rot_dim;      /* rotated elements of a head: a multiple of 16, <= 128      */

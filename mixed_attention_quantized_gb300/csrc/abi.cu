@@ -533,6 +533,7 @@ int mixattn_rope_create(mixattn_rope** rope_out, const mixattn_rope_config* cfg)
   }
   r->mscale = cfg->mscale > 0.0 ? cfg->mscale : m;
   r->table.mscale = (float)r->mscale;
+  r->table.mscale_rest = (float)(r->mscale - (double)r->table.mscale);
   r->table.rot = rot;
   r->table.layout = cfg->layout;
   *rope_out = r;

@@ -183,7 +183,7 @@ struct AttnParams {
 constexpr int kMaxRotPairs = 64;
 struct RopeTable {
   uint64_t turn[kMaxRotPairs];  // round(2^64 f_i / 2 pi)
-  float mscale;
+  float mscale, mscale_rest;    // the multiplier as two fp32 parts
   int32_t rot;                  // rotated elements of a head (0: none)
   int32_t layout;               // mixattn_rope_layout
 };

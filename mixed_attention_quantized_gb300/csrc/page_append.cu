@@ -21,7 +21,7 @@
 // take about 4 us of each call (8201 tokens: 8500 of 27000 cycles pass before the first key or
 // value is loaded).  Measured, 8 heads of 128: 64 tokens in pages of their own 4.1 us,
 // 2048 in a row 7.4, 8201 15.4 (50 MB, 3.3 TB/s), 32768 65 (3.1 TB/s).  With rotated keys and 32 query
-// heads, 2048 tokens 13.1, 8201 49.7; without queries 10.9 and 27.6.
+// heads, 2048 tokens 13.4, 8201 51.2; without queries 11.4 and 29.3.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <string.h>

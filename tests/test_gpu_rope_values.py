@@ -58,3 +58,50 @@ def test_elements_that_are_not_finite(fk, fv, interleaved):
         tol = (0.5 if fk == 1 else 1.0) * step * (1 + 2.0 ** -10) + top * 2.0 ** -11 + 2.0 ** -24 * (127 if fk == 1 else 8)
         err = np.abs(x - want).reshape(n, hkv, d // 32, 32)
         assert (err <= tol).all()
+
+
+@pytest.mark.parametrize("mscale", [1.0, 1.25])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_cosines_and_sines_to_fp32(interleaved, mscale):
+    """Pairs (a, b) that nearly cancel, a cos w = b sin w to about 2^-21, lay bare the last bits of the
+    cosine and the sine: each has to be fp32's nearest but for less than half of half an ulp, the larger
+    product and the result are rounded once more."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    n, rot = 600, 128
+    rng = np.random.default_rng(31)
+    rope = mq.Rope(rot, layout=int(interleaved), mscale=mscale)
+    f = np.array(rope.info()["frequencies"])
+    pos = rng.integers(0, 4096, n).astype(np.int32)
+    w = pos[:, None] * f  # fp64: within 2^-41
+    c, s = mscale * np.cos(w), mscale * np.sin(w)
+    # the a of 11 bits for which b = a c / s (or the other way round) is nearest to 11 bits
+    big = np.abs(c) >= np.abs(s)
+    r = np.where(big, s, c) / np.where(big, c, s)  # |r| <= 1; the larger factor's partner is a r
+    best = np.full((n, rot // 2), np.inf)
+    x = np.zeros((2, n, rot // 2))
+    for lead in range(1024, 2048):
+        exact = lead * r
+        at = np.exp2(np.floor(np.log2(np.maximum(np.abs(exact), 1e-3))) - 10)
+        near = np.round(exact / at) * at
+        left = np.abs(near - exact)
+        better = (left < best) & (np.abs(near) >= 1)
+        best = np.where(better, left, best)
+        x[0] = np.where(better, np.where(big, near, lead), x[0])
+        x[1] = np.where(better, np.where(big, lead, near), x[1])
+    x *= 16
+    a, b = x
+    want = a * c - b * s
+    assert np.median(np.abs(want) / np.maximum(np.abs(a * c), 1)) < 2.0 ** -18
+    k = np.zeros((n, 1, rot), dtype=np.float16)
+    first, second = (np.s_[0::2], np.s_[1::2]) if interleaved else (np.s_[:rot // 2], np.s_[rot // 2:])
+    k[:, 0, first], k[:, 0, second] = a, b
+    assert (k[:, 0, first] == a).all() and (k[:, 0, second] == b).all()
+    got = mq.rope_apply(rope, torch.from_numpy(k).cuda(), torch.from_numpy(pos).cuda()).cpu().numpy()
+    got = got[:, 0, first].astype(np.float64)
+    half = lambda v: np.spacing(np.abs(v).astype(np.float32)).astype(np.float64) / 2
+    tol = 1.5 * (np.abs(a) * half(c) + np.abs(b) * half(s)) + half(a * c) + half(want)
+    tol += 2.0 ** -11 * np.abs(want) + 2.0 ** -25
+    used = np.isfinite(best)
+    assert used.mean() > 0.5
+    assert (np.abs(got - want) <= tol)[used].all(), (np.abs(got - want) / tol)[used].max()
