@@ -179,3 +179,21 @@ def test_scores_that_keep_moving_the_reference(fmt, d, shape):
     codes, scales = _planes(cache, row_slots)
     want, tol = bound.attention(fmt, q, codes, scales, row_slots, rows)
     assert bound.off_by(got, want, tol) <= 1, bound.off_by(got, want, tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_pages_before_the_window_are_not_read(fmt):
+    """Decode and verify rows: whole pages, chunk rows: whole KV tiles of four pages before the first
+    query's window may be given away (ids outside the cache here)."""
+    import mixed_attention_quantized_gb300 as mq
+    mq.device_error(clear=True)
+    rows, window = [(6000, 5999), (3000, 2996), (5000, 4800)], 700
+    cache, pt, row_slots = base._filled(fmt, rows, 2, 128, 701)
+    q = _queries(rows, 8, 128, 702)
+    good = base._attend(cache, pt, rows, _kinds(rows), 8, q, window)
+    bad = pt.copy()
+    for r, (_, off) in enumerate(rows):
+        first = off + 1 - window
+        bad[r, :first // 32 if r < 2 else first // 128 * 4] = cache.num_pages + 7
+    np.testing.assert_array_equal(base._attend(cache, bad, rows, _kinds(rows), 8, q, window), good)
+    assert mq.device_error(clear=True) == 0
