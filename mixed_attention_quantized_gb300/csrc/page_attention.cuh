@@ -465,10 +465,11 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
 // Roles of the 16 warps:
 //   softmax (warps 0-3 and 4-7), thread = TMEM lane = query row: one pass over its 128 scores,
 //     a page's 32 at a time, against the row's reference m; P' as fp16 over the first half of
-//     the page's own scores.  m is an integer, 6 to 7 below the largest x when it was set, so the
+//     the page's own scores.  m is set 6 below the largest x of the row's first page (whose P' is
+//     then 2^6 to fp32's last bits, no fp16 rounding: a row that sees one key gets its value), so the
 //     sum of a page's P', which l needs anyway, is below the fp16 range unless one of its x passes
-//     that one by 4 or more; where it is not, m moves before the P' are stored, and O and the
-//     tile's P' so far are multiplied by a power of two;
+//     that one by 4 or more; where it is not, m moves before the P' are stored, by whole bits, and O and
+//     the tile's P' so far are multiplied by a power of two;
 //   conversion (K 8-11, V 13-15): codes loaded one KV tile ahead into registers, as fp16 into
 //     128-byte-swizzled operand tiles, two buffers each of K and V; a K warp also writes its
 //     page's terms (below);
@@ -529,11 +530,11 @@ __device__ __forceinline__ float4 page_terms(float dk, float dv, bool there, flo
                      there ? tv.x : -CUDART_INF_F, tv.y, 0.f);
 }
 
-// A chunk row's reference: kChunkSet below the (rounded up) largest x when it is set, and moved
+// A chunk row's reference: kChunkSet below the largest x when it is set, and moved to 6 to 7 below
 // when the 32 P' of a page sum to kChunkTop (so one is 2^10.98 or more; none above 65504
 // passes).  The page's largest fp16 P' as the test, by packed integer maxima, with 11 and 2^15: the
 // chunk of 2048 tokens at 32768 keys 1160 -> 1200 us.
-constexpr float kChunkSet = 7.f, kChunkTop = 65000.f, kChunkMoved = 10.9f;
+constexpr float kChunkSet = 6.f, kChunkTop = 65000.f, kChunkMoved = 10.9f;
 
 // The softmax's rare step, for page c (32 scores at s_col + 32 c) of a warp in which some row's
 // P' sum to kChunkTop, or which has rows without a reference: moves the references of the rows
@@ -556,8 +557,10 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
   }
   mx = fmaf(mx, tm.x, tm.y);
   const bool grow = mx > -CUDART_INF_F && (m_run == -CUDART_INF_F || mx >= m_run + kChunkMoved);
-  const float m_new = grow ? ceilf(mx) - kChunkSet : m_run;
-  const float alpha = grow ? ex2(m_run - m_new) : 1.f;  // a power of two, or 0
+  const bool first = m_run == -CUDART_INF_F;
+  const float up = grow ? (first ? 0.f : floorf(mx - m_run - kChunkSet)) : 0.f;  // whole bits
+  const float m_new = grow ? (first ? mx - kChunkSet : m_run + up) : m_run;
+  const float alpha = grow && first ? 0.f : ex2(-up);  // a power of two, or 0
   l_run *= alpha;
   if (scale_o) {
     const uint64_t al2 = f2_pack(alpha, alpha);
@@ -577,7 +580,7 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
     }
   }
   // alpha as two fp16 powers of two, down to 2^-48: below 2^-40 no P' is left of it
-  const float e_all = grow ? fmaxf(m_run - m_new, -48.f) : 0.f, e_half = ceilf(0.5f * e_all);
+  const float e_all = fmaxf(-up, -48.f), e_half = ceilf(0.5f * e_all);
   const float al_1 = ex2(e_half), al_2 = ex2(e_all - e_half);
   const uint32_t al_h = pack_f16x2(al_1, al_1), al_l = pack_f16x2(al_2, al_2);
   tmem_wait_st();  // the P' of the pages before are in place

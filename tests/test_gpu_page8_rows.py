@@ -197,3 +197,29 @@ def test_pages_before_the_window_are_not_read(fmt):
         bad[r, :first // 32 if r < 2 else first // 128 * 4] = cache.num_pages + 7
     np.testing.assert_array_equal(base._attend(cache, bad, rows, _kinds(rows), 8, q, window), good)
     assert mq.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (8, 8), (8, 1)])
+def test_a_query_that_sees_one_key_gets_its_value(fmt, d, hq, hkv):
+    """Window 1, and the first token of a prompt: the one weight is 1 whatever it is rounded to, so the
+    output is the key's value to fp16's own rounding (and 2^-21 for the fp32 steps)."""
+    import mixed_attention_quantized_gb300 as mq
+    rows = [(300, 299), (500, 494), (700, 500), (1100, 0), (200, 0)]
+    cache, pt, row_slots = base._filled(fmt, rows, hkv, d, 801)
+    q = _queries(rows, hq, d, 802)
+    (_, cv), (_, dv) = _planes(cache, row_slots)
+    got = base._attend(cache, pt, rows, _kinds(rows), hq, q, 1)
+    at = 0
+    for r, (seq, off) in enumerate(rows):
+        s = np.asarray(row_slots[r])[off:seq]
+        want = np.repeat(cv[s // 32, :, s % 32] * dv[s // 32].astype(np.float64)[:, :, None], hq // hkv, axis=1)
+        half = np.spacing(np.abs(want).astype(np.float16)).astype(np.float64) / 2
+        assert (np.abs(got[at:at + seq - off] - want) <= half + 2.0 ** -21 * np.abs(want)).all()
+        at += seq - off
+    # without a window, the first token of the two prompts
+    first = base._attend(cache, pt, rows, _kinds(rows), hq, q)
+    for at in (1 + 6 + 200, 1 + 6 + 200 + 1100):
+        np.testing.assert_array_equal(first[at], got[at])
+    assert mq.device_error(clear=True) == 0
