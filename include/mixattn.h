@@ -92,7 +92,9 @@ typedef enum {
 /* Row kinds of one ForwardBatch (§1). */
 typedef enum {
   MIXATTN_ROW_DECODE = 0, /* one query at position seq_len-1; q_offset == seq_len-1 */
-  MIXATTN_ROW_CHUNK = 1   /* seq_len-q_offset queries at positions q_offset..seq_len-1 */
+  MIXATTN_ROW_CHUNK = 1,  /* seq_len-q_offset queries at positions q_offset..seq_len-1 */
+  MIXATTN_ROW_TREE = 3    /* seq_len-q_offset drafted tokens behind q_offset others; which of
+                             one another they see is a mask (mixattn_run_tree)          */
 } mixattn_row_kind;
 
 typedef enum {
@@ -282,7 +284,7 @@ int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope,
  * Rows are packed in order: the queries of row r start at
  * sum_{r'<r} (seq_len[r'] - q_offset[r']).  For every row
  *   decode: q_offset == seq_len - 1, seq_len >= 1
- *   chunk:  0 <= q_offset < seq_len
+ *   chunk, tree:  0 <= q_offset < seq_len
  * and ceil(seq_len / page_size) <= max_pages.  seq_len counts the new tokens,
  * whose K/V must already be in the cache (append first, then attend).
  *
@@ -294,7 +296,7 @@ int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope,
  * are cut into (kv head, page range) split-K tiles whose size depends only on
  * the row's own length; a chunk row of at most 24 (query, head) rows (a
  * speculative-verify pass: up to 6 draft tokens at G = 4) runs on such tiles too,
- * each holding up to 8 (query, head) rows.  So a row's output bits do not depend
+ * each holding up to 8 (query, head) rows; tree rows are cut like chunk rows.  So a row's output bits do not depend
  * on the rest of the batch.
  *
  *   num_q_heads      multiple of cache->num_kv_heads; G = num_q_heads /
@@ -360,6 +362,25 @@ int mixattn_plan_info(const mixattn_plan* plan, int32_t* total_q, int32_t* n_chu
  */
 int mixattn_run(const mixattn_plan* plan, const void* q, const int32_t* page_table, void* o,
                 void* workspace, size_t workspace_bytes, mixattn_stream stream);
+
+/*
+ * The same for a plan with tree rows: drafted tokens that hang together as trees (any order),
+ * whose K/V are appended behind the row's context like those of a chunk row.  Drafted token i of
+ * a row (packed query i of the row, slot q_offset + i) sees every key before q_offset and, of the
+ * row's n = seq_len - q_offset drafted tokens, token j where bit j % 32 of word j / 32 of its mask
+ * is set (itself too only by its own bit).  A token that sees nothing gets zeros.
+ *   tree_mask   device uint32 [sum of n over the plan's tree rows, in row order][mask_words];
+ *               read at run time, so one plan (and one captured graph) serves changing trees.
+ *               Bits from n on are ignored.  May be NULL for a plan without tree rows.
+ *   mask_words  >= ceil(n / 32) of the largest tree row
+ * n <= 1024, else MIXATTN_ERR_UNSUPPORTED from the plan.  In a plan with a window W a drafted token
+ * stands at position q_offset + max(1, bits set in its mask) - 1 (its depth) and sees the context
+ * keys that are less than W before it; n <= W, so that no path is longer than the window.
+ * mixattn_run on a plan with tree rows returns MIXATTN_ERR_INVALID_ARG, and the one-call entry
+ * points do not take such rows (the allocation-free one: MIXATTN_ERR_UNSUPPORTED).
+ */
+int mixattn_run_tree(const mixattn_plan* plan, const void* q, const int32_t* page_table, const uint32_t* tree_mask,
+                     int32_t mask_words, void* o, void* workspace, size_t workspace_bytes, mixattn_stream stream);
 
 void mixattn_plan_destroy(mixattn_plan* plan);
 

@@ -25,7 +25,7 @@ F16, Q8_0, Q4_0 = 0, 1, 2
 I8_PAGE, E4M3_PAGE = 3, 4  # 8-bit codes with one fp32 scale per (page, kv head)
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_RAMP, ROPE_SCALE_BANDS = 0, 1, 2, 3
-ROW_DECODE, ROW_CHUNK = 0, 1
+ROW_DECODE, ROW_CHUNK, ROW_TREE = 0, 1, 3
 PAGE = 32
 
 OK = 0
@@ -38,6 +38,7 @@ LIB_PATH = os.path.join(_HERE, "libmixattn.so")
 EXPORTED = [
     "mixattn_kv_cache_bytes", "mixattn_kv_append_quant", "mixattn_kv_export_blocks",
     "mixattn_plan_create", "mixattn_plan_create_window", "mixattn_plan_update", "mixattn_plan_info", "mixattn_run",
+    "mixattn_run_tree",
     "mixattn_plan_destroy", "mixattn_mixed_attention", "mixattn_workspace_bytes",
     "mixattn_device_error", "mixattn_status_string", "mixattn_version",
     "mixattn_mixed_attention_noalloc",
@@ -119,6 +120,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mixattn_plan_info.restype = ctypes.c_int
     lib.mixattn_run.argtypes = [vp, vp, vp, vp, vp, sz, vp]
     lib.mixattn_run.restype = ctypes.c_int
+    lib.mixattn_run_tree.argtypes = [vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.mixattn_run_tree.restype = ctypes.c_int
     lib.mixattn_plan_destroy.argtypes = [vp]
     lib.mixattn_plan_destroy.restype = None
     lib.mixattn_mixed_attention.argtypes = [cachep, i32, vp, vp, i32, i32, i32p, i32p, i32p, vp, vp, sz, vp]
@@ -444,6 +447,17 @@ def rope_append(cache: KVCache, rope: Rope, q, k_new, v_new, positions, slot_map
     return q_out
 
 
+def _tree_tokens(row_kinds, seq_lens, q_offsets) -> int:
+    return sum(int(s) - int(o) for k, s, o in zip(row_kinds, seq_lens, q_offsets) if k == ROW_TREE)
+
+
+def _check_mask(x, n: int) -> None:
+    rt = _rt or _runtime()
+    if x.dtype is not rt.int32 or x.dim() != 2 or x.shape[0] < n or not x.is_contiguous():
+        raise ValueError(f"tree_mask: contiguous int32 [{n}, words] expected, got {x.dtype} {tuple(x.shape)}")
+    _call_device(rt, x, "tree_mask")
+
+
 class Plan:
     """Host tiling of one ForwardBatch; reusable across layers and re-tileable.
     ``window`` > 0 makes every run sliding-window attention (keys p-window+1..p).
@@ -466,6 +480,7 @@ class Plan:
                                                   int(max_pages), ctypes.byref(ws))
         _check(st, "mixattn_plan_create")
         self.workspace_bytes = int(ws.value)
+        self._tree_tokens = _tree_tokens(row_kinds, seq_lens, q_offsets)
 
     def update(self, row_kinds, seq_lens, q_offsets, max_pages: int) -> None:
         ws = ctypes.c_size_t(0)
@@ -474,6 +489,7 @@ class Plan:
                                            int(max_pages), ctypes.byref(ws))
         _check(st, "mixattn_plan_update")
         self.workspace_bytes = int(ws.value)
+        self._tree_tokens = _tree_tokens(row_kinds, seq_lens, q_offsets)
 
     def info(self):
         tq, nc, nd = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
@@ -481,7 +497,17 @@ class Plan:
                                            ctypes.byref(nd)), "mixattn_plan_info")
         return {"total_q": tq.value, "chunk_tiles": nc.value, "decode_tiles": nd.value}
 
-    def run(self, q, page_table, o, workspace, stream=None) -> None:
+    def run(self, q, page_table, o, workspace, stream=None, tree_mask=None) -> None:
+        """``tree_mask``: int32 ``[drafted tokens of all tree rows, words]``, bit j % 32 of word j / 32
+        set where a token sees drafted token j of its row; a plan with tree rows needs one."""
+        if tree_mask is not None:
+            _check_mask(tree_mask, self._tree_tokens)
+            st = self._lib.mixattn_run_tree(self._handle, _ptr(q), _ptr(page_table), tree_mask.data_ptr(),
+                                            tree_mask.shape[1], _ptr(o), _ptr(workspace), workspace.nbytes,
+                                            _stream_handle(stream))
+            if st:
+                _check(st, "mixattn_run_tree")
+            return
         st = self._lib.mixattn_run(self._handle, _ptr(q), _ptr(page_table), _ptr(o), _ptr(workspace),
                                    workspace.nbytes, _stream_handle(stream))
         if st:

@@ -131,6 +131,15 @@ int check_cache(const mixattn_kv_cache* c) {
 
 cudaError_t dispatch_attention(int k_fmt, int v_fmt, int head_dim, const AttnParams& p, unsigned int* err,
                                cudaStream_t s) {
+  if (p.tree_starts) {
+    if (k_fmt == MIXATTN_KV_I8_PAGE) return launch_tree_attention_i8_page(head_dim, p, err, s);
+    if (k_fmt == MIXATTN_KV_E4M3_PAGE) return launch_tree_attention_e4m3_page(head_dim, p, err, s);
+    if (k_fmt == MIXATTN_KV_F16) return launch_tree_attention_f16_f16(head_dim, p, err, s);
+    if (k_fmt == MIXATTN_KV_Q8_0 && v_fmt == MIXATTN_KV_Q8_0) return launch_tree_attention_q8_q8(head_dim, p, err, s);
+    if (k_fmt == MIXATTN_KV_Q4_0 && v_fmt == MIXATTN_KV_Q4_0) return launch_tree_attention_q4_q4(head_dim, p, err, s);
+    if (k_fmt == MIXATTN_KV_Q8_0) return launch_tree_attention_q8_q4(head_dim, p, err, s);
+    return launch_tree_attention_q4_q8(head_dim, p, err, s);
+  }
   if (k_fmt == MIXATTN_KV_I8_PAGE) return launch_attention_i8_page(head_dim, p, err, s);
   if (k_fmt == MIXATTN_KV_E4M3_PAGE) return launch_attention_e4m3_page(head_dim, p, err, s);
   if (k_fmt == MIXATTN_KV_F16) return launch_attention_f16_f16(head_dim, p, err, s);
@@ -148,6 +157,8 @@ struct Tiling {
   int32_t chunk_kv_tiles = 0;  // KV tiles over all chunk tiles (their mean decides persistence)
   int64_t chunk_kv_halves = 0; // the same, a tile of more than 128 rows counted twice
   int32_t decode_pages = 0;    // pages over all decode tiles
+  bool trees = false;          // any tree row
+  int32_t tree_words = 0;      // mask words that the largest of them needs
   WorkspaceLayout L{};
 };
 
@@ -208,9 +219,11 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   const int hkv = c.num_kv_heads;
   const int T = chunk_rows(c.k_fmt) / G;  // query tokens per chunk tile
   const int QPG = kMaxGroup / G;  // queries per decode-style tile of a verify row
-  bool any_verify = false;
+  bool any_verify = false, any_tree = false;
+  int64_t tree_nodes = 0, tree_words = 0;
 
   std::vector<RowInfo> rows(n_rows);
+  std::vector<int32_t> tree_starts(n_rows, -1);
   struct Chunk {
     TileDesc t;
     int64_t kv_first;  // first KV tile the tile's queries can see
@@ -226,9 +239,18 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
       if (s < 1 || o != s - 1) return MIXATTN_ERR_INVALID_ARG;
     } else if (kinds[r] == MIXATTN_ROW_CHUNK) {
       if (o < 0 || o >= s) return MIXATTN_ERR_INVALID_ARG;
+    } else if (kinds[r] == MIXATTN_ROW_TREE) {
+      if (o < 0 || o >= s) return MIXATTN_ERR_INVALID_ARG;
+      // (the drafted tokens of a path then lie within one window)
+      if (s - o > kMaxTreeNodes || (window > 0 && s - o > window)) return MIXATTN_ERR_UNSUPPORTED;
+      any_tree = true;
+      tree_starts[r] = (int32_t)tree_nodes;
+      tree_nodes += s - o;
+      tree_words = std::max<int64_t>(tree_words, (s - o + 31) / 32);
     } else {
       return MIXATTN_ERR_INVALID_ARG;
     }
+    const bool tree = kinds[r] == MIXATTN_ROW_TREE;
     const int64_t n_pages = (s + kPage - 1) / kPage;
     if (n_pages > max_pages) return MIXATTN_ERR_INVALID_ARG;
     if (n_pages > c.num_pages) return MIXATTN_ERR_INVALID_ARG;
@@ -239,9 +261,9 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
     const int64_t nq = s - o;
     // a short chunk row (speculative verify: q_len * G <= kVerifyMaxRows) runs like decode
     // rows, on split-K tiles of up to 8 (query, head) rows
-    const bool verify = kinds[r] == MIXATTN_ROW_CHUNK && nq * G <= kVerifyMaxRows;
+    const bool verify = kinds[r] != MIXATTN_ROW_DECODE && nq * G <= kVerifyMaxRows;
     any_verify = any_verify || verify;
-    if (kinds[r] == MIXATTN_ROW_CHUNK && !verify) {
+    if (kinds[r] != MIXATTN_ROW_DECODE && !verify) {
       const size_t first_chunk = chunks.size();
       for (int g = 0; g < hkv; ++g) {
         for (int64_t b = 0; b < nq; b += T) {
@@ -252,9 +274,10 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
           ch.t.count = (int32_t)std::min<int64_t>(T, nq - b);
           ch.t.kv0 = ch.t.kv1 = ch.t.part = 0;
           ch.t.nsplit = 1;
-          const int64_t key_end = std::min<int64_t>(s, o + b + ch.t.count);
+          // (a tree's tokens may see any other of the row, and sit at any depth)
+          const int64_t key_end = tree ? s : std::min<int64_t>(s, o + b + ch.t.count);
           // a sliding window skips the KV tiles before the first query's first key
-          ch.kv_first = window_first_key((int)(o + b), window) / kChunkN;
+          ch.kv_first = window_first_key((int)(tree ? o : o + b), window) / kChunkN;
           ch.cost = (key_end + kChunkN - 1) / kChunkN - ch.kv_first;
           ch.split = 1;
           chunks.push_back(ch);
@@ -321,7 +344,9 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   T2.n_decode = (int32_t)decodes.size();
   T2.slot_rows = any_verify ? kMaxGroup : G;
   T2.L = workspace_layout(n_rows, (int)n_tiles, T2.n_decode, T2.slot_rows, c.head_dim, any_split,
-                          chunk_rows(c.k_fmt));
+                          chunk_rows(c.k_fmt), any_tree);
+  T2.trees = any_tree;
+  T2.tree_words = (int32_t)tree_words;
   T2.image.assign(T2.L.upload_end - T2.L.rows, 0);
   memcpy(T2.image.data(), rows.data(), sizeof(RowInfo) * rows.size());
   TileDesc* td = reinterpret_cast<TileDesc*>(T2.image.data() + (T2.L.tiles - T2.L.rows));
@@ -346,6 +371,8 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
   int64_t decode_pages = 0;
   for (const TileDesc& t : decodes) decode_pages += t.count;
   T2.decode_pages = (int32_t)std::min<int64_t>(decode_pages, INT32_MAX);
+  if (any_tree)
+    memcpy(T2.image.data() + (T2.L.tree_starts - T2.L.rows), tree_starts.data(), sizeof(int32_t) * n_rows);
   // counters stay zero: every run starts its split tickets from 0
   return MIXATTN_OK;
 }
@@ -673,12 +700,20 @@ static __global__ void upload_kernel(const uint4* __restrict__ src, uint4* __res
     dst[i] = src[i];
 }
 
-int mixattn_run(const mixattn_plan* plan_c, const void* q, const int32_t* page_table, void* o, void* workspace,
+int mixattn_run(const mixattn_plan* plan, const void* q, const int32_t* page_table, void* o, void* workspace,
                 size_t workspace_bytes, mixattn_stream stream) {
+  return mixattn_run_tree(plan, q, page_table, nullptr, 0, o, workspace, workspace_bytes, stream);
+}
+
+int mixattn_run_tree(const mixattn_plan* plan_c, const void* q, const int32_t* page_table, const uint32_t* tree_mask,
+                     int32_t mask_words, void* o, void* workspace, size_t workspace_bytes, mixattn_stream stream) {
   mixattn_plan* plan = const_cast<mixattn_plan*>(plan_c);
   if (!plan) return MIXATTN_ERR_INVALID_ARG;
   if (!q || !o || !page_table) return MIXATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(page_table, 4)) return MIXATTN_ERR_INVALID_ARG;
+  const bool trees = plan->tiling.trees;
+  if (trees && (!tree_mask || !aligned(tree_mask, 4) || mask_words < plan->tiling.tree_words))
+    return MIXATTN_ERR_INVALID_ARG;
   const WorkspaceLayout& L = plan->tiling.L;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return MIXATTN_ERR_WORKSPACE;
   if (int st = pending_device_check()) return st;
@@ -737,6 +772,11 @@ int mixattn_run(const mixattn_plan* plan_c, const void* q, const int32_t* page_t
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
   p.window = plan->window;
   p.slot_rows = plan->tiling.slot_rows;
+  if (trees) {
+    p.tree_starts = reinterpret_cast<const int32_t*>(ws + L.tree_starts);
+    p.tree_mask = tree_mask;
+    p.tree_words = mask_words;
+  }
   cudaError_t e = dispatch_attention(c.k_fmt, c.v_fmt, c.head_dim, p, err, s);
   return e == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
 }

@@ -219,6 +219,30 @@ __device__ __forceinline__ void decode_sync(int half) {
 __device__ __forceinline__ float h2f_lo(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x & 0xFFFFu))); }
 __device__ __forceinline__ float h2f_hi(uint32_t x) { return __half2float(__ushort_as_half((unsigned short)(x >> 16))); }
 
+// The masked view of one drafted token of a tree row (kernels built with TREE; rows of
+// other kinds in the same batch have start < 0).
+struct TreeView {
+  const uint32_t* mask = nullptr;  // the token's words
+  int n = 0, ctx = 0;              // drafted tokens of the row, keys before them
+  __device__ __forceinline__ uint32_t bits(int key, int words) const { return tree_bits(mask, words, n, key - ctx); }
+};
+
+// View of drafted token i of a tree row, and its first visible key: a token sits as deep in its
+// tree as its mask has bits (a token whose mask is empty, at the context's end).
+__device__ __forceinline__ TreeView tree_view(const AttnParams& p, const RowInfo& ri, int start, int i, int& lo) {
+  TreeView v;
+  v.mask = p.tree_mask + (int64_t)(start + i) * p.tree_words;
+  v.n = ri.seq_len - ri.q_offset;
+  v.ctx = ri.q_offset;
+  lo = 0;
+  if (p.window > 0) {
+    int depth = 0;
+    for (int b = 0; b < v.n; b += 32) depth += __popc(tree_bits(v.mask, p.tree_words, v.n, b));
+    lo = window_first_key(v.ctx + max(depth, 1) - 1, p.window);
+  }
+  return v;
+}
+
 // One decode tile: a page range of one (row, kv head), 8 warps, each warp
 // walking its own pages 16 keys (one M-tile) at a time.
 //
@@ -234,7 +258,7 @@ __device__ __forceinline__ float h2f_hi(uint32_t x) { return __half2float(__usho
 //           A row of -offset * 2^-24 sums the same fp16 P' into row b of `corr`,
 //           added to the block's rows at the end.
 // The 2^24 is folded into the softmax scale (scores) and the epilogue (values).
-template <int FK, int FV, int D, int NS>
+template <int FK, int FV, int D, int NS, bool TREE>
 __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc& t, uint8_t* smem, unsigned int* err,
                                             int half) {
   using S = DecodeSmem<FK, FV, D>;
@@ -262,11 +286,16 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
   const int qg0 = t.kv1, nq = t.nsplit, R = nq * G;
   const int my_q = qg0 + (r < R ? (r >> p.log2_group) : 0), my_h = r & (G - 1);
   const int pos = ri.q_offset + my_q;                // this lane's row sees keys lo .. pos
-  const int lo = window_first_key(pos, p.window);    // (a sliding window starts at lo)
+  int lo = window_first_key(pos, p.window);          // (a sliding window starts at lo)
+  // a tree row's token sees keys lo .. q_offset - 1 and those of its mask
+  const int tree0 = TREE ? p.tree_starts[t.row] : -1;
+  const bool tree = TREE && tree0 >= 0;
+  TreeView tv;
+  if (tree) tv = tree_view(p, ri, tree0, my_q, lo);
   // an M-tile needs masks when it reaches past the group's earliest query or
   // before its latest window start (the same bounds for every lane)
-  const int mask_hi = ri.q_offset + qg0 + 1;
-  const int mask_lo = window_first_key(ri.q_offset + qg0 + nq - 1, p.window);
+  const int mask_hi = tree ? ri.q_offset : ri.q_offset + qg0 + 1;
+  const int mask_lo = window_first_key(tree ? ri.seq_len - 1 : ri.q_offset + qg0 + nq - 1, p.window);
   // the tile's pages spread evenly over its 8 warps (runs differing by at most one
   // page, each at most ppw), so a row's shorter last split also keeps every warp busy
   const int pg_base = t.count / kWarps, pg_rem = t.count - pg_base * kWarps;
@@ -439,7 +468,11 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
       const int key0 = (wp0 + (i >> 1)) * kPage + 16 * (i & 1);  // first key of the M-tile
       // some key of the M-tile lies outside some row's range
       const bool partial = key0 + 16 > mask_hi || key0 < mask_lo;
-      auto seen = [&](int k) { return k <= pos && k >= lo; };  // visible to this lane's row
+      const uint32_t vis = tree && partial ? tv.bits(key0, p.tree_words) : 0u;
+      auto seen = [&](int k) {  // visible to this lane's row
+        if (tree) return ((vis >> (k - key0)) & 1u) != 0u && k >= lo;
+        return k <= pos && k >= lo;
+      };
 
       // ---------------- scales of the M-tile -> fp32, one key per lane ----------------
       if (QK || QV) {
@@ -631,7 +664,7 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
           // fp16: chunks 4h..4h+3 (8 dims each) are rows 0-7 / 8-15 of M-tiles 2h, 2h+1
           uint32_t mk0 = 0xFFFFFFFFu, mk1 = 0xFFFFFFFFu;
           if (partial) {  // zero the keys no row sees, so stale data never reaches the MMA
-            const int lo_first = window_first_key(ri.q_offset + qg0, p.window);
+            const int lo_first = window_first_key(tree ? ri.q_offset : ri.q_offset + qg0, p.window);
             auto any_row = [&](int k) { return k < ri.seq_len && k >= lo_first; };
             mk0 = (any_row(key0 + kv0) ? 0x0000FFFFu : 0u) | (any_row(key0 + kv0 + 1) ? 0xFFFF0000u : 0u);
             mk1 = (any_row(key0 + kv0 + 8) ? 0x0000FFFFu : 0u) | (any_row(key0 + kv0 + 9) ? 0xFFFF0000u : 0u);
@@ -701,6 +734,8 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
   const int n_warps_used = min(kWarps, t.count);
   const bool single = ri.n_splits == 1;
   const int slot_rows = p.slot_rows > 0 ? p.slot_rows : G;  // rows per partial slot
+  // (a drafted token that sees nothing gets zeros)
+  auto mean = [&](float o, float l) { return tree && l == 0.f ? 0.f : o / l; };
   // split partial: O [slot_rows][D], then (m, l) [slot_rows][2]; t.kv0 is the slot of split 0
   float* part = p.partials + (int64_t)(t.kv0 + split) * slot_rows * (D + 2);
   for (int idx = tid; idx < n_out; idx += kThreads) {
@@ -715,7 +750,7 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
       osum += sc * x[16 + h * D + d];
     }
     if (single) {
-      out_of(h)[d] = f16_out(osum / lsum);
+      out_of(h)[d] = f16_out(mean(osum, lsum));
     } else {
       part[h * D + d] = osum;
       if (d == 0) {
@@ -756,7 +791,7 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
       lsum += sc * __ldcg(x + slot_rows * D + 2 * h + 1);
       osum += sc * __ldcg(x + h * D + d);
     }
-    out_of(h)[d] = f16_out(osum / lsum);
+    out_of(h)[d] = f16_out(mean(osum, lsum));
   }
 }
 
@@ -996,7 +1031,7 @@ __device__ __forceinline__ int chunk_tile_of(int c, int k, int C, int n) {
 // issued after PV(jg) by the same thread (the MMAs of one thread run in issue
 // order).  Every wait is bounded; a timeout in any role makes all of them leave
 // their loops.
-template <int FK, int FV, int D>
+template <int FK, int FV, int D, bool TREE>
 __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ctas, uint8_t* smem_raw,
                                           unsigned int* err) {
   using L = ChunkSmem<FK, FV, D>;
@@ -1062,7 +1097,8 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
       const TileDesc t = p.tiles[idx];
       const RowInfo ri = p.rows[t.row];
       const int n_pages_row = (ri.seq_len + kPage - 1) / kPage;
-      const int key_end = min(ri.seq_len, ri.q_offset + t.begin + t.count);
+      const bool tree = TREE && p.tree_starts[t.row] >= 0;  // (its tokens may see any other of the row)
+      const int key_end = tree ? ri.seq_len : min(ri.seq_len, ri.q_offset + t.begin + t.count);
       const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
       const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages + kv0 * kPagesPerKvTile;
       alive = is_k ? dequant_loop<FK, D, L::kKLo>(p.k_quant, p.k_scale, pt_row, n_pages_row - kv0 * kPagesPerKvTile,
@@ -1127,7 +1163,11 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
       const int g = t.kvh;
       const bool row_valid = tok < t.count;
       const int pos = ri.q_offset + t.begin + min(tok, t.count - 1);
-      const int lo = window_first_key(pos, p.window);  // the row's first visible key
+      int lo = window_first_key(pos, p.window);  // the row's first visible key
+      const int tree0 = TREE ? p.tree_starts[t.row] : -1;
+      const bool tree = TREE && tree0 >= 0;
+      TreeView tv;
+      if (tree) tv = tree_view(p, ri, tree0, t.begin + min(tok, t.count - 1), lo);
       const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int j = 0; j < n_kv; ++j) {
@@ -1141,7 +1181,21 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
         const int kbase = (kv0 + j) * kChunkN;
         // causal (and window) mask: only a warp whose tile crosses the diagonal (or the
         // window's start) pays for it
-        const bool diag = __any_sync(0xFFFFFFFFu, kbase + kChunkN - 1 > pos || kbase < lo);
+        const bool diag =
+            __any_sync(0xFFFFFFFFu, kbase + kChunkN - 1 > (tree ? ri.q_offset - 1 : pos) || kbase < lo);
+        // hides the masked ones of scores 32 c .. 32 c + 31
+        auto hide = [&](int c, uint32_t(&x)[32]) {
+          if (tree) {
+            const uint32_t vis = tv.bits(kbase + 32 * c, p.tree_words);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((vis >> e) & 1u) || kbase + 32 * c + e < lo) x[e] = ninf;
+            return;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) x[e] = ninf;
+        };
         uint32_t a[32];
         // pass 1: the row max of the tile's 128 scores, 32 at a time
         float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
@@ -1149,11 +1203,7 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
         for (int c = 0; c < 4; ++c) {
           tmem_ld32(s_col + 32 * c, a);
           tmem_wait_ld();
-          if (diag) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) a[e] = ninf;
-          }
+          if (diag) hide(c, a);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             mx0 = fmax3(mx0, __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
@@ -1176,11 +1226,7 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
         for (int c = 0; c < 4; ++c) {
           tmem_ld32(s_col + 32 * c, a);
           tmem_wait_ld();
-          if (diag) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (kbase + 32 * c + e > pos || kbase + 32 * c + e < lo) a[e] = ninf;
-          }
+          if (diag) hide(c, a);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -1414,12 +1460,12 @@ struct FusedSmem {
   static_assert(DS::total(kDecodeStages) <= kHalfBytes, "decode tile does not fit");
 };
 
-template <int FK, int FV, int D>
+template <int FK, int FV, int D, bool TREE>
 __global__ void __launch_bounds__(kFusedThreads, 1) mixed_attention_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tile = blockIdx.x;
   if (tile < p.n_chunk_ctas) {
-    chunk_cta<FK, FV, D>(p, tile, p.n_chunk_ctas, smem, err);
+    chunk_cta<FK, FV, D, TREE>(p, tile, p.n_chunk_ctas, smem, err);
   } else {
     // two decode tiles per CTA where they fit, one on each half of its warps and
     // shared memory; else one on the first half
@@ -1428,15 +1474,16 @@ __global__ void __launch_bounds__(kFusedThreads, 1) mixed_attention_kernel(AttnP
     if (half && !FS::kTwoDecode) return;
     const int d = FS::kDecodePerCta * (tile - p.n_chunk_ctas) + half;
     if (d >= p.n_decode_tiles) return;
-    decode_tile<FK, FV, D, FS::kDecodeStages>(p, p.tiles[p.n_chunk_tiles + d], smem + half * FS::kHalfBytes, err, half);
+    decode_tile<FK, FV, D, FS::kDecodeStages, TREE>(p, p.tiles[p.n_chunk_tiles + d], smem + half * FS::kHalfBytes, err,
+                                                    half);
   }
 }
 
-template <int FK, int FV, int D, int MINB, int NS>
+template <int FK, int FV, int D, int MINB, int NS, bool TREE>
 __global__ void __launch_bounds__(kThreads, MINB) decode_attention_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tile = blockIdx.x + p.n_chunk_tiles;
-  decode_tile<FK, FV, D, NS>(p, p.tiles[tile], smem, err, 0);
+  decode_tile<FK, FV, D, NS, TREE>(p, p.tiles[tile], smem, err, 0);
 }
 
 // Chunk tiles whose mean KV-tile count is below this are walked by persistent
@@ -1457,7 +1504,7 @@ inline int sm_count() {
   return cached[dev];
 }
 
-template <int FK, int FV, int D>
+template <int FK, int FV, int D, bool TREE = false>
 cudaError_t launch_attention_t(const AttnParams& p, unsigned int* err, cudaStream_t s) {
   using DS = DecodeSmem<FK, FV, D>;
   const int n_tiles = p.n_chunk_tiles + p.n_decode_tiles;
@@ -1473,7 +1520,7 @@ cudaError_t launch_attention_t(const AttnParams& p, unsigned int* err, cudaStrea
   const int n_fused_ctas = q.n_chunk_ctas + (p.n_decode_tiles + kPer - 1) / kPer;
   constexpr int kDec = DS::kTotal;
   constexpr int kFused = FusedSmem<FK, FV, D>::kBytes;
-  auto* dec_kernel = decode_attention_kernel<FK, FV, D, DS::kSoloMinBlocks, DS::kSoloStages>;
+  auto* dec_kernel = decode_attention_kernel<FK, FV, D, DS::kSoloMinBlocks, DS::kSoloStages, TREE>;
   // The shared-memory limit is an attribute of the function in the current
   // device's context: set it once per device (under a lock, host threads may
   // launch concurrently).
@@ -1488,8 +1535,8 @@ cudaError_t launch_attention_t(const AttnParams& p, unsigned int* err, cudaStrea
     if (!configured[dev]) {
       e = cudaFuncSetAttribute(dec_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDec);
       if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(mixed_attention_kernel<FK, FV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kFused);
+        e = cudaFuncSetAttribute(mixed_attention_kernel<FK, FV, D, TREE>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kFused);
       if (e != cudaSuccess) return e;
       configured[dev] = true;
     }
@@ -1497,7 +1544,7 @@ cudaError_t launch_attention_t(const AttnParams& p, unsigned int* err, cudaStrea
   if (p.n_chunk_tiles == 0) {
     dec_kernel<<<p.n_decode_tiles, kThreads, kDec, s>>>(p, err);
   } else {
-    mixed_attention_kernel<FK, FV, D><<<n_fused_ctas, kFusedThreads, kFused, s>>>(q, err);
+    mixed_attention_kernel<FK, FV, D, TREE><<<n_fused_ctas, kFusedThreads, kFused, s>>>(q, err);
   }
   return cudaGetLastError();
 }

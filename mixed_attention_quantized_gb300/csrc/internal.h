@@ -33,6 +33,7 @@ constexpr int kPageMaxPieces = 4;  // pieces of a page-scaled tile's key range, 
 constexpr int kChunkN = 128;       // keys per KV tile of the chunk path (4 pages)
 constexpr int kPagesPerKvTile = kChunkN / kPage;
 constexpr int kMaxGroup = 8;       // q heads per kv head held in one mma N=8 tile
+constexpr int kMaxTreeNodes = 1024;  // drafted tokens of a tree row, at most
 constexpr int kMaxDevices = 64;    // per-device caches of the host side (device ordinals below this)
 constexpr int kVerifyMaxRows = 24; // a chunk row with q_len * G <= this (speculative verify) runs on
                                    // decode-style split-K tiles of up to 8 (query, head) rows: each
@@ -117,6 +118,7 @@ struct WorkspaceLayout {
   size_t counters;        // uint32[n_decode_tiles + n_chunk_tiles]  (zeroed by every run's copy):
                           // decode split tickets (indexed by a group's first partial slot), then
                           // chunk-piece tickets
+  size_t tree_starts;     // int32[n_rows] of a plan with tree rows (else empty): a tree row's first mask row, -1
   size_t upload_end;      // end of the block copied from the plan's host buffer
   size_t partials;        // float[n_decode_tiles][slot_rows][head_dim + 2]
   size_t chunk_partials;  // float[n_chunk_tiles][chunk rows][head_dim + 2] when any chunk tile is split
@@ -131,13 +133,15 @@ MIXATTN_HD size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // slot_rows: rows of one decode partial slot, G (every decode-kind tile holds one
 // query) or 8 when the plan has verify groups
 MIXATTN_HD WorkspaceLayout workspace_layout(int n_rows, int n_tiles, int n_decode_tiles, int slot_rows,
-                                            int head_dim, bool chunk_split, int chunk_m = kChunkM) {
+                                            int head_dim, bool chunk_split, int chunk_m = kChunkM,
+                                            bool trees = false) {
   const size_t n_chunk = (size_t)(n_tiles - n_decode_tiles);
   WorkspaceLayout L;
   L.rows = 256;
   L.tiles = align_up(L.rows + sizeof(RowInfo) * (size_t)n_rows, 16);
   L.counters = align_up(L.tiles + sizeof(TileDesc) * (size_t)n_tiles, 16);
-  L.upload_end = align_up(L.counters + sizeof(uint32_t) * ((size_t)n_decode_tiles + n_chunk), 16);
+  L.tree_starts = align_up(L.counters + sizeof(uint32_t) * ((size_t)n_decode_tiles + n_chunk), 16);
+  L.upload_end = align_up(L.tree_starts + (trees ? sizeof(int32_t) * (size_t)n_rows : 0), 16);
   L.partials = align_up(L.upload_end, 256);
   L.chunk_partials =
       align_up(L.partials + sizeof(float) * (size_t)n_decode_tiles * slot_rows * (head_dim + 2), 256);
@@ -176,6 +180,9 @@ struct AttnParams {
   float scale_log2;           // log2(e) / sqrt(D)
   int32_t window = 0;         // > 0: sliding window, the query at position p sees keys p-window+1 .. p
   int32_t slot_rows = 0;      // rows of a decode partial slot (0: group)
+  const int32_t* tree_starts = nullptr;  // plans with tree rows: [n_rows] first mask row of a tree row, -1 of others
+  const uint32_t* tree_mask = nullptr;   // [drafted tokens of all tree rows][tree_words]
+  int32_t tree_words = 0;
 };
 
 // Rotary positions (rope.cuh): frequencies as 64-bit fractions of a turn, passed to
@@ -199,6 +206,20 @@ MIXATTN_HD int window_first_key(int pos, int window) {
   return (window > 0 && pos + 1 > window) ? pos + 1 - window : 0;
 }
 
+// Which of 32 consecutive keys a drafted token of a tree row sees, bit e for the key `rel` + e
+// places behind the row's context of which it sees all (before the window's start is applied):
+// every key of the context, and of the n drafted tokens those with a bit in the token's mask.
+MIXATTN_HD uint32_t tree_bits(const uint32_t* mask, int words, int n, int rel) {
+  if (rel <= -32) return 0xFFFFFFFFu;
+  if (rel >= n) return 0u;
+  const int sh = rel & 31, w = rel >> 5;  // (rel < 0: w = -1, the context in the low bits)
+  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : (w < words ? mask[w] : 0u);
+  const uint32_t hi = w + 1 < words ? mask[w + 1] : 0u;
+  uint32_t v = sh ? (lo >> sh) | (hi << (32 - sh)) : lo;
+  if (n - rel < 32) v &= (1u << (n - rel)) - 1u;
+  return v;
+}
+
 }  // namespace mixattn
 
 #ifdef __CUDACC__
@@ -214,6 +235,14 @@ MIXATTN_DECLARE_LAUNCH(launch_attention_q8_q4)
 MIXATTN_DECLARE_LAUNCH(launch_attention_q4_q8)
 MIXATTN_DECLARE_LAUNCH(launch_attention_i8_page)
 MIXATTN_DECLARE_LAUNCH(launch_attention_e4m3_page)
+// The same kernels with tree rows, in translation units of their own.
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_f16_f16)
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_q8_q8)
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_q4_q4)
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_q8_q4)
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_q4_q8)
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_i8_page)
+MIXATTN_DECLARE_LAUNCH(launch_tree_attention_e4m3_page)
 #undef MIXATTN_DECLARE_LAUNCH
 cudaError_t launch_kv_append(const mixattn_kv_cache& c, const void* k_new, const void* v_new,
                              const int32_t* slots, int32_t n_new, unsigned int* err, cudaStream_t s);

@@ -104,7 +104,7 @@ int tile_into_upload(const mixattn_kv_cache& c, int hq, int n_rows, const int32_
     } else if (kinds[r] == MIXATTN_ROW_CHUNK) {
       if (o < 0 || o >= s) return MIXATTN_ERR_INVALID_ARG;
     } else {
-      return MIXATTN_ERR_INVALID_ARG;
+      return kinds[r] == MIXATTN_ROW_TREE ? MIXATTN_ERR_UNSUPPORTED : MIXATTN_ERR_INVALID_ARG;
     }
     const int64_t n_pages = (s + kPage - 1) / kPage;
     if (n_pages > max_pages || n_pages > c.num_pages) return MIXATTN_ERR_INVALID_ARG;

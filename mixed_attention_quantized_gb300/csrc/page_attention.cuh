@@ -116,7 +116,7 @@ __device__ __forceinline__ void page_decode_sync(int part) {
 // One decode tile (see decode_tile in attention_kernel.cuh for the roles of the
 // descriptor's fields): pages t.begin .. + t.count of kv head t.kvh for queries
 // t.kv1 .. + t.nsplit of row t.row, G heads each.
-template <int F, int D>
+template <int F, int D, bool TREE>
 __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const TileDesc& t, uint8_t* smem,
                                                  unsigned int* err, int sub) {
   using S = PageDecodeSmem<D>;
@@ -137,11 +137,20 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
   // the lane's scores are those of tile rows 2c and 2c + 1: their positions and window starts
   auto pos_of = [&](int row) { return ri.q_offset + qg0 + (row < R ? (row >> p.log2_group) : 0); };
   const int pos0 = pos_of(2 * c), pos1 = pos_of(2 * c + 1);
-  const int lo0 = window_first_key(pos0, p.window), lo1 = window_first_key(pos1, p.window);
-  const int mask_hi = ri.q_offset + qg0 + 1;
-  const int mask_lo = window_first_key(ri.q_offset + qg0 + nq - 1, p.window);
-  // keys past the group's last query belong to no row of the tile
-  const int last_page = (ri.q_offset + qg0 + nq - 1) / kPage;
+  int lo0 = window_first_key(pos0, p.window), lo1 = window_first_key(pos1, p.window);
+  // a tree row's tokens see keys lo .. q_offset - 1 and those of their masks
+  const int tree0 = TREE ? p.tree_starts[t.row] : -1;
+  const bool tree = TREE && tree0 >= 0;
+  TreeView tv0, tv1;
+  if (tree) {
+    tv0 = tree_view(p, ri, tree0, pos0 - ri.q_offset, lo0);
+    tv1 = tree_view(p, ri, tree0, pos1 - ri.q_offset, lo1);
+  }
+  const int mask_hi = tree ? ri.q_offset : ri.q_offset + qg0 + 1;
+  const int mask_lo = window_first_key(tree ? ri.seq_len - 1 : ri.q_offset + qg0 + nq - 1, p.window);
+  // keys past the group's last query (of a tree, past the row) belong to no row of the tile
+  const int last_key = tree ? ri.seq_len - 1 : ri.q_offset + qg0 + nq - 1;
+  const int last_page = last_key / kPage;
   const int n_here = min(t.count, last_page + 1 - t.begin);
   const int pg_base = n_here > 0 ? n_here / kPageWarps : 0, pg_rem = n_here > 0 ? n_here - pg_base * kPageWarps : 0;
   const int wp0 = t.begin + warp * pg_base + min(warp, pg_rem);
@@ -262,10 +271,18 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
                     fmaf(u[2] + u2[2], a_pg, b_pg - mr0), fmaf(u[3] + u2[3], a_pg, b_pg - mr1)};
       if (partial) {
         const int k0 = key0 + r, k1 = k0 + 8;
-        if (k0 > pos0 || k0 < lo0) x[0] = -CUDART_INF_F;
-        if (k0 > pos1 || k0 < lo1) x[1] = -CUDART_INF_F;
-        if (k1 > pos0 || k1 < lo0) x[2] = -CUDART_INF_F;
-        if (k1 > pos1 || k1 < lo1) x[3] = -CUDART_INF_F;
+        if (tree) {
+          const uint32_t v0 = tv0.bits(key0, p.tree_words) >> r, v1 = tv1.bits(key0, p.tree_words) >> r;
+          if (!(v0 & 1u) || k0 < lo0) x[0] = -CUDART_INF_F;
+          if (!(v1 & 1u) || k0 < lo1) x[1] = -CUDART_INF_F;
+          if (!(v0 & 256u) || k1 < lo0) x[2] = -CUDART_INF_F;
+          if (!(v1 & 256u) || k1 < lo1) x[3] = -CUDART_INF_F;
+        } else {
+          if (k0 > pos0 || k0 < lo0) x[0] = -CUDART_INF_F;
+          if (k0 > pos1 || k0 < lo1) x[1] = -CUDART_INF_F;
+          if (k1 > pos0 || k1 < lo0) x[2] = -CUDART_INF_F;
+          if (k1 > pos1 || k1 < lo1) x[3] = -CUDART_INF_F;
+        }
       }
       // a reference is set 7 below the largest x and follows it lazily: P' stays <= 2^15, inside
       // fp16, and the sums of 8-bit codes times P' far inside fp32
@@ -318,8 +335,8 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
       }
       uint32_t mk0 = 0xFFFFFFFFu, mk1 = 0xFFFFFFFFu;
       if (!kOff && partial) {  // codes of keys that no row sees may be NaN
-        const int lo_first = window_first_key(ri.q_offset + qg0, p.window), hi_last = ri.q_offset + qg0 + nq - 1;
-        auto any_row = [&](int k) { return k <= hi_last && k >= lo_first; };
+        const int lo_first = window_first_key(tree ? ri.q_offset : ri.q_offset + qg0, p.window);
+        auto any_row = [&](int k) { return k <= last_key && k >= lo_first; };
         const int k0 = key0 + 2 * c;
         mk0 = (any_row(k0) ? 0x0000FFFFu : 0u) | (any_row(k0 + 1) ? 0xFFFF0000u : 0u);
         mk1 = (any_row(k0 + 8) ? 0x0000FFFFu : 0u) | (any_row(k0 + 9) ? 0xFFFF0000u : 0u);
@@ -379,6 +396,7 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
   auto store = [&](int h, int d, float o0, float o1, float l) {
     uint16_t* out = static_cast<uint16_t*>(p.o) +
                     ((int64_t)(ri.q_start + qg0 + (h >> p.log2_group)) * p.hq + (int64_t)g * G + (h & (G - 1))) * D + d;
+    if (tree && l == 0.f) l = CUDART_INF_F;  // (a drafted token that sees nothing gets zeros)
     *reinterpret_cast<uint32_t*>(out) = pack_f16x2_out(o0 / l, o1 / l);
   };
   const int64_t stride = (int64_t)slot_rows * (D + 2);
@@ -540,10 +558,15 @@ constexpr float kChunkSet = 6.f, kChunkTop = 65000.f, kChunkMoved = 10.9f;
 // P' sum to kChunkTop, or which has rows without a reference: moves the references of the rows
 // that need it, multiplies O (if there is one yet: `scale_o`), l and the P' of the KV tile's
 // pages before c by the change, a power of two, and writes the page's P'.  Out of line, so
-// that the common path stays short.  Returns (m, l).
-template <int D>
+// that the common path stays short.  Returns (m, l).  The row sees scores c_first .. c_last of the
+// page; TREE: those with a bit in `c_first` from c_last on.
+template <int D, bool TREE>
 __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_col, int c, float4 tm, int c_first,
                                                    int c_last, float m_run, float l_run, bool scale_o) {
+  auto in = [&](int e) {
+    if (TREE) return (((uint32_t)c_first >> e) & 1u) != 0u && e >= c_last;
+    return e >= c_first && e <= c_last;
+  };
   const uint32_t sc = s_col + 32 * c;
   float mx = -CUDART_INF_F;
 #pragma unroll 1
@@ -553,7 +576,7 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      if (16 * b + e >= c_first && 16 * b + e <= c_last) mx = fmaxf(mx, __uint_as_float(o[e]));
+      if (in(16 * b + e)) mx = fmaxf(mx, __uint_as_float(o[e]));
   }
   mx = fmaf(mx, tm.x, tm.y);
   const bool grow = mx > -CUDART_INF_F && (m_run == -CUDART_INF_F || mx >= m_run + kChunkMoved);
@@ -603,8 +626,7 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      const bool in0 = 16 * b + e >= c_first && 16 * b + e <= c_last;
-      const bool in1 = 16 * b + e + 1 >= c_first && 16 * b + e + 1 <= c_last;
+      const bool in0 = in(16 * b + e), in1 = in(16 * b + e + 1);
       const float p0 = in0 ? ex2(fmaf(__uint_as_float(o[e]), tm.x, cb)) : 0.f;
       const float p1 = in1 ? ex2(fmaf(__uint_as_float(o[e + 1]), tm.x, cb)) : 0.f;
       l_page += p0 + p1;
@@ -647,9 +669,9 @@ static_assert(kPageMaxPieces <= 4, "a tile is cut from eight KV tiles on: its pi
 // Joins the pieces of a cut chunk tile for units u, u + u_step, .. below u_end; unit i is 32 rows
 // (block i / (D / 32)) by 32 columns.  o and ml: the first piece's partials.  Out of line, so that
 // it takes no registers from the common path.
-template <int D>
+template <int D, bool TREE>
 __device__ __noinline__ void page_merge_pieces(PageRowsOut out, const float* o, const float2* ml, int nsplit, int u,
-                                               int u_end, int u_step) {
+                                               int u_end, int u_step, bool tree) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (; u < u_end; u += u_step) {
@@ -669,7 +691,7 @@ __device__ __noinline__ void page_merge_pieces(PageRowsOut out, const float* o, 
       s[q].x = s[q].x == -CUDART_INF_F ? 0.f : ex2(s[q].x - m_all);
       if (s[q].x != 0.f) l_all += s[q].x * s[q].y;
     }
-    const float inv_l = 1.f / l_all;
+    const float inv_l = TREE && tree && l_all == 0.f ? 0.f : 1.f / l_all;
     uint32_t x[16];
 #pragma unroll
     for (int c0 = 0; c0 < 8; c0 += 4) {  // the loads of 16 columns together
@@ -700,7 +722,7 @@ __device__ __noinline__ void page_merge_pieces(PageRowsOut out, const float* o, 
 // is touched before that grid is complete.
 __device__ __forceinline__ void wait_for_upload() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-template <int F, int D>
+template <int F, int D, bool TREE>
 __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int n_ctas, uint8_t* smem_raw,
                                                unsigned int* err) {
   using L = PageChunkSmem<D>;
@@ -800,7 +822,11 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
       const bool row_valid = tok < t.count;
       const bool idle = (prow & ~31) >= t.count * G;  // a warp whose rows are all past the tile's only keeps step
       const int pos = ri.q_offset + t.begin + min(tok, t.count - 1);
-      const int lo = window_first_key(pos, p.window);
+      int lo = window_first_key(pos, p.window);
+      const int tree0 = TREE ? p.tree_starts[t.row] : -1;
+      const bool tree = TREE && tree0 >= 0;
+      TreeView tv;
+      if (tree) tv = tree_view(p, ri, tree0, t.begin + min(tok, t.count - 1), lo);
       const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
       const int j0 = two ? 0 : gq, dj = two ? 1 : 2;
       float m_run = -CUDART_INF_F, l_run = 0.f;
@@ -817,14 +843,22 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         const float4* terms = reinterpret_cast<const float4*>(smem + L::kTerms) + 4 * ((jg0 + j) & 3);
         const int kbase = (kv0 + j) * kChunkN;
         // the first and last visible key of the row in this tile (usually 0 and 127)
-        const int first = lo - kbase, last = pos - kbase;
+        const int first = lo - kbase, last = (tree ? ri.q_offset - 1 : pos) - kbase;
         const bool diag = __any_sync(0xFFFFFFFFu, last < kChunkN - 1 || first > 0);
         float4 tn = terms[0];  // (a page ahead: a shared-memory load is slow beside the MMAs' reads)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           const float4 tm = tn;
           tn = terms[(c + 1) & 3];
-          const int c_first = first - 32 * c, c_last = last - 32 * c;
+          // (TREE: the visible scores of the page as bits, and the first of them in the window)
+          int c_first = first - 32 * c, c_last = last - 32 * c;
+          if (TREE) {
+            const int from = c_first;
+            c_first = -1;
+            if (tree) c_first = (int)tv.bits(kbase + 32 * c, p.tree_words);
+            else if (c_last < 31) c_first = c_last < 0 ? 0 : (int)((2u << c_last) - 1u);
+            c_last = from;
+          }
           const uint32_t sc = s_col + 32 * c;
           uint32_t x[32], pk[16];
           tmem_ld32(sc, x);
@@ -834,7 +868,8 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
           if (diag) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (e < c_first || e > c_last) x[e] = __float_as_uint(-CUDART_INF_F);
+              if (TREE ? !(((uint32_t)c_first >> e) & 1u) || e < c_last : e < c_first || e > c_last)
+                x[e] = __float_as_uint(-CUDART_INF_F);
           }
           uint64_t sum_a = f2_pack(0.f, 0.f), sum_b = sum_a;
 #pragma unroll
@@ -858,7 +893,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
             l_run = fmaf(l_page, tm.z, l_run);
             continue;
           }
-          const float2 ml_new = page_move_reference<D>(s_col, o_col, c, tm, c_first, c_last, m_run, l_run, j > j0);
+          const float2 ml_new = page_move_reference<D, TREE>(s_col, o_col, c, tm, c_first, c_last, m_run, l_run, j > j0);
           m_run = ml_new.x;
           l_run = ml_new.y;
         }
@@ -922,7 +957,8 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         };
         if (idle) {
         } else if (t.nsplit == 1) {
-          const float inv_l = 1.f / l_run;  // no key at all (every page bad): 0 / 0
+          // no key at all (every page bad): 0 / 0; a drafted token that sees nothing: zeros
+          const float inv_l = tree && l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll 1
           for (int ch = 0; ch < D / 16; ch += 2) {
             uint32_t w[16];
@@ -972,8 +1008,8 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
           __threadfence();
           constexpr int U = D / 32;
           const int u0 = two ? (row0 / 32) * U : warp, u_end = two ? u0 + U : ((t.count * G + 31) / 32) * U;
-          page_merge_pieces<D>(out, part - (int64_t)t.part * kPageChunkM * D, ml_part - (int64_t)t.part * kPageChunkM, t.nsplit,
-                               u0, u_end, two ? 1 : 8);
+          page_merge_pieces<D, TREE>(out, part - (int64_t)t.part * kPageChunkM * D, ml_part - (int64_t)t.part * kPageChunkM, t.nsplit,
+                               u0, u_end, two ? 1 : 8, tree);
         }
       }
       k = kn;
@@ -1005,7 +1041,9 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
       if (idx < 0) continue;
       const TileDesc t = p.tiles[idx];
       const RowInfo ri = p.rows[t.row];
-      const int key_end = min(ri.seq_len, ri.q_offset + t.begin + t.count) - t.kv0 * kChunkN;  // keys of the KV range
+      const bool tree = TREE && p.tree_starts[t.row] >= 0;  // (its tokens may see any other of the row)
+      const int key_end = (tree ? ri.seq_len : min(ri.seq_len, ri.q_offset + t.begin + t.count)) -
+                          t.kv0 * kChunkN;  // keys of the KV range
       const int n_kv = t.kv1 - t.kv0;
       const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages + t.kv0 * kPagesPerKvTile;
       // the ids of the warp's two pages of KV tile j
@@ -1190,11 +1228,11 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
   }
 }
 
-template <int F, int D>
+template <int F, int D, bool TREE>
 __global__ void __launch_bounds__(kPageThreads, PageDecodeSmem<D>::kCtas) page_decode_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   wait_for_upload();
-  page_decode_tile<F, D>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
+  page_decode_tile<F, D, TREE>(p, p.tiles[blockIdx.x + p.n_chunk_tiles], smem, err, 0);
 }
 
 constexpr double kChunkShare = 1.15, kHalf = 2000.0;
@@ -1208,23 +1246,23 @@ struct PageFusedSmem {
   static_assert(kBytes <= 227 * 1024, "fused CTA does not fit in shared memory");
 };
 
-template <int F, int D>
+template <int F, int D, bool TREE>
 __global__ void __launch_bounds__(kFusedThreads, 1) page_mixed_kernel(AttnParams p, unsigned int* err) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int cta = blockIdx.x;
   if (cta < p.n_chunk_ctas) {  // (waits for the upload when its barriers and TMEM are set up)
-    page_chunk_cta<F, D>(p, cta, p.n_chunk_ctas, smem, err);
+    page_chunk_cta<F, D, TREE>(p, cta, p.n_chunk_ctas, smem, err);
   } else {
     using FS = PageFusedSmem<D>;
     const int sub = threadIdx.x / kPageThreads;
     const int d = FS::kTiles * (cta - p.n_chunk_ctas) + sub;
     if (d >= p.n_decode_tiles) return;
     wait_for_upload();
-    page_decode_tile<F, D>(p, p.tiles[p.n_chunk_tiles + d], smem + sub * FS::kPart, err, sub);
+    page_decode_tile<F, D, TREE>(p, p.tiles[p.n_chunk_tiles + d], smem + sub * FS::kPart, err, sub);
   }
 }
 
-template <int F, int D>
+template <int F, int D, bool TREE = false>
 cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cudaStream_t s) {
   if (p.n_chunk_tiles + p.n_decode_tiles == 0) return cudaSuccess;
   constexpr int kDec = PageDecodeSmem<D>::kTotal, kFused = PageFusedSmem<D>::kBytes;
@@ -1237,9 +1275,9 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev]) {
-      e = cudaFuncSetAttribute(page_decode_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDec);
+      e = cudaFuncSetAttribute(page_decode_kernel<F, D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDec);
       if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(page_mixed_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFused);
+        e = cudaFuncSetAttribute(page_mixed_kernel<F, D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFused);
       if (e != cudaSuccess) return e;
       configured[dev] = true;
     }
@@ -1255,7 +1293,7 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
     cfg.gridDim = dim3(p.n_decode_tiles);
     cfg.blockDim = dim3(kPageThreads);
     cfg.dynamicSmemBytes = kDec;
-    return cudaLaunchKernelEx(&cfg, page_decode_kernel<F, D>, p, err);
+    return cudaLaunchKernelEx(&cfg, page_decode_kernel<F, D, TREE>, p, err);
   }
   AttnParams q = p;
   const bool persist = p.chunk_kv_tiles < kPersistMaxKvTiles * p.n_chunk_tiles;
@@ -1277,7 +1315,7 @@ cudaError_t launch_page_attention_t(const AttnParams& p, unsigned int* err, cuda
   cfg.gridDim = dim3(q.n_chunk_ctas + (p.n_decode_tiles + kTiles - 1) / kTiles);
   cfg.blockDim = dim3(kFusedThreads);
   cfg.dynamicSmemBytes = kFused;
-  return cudaLaunchKernelEx(&cfg, page_mixed_kernel<F, D>, q, err);
+  return cudaLaunchKernelEx(&cfg, page_mixed_kernel<F, D, TREE>, q, err);
 }
 
 }  // namespace mixattn
