@@ -2,7 +2,8 @@
 block-quantised paged KV cache, GB300 (sm_103a).
 
 This module only marshals arguments (torch tensors -> device pointers, the
-current CUDA stream) into the C ABI declared in ``include/mixattn.h``; every
+current CUDA stream) into the C ABI declared in ``include/mixattn.h`` (and
+``mixattn_latent.h``, ``mixattn_sched.h`` beside it); every
 step of the path runs in the library's CUDA kernels.  There is no CPU
 fallback: if the library is missing or fails to load, every call raises.
 
@@ -43,6 +44,9 @@ EXPORTED = [
     "mixattn_device_error", "mixattn_status_string", "mixattn_version",
     "mixattn_mixed_attention_noalloc",
     "mixattn_rope_create", "mixattn_rope_destroy", "mixattn_rope_info", "mixattn_rope_apply", "mixattn_rope_append",
+    "mixattn_latent_cache_bytes", "mixattn_latent_append", "mixattn_latent_export", "mixattn_latent_plan_create",
+    "mixattn_latent_plan_update", "mixattn_latent_run", "mixattn_latent_plan_destroy", "mixattn_expanded_plan_create",
+    "mixattn_expanded_plan_update", "mixattn_expanded_run", "mixattn_expanded_plan_destroy",
     "mixattn_sched_default_config", "mixattn_sched_create", "mixattn_sched_destroy", "mixattn_sched_submit",
     "mixattn_sched_next_batch", "mixattn_sched_complete", "mixattn_sched_request_info", "mixattn_sched_counts",
 ]
@@ -83,6 +87,17 @@ class RopeConfig(ctypes.Structure):
         ("base", ctypes.c_double), ("factor", ctypes.c_double),
         ("low", ctypes.c_double), ("high", ctypes.c_double), ("mscale", ctypes.c_double),
     ]
+
+
+class LatentCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("data", ctypes.c_void_p),
+    ]
+
+
+class HeadsDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -147,6 +162,29 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mixattn_rope_apply.restype = ctypes.c_int
     lib.mixattn_rope_append.argtypes = [cachep, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp]
     lib.mixattn_rope_append.restype = ctypes.c_int
+    latentp, headsp, szp = ctypes.POINTER(LatentCacheDesc), ctypes.POINTER(HeadsDesc), ctypes.POINTER(sz)
+    lib.mixattn_latent_cache_bytes.argtypes = [latentp]
+    lib.mixattn_latent_cache_bytes.restype = sz
+    lib.mixattn_latent_append.argtypes = [latentp, vp, i32, headsp, headsp, vp, i64, vp, i64, vp, vp, i32, vp]
+    lib.mixattn_latent_append.restype = ctypes.c_int
+    lib.mixattn_latent_export.argtypes = [latentp, vp, i32, vp, vp]
+    lib.mixattn_latent_export.restype = ctypes.c_int
+    lib.mixattn_latent_plan_create.argtypes = [ctypes.POINTER(vp), latentp, i32, dbl, i32, i32p, i32p, i32p, i32, szp]
+    lib.mixattn_latent_plan_create.restype = ctypes.c_int
+    lib.mixattn_latent_plan_update.argtypes = [vp, i32, i32p, i32p, i32p, i32, szp]
+    lib.mixattn_latent_plan_update.restype = ctypes.c_int
+    lib.mixattn_latent_run.argtypes = [vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.mixattn_latent_run.restype = ctypes.c_int
+    lib.mixattn_latent_plan_destroy.argtypes = [vp]
+    lib.mixattn_latent_plan_destroy.restype = None
+    lib.mixattn_expanded_plan_create.argtypes = [ctypes.POINTER(vp), i32, dbl, i32, i32p, i32p, szp]
+    lib.mixattn_expanded_plan_create.restype = ctypes.c_int
+    lib.mixattn_expanded_plan_update.argtypes = [vp, i32, i32p, i32p, szp]
+    lib.mixattn_expanded_plan_update.restype = ctypes.c_int
+    lib.mixattn_expanded_run.argtypes = [vp, headsp, headsp, vp, i64, headsp, vp, vp, sz, vp]
+    lib.mixattn_expanded_run.restype = ctypes.c_int
+    lib.mixattn_expanded_plan_destroy.argtypes = [vp]
+    lib.mixattn_expanded_plan_destroy.restype = None
     cfgp = ctypes.POINTER(SchedConfig)
     i64p = ctypes.POINTER(ctypes.c_int64)
     lib.mixattn_sched_default_config.argtypes = [cfgp]
@@ -516,6 +554,253 @@ class Plan:
     def close(self) -> None:
         if self._handle and self._handle.value:
             self._lib.mixattn_plan_destroy(self._handle)
+            self._handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+@dataclass
+class LatentCache:
+    """A paged latent cache: fp16 ``data [num_pages, 32, latent_dim + rope_dim]`` (torch owns the memory)."""
+    num_pages: int
+    latent_dim: int = 512
+    rope_dim: int = 64
+    data: "object" = None
+
+    @classmethod
+    def allocate(cls, num_pages: int, latent_dim: int = 512, rope_dim: int = 64, device="cuda",
+                 fill: Optional[int] = 0) -> "LatentCache":
+        import torch
+        c = cls(num_pages, latent_dim, rope_dim)
+        n = int(load().mixattn_latent_cache_bytes(ctypes.byref(c.desc())))
+        if n == 0:
+            raise MixattnError(ERR_INVALID_ARG, "LatentCache.allocate")
+        t = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        t = t[(-t.data_ptr()) % 256:][:n]
+        if fill is not None:
+            t.fill_(fill)
+        c.data = t.view(torch.float16).view(num_pages, PAGE, latent_dim + rope_dim)
+        return c
+
+    def desc(self) -> LatentCacheDesc:
+        x = self.data
+        if x is not None:
+            if str(x.dtype) != "torch.float16" or not x.is_contiguous() or tuple(x.shape) != (
+                    self.num_pages, PAGE, self.latent_dim + self.rope_dim):
+                raise ValueError(f"data: contiguous fp16 [{self.num_pages}, {PAGE}, {self.latent_dim + self.rope_dim}] "
+                                 f"expected, got {x.dtype} {tuple(x.shape)}")
+        return LatentCacheDesc(self.num_pages, PAGE, self.latent_dim, self.rope_dim, _ptr(x))
+
+    def _ref(self):
+        """byref(desc()), the structure kept while nothing in it has changed."""
+        x = self.data
+        key = (self.num_pages, self.latent_dim, self.rope_dim, x.data_ptr() if x is not None else 0,
+               x.shape if x is not None else None)
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != key:
+            desc = self.desc()
+            kept = self.__dict__["_kept"] = (key, desc, ctypes.byref(desc))
+        return kept[2]
+
+    def __getstate__(self):
+        """Everything but the kept descriptor, which holds addresses and cannot be copied or pickled."""
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
+
+
+def _strided_heads(rt: _Runtime, here: int, x, n: int, name: str, heads: int, dim: int) -> HeadsDesc:
+    """fp16 ``[n, heads, dim]`` on device ``here`` with any token and head strides."""
+    shape = x.shape
+    if x.dtype is not rt.float16 or len(shape) != 3 or shape[0] != n or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: fp16 [{n}, {heads}, {dim}] expected, got {x.dtype} {tuple(shape)}")
+    s0, s1, s2 = x.stride()
+    if s2 != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if x.get_device() != here:
+        _wrong_device(x, name)
+    # (the stride of a single token or head is not used, and torch leaves it anything)
+    return HeadsDesc(x.data_ptr(), s0 if n > 1 else heads * dim, s1 if heads > 1 else dim)
+
+
+def _strided_rows(rt: _Runtime, here: int, x, n: int, name: str, dim: int) -> int:
+    """Stride in elements of fp16 ``[n, dim]`` on device ``here``, the rows contiguous."""
+    if x.dtype is not rt.float16 or x.shape != (n, dim) or x.stride(1) != 1:
+        raise ValueError(f"{name}: fp16 [{n}, {dim}] with contiguous rows expected, got {x.dtype} {tuple(x.shape)}")
+    if x.get_device() != here:
+        _wrong_device(x, name)
+    return x.stride(0) if n > 1 else dim
+
+
+def latent_append(cache: LatentCache, rope: Rope, q_rope, c_new, k_rope, positions, slot_mapping, q_out=None,
+                  stream=None):
+    """A step's new tokens into a latent cache: ``c_new [n, 512]`` as it is and ``k_rope [n, 64]`` rotated by
+    int32 ``positions [n]``, into the slots ``slot_mapping``; and the queries' position parts ``q_rope
+    [n, heads, 64]`` (may be None) rotated into ``q_out`` (for instance the end of absorbed queries
+    ``[n, heads, 576]``; may be ``q_rope`` itself).  Token, head and row strides are free.  One launch; returns
+    the rotated queries."""
+    rt = _rt or _runtime()
+    n = positions.shape[0]
+    here = _call_device(rt, positions, "positions")
+    cs = _strided_rows(rt, here, c_new, n, "c_new", cache.latent_dim)
+    ks = _strided_rows(rt, here, k_rope, n, "k_rope", cache.rope_dim)
+    heads, qd, od = 0, None, None
+    if q_rope is not None:
+        if q_rope.dim() != 3:
+            raise ValueError(f"q_rope: fp16 [{n}, heads, {cache.rope_dim}] expected, got {tuple(q_rope.shape)}")
+        heads = q_rope.shape[1]
+        if q_out is None:
+            q_out = _empty(q_rope, stream)
+        qd = ctypes.byref(_strided_heads(rt, here, q_rope, n, "q_rope", heads, cache.rope_dim))
+        od = ctypes.byref(_strided_heads(rt, here, q_out, n, "q_out", heads, cache.rope_dim))
+    else:
+        q_out = None
+    _int_list(rt, here, positions, n, "positions")
+    _int_list(rt, here, slot_mapping, n, "slot_mapping")
+    if cache.data.get_device() != here:
+        _wrong_device(cache.data, "cache")
+    st = (_lib or load()).mixattn_latent_append(
+        cache._ref(), rope._handle, heads, qd, od, c_new.data_ptr(), cs, k_rope.data_ptr(), ks, positions.data_ptr(),
+        slot_mapping.data_ptr(), n, stream.cuda_stream if stream is not None else rt.raw_stream(here))
+    if st:
+        _check(st, "mixattn_latent_append")
+    return q_out
+
+
+def latent_export(cache: LatentCache, slots, stream=None):
+    """Rows ``[n, 576]`` (fp16, latent vector first) of the int32 slots."""
+    rt = _rt or _runtime()
+    n = int(slots.shape[0])
+    here = _call_device(rt, slots, "slots")
+    _int_list(rt, here, slots, n, "slots")
+    if cache.data.get_device() != here:
+        _wrong_device(cache.data, "cache")
+    out = _empty(slots, stream, (n, cache.latent_dim + cache.rope_dim), rt.float16)
+    st = load().mixattn_latent_export(cache._ref(), slots.data_ptr(), n, out.data_ptr(), _stream_handle(stream))
+    _check(st, "mixattn_latent_export")
+    return out
+
+
+def _dense(rt: _Runtime, here: int, x, shape, name: str) -> int:
+    if x.dtype is not rt.float16 or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name}: contiguous fp16 {list(shape)} expected, got {x.dtype} {tuple(x.shape)}")
+    if x.get_device() != here:
+        _wrong_device(x, name)
+    return x.data_ptr()
+
+
+class LatentPlan:
+    """Tiling of one batch of absorbed latent attention: rows of any kind (ROW_DECODE, ROW_CHUNK, ROW_TREE) over a
+    ``LatentCache``; reusable across layers and re-tileable, with ``Plan``'s rules for captured graphs."""
+
+    def __init__(self, cache: LatentCache, num_heads: int, row_kinds, seq_lens, q_offsets, max_pages: int,
+                 softmax_scale: float):
+        self._lib = load()
+        self.cache, self.num_heads = cache, int(num_heads)
+        self._handle = ctypes.c_void_p(0)
+        ws = ctypes.c_size_t(0)
+        st = self._lib.mixattn_latent_plan_create(
+            ctypes.byref(self._handle), cache._ref(), self.num_heads, float(softmax_scale), len(seq_lens),
+            _i32_array(row_kinds), _i32_array(seq_lens), _i32_array(q_offsets), int(max_pages), ctypes.byref(ws))
+        _check(st, "mixattn_latent_plan_create")
+        self._keep(ws, row_kinds, seq_lens, q_offsets, max_pages)
+
+    def _keep(self, ws, row_kinds, seq_lens, q_offsets, max_pages) -> None:
+        self.workspace_bytes = int(ws.value)
+        self._total_q = sum(int(s) - int(o) for s, o in zip(seq_lens, q_offsets))
+        self._tree_tokens = _tree_tokens(row_kinds, seq_lens, q_offsets)
+        self._table = (len(seq_lens), int(max_pages))
+
+    def update(self, row_kinds, seq_lens, q_offsets, max_pages: int) -> None:
+        ws = ctypes.c_size_t(0)
+        st = self._lib.mixattn_latent_plan_update(self._handle, len(seq_lens), _i32_array(row_kinds),
+                                                  _i32_array(seq_lens), _i32_array(q_offsets), int(max_pages),
+                                                  ctypes.byref(ws))
+        _check(st, "mixattn_latent_plan_update")
+        self._keep(ws, row_kinds, seq_lens, q_offsets, max_pages)
+
+    def run(self, q, page_table, o, workspace, stream=None, tree_mask=None) -> None:
+        """``q [total_q, heads, 576]``, ``o [total_q, heads, 512]`` (fp16), ``page_table [rows, max_pages]``
+        (int32); ``tree_mask`` as for ``Plan.run``."""
+        rt = _rt or _runtime()
+        here = _call_device(rt, q, "q")
+        c, h, t = self.cache, self.num_heads, self._total_q
+        qp = _dense(rt, here, q, (t, h, c.latent_dim + c.rope_dim), "q")
+        op = _dense(rt, here, o, (t, h, c.latent_dim), "o")
+        if page_table.dtype is not rt.int32 or page_table.shape != self._table or not page_table.is_contiguous():
+            raise ValueError(f"page_table: contiguous int32 {list(self._table)} expected, got {page_table.dtype} "
+                             f"{tuple(page_table.shape)}")
+        if page_table.get_device() != here:
+            _wrong_device(page_table, "page_table")
+        if tree_mask is not None:
+            _check_mask(tree_mask, self._tree_tokens)
+        st = self._lib.mixattn_latent_run(
+            self._handle, qp, page_table.data_ptr(), _ptr(tree_mask), tree_mask.shape[1] if tree_mask is not None else 0,
+            op, workspace.data_ptr(), workspace.nbytes, stream.cuda_stream if stream is not None else rt.raw_stream(here))
+        if st:
+            _check(st, "mixattn_latent_run")
+
+    def close(self) -> None:
+        if self._handle and self._handle.value:
+            self._lib.mixattn_latent_plan_destroy(self._handle)
+            self._handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class ExpandedPlan:
+    """Tiling of one batch of expanded latent attention: causal rows, whose keys 0 .. seq_len - 1 and queries
+    q_offset .. seq_len - 1 are packed in row order; reusable across layers and re-tileable."""
+
+    def __init__(self, num_heads: int, seq_lens, q_offsets, softmax_scale: float):
+        self._lib = load()
+        self.num_heads = int(num_heads)
+        self._handle = ctypes.c_void_p(0)
+        ws = ctypes.c_size_t(0)
+        st = self._lib.mixattn_expanded_plan_create(ctypes.byref(self._handle), self.num_heads, float(softmax_scale),
+                                                    len(seq_lens), _i32_array(seq_lens), _i32_array(q_offsets),
+                                                    ctypes.byref(ws))
+        _check(st, "mixattn_expanded_plan_create")
+        self._keep(ws, seq_lens, q_offsets)
+
+    def _keep(self, ws, seq_lens, q_offsets) -> None:
+        self.workspace_bytes = int(ws.value)
+        self._total_k = sum(int(s) for s in seq_lens)
+        self._total_q = self._total_k - sum(int(o) for o in q_offsets)
+
+    def update(self, seq_lens, q_offsets) -> None:
+        ws = ctypes.c_size_t(0)
+        st = self._lib.mixattn_expanded_plan_update(self._handle, len(seq_lens), _i32_array(seq_lens),
+                                                    _i32_array(q_offsets), ctypes.byref(ws))
+        _check(st, "mixattn_expanded_plan_update")
+        self._keep(ws, seq_lens, q_offsets)
+
+    def run(self, q, k, k_rope, v, o, workspace, stream=None) -> None:
+        """``q [total_q, heads, 192]`` (position part last), ``k`` and ``v [total_k, heads, 128]``, ``k_rope
+        [total_k, 64]``, all fp16 with free token and head strides; ``o [total_q, heads, 128]`` dense."""
+        rt = _rt or _runtime()
+        here = _call_device(rt, q, "q")
+        h, nq, nk = self.num_heads, self._total_q, self._total_k
+        qd = _strided_heads(rt, here, q, nq, "q", h, 192)
+        kd = _strided_heads(rt, here, k, nk, "k", h, 128)
+        vd = _strided_heads(rt, here, v, nk, "v", h, 128)
+        ks = _strided_rows(rt, here, k_rope, nk, "k_rope", 64)
+        op = _dense(rt, here, o, (nq, h, 128), "o")
+        st = self._lib.mixattn_expanded_run(
+            self._handle, ctypes.byref(qd), ctypes.byref(kd), k_rope.data_ptr(), ks, ctypes.byref(vd), op,
+            workspace.data_ptr(), workspace.nbytes, stream.cuda_stream if stream is not None else rt.raw_stream(here))
+        if st:
+            _check(st, "mixattn_expanded_run")
+
+    def close(self) -> None:
+        if self._handle and self._handle.value:
+            self._lib.mixattn_expanded_plan_destroy(self._handle)
             self._handle = ctypes.c_void_p(0)
 
     def __del__(self):

@@ -18,6 +18,7 @@
 
 #include "../../include/mixattn_sched.h"
 #include "internal.h"
+#include "plan_list.h"
 
 namespace mixattn {
 
@@ -43,6 +44,8 @@ unsigned int* error_word() {
   }
   return g_err_word[dev];
 }
+
+}  // namespace
 
 // Arms the host-mapped flag of the current device (once): a pinned, mapped
 // word whose device address is stored in the error block, so kernels that set
@@ -96,6 +99,8 @@ int pending_device_check() {
   volatile unsigned int* f = g_err_flag[dev];
   return (f && *f) ? MIXATTN_ERR_DEVICE_CHECK : MIXATTN_OK;
 }
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -379,6 +384,80 @@ int build_tiling(const mixattn_kv_cache& c, int hq, int n_rows, const int32_t* k
 
 }  // namespace
 
+// Copies n16 16-byte words of a plan's tile list from its mapped pinned buffer
+// into the workspace.
+static __global__ void upload_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, size_t n16) {
+  // an attention kernel launched to overlap this one may start setting up (it waits for
+  // this grid's end before it reads the list)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x)
+    dst[i] = src[i];
+}
+
+int PlanList::fill(const std::vector<uint8_t>& image) {
+  if (!copied_ && cudaEventCreateWithFlags(&copied_, cudaEventDisableTiming) != cudaSuccess) {
+    copied_ = nullptr;
+    return MIXATTN_ERR_CUDA;
+  }
+  // the previous run may still be copying from the pinned buffer
+  if (copy_recorded_) {
+    if (cudaEventSynchronize(copied_) != cudaSuccess) return MIXATTN_ERR_CUDA;
+    copy_recorded_ = false;
+  }
+  if (image.size() > cap_) {
+    if (buf_) cudaFreeHost(buf_);
+    buf_ = nullptr;
+    dev_ = nullptr;
+    cap_ = size_ = 0;
+    const size_t cap = std::max<size_t>(image.size(), 4096);
+    if (cudaHostAlloc(reinterpret_cast<void**>(&buf_), cap, cudaHostAllocMapped | cudaHostAllocPortable) !=
+        cudaSuccess) {
+      buf_ = nullptr;
+      return MIXATTN_ERR_CUDA;
+    }
+    void* dv = nullptr;
+    if (cudaHostGetDevicePointer(&dv, buf_, 0) != cudaSuccess || !dv) {
+      cudaFreeHost(buf_);
+      buf_ = nullptr;
+      return MIXATTN_ERR_CUDA;
+    }
+    dev_ = static_cast<const uint8_t*>(dv);
+    cap_ = cap;
+  }
+  memcpy(buf_, image.data(), image.size());
+  size_ = image.size();
+  return MIXATTN_OK;
+}
+
+// The tile list comes in through a small kernel reading the mapped pinned buffer
+// rather than a copy-engine transfer, which would queue behind any large
+// host-to-device copy the caller has in flight on another stream.
+int PlanList::upload(uint8_t* dst, size_t bytes, cudaStream_t s) {
+  if (!dev_ || bytes > size_) return MIXATTN_ERR_INVALID_ARG;  // (an update that failed left no list)
+  const size_t n16 = bytes / 16;
+  const int blocks = (int)std::min<size_t>((n16 + 255) / 256, 128);
+  upload_kernel<<<blocks, 256, 0, s>>>(reinterpret_cast<const uint4*>(dev_), reinterpret_cast<uint4*>(dst), n16);
+  if (cudaGetLastError() != cudaSuccess) return MIXATTN_ERR_CUDA;
+  // a captured run replays whenever its graph does, so no event can tell when the buffer
+  // is free: the plan then keeps its tile list (an event recorded into the graph would
+  // also fail every later wait for it)
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MIXATTN_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) {
+    captured_ = true;
+  } else {
+    if (cudaEventRecord(copied_, s) != cudaSuccess) return MIXATTN_ERR_CUDA;
+    copy_recorded_ = true;
+  }
+  return MIXATTN_OK;
+}
+
+PlanList::~PlanList() {
+  if (copy_recorded_ && copied_) cudaEventSynchronize(copied_);
+  if (copied_) cudaEventDestroy(copied_);
+  if (buf_) cudaFreeHost(buf_);
+}
+
 // Address of this device's error word, for launchers in other translation units.
 unsigned int* device_error_address() { return error_word(); }
 
@@ -391,18 +470,7 @@ struct mixattn_plan {
   int32_t hq = 0, group = 0, log2_group = 0, n_rows = 0, max_pages = 0;
   int32_t window = 0;  // sliding window of every run of the plan (0: full causal attention)
   Tiling tiling;
-  uint8_t* host_buf = nullptr;  // pinned, mapped copy of tiling.image
-  const uint8_t* host_dev = nullptr;  // the same buffer as the device sees it
-  size_t host_cap = 0;
-  cudaEvent_t copied = nullptr;
-  bool copy_recorded = false;
-  bool captured = false;        // some run was captured: replays read the pinned buffer at any time
-};
-
-struct mixattn_rope {
-  double freq[kMaxRotPairs] = {};
-  double mscale = 1.0;
-  RopeTable table{};
+  PlanList list;       // pinned, mapped copy of tiling.image
 };
 
 namespace {
@@ -428,36 +496,11 @@ bool check_rotate_overlap(const void* x, int64_t xs, const void* out, int64_t os
 
 int plan_fill(mixattn_plan* p, int32_t n_rows, const int32_t* kinds, const int32_t* seq, const int32_t* off,
               int32_t max_pages, size_t* ws_bytes) {
-  if (p->captured) return MIXATTN_ERR_UNSUPPORTED;
+  if (p->list.captured()) return MIXATTN_ERR_UNSUPPORTED;
   Tiling t;
   int st = build_tiling(p->cache, p->hq, n_rows, kinds, seq, off, max_pages, device_sm_count(), p->window, &t);
   if (st != MIXATTN_OK) return st;
-  // the previous run may still be copying from the pinned buffer
-  if (p->copy_recorded) {
-    if (cudaEventSynchronize(p->copied) != cudaSuccess) return MIXATTN_ERR_CUDA;
-    p->copy_recorded = false;
-  }
-  if (t.image.size() > p->host_cap) {
-    if (p->host_buf) cudaFreeHost(p->host_buf);
-    p->host_buf = nullptr;
-    p->host_dev = nullptr;
-    p->host_cap = 0;
-    size_t cap = std::max<size_t>(t.image.size(), 4096);
-    if (cudaHostAlloc(reinterpret_cast<void**>(&p->host_buf), cap, cudaHostAllocMapped | cudaHostAllocPortable) !=
-        cudaSuccess) {
-      p->host_buf = nullptr;
-      return MIXATTN_ERR_CUDA;
-    }
-    void* dv = nullptr;
-    if (cudaHostGetDevicePointer(&dv, p->host_buf, 0) != cudaSuccess || !dv) {
-      cudaFreeHost(p->host_buf);
-      p->host_buf = nullptr;
-      return MIXATTN_ERR_CUDA;
-    }
-    p->host_dev = static_cast<const uint8_t*>(dv);
-    p->host_cap = cap;
-  }
-  memcpy(p->host_buf, t.image.data(), t.image.size());
+  if ((st = p->list.fill(t.image)) != MIXATTN_OK) return st;
   p->n_rows = n_rows;
   p->max_pages = max_pages;
   p->tiling = std::move(t);
@@ -665,8 +708,6 @@ int mixattn_plan_create_window(mixattn_plan** plan_out, const mixattn_kv_cache* 
   p->log2_group = 0;
   while ((1 << p->log2_group) < p->group) ++p->log2_group;
   st = plan_fill(p, n_rows, row_kinds, seq_lens, q_offsets, max_pages, workspace_bytes);
-  if (st == MIXATTN_OK && cudaEventCreateWithFlags(&p->copied, cudaEventDisableTiming) != cudaSuccess)
-    st = MIXATTN_ERR_CUDA;
   if (st != MIXATTN_OK) {
     mixattn_plan_destroy(p);
     return st;
@@ -690,16 +731,6 @@ int mixattn_plan_info(const mixattn_plan* plan, int32_t* total_q, int32_t* n_chu
   return MIXATTN_OK;
 }
 
-// Copies n16 16-byte words of a plan's tile list from its mapped pinned buffer
-// into the workspace.
-static __global__ void upload_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, size_t n16) {
-  // an attention kernel launched to overlap this one may start setting up (it waits for
-  // this grid's end before it reads the list)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x)
-    dst[i] = src[i];
-}
-
 int mixattn_run(const mixattn_plan* plan, const void* q, const int32_t* page_table, void* o, void* workspace,
                 size_t workspace_bytes, mixattn_stream stream) {
   return mixattn_run_tree(plan, q, page_table, nullptr, 0, o, workspace, workspace_bytes, stream);
@@ -721,27 +752,7 @@ int mixattn_run_tree(const mixattn_plan* plan_c, const void* q, const int32_t* p
   if (!err) return MIXATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  // the tile list comes in through a small kernel reading the mapped pinned buffer
-  // rather than a copy-engine transfer, which would queue behind any large
-  // host-to-device copy the caller has in flight on another stream
-  {
-    const size_t n16 = (L.upload_end - L.rows) / 16;
-    const int blocks = (int)std::min<size_t>((n16 + 255) / 256, 128);
-    upload_kernel<<<blocks, 256, 0, s>>>(reinterpret_cast<const uint4*>(plan->host_dev),
-                                         reinterpret_cast<uint4*>(ws + L.rows), n16);
-    if (cudaGetLastError() != cudaSuccess) return MIXATTN_ERR_CUDA;
-  }
-  // a captured run replays whenever its graph does, so no event can tell when the buffer
-  // is free: the plan then keeps its tile list (an event recorded into the graph would
-  // also fail every later wait for it)
-  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MIXATTN_ERR_CUDA;
-  if (capture != cudaStreamCaptureStatusNone) {
-    plan->captured = true;
-  } else {
-    if (cudaEventRecord(plan->copied, s) != cudaSuccess) return MIXATTN_ERR_CUDA;
-    plan->copy_recorded = true;
-  }
+  if (int st = plan->list.upload(ws + L.rows, L.upload_end - L.rows, s)) return st;
 
   AttnParams p;
   const mixattn_kv_cache& c = plan->cache;
@@ -781,13 +792,7 @@ int mixattn_run_tree(const mixattn_plan* plan_c, const void* q, const int32_t* p
   return e == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
 }
 
-void mixattn_plan_destroy(mixattn_plan* plan) {
-  if (!plan) return;
-  if (plan->copy_recorded && plan->copied) cudaEventSynchronize(plan->copied);
-  if (plan->copied) cudaEventDestroy(plan->copied);
-  if (plan->host_buf) cudaFreeHost(plan->host_buf);
-  delete plan;
-}
+void mixattn_plan_destroy(mixattn_plan* plan) { delete plan; }
 
 int mixattn_workspace_bytes(const mixattn_kv_cache* cache, int32_t num_q_heads, int32_t n_rows,
                             const int32_t* row_kinds, const int32_t* seq_lens, const int32_t* q_offsets,

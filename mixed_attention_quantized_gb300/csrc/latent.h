@@ -1,0 +1,88 @@
+// latent.h -- structures shared by the host planners and the kernels of the latent-cache
+// operators (mixattn_latent.h).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/mixattn_latent.h"
+#include "internal.h"
+
+namespace mixattn {
+
+constexpr int kLatent = 512, kLatentRope = 64, kLatentRow = kLatent + kLatentRope;
+constexpr int kNopeDim = 128, kExpandedV = 128, kExpandedQ = kNopeDim + kLatentRope;
+
+// ---------------------------------------------------------------------------
+// Absorbed form
+// ---------------------------------------------------------------------------
+
+struct LatentRowInfo {
+  int32_t q_start, seq_len, q_offset;
+  int32_t tree_start;  // first mask row of a tree row, -1 of others
+};
+
+// Pages page0 .. + n_pages of a row for the tiles mt0 .. + team - 1 of its (query, head) rows,
+// one for each CTA of a team.  A tile whose keys lie in several items (n_parts > 1) leaves
+// partial results in slots: member m's part p in slot + m * n_parts + p.
+struct LatentItem {
+  int32_t row, mt0, page0, n_pages, part, n_parts, slot, pad;
+};
+
+// A tile whose parts are to be joined.
+struct LatentCut {
+  int32_t row, mt, slot, n_parts;
+};
+
+struct LatentParams {
+  const LatentRowInfo* rows;
+  const LatentItem* items;
+  const int32_t* team_first;  // [n_teams + 1]
+  const LatentCut* cuts;
+  const int32_t* page_table;
+  const uint32_t* tree_mask;
+  uint16_t* o;
+  float* part_o;    // [slots][tile rows][512], unnormalised
+  float2* part_ml;  // [slots][tile rows]: reference (log2 units) and sum
+  int32_t tree_words, max_pages, num_pages, heads, team, n_teams, n_cuts;
+  float scale_log2;
+};
+
+// tile_rows: 16, 32 or 64 (query, head) rows a CTA
+cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& q, const CUtensorMap& kv, const LatentParams& p,
+                                    unsigned int* err, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Expanded form
+// ---------------------------------------------------------------------------
+
+constexpr int kExpandedRows = 256;  // queries of a tile: two groups of 128
+
+// KV tiles (128 keys) kv0 .. kv1 - 1 of one head's queries q_start .. + count; a tile whose keys
+// lie in several items (n_parts > 1) leaves partial results in slots slot + part.
+struct ExpandedItem {
+  int32_t q_start, k_start;  // packed first query of the tile, packed first key of its row
+  int32_t head, count;
+  int32_t pos, seq_len;      // position of the first query; keys of the row
+  int32_t kv0, kv1, part, n_parts, slot, pad;
+};
+
+struct ExpandedCut {
+  int32_t q_start, head, count, slot, n_parts, pad;
+};
+
+struct ExpandedParams {
+  const ExpandedItem* items;
+  const int32_t* cta_first;  // [n_ctas + 1]
+  const ExpandedCut* cuts;
+  uint16_t* o;
+  float* part_o;    // [slots][256][128], unnormalised
+  float2* part_ml;  // [slots][256]
+  int32_t heads, n_ctas, n_cuts;
+  float scale_log2;
+};
+
+cudaError_t launch_expanded_attention(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& kr,
+                                      const CUtensorMap& v, const ExpandedParams& p, unsigned int* err, cudaStream_t s);
+
+}  // namespace mixattn

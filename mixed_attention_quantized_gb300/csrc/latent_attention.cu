@@ -1,0 +1,576 @@
+// latent_attention.cu -- absorbed latent attention: every (query, head) row of a token meets the
+// cached rows [c | r] of 512 + 64 fp16 elements, whose first 512 are the values too:
+//     S = q [c | r]^T,   P = 2^(scale S - m),   O = sum P c,   o = O / sum P.
+//
+// A CTA takes a tile of N (16, 32 or 64) rows and walks a range of the row's pages, 64 keys (two
+// pages) a step, each loaded once into shared memory by TMA and used from there by both products:
+//   S   [64 rows][64 keys]   = Q (A, rows of 576) x K^T (B): M = 64, rows past N unused
+//   O^T [512 elements][N]   += c^T (A, the same bytes read MN-major) x P^T (B): four blocks of 128
+// O^T rather than O because 64 rows of 512 fp32 would fill TMEM alone, and because N then follows
+// the number of rows: 16 heads cost a quarter of the operand reads that 64 do.
+//
+// Roles: softmax (warps 0-3), TMA (warp 4), MMA (one thread of warp 5).  A step's four 128-element
+// units of c and its r come through rings of slots with barriers of their own, so that a unit is
+// refilled as soon as its block of O^T is done.  The MMA thread issues QK(g+1) before PV(g).
+//
+// The last page of a sequence is loaded with its first row pushed to the box's end (a box that
+// starts above the page's first row reads zeros there): rows past the sequence's end, which may
+// hold anything, never reach shared memory.
+#include <mutex>
+
+#include "attention_kernel.cuh"
+#include "latent.h"
+#include "tma.cuh"
+
+namespace mixattn {
+
+namespace {
+
+constexpr int kSoftmaxWarps = 4;
+constexpr int kLatentThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kStepKeys = 64;  // keys of a step: two pages
+
+template <int N>
+struct LatentSmem {
+  static constexpr int kQSlab = N * 128;                 // 64 elements of N rows, swizzled
+  static constexpr int kQ = 0;                           // 9 slabs
+  static constexpr int kP = kQ + 9 * kQSlab;             // [N][64 keys]
+  static constexpr int kRope = (kP + N * 128 + 1023) / 1024 * 1024;  // 2 slots of [64 keys][64]
+  static constexpr int kUnit0 = kRope + 2 * 8192;        // slots of [2][64 keys][64]
+  static constexpr int kUnits = N == 64 ? 8 : (N == 32 ? 10 : 11);
+  static constexpr int kStat = kUnit0 + kUnits * 16384;  // alpha[64], l[64]
+  static constexpr int kBar = kStat + 512;
+  static constexpr int kTotal = kBar + 512 + 1024;       // + slack for 1024-byte alignment
+  static_assert(kTotal <= 227 * 1024, "the tile does not fit in shared memory");
+  // the A operand of S reads 64 rows a slab: past N, whatever follows in shared memory
+  static_assert(kQ + 8 * kQSlab + 8192 <= kTotal, "rows past N");
+};
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
+
+// 16 lanes x 64 columns of 32-bit TMEM: register 4 j + 2 h + e holds row lane / 4 + 8 h, column
+// 8 j + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// What one tile of an item covers.
+struct LatentTile {
+  int f0, rows;           // first (query, head) row of the row's, rows here
+  int n_pages;            // pages with a key that some query of the tile sees
+  bool there;
+};
+
+__device__ __forceinline__ LatentTile tile_of(const LatentParams& p, const LatentItem& it, const LatentRowInfo& ri,
+                                              int member, int N) {
+  LatentTile t;
+  const int total = (ri.seq_len - ri.q_offset) * p.heads;
+  t.f0 = (it.mt0 + member) * N;
+  t.rows = min(N, total - t.f0);
+  t.there = t.rows > 0;
+  const int last = ri.tree_start >= 0 ? ri.seq_len - 1 : ri.q_offset + (t.f0 + max(t.rows, 1) - 1) / p.heads;
+  t.n_pages = max(0, min(it.n_pages, last / kPage + 1 - it.page0));
+  return t;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kLatentThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+                  const LatentParams p, unsigned int* err) {
+  using L = LatentSmem<N>;
+  constexpr int NU = L::kUnits;
+  constexpr uint32_t kOCol = 0, kSCol = 4 * N;  // O^T blocks, then two S buffers of 64 columns
+  constexpr uint32_t kTmemCols = N == 64 ? 512 : 256;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* unit_full = bars;              // [NU] by TMA
+  uint64_t* unit_empty = unit_full + NU;   // [NU] by a commit: the unit's block of O^T done
+  uint64_t* rope_full = unit_empty + NU;   // [2]
+  uint64_t* rope_empty = rope_full + 2;    // [2]
+  uint64_t* q_full = rope_empty + 2;       // the item's queries
+  uint64_t* q_empty = q_full + 1;          // the item's last S done
+  uint64_t* s_full = q_empty + 1;          // [2] S(g) in buffer g % 2
+  uint64_t* p_full = s_full + 2;           // by the softmax warps: P(g) written, O^T rescaled
+  uint64_t* pv_done = p_full + 1;          // PV(g) done
+  uint64_t* o_free = pv_done + 1;          // by the softmax warps: the item's O^T read
+  uint64_t* fin = o_free + 1;
+  constexpr int kNumBars = 2 * NU + 12;
+  static_assert(8 * kNumBars + 8 <= 512, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
+    mbar_init(p_full, kSoftmaxWarps);
+    mbar_init(o_free, kSoftmaxWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&q_map);
+    tma_prefetch_map(&kv_map);
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the item list is written by the grid before
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int team = blockIdx.x / p.team, member = blockIdx.x - team * p.team;
+  const int it0 = p.team_first[team], it1 = p.team_first[team + 1];
+
+  if (warp == kSoftmaxWarps) {
+    // ======================= TMA =======================
+    int slot = 0, round = 0, g = 0, n_item = 0, n_rope = 0;
+    bool ok = true;
+    for (int i = it0; ok && i < it1; ++i) {
+      const LatentItem it = p.items[i];
+      const LatentRowInfo ri = p.rows[it.row];
+      const LatentTile t = tile_of(p, it, ri, member, N);
+      if (!t.there || t.n_pages == 0) continue;
+      if (n_item > 0) ok = mbar_wait(q_empty, (uint32_t)((n_item - 1) & 1), err);
+      ok = __all_sync(0xFFFFFFFFu, ok) && !*abort_flag;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      ++n_item;
+      if (lane == 0) {
+        const int y = ri.q_start * p.heads + t.f0;
+        mbar_arrive_expect_tx(q_full, 9 * L::kQSlab);
+        for (int s = 0; s < 9; ++s)
+          tma_load_2d(smem_u32(smem + L::kQ + s * L::kQSlab), &q_map, 64 * s, y, smem_u32(q_full));
+      }
+      const int32_t* pt_row = p.page_table + (int64_t)it.row * p.max_pages + it.page0;
+      const int last_page = (ri.seq_len - 1) / kPage, last_shift = kPage * (last_page + 1) - ri.seq_len;
+      const int n_steps = (t.n_pages + 1) / 2;
+      int pid = 0;
+      for (int s = 0; ok && s < n_steps; ++s, ++g) {
+        if ((s & 15) == 0) pid = 2 * s + lane < t.n_pages ? pt_row[2 * s + lane] : -1;
+        // a page's id and the box's first row in it: a page that is not there reads as zeros
+        int id[2], y[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int pg = 2 * s + h;
+          id[h] = __shfl_sync(0xFFFFFFFFu, pid, pg & 31);
+          y[h] = it.page0 + pg == last_page ? -last_shift : 0;
+          if (id[h] < 0 || id[h] >= p.num_pages) {
+            if (pg < t.n_pages && lane == 0) set_device_error(err, MIXATTN_DEVERR_PAGE_ID);
+            id[h] = 0;
+            y[h] = kPage;
+          }
+        }
+        if (g >= 2) ok = mbar_wait(&rope_empty[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        ++n_rope;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&rope_full[g & 1]), dst = smem_u32(smem + L::kRope + (g & 1) * 8192);
+          mbar_arrive_expect_tx(&rope_full[g & 1], 8192);
+          tma_load_3d(dst, &kv_map, kLatent, y[0], id[0], bar);
+          tma_load_3d(dst + 4096, &kv_map, kLatent, y[1], id[1], bar);
+        }
+        for (int b = 0; b < 4; ++b) {
+          if (round > 0) ok = mbar_wait(&unit_empty[slot], (uint32_t)((round - 1) & 1), err);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&unit_full[slot]), dst = smem_u32(smem + L::kUnit0 + slot * 16384);
+            mbar_arrive_expect_tx(&unit_full[slot], 16384);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tma_load_3d(dst + c * 8192, &kv_map, 128 * b + 64 * c, y[0], id[0], bar);
+              tma_load_3d(dst + c * 8192 + 4096, &kv_map, 128 * b + 64 * c, y[1], id[1], bar);
+            }
+          }
+          if (++slot == NU) {
+            slot = 0;
+            ++round;
+          }
+        }
+        if (*abort_flag) ok = false;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+    }
+    if (lane == 0) {
+      if (!ok) *abort_flag = 1;
+      // nothing asked for may still be on its way when the CTA ends (which, but for an error, it is not)
+      for (int k = 0; k < NU; ++k) {
+        const int rd = k < slot ? round : round - 1;
+        if (rd >= 0) mbar_wait(&unit_full[k], (uint32_t)(rd & 1), err);
+      }
+      for (int k = max(0, n_rope - 2); k < n_rope; ++k) mbar_wait(&rope_full[k & 1], (uint32_t)((k >> 1) & 1), err);
+      if (n_item > 0) mbar_wait(q_full, (uint32_t)((n_item - 1) & 1), err);
+    }
+    __syncwarp();
+  } else if (warp == kSoftmaxWarps + 1) {
+    // ======================= MMA (one thread) =======================
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_f16_f32(64, kStepKeys, false, false);
+      constexpr uint32_t kIdescO = idesc_f16_f32(128, N, true, false);
+      const uint64_t dQ = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
+      const uint64_t dP = sw128_desc(smem_u32(smem + L::kP), 16, 1024);
+      const uint64_t dR = sw128_desc(smem_u32(smem + L::kRope), 16, 1024);
+      const uint64_t dK = sw128_desc(smem_u32(smem + L::kUnit0), 16, 1024);
+      const uint64_t dV = sw128_desc(smem_u32(smem + L::kUnit0), 8192, 1024);  // slabs of 64 elements 8 KB apart
+      bool ok = true;
+      int g0 = 0, n_item = 0;
+      int ks = 0, kr = 0, vs = 0;  // slot and round of QK's next unit, slot of PV's
+      for (int i = it0; ok && i < it1; ++i) {
+        const LatentItem it = p.items[i];
+        const LatentRowInfo ri = p.rows[it.row];
+        const LatentTile t = tile_of(p, it, ri, member, N);
+        if (!t.there || t.n_pages == 0) continue;
+        const int n_steps = (t.n_pages + 1) / 2;
+        ok = mbar_wait(q_full, (uint32_t)(n_item & 1), err);
+        if (!ok) break;
+        for (int s = 0; s <= n_steps; ++s) {
+          if (s < n_steps) {
+            const int g = g0 + s;
+            const uint32_t s_tm = tmem + kSCol + 64 * (g & 1);
+            ok = mbar_wait(&rope_full[g & 1], (uint32_t)((g >> 1) & 1), err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_ss(s_tm, dQ + ((8 * L::kQSlab + 32 * k) >> 4), dR + (((g & 1) * 8192 + 32 * k) >> 4), kIdescS,
+                        k > 0 ? 1u : 0u);
+            tc_commit(&rope_empty[g & 1]);
+            for (int b = 0; b < 4; ++b) {
+              ok = mbar_wait(&unit_full[ks], (uint32_t)(kr & 1), err);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc_mma_ss(s_tm, dQ + (((2 * b + (k >> 2)) * L::kQSlab + 32 * (k & 3)) >> 4),
+                          dK + ((ks * 16384 + (k >> 2) * 8192 + 32 * (k & 3)) >> 4), kIdescS, 1u);
+              if (++ks == NU) {
+                ks = 0;
+                ++kr;
+              }
+            }
+            if (!ok) break;
+            tc_commit(&s_full[g & 1]);
+            if (s == n_steps - 1) tc_commit(q_empty);
+          }
+          if (s > 0) {
+            const int g = g0 + s - 1;
+            ok = mbar_wait(p_full, (uint32_t)(g & 1), err);
+            if (ok && s == 1 && n_item > 0) ok = mbar_wait(o_free, (uint32_t)((n_item - 1) & 1), err);
+            if (!ok) break;
+            tc_fence_after();
+            for (int b = 0; b < 4; ++b) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_ss(tmem + kOCol + N * b, dV + ((vs * 16384 + 2048 * k) >> 4), dP + ((32 * k) >> 4), kIdescO,
+                          s > 1 || k > 0 ? 1u : 0u);
+              tc_commit(&unit_empty[vs]);
+              if (++vs == NU) vs = 0;
+            }
+            tc_commit(pv_done);
+          }
+          if (*abort_flag) {
+            ok = false;
+            break;
+          }
+        }
+        g0 += n_steps;
+        ++n_item;
+      }
+      if (!ok) *abort_flag = 1;
+      // nothing this thread started may still run when TMEM is released
+      tc_commit(fin);
+      mbar_wait(fin, 0u, err);
+    }
+    __syncwarp();
+  } else {
+    // ======================= softmax =======================
+    constexpr int kGroup = 32 * kSoftmaxWarps;
+    constexpr float kTop = 15.f, kSet = 7.f;  // as page_decode_tile: P up to 2^15, set at 2^7
+    constexpr int kBarGroup = 1;
+    const int r = lane >> 2, c = lane & 3;
+    const bool rows_here = 16 * warp < N;  // the warp's 16 rows of S; every warp has 32 elements of each O^T block
+    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+    float* alpha_s = reinterpret_cast<float*>(smem + L::kStat);
+    float* l_s = alpha_s + 64;
+    const int rr0 = 16 * warp + r;  // rows rr0 and rr0 + 8
+    bool ok = true;
+    int g = 0;
+    for (int i = it0; i < it1; ++i) {
+      const LatentItem it = p.items[i];
+      const LatentRowInfo ri = p.rows[it.row];
+      const LatentTile t = tile_of(p, it, ri, member, N);
+      if (!t.there) continue;
+      const int64_t part = (int64_t)it.slot + (int64_t)member * it.n_parts + it.part;
+      if (t.n_pages == 0) {  // (a part past the tile's last key)
+        if (tid < N) p.part_ml[part * N + tid] = make_float2(-CUDART_INF_F, 0.f);
+        continue;
+      }
+      const int n_steps = (t.n_pages + 1) / 2;
+      const bool tree = ri.tree_start >= 0;
+      const int qi0 = (t.f0 + min(rr0, t.rows - 1)) / p.heads, qi1 = (t.f0 + min(rr0 + 8, t.rows - 1)) / p.heads;
+      const int pos0 = ri.q_offset + qi0, pos1 = ri.q_offset + qi1;
+      const int mask_hi = tree ? ri.q_offset : ri.q_offset + t.f0 / p.heads + 1;  // keys below: seen by every row
+      const int n_nodes = ri.seq_len - ri.q_offset;
+      const uint32_t* tm0 = tree ? p.tree_mask + (int64_t)(ri.tree_start + qi0) * p.tree_words : nullptr;
+      const uint32_t* tm1 = tree ? p.tree_mask + (int64_t)(ri.tree_start + qi1) * p.tree_words : nullptr;
+      const int32_t* pt_row = p.page_table + (int64_t)it.row * p.max_pages + it.page0;
+      const int last_page = (ri.seq_len - 1) / kPage, last_shift = kPage * (last_page + 1) - ri.seq_len;
+      float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+      uint32_t good = 0;
+      bool stop = false;
+      for (int s = 0; s < n_steps; ++s, ++g) {
+        if ((s & 15) == 0) {
+          const int pid = 2 * s + lane < t.n_pages ? pt_row[2 * s + lane] : -1;
+          good = __ballot_sync(0xFFFFFFFFu, pid >= 0 && pid < p.num_pages);
+        }
+        const bool ok_a = (good >> ((2 * s) & 31)) & 1u, ok_b = (good >> ((2 * s + 1) & 31)) & 1u;
+        float x[32];
+        float al0 = 1.f, al1 = 1.f;
+        bool need = false;
+        if (rows_here) {
+          ok = mbar_wait(&s_full[g & 1], (uint32_t)((g >> 1) & 1), err) && ok;
+          tc_fence_after();
+          uint32_t v[32];
+          tmem_ld_16x64(tmem + lane_base + kSCol + 64 * (g & 1), v);
+          tmem_wait_ld();
+          tc_fence_before();
+          const int key0 = kPage * (it.page0 + 2 * s);
+          if (!ok_a || !ok_b || key0 + kStepKeys > mask_hi) {
+            uint32_t vis[2][2];  // [row][page]
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int pg = it.page0 + 2 * s + h, sh = pg == last_page ? last_shift : 0, k0 = kPage * pg - sh;
+              const uint32_t in = (h ? ok_b : ok_a) ? ~low_bits(sh) : 0u;
+              if (tree) {
+                vis[0][h] = tree_bits(tm0, p.tree_words, n_nodes, k0 - ri.q_offset) & in;
+                vis[1][h] = tree_bits(tm1, p.tree_words, n_nodes, k0 - ri.q_offset) & in;
+              } else {
+                vis[0][h] = low_bits(pos0 + 1 - k0) & in;
+                vis[1][h] = low_bits(pos1 + 1 - k0) & in;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int j = e >> 2, col = 8 * (j & 3) + 2 * c + (e & 1);
+              if (!((vis[(e >> 1) & 1][j >> 2] >> col) & 1u)) v[e] = __float_as_uint(-CUDART_INF_F);
+            }
+          }
+          float t0 = -CUDART_INF_F, t1 = -CUDART_INF_F;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            t0 = fmax3(t0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            t1 = fmax3(t1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+          }
+          t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 1));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 1));
+          t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 2)) * p.scale_log2;
+          t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 2)) * p.scale_log2;
+          const bool g0 = m0 == -CUDART_INF_F ? t0 > m0 : t0 > m0 + kTop;
+          const bool g1 = m1 == -CUDART_INF_F ? t1 > m1 : t1 > m1 + kTop;
+          if (g0) {
+            al0 = ex2(m0 - (t0 - kSet));
+            m0 = t0 - kSet;
+            l0 *= al0;
+          }
+          if (g1) {
+            al1 = ex2(m1 - (t1 - kSet));
+            m1 = t1 - kSet;
+            l1 *= al1;
+          }
+          need = g0 || g1;
+          const float n0 = m0 == -CUDART_INF_F ? 0.f : -m0, n1 = m1 == -CUDART_INF_F ? 0.f : -m1;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[e] = ex2(fmaf(__uint_as_float(v[e]), p.scale_log2, (e & 2) ? n1 : n0));
+          float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            a0 += x[e] + x[e + 1];
+            a1 += x[e + 2] + x[e + 3];
+          }
+          l0 += a0;
+          l1 += a1;
+        }
+        if (bar_any(kBarGroup, kGroup, need) && s > 0) {  // some row's reference moved: O^T takes the factor
+          if (rows_here && c == 0) {
+            alpha_s[rr0] = al0;
+            alpha_s[rr0 + 8] = al1;
+          }
+          bar_any(kBarGroup, kGroup, false);
+          ok = mbar_wait(pv_done, (uint32_t)((g - 1) & 1), err) && ok;
+          tc_fence_after();
+#pragma unroll 1
+          for (int b = 0; b < 4 * N / 16; ++b) {
+            uint32_t o[16];
+            tmem_ld16(tmem + lane_base + kOCol + 16 * b, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_s[(16 * b + e) % N]);
+            tmem_st16(tmem + lane_base + kOCol + 16 * b, o);
+          }
+          tmem_wait_st();
+        } else if (g > 0) {
+          ok = mbar_wait(pv_done, (uint32_t)((g - 1) & 1), err) && ok;  // P(g - 1) has been read
+        }
+        if (rows_here) {
+          uint8_t* p0 = smem + L::kP + rr0 * 128 + 4 * c;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            *reinterpret_cast<uint32_t*>(p0 + ((j ^ (rr0 & 7)) << 4)) = pack_f16x2(x[4 * j], x[4 * j + 1]);
+            *reinterpret_cast<uint32_t*>(p0 + 1024 + ((j ^ (rr0 & 7)) << 4)) = pack_f16x2(x[4 * j + 2], x[4 * j + 3]);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        if (bar_any(kBarGroup, kGroup, !ok || *abort_flag)) {  // one decision for the group
+          stop = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      if (stop) {
+        *abort_flag = 1;
+        break;
+      }
+      // ---- the item's output ----
+      ok = mbar_wait(pv_done, (uint32_t)((g - 1) & 1), err);
+      tc_fence_after();
+      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
+      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
+      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2);
+      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
+      if (rows_here && c == 0) {
+        if (it.n_parts == 1) {
+          l_s[rr0] = l0 > 0.f ? 1.f / l0 : 0.f;
+          l_s[rr0 + 8] = l1 > 0.f ? 1.f / l1 : 0.f;
+        } else {
+          p.part_ml[part * N + rr0] = make_float2(m0, l0);
+          p.part_ml[part * N + rr0 + 8] = make_float2(m1, l1);
+        }
+      }
+      if (bar_any(kBarGroup, kGroup, !ok)) {
+        *abort_flag = 1;
+        break;
+      }
+      const int64_t row0 = (int64_t)ri.q_start * p.heads + t.f0;
+#pragma unroll 1
+      for (int b = 0; b < 4 * N / 16; ++b) {
+        const int d = 128 * (16 * b / N) + 32 * warp + lane, col0 = (16 * b) % N;
+        uint32_t o[16];
+        tmem_ld16(tmem + lane_base + kOCol + 16 * b, o);
+        tmem_wait_ld();
+        if (it.n_parts == 1) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (col0 + e < t.rows) p.o[(row0 + col0 + e) * kLatent + d] = f16_out(__uint_as_float(o[e]) * l_s[col0 + e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (col0 + e < t.rows) p.part_o[(part * N + col0 + e) * kLatent + d] = __uint_as_float(o[e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      bar_any(kBarGroup, kGroup, false);  // (l_s is written again by the next item)
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of cut tiles: one CTA a (query, head) row, four elements a thread.
+__global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, int tile_rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const LatentCut cut = p.cuts[blockIdx.x / tile_rows];
+  const int rr = blockIdx.x % tile_rows;
+  const LatentRowInfo ri = p.rows[cut.row];
+  const int f = cut.mt * tile_rows + rr;
+  if (f >= (ri.seq_len - ri.q_offset) * p.heads) return;
+  const float2* ml = p.part_ml + (int64_t)cut.slot * tile_rows + rr;
+  float m = -CUDART_INF_F;
+  for (int q = 0; q < cut.n_parts; ++q) m = fmaxf(m, ml[(int64_t)q * tile_rows].x);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* src = p.part_o + ((int64_t)cut.slot * tile_rows + rr) * kLatent + 4 * threadIdx.x;
+#pragma unroll 4
+  for (int q = 0; q < cut.n_parts; ++q) {
+    const float2 x = ml[(int64_t)q * tile_rows];
+    if (x.x == -CUDART_INF_F) continue;  // (no key of the row in this part: any value may stand there)
+    const float w = ex2(x.x - m);
+    const float4 y = *reinterpret_cast<const float4*>(src + (int64_t)q * tile_rows * kLatent);
+    l += w * x.y;
+    o.x += w * y.x;
+    o.y += w * y.y;
+    o.z += w * y.z;
+    o.w += w * y.w;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(p.o + ((int64_t)ri.q_start * p.heads + f) * kLatent + 4 * threadIdx.x) =
+      make_uint2(pack_f16x2_out(o.x * inv, o.y * inv), pack_f16x2_out(o.z * inv, o.w * inv));
+}
+
+template <int N>
+cudaError_t launch_n(const CUtensorMap& q, const CUtensorMap& kv, const LatentParams& p, unsigned int* err,
+                     cudaStream_t s) {
+  {
+    static std::mutex mu;
+    static bool configured[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!configured[dev]) {
+      e = cudaFuncSetAttribute(latent_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, LatentSmem<N>::kTotal);
+      if (e != cudaSuccess) return e;
+      configured[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(p.n_teams * p.team);
+  cfg.blockDim = dim3(kLatentThreads);
+  cfg.dynamicSmemBytes = LatentSmem<N>::kTotal;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, q, kv, p, err);
+  if (e != cudaSuccess || p.n_cuts == 0) return e;
+  cfg.gridDim = dim3(p.n_cuts * N);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, N);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& q, const CUtensorMap& kv, const LatentParams& p,
+                                    unsigned int* err, cudaStream_t s) {
+  if (tile_rows == 16) return launch_n<16>(q, kv, p, err, s);
+  if (tile_rows == 32) return launch_n<32>(q, kv, p, err, s);
+  return launch_n<64>(q, kv, p, err, s);
+}
+
+}  // namespace mixattn
