@@ -284,13 +284,13 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
   for (int r = 0; r < n_rows; ++r)
     for (int64_t mt0 = 0; mt0 < tiles_of(r); mt0 += T.team) total += (double)pages_of(r, mt0 + T.team) + kItemPages;
   const double share = (total + (double)kItemPages * T.n_teams) / T.n_teams;
-  double used = 0.0;  // of the current team
+  double used = 0.0;  // of all teams so far: what one took too much or too little, the next ones even out
   int team = 0;
   auto next_team = [&] {
     team_first.push_back((int32_t)items.size());
     ++team;
-    used = 0.0;
   };
+  auto empty = [&] { return team_first.back() == (int32_t)items.size(); };
   for (int r = 0; r < n_rows; ++r) {
     const int64_t n_tiles = tiles_of(r);
     for (int64_t mt0 = 0; mt0 < n_tiles; mt0 += T.team) {
@@ -302,8 +302,8 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
         const bool last_team = team == T.n_teams - 1;
         int64_t take = left;
         if (!last_team) {
-          const int64_t room = (int64_t)(share - used - kItemPages + 0.5);
-          if (room < kMinItemPages && used > 0.0) {
+          const int64_t room = (int64_t)(share * (team + 1) - used - kItemPages + 0.5);
+          if (room < kMinItemPages && !empty()) {
             next_team();
             continue;
           }
@@ -314,7 +314,7 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
         items.push_back(LatentItem{r, (int32_t)mt0, (int32_t)at, (int32_t)take, 0, 1, 0, 0});
         at += take;
         used += (double)(take + kItemPages);
-        if (!last_team && used >= share - 1.0) next_team();
+        if (!last_team && used >= share * (team + 1) - 1.0) next_team();
       }
       const int32_t parts = (int32_t)(items.size() - first);
       if (parts > 1) {
@@ -389,13 +389,13 @@ int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32
   }
   if (n_tiles > 1 << 28) return MIXATTN_ERR_INVALID_ARG;
   const double share = total / n_sm + kExpandedItemCost;
-  double used = 0.0;
+  double used = 0.0;  // of all so far: what one took too much or too little, the next ones even out
   int cta = 0;
   auto next_cta = [&] {
     cta_first.push_back((int32_t)items.size());
     ++cta;
-    used = 0.0;
   };
+  auto empty = [&] { return cta_first.back() == (int32_t)items.size(); };
   int64_t slots = 0, q0 = 0, k0 = 0;
   for (int r = 0; r < n_rows; ++r) {
     const int64_t s = seq[r], o = off[r];
@@ -409,8 +409,8 @@ int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32
           const bool last = cta == n_sm - 1;
           int64_t take = n - at;
           if (!last) {
-            const int64_t room = (int64_t)((share - used - kExpandedItemCost) / w + 0.5);
-            if (room < std::min<int64_t>(kMinItemTiles, take) && used > 0.0) {
+            const int64_t room = (int64_t)((share * (cta + 1) - used - kExpandedItemCost) / w + 0.5);
+            if (room < std::min<int64_t>(kMinItemTiles, take) && !empty()) {
               next_cta();
               continue;
             }
@@ -421,7 +421,7 @@ int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32
                                        (int32_t)at, (int32_t)(at + take), 0, 1, 0, 0});
           at += take;
           used += (double)(take * w + kExpandedItemCost);
-          if (!last && used >= share - 1.0) next_cta();
+          if (!last && used >= share * (cta + 1) - 1.0) next_cta();
         }
         const int32_t parts = (int32_t)(items.size() - first);
         if (parts > 1) {
@@ -465,7 +465,6 @@ struct mixattn_latent_plan {
   mixattn_latent_cache cache;
   int32_t heads = 0, max_pages = 0;
   double scale = 0.0;
-  CUtensorMap kv_map;
   LatentTiling tiling;
   PlanList list;
 };
@@ -553,12 +552,6 @@ int mixattn_latent_plan_create(mixattn_latent_plan** plan_out, const mixattn_lat
   p->heads = num_heads;
   p->scale = softmax_scale;
   st = mixattn_latent_plan_update(p, n_rows, row_kinds, seq_lens, q_offsets, max_pages, workspace_bytes);
-  if (st == MIXATTN_OK) {
-    const uint64_t dims[3] = {kLatentRow, kPage, (uint64_t)cache->num_pages};
-    const int64_t strides[2] = {kLatentRow, kLatentRow * kPage};
-    const uint32_t box[3] = {64, kPage, 1};
-    if (!make_map(&p->kv_map, cache->data, 3, dims, strides, box)) st = MIXATTN_ERR_CUDA;
-  }
   if (st != MIXATTN_OK) {
     delete p;
     return st;
@@ -613,6 +606,7 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.items = reinterpret_cast<const LatentItem*>(ws + T.items);
   p.team_first = reinterpret_cast<const int32_t*>(ws + T.team_first);
   p.cuts = reinterpret_cast<const LatentCut*>(ws + T.cuts);
+  p.data = static_cast<const uint16_t*>(plan->cache.data);
   p.page_table = page_table;
   p.tree_mask = tree_mask;
   p.o = static_cast<uint16_t*>(o);
@@ -626,7 +620,7 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.n_teams = T.n_teams;
   p.n_cuts = T.n_cuts;
   p.scale_log2 = (float)(plan->scale * kLog2e);
-  return launch_latent_attention(T.tile_rows, q_map, plan->kv_map, p, err, s) == cudaSuccess ? MIXATTN_OK
+  return launch_latent_attention(T.tile_rows, q_map, p, err, s) == cudaSuccess ? MIXATTN_OK
                                                                                             : MIXATTN_ERR_CUDA;
 }
 

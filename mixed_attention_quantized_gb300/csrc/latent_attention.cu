@@ -3,23 +3,23 @@
 //     S = q [c | r]^T,   P = 2^(scale S - m),   O = sum P c,   o = O / sum P.
 //
 // A CTA takes a tile of N (16, 32 or 64) rows and walks a range of the row's pages, 64 keys (two
-// pages) a step, each loaded once into shared memory by TMA and used from there by both products:
+// pages) a step, each loaded once into shared memory and used from there by both products:
 //   S   [64 rows][64 keys]   = Q (A, rows of 576) x K^T (B): M = 64, rows past N unused
 //   O^T [512 elements][N]   += c^T (A, the same bytes read MN-major) x P^T (B): four blocks of 128
 // O^T rather than O because 64 rows of 512 fp32 would fill TMEM alone, and because N then follows
 // the number of rows: 16 heads cost a quarter of the operand reads that 64 do.
 //
-// Roles: softmax (warps 0-3), TMA (warp 4), MMA (one thread of warp 5).  A step's four 128-element
-// units of c and its r come through rings of slots with barriers of their own, so that a unit is
-// refilled as soon as its block of O^T is done.  The MMA thread issues QK(g+1) before PV(g).
+// Roles: softmax (warps 0-3), loads (warps 4-7), MMA (the elected lane of warp 8). A step's four
+// 128-element units of c and its r come through rings of slots with barriers of their own, so that a
+// unit is refilled as soon as its block of O^T is done.  The MMA warp issues S(g+1) before PV(g), if its keys are there.
 //
-// The last page of a sequence is loaded with its first row pushed to the box's end (a box that
-// starts above the page's first row reads zeros there): rows past the sequence's end, which may
-// hold anything, never reach shared memory.
+// The loads are 16-byte cp.async by four warps, swizzled by address, and not TMA boxes: a box of 128-byte
+// rows moves 49 bytes a ns and SM at most (7.4 TB/s over all, measured with 192 KB in flight an SM, from
+// HBM and from L2 alike), these 130 from L2.
 #include <mutex>
 
-#include "attention_kernel.cuh"
 #include "latent.h"
+#include "page_attention.cuh"
 #include "tma.cuh"
 
 namespace mixattn {
@@ -27,7 +27,9 @@ namespace mixattn {
 namespace {
 
 constexpr int kSoftmaxWarps = 4;
-constexpr int kLatentThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kLoadWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kLatentThreads = 32 * (kMmaWarp + 1);
 constexpr int kStepKeys = 64;  // keys of a step: two pages
 
 template <int N>
@@ -63,6 +65,18 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
       : "r"(taddr));
 }
 
+// A whole warp waits, each lane that has a need for a barrier of its own: a poll takes as long for
+// one barrier as for several (~150 cycles beside the MMAs).
+__device__ __forceinline__ bool warp_wait_each(bool need, uint64_t* bar, uint32_t parity, unsigned int* err) {
+  const uint32_t at = smem_u32(bar);
+  for (uint32_t i = 0; i < (1u << 21); ++i) {
+    const bool done = !need || mbar_try_wait_s(at, parity);
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+  }
+  if (need) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
+  return false;
+}
+
 // What one tile of an item covers.
 struct LatentTile {
   int f0, rows;           // first (query, head) row of the row's, rows here
@@ -84,8 +98,7 @@ __device__ __forceinline__ LatentTile tile_of(const LatentParams& p, const Laten
 
 template <int N>
 __global__ void __launch_bounds__(kLatentThreads, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                  const LatentParams p, unsigned int* err) {
+    latent_kernel(const __grid_constant__ CUtensorMap q_map, const LatentParams p, unsigned int* err) {
   using L = LatentSmem<N>;
   constexpr int NU = L::kUnits;
   constexpr uint32_t kOCol = 0, kSCol = 4 * N;  // O^T blocks, then two S buffers of 64 columns
@@ -93,9 +106,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* unit_full = bars;              // [NU] by TMA
+  uint64_t* unit_full = bars;              // [NU] by the copies of a warp's lanes
   uint64_t* unit_empty = unit_full + NU;   // [NU] by a commit: the unit's block of O^T done
-  uint64_t* rope_full = unit_empty + NU;   // [2]
+  uint64_t* rope_full = unit_empty + NU;   // [2] by the copies of all load warps' lanes
   uint64_t* rope_empty = rope_full + 2;    // [2]
   uint64_t* q_full = rope_empty + 2;       // the item's queries
   uint64_t* q_empty = q_full + 1;          // the item's last S done
@@ -112,12 +125,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < NU; ++i) mbar_init(unit_full + i, 32);
+    for (int i = 0; i < 2; ++i) mbar_init(rope_full + i, 32 * kLoadWarps);
     mbar_init(p_full, kSoftmaxWarps);
     mbar_init(o_free, kSoftmaxWarps);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&q_map);
-    tma_prefetch_map(&kv_map);
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, kTmemCols);
@@ -133,164 +147,204 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   const int team = blockIdx.x / p.team, member = blockIdx.x - team * p.team;
   const int it0 = p.team_first[team], it1 = p.team_first[team + 1];
 
-  if (warp == kSoftmaxWarps) {
-    // ======================= TMA =======================
-    int slot = 0, round = 0, g = 0, n_item = 0, n_rope = 0;
+  if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
+    // ======================= load (warp w: unit w of every step) =======================
+    const int w = warp - kSoftmaxWarps;
+    int slot = w, round = 0, g = 0, n_item = 0;
     bool ok = true;
+    const int ch = lane & 15, kk = lane >> 4;  // the lane's 16-byte chunk of a key's 256 bytes, and its key of two
+    const uint32_t dst_lane = smem_u32(smem + L::kUnit0) + (ch >> 3) * 8192 + kk * 128;
+    // position keys: the warp's 16 of a step, chunk lane % 8 of keys lane / 8 + 4 q
+    const int r_key = 16 * w + (lane >> 3);
+    const uint32_t r_dst = smem_u32(smem + L::kRope) + sw128_off(r_key, lane & 7);
     for (int i = it0; ok && i < it1; ++i) {
       const LatentItem it = p.items[i];
       const LatentRowInfo ri = p.rows[it.row];
       const LatentTile t = tile_of(p, it, ri, member, N);
       if (!t.there || t.n_pages == 0) continue;
-      if (n_item > 0) ok = mbar_wait(q_empty, (uint32_t)((n_item - 1) & 1), err);
-      ok = __all_sync(0xFFFFFFFFu, ok) && !*abort_flag;
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+      if (w == 0) {  // the item's queries
+        if (n_item > 0) ok = warp_wait(q_empty, (uint32_t)((n_item - 1) & 1), err);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(q_full, 9 * L::kQSlab);
+          for (int s = 0; s < 9; ++s)
+            tma_load_2d(smem_u32(smem + L::kQ) + s * L::kQSlab, &q_map, 64 * s, ri.q_start * p.heads + t.f0,
+                        smem_u32(q_full));
+        }
+        __syncwarp();
+      }
       ++n_item;
-      if (lane == 0) {
-        const int y = ri.q_start * p.heads + t.f0;
-        mbar_arrive_expect_tx(q_full, 9 * L::kQSlab);
-        for (int s = 0; s < 9; ++s)
-          tma_load_2d(smem_u32(smem + L::kQ + s * L::kQSlab), &q_map, 64 * s, y, smem_u32(q_full));
-      }
       const int32_t* pt_row = p.page_table + (int64_t)it.row * p.max_pages + it.page0;
-      const int last_page = (ri.seq_len - 1) / kPage, last_shift = kPage * (last_page + 1) - ri.seq_len;
       const int n_steps = (t.n_pages + 1) / 2;
-      int pid = 0;
-      for (int s = 0; ok && s < n_steps; ++s, ++g) {
-        if ((s & 15) == 0) pid = 2 * s + lane < t.n_pages ? pt_row[2 * s + lane] : -1;
-        // a page's id and the box's first row in it: a page that is not there reads as zeros
-        int id[2], y[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int pg = 2 * s + h;
-          id[h] = __shfl_sync(0xFFFFFFFFu, pid, pg & 31);
-          y[h] = it.page0 + pg == last_page ? -last_shift : 0;
-          if (id[h] < 0 || id[h] >= p.num_pages) {
-            if (pg < t.n_pages && lane == 0) set_device_error(err, MIXATTN_DEVERR_PAGE_ID);
-            id[h] = 0;
-            y[h] = kPage;
+      int pid = -1;
+      for (int s = 0; s < n_steps; ++s, ++g) {
+        if ((s & 15) == 0) {  // lane l: page 2 s + l of the item
+          pid = 2 * s + lane < t.n_pages ? pt_row[2 * s + lane] : -1;
+          if (pid < 0 || pid >= p.num_pages) {
+            if (2 * s + lane < t.n_pages) set_device_error(err, MIXATTN_DEVERR_PAGE_ID);
+            pid = -1;
           }
         }
-        if (g >= 2) ok = mbar_wait(&rope_empty[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        const int ia = __shfl_sync(0xFFFFFFFFu, pid, (2 * s) & 31), ib = __shfl_sync(0xFFFFFFFFu, pid, (2 * s + 1) & 31);
+        {  // lane 0: the unit's slot, lane 1: the position keys'
+          const bool unit = lane == 0 && round > 0, rope = lane == 1 && g >= 2;
+          ok = warp_wait_each(unit || rope, lane == 0 ? &unit_empty[slot] : &rope_empty[g & 1],
+                              (uint32_t)((lane == 0 ? round - 1 : (g >> 1) - 1) & 1), err);
+        }
         if (!ok) break;
-        ++n_rope;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&rope_full[g & 1]), dst = smem_u32(smem + L::kRope + (g & 1) * 8192);
-          mbar_arrive_expect_tx(&rope_full[g & 1], 8192);
-          tma_load_3d(dst, &kv_map, kLatent, y[0], id[0], bar);
-          tma_load_3d(dst + 4096, &kv_map, kLatent, y[1], id[1], bar);
-        }
-        for (int b = 0; b < 4; ++b) {
-          if (round > 0) ok = mbar_wait(&unit_empty[slot], (uint32_t)((round - 1) & 1), err);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&unit_full[slot]), dst = smem_u32(smem + L::kUnit0 + slot * 16384);
-            mbar_arrive_expect_tx(&unit_full[slot], 16384);
+        // Keys past the row's end, and those of a page that is not there, are zeros: what the cache
+        // holds there may be anything, and 0 x NaN is not 0.
+        const int key0 = kPage * (it.page0 + 2 * s);
+        const int valid = ri.seq_len - key0;  // keys of the step that exist
+        const bool whole = ia >= 0 && ib >= 0 && valid >= kStepKeys;
+        const uint16_t* pa = p.data + (int64_t)max(ia, 0) * (kPage * kLatentRow);
+        const uint16_t* pb = p.data + (int64_t)max(ib, 0) * (kPage * kLatentRow);
+        const uint16_t* sa = pa + kk * kLatentRow + 128 * w + 8 * ch;
+        const uint16_t* sb = pb + kk * kLatentRow + 128 * w + 8 * ch;
+        const uint32_t dst = dst_lane + slot * 16384;
+        const uint16_t* rs = (w < 2 ? pa : pb) + (r_key & 31) * kLatentRow + kLatent + 8 * (lane & 7);
+        const uint32_t rd = r_dst + (g & 1) * 8192;
+        if (whole) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tma_load_3d(dst + c * 8192, &kv_map, 128 * b + 64 * c, y[0], id[0], bar);
-              tma_load_3d(dst + c * 8192 + 4096, &kv_map, 128 * b + 64 * c, y[1], id[1], bar);
-            }
+          for (int q = 0; q < 4; ++q)  // (keys 4 apart: chunk bit 2 flips)
+            cp_async16_s((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow));
+          cp_async_arrive(&rope_full[g & 1]);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            cp_async16_s(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
+                         (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = r_key + 4 * q;
+            cp_async16_or_zero((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow),
+                               (w < 2 ? ia : ib) >= 0 && key < valid);
           }
-          if (++slot == NU) {
-            slot = 0;
-            ++round;
-          }
+          cp_async_arrive(&rope_full[g & 1]);
+#pragma unroll 4
+          for (int q = 0; q < 32; ++q)
+            cp_async16_or_zero(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
+                               (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow),
+                               (q < 16 ? ia : ib) >= 0 && 2 * q + kk < valid);
         }
-        if (*abort_flag) ok = false;
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        cp_async_arrive(&unit_full[slot]);
+        slot += 4;
+        if (slot >= NU) {
+          slot -= NU;
+          ++round;
+        }
+        if (__any_sync(0xFFFFFFFFu, *abort_flag)) ok = false;
+        if (!ok) break;
       }
     }
-    if (lane == 0) {
-      if (!ok) *abort_flag = 1;
-      // nothing asked for may still be on its way when the CTA ends (which, but for an error, it is not)
-      for (int k = 0; k < NU; ++k) {
-        const int rd = k < slot ? round : round - 1;
-        if (rd >= 0) mbar_wait(&unit_full[k], (uint32_t)(rd & 1), err);
-      }
-      for (int k = max(0, n_rope - 2); k < n_rope; ++k) mbar_wait(&rope_full[k & 1], (uint32_t)((k >> 1) & 1), err);
-      if (n_item > 0) mbar_wait(q_full, (uint32_t)((n_item - 1) & 1), err);
-    }
+    if (!ok && lane == 0) *abort_flag = 1;
+    // nothing asked for may still be on its way when the CTA ends
+    cp_async_wait_all();
+    if (w == 0 && lane == 0 && n_item > 0) mbar_wait(q_full, (uint32_t)((n_item - 1) & 1), err);
     __syncwarp();
-  } else if (warp == kSoftmaxWarps + 1) {
-    // ======================= MMA (one thread) =======================
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_f16_f32(64, kStepKeys, false, false);
-      constexpr uint32_t kIdescO = idesc_f16_f32(128, N, true, false);
-      const uint64_t dQ = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
-      const uint64_t dP = sw128_desc(smem_u32(smem + L::kP), 16, 1024);
-      const uint64_t dR = sw128_desc(smem_u32(smem + L::kRope), 16, 1024);
-      const uint64_t dK = sw128_desc(smem_u32(smem + L::kUnit0), 16, 1024);
-      const uint64_t dV = sw128_desc(smem_u32(smem + L::kUnit0), 8192, 1024);  // slabs of 64 elements 8 KB apart
-      bool ok = true;
-      int g0 = 0, n_item = 0;
-      int ks = 0, kr = 0, vs = 0;  // slot and round of QK's next unit, slot of PV's
-      for (int i = it0; ok && i < it1; ++i) {
-        const LatentItem it = p.items[i];
-        const LatentRowInfo ri = p.rows[it.row];
-        const LatentTile t = tile_of(p, it, ri, member, N);
-        if (!t.there || t.n_pages == 0) continue;
-        const int n_steps = (t.n_pages + 1) / 2;
-        ok = mbar_wait(q_full, (uint32_t)(n_item & 1), err);
+  } else if (warp == kMmaWarp) {
+    // ======================= MMA (its elected lane) =======================
+    constexpr uint32_t kIdescS = idesc_f16_f32(64, kStepKeys, false, false);
+    constexpr uint32_t kIdescO = idesc_f16_f32(128, N, true, false);
+    auto lo = [](uint64_t d) { return (uint32_t)d; };
+    const uint32_t dQ = lo(sw128_desc(smem_u32(smem + L::kQ), 16, 1024));
+    const uint32_t dP = lo(sw128_desc(smem_u32(smem + L::kP), 16, 1024));
+    const uint32_t dR = lo(sw128_desc(smem_u32(smem + L::kRope), 16, 1024));
+    const uint32_t dK = lo(sw128_desc(smem_u32(smem + L::kUnit0), 16, 1024));
+    const uint32_t dV = lo(sw128_desc(smem_u32(smem + L::kUnit0), 8192, 1024));  // slabs of 64 elements 8 KB apart
+    constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);              // the upper word of them all
+    bool ok = true;
+    int g0 = 0, n_item = 0;
+    int ks = 0, kr = 0, vs = 0;  // slot and round of QK's next unit, slot of PV's
+    const int first = __shfl_sync(0xFFFFFFFFu, it0, 0), end = __shfl_sync(0xFFFFFFFFu, it1, 0);
+    for (int i = first; ok && i < end; ++i) {
+      const LatentItem it = p.items[i];
+      const LatentTile t = tile_of(p, it, p.rows[it.row], member, N);
+      // (control flow and operands the same in all lanes, and known to be)
+      const int n_steps = __shfl_sync(0xFFFFFFFFu, t.there ? (t.n_pages + 1) / 2 : 0, 0);
+      if (n_steps == 0) continue;
+      ok = warp_wait(q_full, (uint32_t)(n_item & 1), err);
+      // S(nq) and the PV of step np are next.  S(nq) may overwrite its buffer once P(nq - 2) is written,
+      // so it may be one step ahead; whichever can run does, S first: a PV that waited behind S for
+      // keys still on their way would hold the slots that the keys after them need.
+      int nq = 0, np = 0;
+      while (ok && np < n_steps) {
+        const int gq = g0 + nq, gp = g0 + np;
+        const bool can_s = nq < n_steps && nq - np <= 1, can_p = np < nq;
+        bool run_s = false;
+        {  // lanes 0 - 3: the step's units, 4: its position keys; 5: P, 6: the last item's output read
+          const int k = ks + lane, sl = k >= NU ? k - NU : k, rd = k >= NU ? kr + 1 : kr;
+          const bool need = (lane < 5 && can_s) || (lane == 5 && can_p) || (lane == 6 && can_p && np == 0 && n_item > 0);
+          const uint32_t bar = smem_u32(lane < 4 ? &unit_full[sl] : (lane == 4 ? &rope_full[gq & 1] : (lane == 5 ? p_full : o_free)));
+          const uint32_t parity = (uint32_t)(lane < 4 ? rd : (lane == 4 ? gq >> 1 : (lane == 5 ? gp : n_item - 1))) & 1u;
+          uint32_t i = 0;
+          for (; i < (1u << 24); ++i) {
+            const uint32_t done = __ballot_sync(0xFFFFFFFFu, !need || mbar_test_s(bar, parity));
+            run_s = can_s && (done & 0x1Fu) == 0x1Fu;
+            if (run_s || (can_p && (done & 0x60u) == 0x60u)) break;
+          }
+          ok = i < (1u << 24);
+          if (!ok && lane == 0) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
+        }
         if (!ok) break;
-        for (int s = 0; s <= n_steps; ++s) {
-          if (s < n_steps) {
-            const int g = g0 + s;
-            const uint32_t s_tm = tmem + kSCol + 64 * (g & 1);
-            ok = mbar_wait(&rope_full[g & 1], (uint32_t)((g >> 1) & 1), err);
-            if (!ok) break;
-            tc_fence_after();
+        tc_fence_after();
+        if (run_s) {
+          const uint32_t s_tm = tmem + kSCol + 64 * (gq & 1);
+          fence_proxy_async_smem();  // (the copies are the generic proxy's)
+          if (elect_one()) {
+            const uint32_t rd = dR + (gq & 1) * (8192 >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_ss(s_tm, dQ + ((8 * L::kQSlab + 32 * k) >> 4), dR + (((g & 1) * 8192 + 32 * k) >> 4), kIdescS,
-                        k > 0 ? 1u : 0u);
-            tc_commit(&rope_empty[g & 1]);
-            for (int b = 0; b < 4; ++b) {
-              ok = mbar_wait(&unit_full[ks], (uint32_t)(kr & 1), err);
-              if (!ok) break;
-              tc_fence_after();
+              tc_mma_ss_w(s_tm, dQ + ((8 * L::kQSlab + 32 * k) >> 4), kHi, rd + ((32 * k) >> 4), kHi, kIdescS,
+                          k > 0 ? 1u : 0u);
+            tc_commit(&rope_empty[gq & 1]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (elect_one()) {
+              const uint32_t kd = dK + ks * (16384 >> 4);
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                tc_mma_ss(s_tm, dQ + (((2 * b + (k >> 2)) * L::kQSlab + 32 * (k & 3)) >> 4),
-                          dK + ((ks * 16384 + (k >> 2) * 8192 + 32 * (k & 3)) >> 4), kIdescS, 1u);
-              if (++ks == NU) {
-                ks = 0;
-                ++kr;
+                tc_mma_ss_w(s_tm, dQ + (((2 * b + (k >> 2)) * L::kQSlab + 32 * (k & 3)) >> 4), kHi,
+                            kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, 1u);
+              if (b == 3) {
+                tc_commit(&s_full[gq & 1]);
+                if (nq == n_steps - 1) tc_commit(q_empty);
               }
             }
-            if (!ok) break;
-            tc_commit(&s_full[g & 1]);
-            if (s == n_steps - 1) tc_commit(q_empty);
+            __syncwarp();
+            if (++ks == NU) {
+              ks = 0;
+              ++kr;
+            }
           }
-          if (s > 0) {
-            const int g = g0 + s - 1;
-            ok = mbar_wait(p_full, (uint32_t)(g & 1), err);
-            if (ok && s == 1 && n_item > 0) ok = mbar_wait(o_free, (uint32_t)((n_item - 1) & 1), err);
-            if (!ok) break;
-            tc_fence_after();
-            for (int b = 0; b < 4; ++b) {
+          ++nq;
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (elect_one()) {
+              const uint32_t vd = dV + vs * (16384 >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                tc_mma_ss(tmem + kOCol + N * b, dV + ((vs * 16384 + 2048 * k) >> 4), dP + ((32 * k) >> 4), kIdescO,
-                          s > 1 || k > 0 ? 1u : 0u);
+                tc_mma_ss_w(tmem + kOCol + N * b, vd + ((2048 * k) >> 4), kHi, dP + ((32 * k) >> 4), kHi, kIdescO,
+                            k > 0 ? 1u : (np > 0 ? 1u : 0u));
               tc_commit(&unit_empty[vs]);
-              if (++vs == NU) vs = 0;
+              if (b == 3) tc_commit(pv_done);
             }
-            tc_commit(pv_done);
+            __syncwarp();
+            if (++vs == NU) vs = 0;
           }
-          if (*abort_flag) {
-            ok = false;
-            break;
-          }
+          ++np;
         }
-        g0 += n_steps;
-        ++n_item;
+        if (__any_sync(0xFFFFFFFFu, *abort_flag)) ok = false;
       }
+      g0 += n_steps;
+      ++n_item;
+    }
+    // nothing the lane started may still run when TMEM is released
+    if (elect_one()) {
       if (!ok) *abort_flag = 1;
-      // nothing this thread started may still run when TMEM is released
       tc_commit(fin);
       mbar_wait(fin, 0u, err);
     }
@@ -327,7 +381,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       const uint32_t* tm0 = tree ? p.tree_mask + (int64_t)(ri.tree_start + qi0) * p.tree_words : nullptr;
       const uint32_t* tm1 = tree ? p.tree_mask + (int64_t)(ri.tree_start + qi1) * p.tree_words : nullptr;
       const int32_t* pt_row = p.page_table + (int64_t)it.row * p.max_pages + it.page0;
-      const int last_page = (ri.seq_len - 1) / kPage, last_shift = kPage * (last_page + 1) - ri.seq_len;
       float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
       uint32_t good = 0;
       bool stop = false;
@@ -352,8 +405,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             uint32_t vis[2][2];  // [row][page]
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int pg = it.page0 + 2 * s + h, sh = pg == last_page ? last_shift : 0, k0 = kPage * pg - sh;
-              const uint32_t in = (h ? ok_b : ok_a) ? ~low_bits(sh) : 0u;
+              const int k0 = key0 + kPage * h;
+              const uint32_t in = (h ? ok_b : ok_a) ? 0xFFFFFFFFu : 0u;
               if (tree) {
                 vis[0][h] = tree_bits(tm0, p.tree_words, n_nodes, k0 - ri.q_offset) & in;
                 vis[1][h] = tree_bits(tm1, p.tree_words, n_nodes, k0 - ri.q_offset) & in;
@@ -530,8 +583,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, 
 }
 
 template <int N>
-cudaError_t launch_n(const CUtensorMap& q, const CUtensorMap& kv, const LatentParams& p, unsigned int* err,
-                     cudaStream_t s) {
+cudaError_t launch_n(const CUtensorMap& q, const LatentParams& p, unsigned int* err, cudaStream_t s) {
   {
     static std::mutex mu;
     static bool configured[kMaxDevices] = {};
@@ -556,7 +608,7 @@ cudaError_t launch_n(const CUtensorMap& q, const CUtensorMap& kv, const LatentPa
   cfg.gridDim = dim3(p.n_teams * p.team);
   cfg.blockDim = dim3(kLatentThreads);
   cfg.dynamicSmemBytes = LatentSmem<N>::kTotal;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, q, kv, p, err);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, q, p, err);
   if (e != cudaSuccess || p.n_cuts == 0) return e;
   cfg.gridDim = dim3(p.n_cuts * N);
   cfg.blockDim = dim3(128);
@@ -566,11 +618,11 @@ cudaError_t launch_n(const CUtensorMap& q, const CUtensorMap& kv, const LatentPa
 
 }  // namespace
 
-cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& q, const CUtensorMap& kv, const LatentParams& p,
-                                    unsigned int* err, cudaStream_t s) {
-  if (tile_rows == 16) return launch_n<16>(q, kv, p, err, s);
-  if (tile_rows == 32) return launch_n<32>(q, kv, p, err, s);
-  return launch_n<64>(q, kv, p, err, s);
+cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& q, const LatentParams& p, unsigned int* err,
+                                    cudaStream_t s) {
+  if (tile_rows == 16) return launch_n<16>(q, p, err, s);
+  if (tile_rows == 32) return launch_n<32>(q, p, err, s);
+  return launch_n<64>(q, p, err, s);
 }
 
 }  // namespace mixattn
