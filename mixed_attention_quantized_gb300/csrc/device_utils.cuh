@@ -357,6 +357,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   return false;
 }
 
+// The same for a whole warp, of which one lane polls: polls are served lane by lane, and those of 128
+// threads hold up every other barrier operation of the SM (by ~500 cycles each).
+__device__ __forceinline__ bool warp_wait_one(uint64_t* bar, uint32_t parity, unsigned int* err) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err);
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
 // 1-D bulk copy global -> shared through the TMA engine, completing on `bar`.
 // dst, src 16-byte aligned; bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

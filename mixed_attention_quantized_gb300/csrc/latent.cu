@@ -593,11 +593,6 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   if (int st = pending_device_check()) return st;
   unsigned int* err = device_error_address();
   if (!err) return MIXATTN_ERR_CUDA;
-  CUtensorMap q_map;
-  const uint64_t dims[2] = {kLatentRow, (uint64_t)T.total_q * plan->heads};
-  const int64_t strides[1] = {kLatentRow};
-  const uint32_t box[2] = {64, (uint32_t)T.tile_rows};
-  if (!make_map(&q_map, q, 2, dims, strides, box)) return MIXATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (int st = plan->list.upload(ws + 256, T.image.bytes.size(), s)) return st;
@@ -606,6 +601,7 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.items = reinterpret_cast<const LatentItem*>(ws + T.items);
   p.team_first = reinterpret_cast<const int32_t*>(ws + T.team_first);
   p.cuts = reinterpret_cast<const LatentCut*>(ws + T.cuts);
+  p.q = static_cast<const uint16_t*>(q);
   p.data = static_cast<const uint16_t*>(plan->cache.data);
   p.page_table = page_table;
   p.tree_mask = tree_mask;
@@ -620,7 +616,7 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.n_teams = T.n_teams;
   p.n_cuts = T.n_cuts;
   p.scale_log2 = (float)(plan->scale * kLog2e);
-  return launch_latent_attention(T.tile_rows, q_map, p, err, s) == cudaSuccess ? MIXATTN_OK
+  return launch_latent_attention(T.tile_rows, p, err, s) == cudaSuccess ? MIXATTN_OK
                                                                                             : MIXATTN_ERR_CUDA;
 }
 

@@ -39,6 +39,7 @@ struct LatentParams {
   const LatentItem* items;
   const int32_t* team_first;  // [n_teams + 1]
   const LatentCut* cuts;
+  const uint16_t* q;          // [total_q][heads][576]
   const uint16_t* data;       // the cache
   const int32_t* page_table;
   const uint32_t* tree_mask;
@@ -50,8 +51,7 @@ struct LatentParams {
 };
 
 // tile_rows: 16, 32 or 64 (query, head) rows a CTA
-cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& q, const LatentParams& p, unsigned int* err,
-                                    cudaStream_t s);
+cudaError_t launch_latent_attention(int tile_rows, const LatentParams& p, unsigned int* err, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Expanded form

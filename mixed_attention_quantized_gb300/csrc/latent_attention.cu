@@ -4,7 +4,9 @@
 //
 // A CTA takes a tile of N (16, 32 or 64) rows and walks a range of the row's pages, 64 keys (two
 // pages) a step, each loaded once into shared memory and used from there by both products:
-//   S   [64 rows][64 keys]   = Q (A, rows of 576) x K^T (B): M = 64, rows past N unused
+//   S   [64 rows][64 keys]   = Q (A, rows of 576) x K^T (B): M = 64, rows past N unused; Q in TMEM as far
+//                              as there is room (N = 64: 256 elements of 576), or its reads and those of K
+//                              fill shared memory's bandwidth, and copies and barriers wait behind them
 //   O^T [512 elements][N]   += c^T (A, the same bytes read MN-major) x P^T (B): four blocks of 128
 // O^T rather than O because 64 rows of 512 fp32 would fill TMEM alone, and because N then follows
 // the number of rows: 16 heads cost a quarter of the operand reads that 64 do.
@@ -20,7 +22,6 @@
 
 #include "latent.h"
 #include "page_attention.cuh"
-#include "tma.cuh"
 
 namespace mixattn {
 
@@ -34,18 +35,17 @@ constexpr int kStepKeys = 64;  // keys of a step: two pages
 
 template <int N>
 struct LatentSmem {
+  static constexpr int kTmemSlabs = N == 64 ? 4 : (N == 32 ? 8 : 9);  // of a row's nine 64-element slabs, those held in TMEM
   static constexpr int kQSlab = N * 128;                 // 64 elements of N rows, swizzled
-  static constexpr int kQ = 0;                           // 9 slabs
-  static constexpr int kP = kQ + 9 * kQSlab;             // [N][64 keys]
+  static constexpr int kQ = 0;                           // the other slabs
+  static constexpr int kP = kQ + (9 - kTmemSlabs) * kQSlab;          // [N][64 keys]
   static constexpr int kRope = (kP + N * 128 + 1023) / 1024 * 1024;  // 2 slots of [64 keys][64]
   static constexpr int kUnit0 = kRope + 2 * 8192;        // slots of [2][64 keys][64]
-  static constexpr int kUnits = N == 64 ? 8 : (N == 32 ? 10 : 11);
+  static constexpr int kUnits = N == 64 ? 10 : 12;
   static constexpr int kStat = kUnit0 + kUnits * 16384;  // alpha[64], l[64]
   static constexpr int kBar = kStat + 512;
   static constexpr int kTotal = kBar + 512 + 1024;       // + slack for 1024-byte alignment
   static_assert(kTotal <= 227 * 1024, "the tile does not fit in shared memory");
-  // the A operand of S reads 64 rows a slab: past N, whatever follows in shared memory
-  static_assert(kQ + 8 * kQSlab + 8192 <= kTotal, "rows past N");
 };
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
@@ -77,6 +77,27 @@ __device__ __forceinline__ bool warp_wait_each(bool need, uint64_t* bar, uint32_
   return false;
 }
 
+// The same layout the other way.
+__device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // What one tile of an item covers.
 struct LatentTile {
   int f0, rows;           // first (query, head) row of the row's, rows here
@@ -98,26 +119,28 @@ __device__ __forceinline__ LatentTile tile_of(const LatentParams& p, const Laten
 
 template <int N>
 __global__ void __launch_bounds__(kLatentThreads, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap q_map, const LatentParams p, unsigned int* err) {
+    latent_kernel(const __grid_constant__ LatentParams p, unsigned int* err) {
   using L = LatentSmem<N>;
   constexpr int NU = L::kUnits;
-  constexpr uint32_t kOCol = 0, kSCol = 4 * N;  // O^T blocks, then two S buffers of 64 columns
-  constexpr uint32_t kTmemCols = N == 64 ? 512 : 256;
+  // O^T blocks; two buffers of S, 64 rows in the lower 16 lanes of each warp's 32; the slabs of Q held
+  // here, two elements a column, in the same lanes
+  constexpr int QT = L::kTmemSlabs;
+  constexpr uint32_t kOCol = 0, kSCol = 4 * N, kSBuf = 64, kQCol = kSCol + 2 * kSBuf;
+  constexpr uint32_t kTmemCols = 512;
+  static_assert(kQCol + 32 * QT <= kTmemCols, "TMEM");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* unit_full = bars;              // [NU] by the copies of a warp's lanes
-  uint64_t* unit_empty = unit_full + NU;   // [NU] by a commit: the unit's block of O^T done
-  uint64_t* rope_full = unit_empty + NU;   // [2] by the copies of all load warps' lanes
-  uint64_t* rope_empty = rope_full + 2;    // [2]
-  uint64_t* q_full = rope_empty + 2;       // the item's queries
-  uint64_t* q_empty = q_full + 1;          // the item's last S done
-  uint64_t* s_full = q_empty + 1;          // [2] S(g) in buffer g % 2
+  uint64_t* full = bars;                   // [4] step g's keys, in g % 4, by the copies of all load warps' lanes
+  uint64_t* unit_empty = full + 4;         // [NU] by a commit: the unit's block of O^T done
+  uint64_t* rope_empty = unit_empty + NU;  // [2] by a commit
+  uint64_t* q_full = rope_empty + 2;       // by the softmax warps: the item's queries written
+  uint64_t* s_full = q_full + 1;           // [2] S(g) in buffer g % 2
   uint64_t* p_full = s_full + 2;           // by the softmax warps: P(g) written, O^T rescaled
   uint64_t* pv_done = p_full + 1;          // PV(g) done
   uint64_t* o_free = pv_done + 1;          // by the softmax warps: the item's O^T read
   uint64_t* fin = o_free + 1;
-  constexpr int kNumBars = 2 * NU + 12;
+  constexpr int kNumBars = NU + 13;
   static_assert(8 * kNumBars + 8 <= 512, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -125,13 +148,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
-    for (int i = 0; i < NU; ++i) mbar_init(unit_full + i, 32);
-    for (int i = 0; i < 2; ++i) mbar_init(rope_full + i, 32 * kLoadWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(full + i, 32 * kLoadWarps);
     mbar_init(p_full, kSoftmaxWarps);
     mbar_init(o_free, kSoftmaxWarps);
+    mbar_init(q_full, kSoftmaxWarps);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_map(&q_map);
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, kTmemCols);
@@ -150,7 +172,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
     // ======================= load (warp w: unit w of every step) =======================
     const int w = warp - kSoftmaxWarps;
-    int slot = w, round = 0, g = 0, n_item = 0;
+    int slot = w, round = 0, g = 0;
     bool ok = true;
     const int ch = lane & 15, kk = lane >> 4;  // the lane's 16-byte chunk of a key's 256 bytes, and its key of two
     const uint32_t dst_lane = smem_u32(smem + L::kUnit0) + (ch >> 3) * 8192 + kk * 128;
@@ -162,18 +184,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       const LatentRowInfo ri = p.rows[it.row];
       const LatentTile t = tile_of(p, it, ri, member, N);
       if (!t.there || t.n_pages == 0) continue;
-      if (w == 0) {  // the item's queries
-        if (n_item > 0) ok = warp_wait(q_empty, (uint32_t)((n_item - 1) & 1), err);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(q_full, 9 * L::kQSlab);
-          for (int s = 0; s < 9; ++s)
-            tma_load_2d(smem_u32(smem + L::kQ) + s * L::kQSlab, &q_map, 64 * s, ri.q_start * p.heads + t.f0,
-                        smem_u32(q_full));
-        }
-        __syncwarp();
-      }
-      ++n_item;
       const int32_t* pt_row = p.page_table + (int64_t)it.row * p.max_pages + it.page0;
       const int n_steps = (t.n_pages + 1) / 2;
       int pid = -1;
@@ -208,7 +218,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // (keys 4 apart: chunk bit 2 flips)
             cp_async16_s((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow));
-          cp_async_arrive(&rope_full[g & 1]);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
             cp_async16_s(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
@@ -220,14 +229,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             cp_async16_or_zero((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow),
                                (w < 2 ? ia : ib) >= 0 && key < valid);
           }
-          cp_async_arrive(&rope_full[g & 1]);
 #pragma unroll 4
           for (int q = 0; q < 32; ++q)
             cp_async16_or_zero(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
                                (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow),
                                (q < 16 ? ia : ib) >= 0 && 2 * q + kk < valid);
         }
-        cp_async_arrive(&unit_full[slot]);
+        cp_async_arrive(&full[g & 3]);  // (a slot is taken again four steps on, long after its MMAs)
         slot += 4;
         if (slot >= NU) {
           slot -= NU;
@@ -240,8 +248,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (!ok && lane == 0) *abort_flag = 1;
     // nothing asked for may still be on its way when the CTA ends
     cp_async_wait_all();
-    if (w == 0 && lane == 0 && n_item > 0) mbar_wait(q_full, (uint32_t)((n_item - 1) & 1), err);
-    __syncwarp();
   } else if (warp == kMmaWarp) {
     // ======================= MMA (its elected lane) =======================
     constexpr uint32_t kIdescS = idesc_f16_f32(64, kStepKeys, false, false);
@@ -253,9 +259,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const uint32_t dK = lo(sw128_desc(smem_u32(smem + L::kUnit0), 16, 1024));
     const uint32_t dV = lo(sw128_desc(smem_u32(smem + L::kUnit0), 8192, 1024));  // slabs of 64 elements 8 KB apart
     constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);              // the upper word of them all
+    // 16 of the elements of Q's slab against those of the keys at `kd`
+    auto s_mma = [&](uint32_t s_tm, int slab, int k, uint32_t kd, uint32_t acc) {
+      if (slab < QT) tc_mma_ts_w(s_tm, tmem + kQCol + 32 * slab + 8 * k, kd, kHi, kIdescS, acc);
+      else tc_mma_ss_w(s_tm, dQ + (((slab - QT) * L::kQSlab + 32 * k) >> 4), kHi, kd, kHi, kIdescS, acc);
+    };
     bool ok = true;
     int g0 = 0, n_item = 0;
-    int ks = 0, kr = 0, vs = 0;  // slot and round of QK's next unit, slot of PV's
+    int ks = 0, vs = 0;  // slots of S's next unit and of PV's
     const int first = __shfl_sync(0xFFFFFFFFu, it0, 0), end = __shfl_sync(0xFFFFFFFFu, it1, 0);
     for (int i = first; ok && i < end; ++i) {
       const LatentItem it = p.items[i];
@@ -263,7 +274,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       // (control flow and operands the same in all lanes, and known to be)
       const int n_steps = __shfl_sync(0xFFFFFFFFu, t.there ? (t.n_pages + 1) / 2 : 0, 0);
       if (n_steps == 0) continue;
-      ok = warp_wait(q_full, (uint32_t)(n_item & 1), err);
+      ok = warp_wait_one(q_full, (uint32_t)(n_item & 1), err);
       // S(nq) and the PV of step np are next.  S(nq) may overwrite its buffer once P(nq - 2) is written,
       // so it may be one step ahead; whichever can run does, S first: a PV that waited behind S for
       // keys still on their way would hold the slots that the keys after them need.
@@ -272,31 +283,32 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         const int gq = g0 + nq, gp = g0 + np;
         const bool can_s = nq < n_steps && nq - np <= 1, can_p = np < nq;
         bool run_s = false;
-        {  // lanes 0 - 3: the step's units, 4: its position keys; 5: P, 6: the last item's output read
-          const int k = ks + lane, sl = k >= NU ? k - NU : k, rd = k >= NU ? kr + 1 : kr;
-          const bool need = (lane < 5 && can_s) || (lane == 5 && can_p) || (lane == 6 && can_p && np == 0 && n_item > 0);
-          const uint32_t bar = smem_u32(lane < 4 ? &unit_full[sl] : (lane == 4 ? &rope_full[gq & 1] : (lane == 5 ? p_full : o_free)));
-          const uint32_t parity = (uint32_t)(lane < 4 ? rd : (lane == 4 ? gq >> 1 : (lane == 5 ? gp : n_item - 1))) & 1u;
+        {  // lane 0: the step's keys, 1: P, 2: the last item's output read
+          const bool need = lane == 0 ? can_s : (lane == 1 ? can_p : lane == 2 && can_p && np == 0 && n_item > 0);
+          const uint32_t bar = smem_u32(lane == 0 ? &full[gq & 3] : (lane == 1 ? p_full : o_free));
+          const uint32_t parity = (uint32_t)(lane == 0 ? gq >> 2 : (lane == 1 ? gp : n_item - 1)) & 1u;
           uint32_t i = 0;
           for (; i < (1u << 24); ++i) {
-            const uint32_t done = __ballot_sync(0xFFFFFFFFu, !need || mbar_test_s(bar, parity));
-            run_s = can_s && (done & 0x1Fu) == 0x1Fu;
-            if (run_s || (can_p && (done & 0x60u) == 0x60u)) break;
+            bool done = !need;
+            if (need) done = mbar_test_s(bar, parity);  // (three lanes: a poll takes time for every lane)
+            const uint32_t all = __ballot_sync(0xFFFFFFFFu, done);
+            run_s = can_s && (all & 1u);
+            if (run_s || (can_p && (all & 6u) == 6u)) break;
+            if ((i & 1023u) == 1023u && __any_sync(0xFFFFFFFFu, *abort_flag)) i = 1u << 24;
           }
           ok = i < (1u << 24);
-          if (!ok && lane == 0) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
+          if (!ok && lane == 0 && !*abort_flag) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
         }
         if (!ok) break;
         tc_fence_after();
         if (run_s) {
-          const uint32_t s_tm = tmem + kSCol + 64 * (gq & 1);
+          const uint32_t s_tm = tmem + kSCol + kSBuf * (gq & 1);
           fence_proxy_async_smem();  // (the copies are the generic proxy's)
           if (elect_one()) {
             const uint32_t rd = dR + (gq & 1) * (8192 >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_ss_w(s_tm, dQ + ((8 * L::kQSlab + 32 * k) >> 4), kHi, rd + ((32 * k) >> 4), kHi, kIdescS,
-                          k > 0 ? 1u : 0u);
+              s_mma(s_tm, 8, k, rd + ((32 * k) >> 4), k > 0 ? 1u : 0u);
             tc_commit(&rope_empty[gq & 1]);
           }
           __syncwarp();
@@ -306,18 +318,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
               const uint32_t kd = dK + ks * (16384 >> 4);
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                tc_mma_ss_w(s_tm, dQ + (((2 * b + (k >> 2)) * L::kQSlab + 32 * (k & 3)) >> 4), kHi,
-                            kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, 1u);
-              if (b == 3) {
-                tc_commit(&s_full[gq & 1]);
-                if (nq == n_steps - 1) tc_commit(q_empty);
-              }
+                s_mma(s_tm, 2 * b + (k >> 2), k & 3, kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), 1u);
+              if (b == 3) tc_commit(&s_full[gq & 1]);
             }
             __syncwarp();
-            if (++ks == NU) {
-              ks = 0;
-              ++kr;
-            }
+            if (++ks == NU) ks = 0;
           }
           ++nq;
         } else {
@@ -337,7 +342,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
           ++np;
         }
-        if (__any_sync(0xFFFFFFFFu, *abort_flag)) ok = false;
       }
       g0 += n_steps;
       ++n_item;
@@ -362,6 +366,63 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const int rr0 = 16 * warp + r;  // rows rr0 and rr0 + 8
     bool ok = true;
     int g = 0;
+    // Writes the queries of the CTA's next item from i on that has work.  A quad of lanes takes 16
+    // elements of a row: 32 bytes.
+    auto write_q = [&](int i) {
+      for (; i < it1; ++i) {
+        const LatentItem it = p.items[i];
+        const LatentRowInfo ri = p.rows[it.row];
+        const LatentTile t = tile_of(p, it, ri, member, N);
+        if (!t.there || t.n_pages == 0) continue;
+        if (rows_here) {
+          const uint16_t* q0 = p.q + ((int64_t)ri.q_start * p.heads + t.f0 + rr0) * kLatentRow + 4 * c;
+          const uint16_t* q1 = q0 + 8 * kLatentRow;
+          const bool in0 = rr0 < t.rows, in1 = rr0 + 8 < t.rows;
+          // (all loads together: behind the first keys' a load takes several us)
+          uint32_t v[5][32];
+#pragma unroll
+          for (int b = 0; b < 5; ++b)  // 128 elements each, the last 64
+#pragma unroll
+            for (int j = 0; j < (b < 4 ? 8 : 4); ++j) {
+              const uint2 x = ldg_u64_pred(q0 + 128 * b + 16 * j, in0), y = ldg_u64_pred(q1 + 128 * b + 16 * j, in1);
+              v[b][4 * j] = x.x;
+              v[b][4 * j + 1] = x.y;
+              v[b][4 * j + 2] = y.x;
+              v[b][4 * j + 3] = y.y;
+            }
+#pragma unroll
+          for (int b = 0; b < 5; ++b) {
+            if (2 * b < QT) {
+              if (b < 4) {
+                tmem_st_16x64(tmem + lane_base + kQCol + 64 * b, v[b]);
+              } else {
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = v[b][e];
+                tmem_st_16x32(tmem + lane_base + kQCol + 64 * b, u);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < (b < 4 ? 8 : 4); ++j) {
+                // elements 16 (j % 4) + 4 c of slab 2 b + j / 4: half of chunk 2 (j % 4) + c / 2
+                uint8_t* at = smem + L::kQ + (2 * b + (j >> 2) - QT) * L::kQSlab + 8 * (c & 1);
+                *reinterpret_cast<uint2*>(at + sw128_off(rr0, 2 * (j & 3) + (c >> 1))) =
+                    make_uint2(v[b][4 * j], v[b][4 * j + 1]);
+                *reinterpret_cast<uint2*>(at + sw128_off(rr0 + 8, 2 * (j & 3) + (c >> 1))) =
+                    make_uint2(v[b][4 * j + 2], v[b][4 * j + 3]);
+              }
+            }
+          }
+          tmem_wait_st();
+          if (QT < 9) fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        return;
+      }
+    };
+    write_q(it0);
     for (int i = it0; i < it1; ++i) {
       const LatentItem it = p.items[i];
       const LatentRowInfo ri = p.rows[it.row];
@@ -394,10 +455,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         float al0 = 1.f, al1 = 1.f;
         bool need = false;
         if (rows_here) {
-          ok = mbar_wait(&s_full[g & 1], (uint32_t)((g >> 1) & 1), err) && ok;
+          ok = warp_wait_one(&s_full[g & 1], (uint32_t)((g >> 1) & 1), err) && ok;
           tc_fence_after();
           uint32_t v[32];
-          tmem_ld_16x64(tmem + lane_base + kSCol + 64 * (g & 1), v);
+          tmem_ld_16x64(tmem + lane_base + kSCol + kSBuf * (g & 1), v);
           tmem_wait_ld();
           tc_fence_before();
           const int key0 = kPage * (it.page0 + 2 * s);
@@ -463,7 +524,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             alpha_s[rr0 + 8] = al1;
           }
           bar_any(kBarGroup, kGroup, false);
-          ok = mbar_wait(pv_done, (uint32_t)((g - 1) & 1), err) && ok;
+          ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err) && ok;
           tc_fence_after();
 #pragma unroll 1
           for (int b = 0; b < 4 * N / 16; ++b) {
@@ -477,7 +538,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
           tmem_wait_st();
         } else if (g > 0) {
-          ok = mbar_wait(pv_done, (uint32_t)((g - 1) & 1), err) && ok;  // P(g - 1) has been read
+          ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err) && ok;  // P(g - 1) has been read
         }
         if (rows_here) {
           uint8_t* p0 = smem + L::kP + rr0 * 128 + 4 * c;
@@ -499,8 +560,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         *abort_flag = 1;
         break;
       }
+      // the next item's queries: the last S of this one is done
+      write_q(i + 1);
       // ---- the item's output ----
-      ok = mbar_wait(pv_done, (uint32_t)((g - 1) & 1), err);
+      ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err);
       tc_fence_after();
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
@@ -520,20 +583,28 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         break;
       }
       const int64_t row0 = (int64_t)ri.q_start * p.heads + t.f0;
+      const int odd = lane & 1;
 #pragma unroll 1
       for (int b = 0; b < 4 * N / 16; ++b) {
         const int d = 128 * (16 * b / N) + 32 * warp + lane, col0 = (16 * b) % N;
         uint32_t o[16];
         tmem_ld16(tmem + lane_base + kOCol + 16 * b, o);
         tmem_wait_ld();
-        if (it.n_parts == 1) {
+        // lanes 2 k, 2 k + 1 hold two neighbouring elements of every row: the even lane takes both of
+        // every other row, the odd one those of the rows between
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (col0 + e < t.rows) p.o[(row0 + col0 + e) * kLatent + d] = f16_out(__uint_as_float(o[e]) * l_s[col0 + e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (col0 + e < t.rows) p.part_o[(part * N + col0 + e) * kLatent + d] = __uint_as_float(o[e]);
+        for (int e = 0; e < 16; e += 2) {
+          const float mine = __uint_as_float(odd ? o[e + 1] : o[e]);
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(odd ? o[e] : o[e + 1]), 1);
+          const float x = odd ? other : mine, y = odd ? mine : other;
+          const int col = col0 + e + odd;
+          if (col >= t.rows) continue;
+          if (it.n_parts == 1) {
+            const float inv = l_s[col];
+            *reinterpret_cast<uint32_t*>(p.o + (row0 + col) * kLatent + d - odd) = pack_f16x2_out(x * inv, y * inv);
+          } else {
+            *reinterpret_cast<float2*>(p.part_o + (part * N + col) * kLatent + d - odd) = make_float2(x, y);
+          }
         }
       }
       tc_fence_before();
@@ -583,7 +654,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, 
 }
 
 template <int N>
-cudaError_t launch_n(const CUtensorMap& q, const LatentParams& p, unsigned int* err, cudaStream_t s) {
+cudaError_t launch_n(const LatentParams& p, unsigned int* err, cudaStream_t s) {
   {
     static std::mutex mu;
     static bool configured[kMaxDevices] = {};
@@ -608,7 +679,7 @@ cudaError_t launch_n(const CUtensorMap& q, const LatentParams& p, unsigned int* 
   cfg.gridDim = dim3(p.n_teams * p.team);
   cfg.blockDim = dim3(kLatentThreads);
   cfg.dynamicSmemBytes = LatentSmem<N>::kTotal;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, q, p, err);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, p, err);
   if (e != cudaSuccess || p.n_cuts == 0) return e;
   cfg.gridDim = dim3(p.n_cuts * N);
   cfg.blockDim = dim3(128);
@@ -618,11 +689,10 @@ cudaError_t launch_n(const CUtensorMap& q, const LatentParams& p, unsigned int* 
 
 }  // namespace
 
-cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& q, const LatentParams& p, unsigned int* err,
-                                    cudaStream_t s) {
-  if (tile_rows == 16) return launch_n<16>(q, p, err, s);
-  if (tile_rows == 32) return launch_n<32>(q, p, err, s);
-  return launch_n<64>(q, p, err, s);
+cudaError_t launch_latent_attention(int tile_rows, const LatentParams& p, unsigned int* err, cudaStream_t s) {
+  if (tile_rows == 16) return launch_n<16>(p, err, s);
+  if (tile_rows == 32) return launch_n<32>(p, err, s);
+  return launch_n<64>(p, err, s);
 }
 
 }  // namespace mixattn
