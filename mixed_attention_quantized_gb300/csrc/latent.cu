@@ -206,7 +206,7 @@ struct Image {
 struct LatentTiling {
   Image image;
   size_t rows = 0, items = 0, team_first = 0, cuts = 0, part_o = 0, part_ml = 0, total = 0;
-  int tile_rows = 16, team = 1, n_teams = 1, n_cuts = 0;
+  int tile_rows = 16, team = 1, n_teams = 1, n_cuts = 0, max_parts = 0;
   int64_t total_q = 0;
   bool trees = false;
   int32_t tree_words = 0;
@@ -326,6 +326,7 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
         for (int64_t m = 0; m < T.team && mt0 + m < n_tiles; ++m)
           cuts.push_back(LatentCut{r, (int32_t)(mt0 + m), (int32_t)(slots + m * parts), parts});
         slots += (int64_t)parts * T.team;
+        T.max_parts = std::max<int>(T.max_parts, parts);
         if (slots > INT32_MAX) return MIXATTN_ERR_INVALID_ARG;
       }
     }
@@ -465,6 +466,7 @@ struct mixattn_latent_plan {
   mixattn_latent_cache cache;
   int32_t heads = 0, max_pages = 0;
   double scale = 0.0;
+  CUtensorMap kv_map;
   LatentTiling tiling;
   PlanList list;
 };
@@ -552,6 +554,12 @@ int mixattn_latent_plan_create(mixattn_latent_plan** plan_out, const mixattn_lat
   p->heads = num_heads;
   p->scale = softmax_scale;
   st = mixattn_latent_plan_update(p, n_rows, row_kinds, seq_lens, q_offsets, max_pages, workspace_bytes);
+  if (st == MIXATTN_OK) {
+    const uint64_t dims[3] = {kLatentRow, kPage, (uint64_t)cache->num_pages};
+    const int64_t strides[2] = {kLatentRow, kLatentRow * kPage};
+    const uint32_t box[3] = {64, kPage, 1};
+    if (!make_map(&p->kv_map, cache->data, 3, dims, strides, box)) st = MIXATTN_ERR_CUDA;
+  }
   if (st != MIXATTN_OK) {
     delete p;
     return st;
@@ -615,8 +623,9 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.team = T.team;
   p.n_teams = T.n_teams;
   p.n_cuts = T.n_cuts;
+  p.max_parts = T.max_parts;
   p.scale_log2 = (float)(plan->scale * kLog2e);
-  return launch_latent_attention(T.tile_rows, p, err, s) == cudaSuccess ? MIXATTN_OK
+  return launch_latent_attention(T.tile_rows, plan->kv_map, p, err, s) == cudaSuccess ? MIXATTN_OK
                                                                                             : MIXATTN_ERR_CUDA;
 }
 

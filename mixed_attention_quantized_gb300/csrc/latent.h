@@ -44,14 +44,15 @@ struct LatentParams {
   const int32_t* page_table;
   const uint32_t* tree_mask;
   uint16_t* o;
-  float* part_o;    // [slots][tile rows][512], unnormalised
+  float* part_o;    // [slots][block of 128 elements][16 rows at a time][128][16], unnormalised
   float2* part_ml;  // [slots][tile rows]: reference (log2 units) and sum
-  int32_t tree_words, max_pages, num_pages, heads, team, n_teams, n_cuts;
+  int32_t tree_words, max_pages, num_pages, heads, team, n_teams, n_cuts, max_parts;
   float scale_log2;
 };
 
 // tile_rows: 16, 32 or 64 (query, head) rows a CTA
-cudaError_t launch_latent_attention(int tile_rows, const LatentParams& p, unsigned int* err, cudaStream_t s);
+cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& kv, const LatentParams& p, unsigned int* err,
+                                    cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Expanded form

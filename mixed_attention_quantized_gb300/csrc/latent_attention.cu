@@ -11,9 +11,9 @@
 // O^T rather than O because 64 rows of 512 fp32 would fill TMEM alone, and because N then follows
 // the number of rows: 16 heads cost a quarter of the operand reads that 64 do.
 //
-// Roles: softmax (warps 0-3), loads (warps 4-7), MMA (the elected lane of warp 8). A step's four
+// Roles: softmax (warps 0-3), loads (warps 4-7), MMA (the elected lanes of warps 8 and 9). A step's four
 // 128-element units of c and its r come through rings of slots with barriers of their own, so that a
-// unit is refilled as soon as its block of O^T is done.  The MMA warp issues S(g+1) before PV(g), if its keys are there.
+// unit is refilled as soon as its block of O^T is done.
 //
 // The loads are 16-byte cp.async by four warps, swizzled by address, and not TMA boxes: a box of 128-byte
 // rows moves 49 bytes a ns and SM at most (7.4 TB/s over all, measured with 192 KB in flight an SM, from
@@ -22,6 +22,7 @@
 
 #include "latent.h"
 #include "page_attention.cuh"
+#include "tma.cuh"
 
 namespace mixattn {
 
@@ -29,8 +30,9 @@ namespace {
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kLoadWarps = 4;
+constexpr int kTmaWarps = 2;  // of these, whose units TMA loads
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kLatentThreads = 32 * (kMmaWarp + 1);
+constexpr int kLatentThreads = 32 * (kMmaWarp + 2);
 constexpr int kStepKeys = 64;  // keys of a step: two pages
 
 template <int N>
@@ -119,7 +121,7 @@ __device__ __forceinline__ LatentTile tile_of(const LatentParams& p, const Laten
 
 template <int N>
 __global__ void __launch_bounds__(kLatentThreads, 1)
-    latent_kernel(const __grid_constant__ LatentParams p, unsigned int* err) {
+    latent_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ LatentParams p, unsigned int* err) {
   using L = LatentSmem<N>;
   constexpr int NU = L::kUnits;
   // O^T blocks; two buffers of S, 64 rows in the lower 16 lanes of each warp's 32; the slabs of Q held
@@ -136,11 +138,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   uint64_t* rope_empty = unit_empty + NU;  // [2] by a commit
   uint64_t* q_full = rope_empty + 2;       // by the softmax warps: the item's queries written
   uint64_t* s_full = q_full + 1;           // [2] S(g) in buffer g % 2
-  uint64_t* p_full = s_full + 2;           // by the softmax warps: P(g) written, O^T rescaled
-  uint64_t* pv_done = p_full + 1;          // PV(g) done
+  uint64_t* p_full = s_full + 2;           // [2] by the softmax warps: S(g) read, P(g) written, O^T rescaled
+  uint64_t* pv_done = p_full + 2;          // PV(g) done
   uint64_t* o_free = pv_done + 1;          // by the softmax warps: the item's O^T read
-  uint64_t* fin = o_free + 1;
-  constexpr int kNumBars = NU + 13;
+  uint64_t* q_asked = o_free + 1;          // by the softmax warps: the first item's queries are on their way
+  uint64_t* fin = q_asked + 1;             // [2]
+  constexpr int kNumBars = NU + 16;
   static_assert(8 * kNumBars + 8 <= 512, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -149,9 +152,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
     for (int i = 0; i < 4; ++i) mbar_init(full + i, 32 * kLoadWarps);
-    mbar_init(p_full, kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(p_full + i, kSoftmaxWarps);
     mbar_init(o_free, kSoftmaxWarps);
     mbar_init(q_full, kSoftmaxWarps);
+    mbar_init(q_asked, kSoftmaxWarps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -179,6 +183,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // position keys: the warp's 16 of a step, chunk lane % 8 of keys lane / 8 + 4 q
     const int r_key = 16 * w + (lane >> 3);
     const uint32_t r_dst = smem_u32(smem + L::kRope) + sw128_off(r_key, lane & 7);
+    // The queries go first: behind the keys of 2.5 steps, asked for by every SM at once, they would take
+    // 5 us, and nothing starts without them.
+    if (it0 < it1) ok = warp_wait_one(q_asked, 0u, err);
     for (int i = it0; ok && i < it1; ++i) {
       const LatentItem it = p.items[i];
       const LatentRowInfo ri = p.rows[it.row];
@@ -218,10 +225,23 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // (keys 4 apart: chunk bit 2 flips)
             cp_async16_s((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow));
+          if (w < kTmaWarps) {
+            if (elect_one()) {
+              const uint32_t bar = smem_u32(&full[g & 3]), at = smem_u32(smem + L::kUnit0) + slot * 16384;
+              mbar_expect_tx(&full[g & 3], 16384);
 #pragma unroll
-          for (int q = 0; q < 32; ++q)
-            cp_async16_s(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
-                         (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow));
+              for (int c = 0; c < 2; ++c) {
+                tma_load_3d(at + c * 8192, &kv_map, 128 * w + 64 * c, 0, ia, bar);
+                tma_load_3d(at + c * 8192 + 4096, &kv_map, 128 * w + 64 * c, 0, ib, bar);
+              }
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              cp_async16_s(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
+                           (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow));
+          }
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -248,8 +268,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (!ok && lane == 0) *abort_flag = 1;
     // nothing asked for may still be on its way when the CTA ends
     cp_async_wait_all();
-  } else if (warp == kMmaWarp) {
-    // ======================= MMA (its elected lane) =======================
+    for (int k = max(0, g - 4); k < g; ++k) warp_wait_one(&full[k & 3], (uint32_t)((k >> 2) & 1), err);
+  } else if (warp >= kMmaWarp) {
+    // ======================= MMA: S (the first warp's elected lane), PV (the second's) =======================
+    // (Two warps: one that did both would hold a PV that could run behind an S whose keys are still on
+    // their way, and with it the slots for the keys after those.)
     constexpr uint32_t kIdescS = idesc_f16_f32(64, kStepKeys, false, false);
     constexpr uint32_t kIdescO = idesc_f16_f32(128, N, true, false);
     auto lo = [](uint64_t d) { return (uint32_t)d; };
@@ -259,14 +282,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const uint32_t dK = lo(sw128_desc(smem_u32(smem + L::kUnit0), 16, 1024));
     const uint32_t dV = lo(sw128_desc(smem_u32(smem + L::kUnit0), 8192, 1024));  // slabs of 64 elements 8 KB apart
     constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);              // the upper word of them all
-    // 16 of the elements of Q's slab against those of the keys at `kd`
-    auto s_mma = [&](uint32_t s_tm, int slab, int k, uint32_t kd, uint32_t acc) {
-      if (slab < QT) tc_mma_ts_w(s_tm, tmem + kQCol + 32 * slab + 8 * k, kd, kHi, kIdescS, acc);
-      else tc_mma_ss_w(s_tm, dQ + (((slab - QT) * L::kQSlab + 32 * k) >> 4), kHi, kd, kHi, kIdescS, acc);
-    };
+    const bool is_s = warp == kMmaWarp;
     bool ok = true;
-    int g0 = 0, n_item = 0;
-    int ks = 0, vs = 0;  // slots of S's next unit and of PV's
+    int g = 0, n_item = 0, slot = 0;
     const int first = __shfl_sync(0xFFFFFFFFu, it0, 0), end = __shfl_sync(0xFFFFFFFFu, it1, 0);
     for (int i = first; ok && i < end; ++i) {
       const LatentItem it = p.items[i];
@@ -274,83 +292,81 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       // (control flow and operands the same in all lanes, and known to be)
       const int n_steps = __shfl_sync(0xFFFFFFFFu, t.there ? (t.n_pages + 1) / 2 : 0, 0);
       if (n_steps == 0) continue;
-      ok = warp_wait_one(q_full, (uint32_t)(n_item & 1), err);
-      // S(nq) and the PV of step np are next.  S(nq) may overwrite its buffer once P(nq - 2) is written,
-      // so it may be one step ahead; whichever can run does, S first: a PV that waited behind S for
-      // keys still on their way would hold the slots that the keys after them need.
-      int nq = 0, np = 0;
-      while (ok && np < n_steps) {
-        const int gq = g0 + nq, gp = g0 + np;
-        const bool can_s = nq < n_steps && nq - np <= 1, can_p = np < nq;
-        bool run_s = false;
-        {  // lane 0: the step's keys, 1: P, 2: the last item's output read
-          const bool need = lane == 0 ? can_s : (lane == 1 ? can_p : lane == 2 && can_p && np == 0 && n_item > 0);
-          const uint32_t bar = smem_u32(lane == 0 ? &full[gq & 3] : (lane == 1 ? p_full : o_free));
-          const uint32_t parity = (uint32_t)(lane == 0 ? gq >> 2 : (lane == 1 ? gp : n_item - 1)) & 1u;
-          uint32_t i = 0;
-          for (; i < (1u << 24); ++i) {
-            bool done = !need;
-            if (need) done = mbar_test_s(bar, parity);  // (three lanes: a poll takes time for every lane)
-            const uint32_t all = __ballot_sync(0xFFFFFFFFu, done);
-            run_s = can_s && (all & 1u);
-            if (run_s || (can_p && (all & 6u) == 6u)) break;
-            if ((i & 1023u) == 1023u && __any_sync(0xFFFFFFFFu, *abort_flag)) i = 1u << 24;
-          }
-          ok = i < (1u << 24);
-          if (!ok && lane == 0 && !*abort_flag) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
-        }
-        if (!ok) break;
-        tc_fence_after();
-        if (run_s) {
-          const uint32_t s_tm = tmem + kSCol + kSBuf * (gq & 1);
+      if (is_s) {
+        ok = warp_wait_one(q_full, (uint32_t)(n_item & 1), err);
+        for (int s = 0; ok && s < n_steps; ++s, ++g) {
+          ok = warp_wait_one(&full[g & 3], (uint32_t)((g >> 2) & 1), err);
+          if (ok && g >= 2) ok = warp_wait_one(&p_full[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);  // S(g - 2) read
+          if (!ok) break;
           fence_proxy_async_smem();  // (the copies are the generic proxy's)
-          if (elect_one()) {
-            const uint32_t rd = dR + (gq & 1) * (8192 >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              s_mma(s_tm, 8, k, rd + ((32 * k) >> 4), k > 0 ? 1u : 0u);
-            tc_commit(&rope_empty[gq & 1]);
-          }
-          __syncwarp();
-#pragma unroll
+          tc_fence_after();
+          const uint32_t s_tm = tmem + kSCol + kSBuf * (g & 1);
+          // 128 elements of Q against a unit of the keys, those of Q in TMEM first
+#pragma unroll 1
           for (int b = 0; b < 4; ++b) {
-            if (elect_one()) {
-              const uint32_t kd = dK + ks * (16384 >> 4);
+            const uint32_t kd = dK + slot * (16384 >> 4), acc = b > 0 ? 1u : 0u;
+            if (2 * b < QT) {
+              if (elect_one()) {
+                const uint32_t qt = tmem + kQCol + 64 * b;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                s_mma(s_tm, 2 * b + (k >> 2), k & 3, kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), 1u);
-              if (b == 3) tc_commit(&s_full[gq & 1]);
+                for (int k = 0; k < 8; ++k)
+                  tc_mma_ts_w(s_tm, qt + 8 * k, kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, k > 0 ? 1u : acc);
+              }
+            } else {
+              if (elect_one()) {
+                const uint32_t qd = dQ + (2 * b - QT) * (L::kQSlab >> 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  tc_mma_ss_w(s_tm, qd + (((k >> 2) * L::kQSlab + 32 * (k & 3)) >> 4), kHi,
+                              kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, k > 0 ? 1u : acc);
+              }
             }
             __syncwarp();
-            if (++ks == NU) ks = 0;
+            if (++slot == NU) slot = 0;
           }
-          ++nq;
-        } else {
+          if (elect_one()) {
+            const uint32_t rd = dR + (g & 1) * (8192 >> 4);
 #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (QT == 9) tc_mma_ts_w(s_tm, tmem + kQCol + 256 + 8 * k, rd + ((32 * k) >> 4), kHi, kIdescS, 1u);
+              else tc_mma_ss_w(s_tm, dQ + (((8 - QT) * L::kQSlab + 32 * k) >> 4), kHi, rd + ((32 * k) >> 4), kHi, kIdescS, 1u);
+            }
+            tc_commit(&s_full[g & 1]);
+            tc_commit(&rope_empty[g & 1]);
+          }
+          __syncwarp();
+        }
+      } else {
+        for (int s = 0; ok && s < n_steps; ++s, ++g) {
+          ok = warp_wait_one(&p_full[g & 1], (uint32_t)((g >> 1) & 1), err);
+          if (ok && s == 0 && n_item > 0) ok = warp_wait_one(o_free, (uint32_t)((n_item - 1) & 1), err);
+          if (!ok) break;
+          // (the keys landed before S(g), and were fenced there: by another thread, so once more here)
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t acc = s > 0 ? 1u : 0u;
+#pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             if (elect_one()) {
-              const uint32_t vd = dV + vs * (16384 >> 4);
+              const uint32_t vd = dV + slot * (16384 >> 4), o_tm = tmem + kOCol + N * b;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                tc_mma_ss_w(tmem + kOCol + N * b, vd + ((2048 * k) >> 4), kHi, dP + ((32 * k) >> 4), kHi, kIdescO,
-                            k > 0 ? 1u : (np > 0 ? 1u : 0u));
-              tc_commit(&unit_empty[vs]);
+                tc_mma_ss_w(o_tm, vd + ((2048 * k) >> 4), kHi, dP + ((32 * k) >> 4), kHi, kIdescO, k > 0 ? 1u : acc);
+              tc_commit(&unit_empty[slot]);
               if (b == 3) tc_commit(pv_done);
             }
             __syncwarp();
-            if (++vs == NU) vs = 0;
+            if (++slot == NU) slot = 0;
           }
-          ++np;
         }
       }
-      g0 += n_steps;
       ++n_item;
     }
     // nothing the lane started may still run when TMEM is released
     if (elect_one()) {
       if (!ok) *abort_flag = 1;
-      tc_commit(fin);
-      mbar_wait(fin, 0u, err);
+      tc_commit(is_s ? fin : fin + 1);
+      mbar_wait(is_s ? fin : fin + 1, 0u, err);
     }
     __syncwarp();
   } else {
@@ -368,7 +384,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     int g = 0;
     // Writes the queries of the CTA's next item from i on that has work.  A quad of lanes takes 16
     // elements of a row: 32 bytes.
-    auto write_q = [&](int i) {
+    auto write_q = [&](int i, bool first) {
       for (; i < it1; ++i) {
         const LatentItem it = p.items[i];
         const LatentRowInfo ri = p.rows[it.row];
@@ -390,6 +406,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
               v[b][4 * j + 2] = y.x;
               v[b][4 * j + 3] = y.y;
             }
+          if (first && lane == 0) mbar_arrive(q_asked);
+          first = false;
 #pragma unroll
           for (int b = 0; b < 5; ++b) {
             if (2 * b < QT) {
@@ -415,14 +433,17 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
           tmem_wait_st();
           if (QT < 9) fence_proxy_async_smem();
+        } else if (first && lane == 0) {
+          mbar_arrive(q_asked);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         return;
       }
+      if (first && lane == 0) mbar_arrive(q_asked);  // (no item with work)
     };
-    write_q(it0);
+    write_q(it0, true);
     for (int i = it0; i < it1; ++i) {
       const LatentItem it = p.items[i];
       const LatentRowInfo ri = p.rows[it.row];
@@ -554,14 +575,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           stop = true;
           break;
         }
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(&p_full[g & 1]);
       }
       if (stop) {
         *abort_flag = 1;
         break;
       }
       // the next item's queries: the last S of this one is done
-      write_q(i + 1);
+      write_q(i + 1, false);
       // ---- the item's output ----
       ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err);
       tc_fence_after();
@@ -590,21 +611,23 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         uint32_t o[16];
         tmem_ld16(tmem + lane_base + kOCol + 16 * b, o);
         tmem_wait_ld();
+        if (it.n_parts > 1) {  // [16 rows of a block][element][row]: 64 bytes a lane
+          float* dst = p.part_o + ((part * (4 * N / 16) + b) * 128 + 32 * warp + lane) * 16;
+          stg256(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+          stg256(dst + 8, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
+          continue;
+        }
         // lanes 2 k, 2 k + 1 hold two neighbouring elements of every row: the even lane takes both of
         // every other row, the odd one those of the rows between
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float mine = __uint_as_float(odd ? o[e + 1] : o[e]);
           const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(odd ? o[e] : o[e + 1]), 1);
-          const float x = odd ? other : mine, y = odd ? mine : other;
           const int col = col0 + e + odd;
           if (col >= t.rows) continue;
-          if (it.n_parts == 1) {
-            const float inv = l_s[col];
-            *reinterpret_cast<uint32_t*>(p.o + (row0 + col) * kLatent + d - odd) = pack_f16x2_out(x * inv, y * inv);
-          } else {
-            *reinterpret_cast<float2*>(p.part_o + (part * N + col) * kLatent + d - odd) = make_float2(x, y);
-          }
+          const float inv = l_s[col];
+          *reinterpret_cast<uint32_t*>(p.o + (row0 + col) * kLatent + d - odd) =
+              pack_f16x2_out((odd ? other : mine) * inv, (odd ? mine : other) * inv);
         }
       }
       tc_fence_before();
@@ -622,39 +645,80 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   }
 }
 
-// Joins the parts of cut tiles: one CTA a (query, head) row, four elements a thread.
+// Joins the parts of cut tiles: a CTA takes 32 elements of 16 rows, warp w every fourth part.
 __global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, int tile_rows) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ float weights[];  // [parts][16]
+  __shared__ float inv_l[16];
+  __shared__ float sums[3][16][33];
+  wait_for_upload();
   const LatentCut cut = p.cuts[blockIdx.x / tile_rows];
-  const int rr = blockIdx.x % tile_rows;
+  const int u = blockIdx.x % tile_rows, n = tile_rows / 4;       // n units of 16 rows by 128 elements
+  const int b = u >> 2, d0 = 128 * (16 * b / tile_rows) + 32 * (u & 3), col0 = 16 * b % tile_rows;
   const LatentRowInfo ri = p.rows[cut.row];
-  const int f = cut.mt * tile_rows + rr;
-  if (f >= (ri.seq_len - ri.q_offset) * p.heads) return;
-  const float2* ml = p.part_ml + (int64_t)cut.slot * tile_rows + rr;
-  float m = -CUDART_INF_F;
-  for (int q = 0; q < cut.n_parts; ++q) m = fmaxf(m, ml[(int64_t)q * tile_rows].x);
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* src = p.part_o + ((int64_t)cut.slot * tile_rows + rr) * kLatent + 4 * threadIdx.x;
-#pragma unroll 4
-  for (int q = 0; q < cut.n_parts; ++q) {
-    const float2 x = ml[(int64_t)q * tile_rows];
-    if (x.x == -CUDART_INF_F) continue;  // (no key of the row in this part: any value may stand there)
-    const float w = ex2(x.x - m);
-    const float4 y = *reinterpret_cast<const float4*>(src + (int64_t)q * tile_rows * kLatent);
-    l += w * x.y;
-    o.x += w * y.x;
-    o.y += w * y.y;
-    o.z += w * y.z;
-    o.w += w * y.w;
+  const int rows = min(tile_rows, (ri.seq_len - ri.q_offset) * p.heads - cut.mt * tile_rows) - col0;  // here
+  if (rows <= 0) return;
+  {
+    // eight threads a row form its parts' weights; a part without a key of the row weighs nothing
+    const int row = threadIdx.x >> 3, k = threadIdx.x & 7;
+    const float2* ml = p.part_ml + (int64_t)cut.slot * tile_rows + col0 + row;
+    float m = -CUDART_INF_F, l = 0.f;
+    if (row < rows)
+      for (int q = k; q < cut.n_parts; q += 8) m = fmaxf(m, ml[(int64_t)q * tile_rows].x);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int q = k; q < cut.n_parts; q += 8) {
+      const float2 x = row < rows ? ml[(int64_t)q * tile_rows] : make_float2(-CUDART_INF_F, 0.f);
+      const float w = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - m);
+      weights[16 * q + row] = w;
+      if (w != 0.f) l += w * x.y;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    if (k == 0) inv_l[row] = l > 0.f ? 1.f / l : 0.f;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(p.o + ((int64_t)ri.q_start * p.heads + f) * kLatent + 4 * threadIdx.x) =
-      make_uint2(pack_f16x2_out(o.x * inv, o.y * inv), pack_f16x2_out(o.z * inv, o.w * inv));
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float* src = p.part_o + (((int64_t)cut.slot * n + b) * 128 + 32 * (u & 3) + lane) * 16;
+  float acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int q = warp; q < cut.n_parts; q += 4) {
+    const float4* x = reinterpret_cast<const float4*>(src + (int64_t)q * n * 128 * 16);
+    const float4* w = reinterpret_cast<const float4*>(weights + 16 * q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 y = __ldcs(x + e), f = w[e];
+      // (where a part has no key of the row any value may stand)
+      acc[4 * e] = fmaf(f.x, f.x != 0.f ? y.x : 0.f, acc[4 * e]);
+      acc[4 * e + 1] = fmaf(f.y, f.y != 0.f ? y.y : 0.f, acc[4 * e + 1]);
+      acc[4 * e + 2] = fmaf(f.z, f.z != 0.f ? y.z : 0.f, acc[4 * e + 2]);
+      acc[4 * e + 3] = fmaf(f.w, f.w != 0.f ? y.w : 0.f, acc[4 * e + 3]);
+    }
+  }
+  if (warp > 0) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sums[warp - 1][e][lane] = acc[e];
+  }
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = ((acc[e] + sums[0][e][lane]) + sums[1][e][lane]) + sums[2][e][lane];
+  const int odd = lane & 1;
+  uint16_t* dst = p.o + ((int64_t)ri.q_start * p.heads + cut.mt * tile_rows + col0) * kLatent + d0 + lane - odd;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {  // (as the attention kernel writes its output)
+    const float mine = odd ? acc[e + 1] : acc[e];
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[e] : acc[e + 1], 1);
+    if (e + odd >= rows) continue;
+    const float inv = inv_l[e + odd];
+    *reinterpret_cast<uint32_t*>(dst + (int64_t)(e + odd) * kLatent) =
+        pack_f16x2_out((odd ? other : mine) * inv, (odd ? mine : other) * inv);
+  }
 }
 
 template <int N>
-cudaError_t launch_n(const LatentParams& p, unsigned int* err, cudaStream_t s) {
+cudaError_t launch_n(const CUtensorMap& kv, const LatentParams& p, unsigned int* err, cudaStream_t s) {
   {
     static std::mutex mu;
     static bool configured[kMaxDevices] = {};
@@ -679,20 +743,21 @@ cudaError_t launch_n(const LatentParams& p, unsigned int* err, cudaStream_t s) {
   cfg.gridDim = dim3(p.n_teams * p.team);
   cfg.blockDim = dim3(kLatentThreads);
   cfg.dynamicSmemBytes = LatentSmem<N>::kTotal;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, p, err);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, kv, p, err);
   if (e != cudaSuccess || p.n_cuts == 0) return e;
   cfg.gridDim = dim3(p.n_cuts * N);
   cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = p.max_parts * 16 * sizeof(float);  // (at most one part a team: 10 KB)
   return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, N);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_attention(int tile_rows, const LatentParams& p, unsigned int* err, cudaStream_t s) {
-  if (tile_rows == 16) return launch_n<16>(p, err, s);
-  if (tile_rows == 32) return launch_n<32>(p, err, s);
-  return launch_n<64>(p, err, s);
+cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& kv, const LatentParams& p, unsigned int* err,
+                                    cudaStream_t s) {
+  if (tile_rows == 16) return launch_n<16>(kv, p, err, s);
+  if (tile_rows == 32) return launch_n<32>(kv, p, err, s);
+  return launch_n<64>(kv, p, err, s);
 }
 
 }  // namespace mixattn
