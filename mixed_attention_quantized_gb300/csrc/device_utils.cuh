@@ -370,12 +370,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   return false;
 }
 
-// The same for a whole warp, of which one lane polls: polls are served lane by lane, and those of 128
-// threads hold up every other barrier operation of the SM (by ~500 cycles each).
-__device__ __forceinline__ bool warp_wait_one(uint64_t* bar, uint32_t parity, unsigned int* err) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err);
-  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+static __device__ __noinline__ void wait_gave_up(unsigned int* err) { set_device_error(err, MIXATTN_DEVERR_TIMEOUT); }
+
+// The same for a converged warp, in as few instructions as it takes: beside busy warps of other roles
+// a role's instructions are fetched slowly (a wait of ~35 instructions for a barrier that was already
+// complete took 350 cycles).
+__device__ __forceinline__ bool warp_wait_fast(uint64_t* bar, uint32_t parity, unsigned int* err) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n add.u32 n, n, 1;\n"
+      " setp.lt.u32 q, n, 0x200000;\n @q bra POLL;\nDONE:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
+  wait_gave_up(err);
+  return false;
 }
 
 // 1-D bulk copy global -> shared through the TMA engine, completing on `bar`.

@@ -67,18 +67,6 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
       : "r"(taddr));
 }
 
-// A whole warp waits, each lane that has a need for a barrier of its own: a poll takes as long for
-// one barrier as for several (~150 cycles beside the MMAs).
-__device__ __forceinline__ bool warp_wait_each(bool need, uint64_t* bar, uint32_t parity, unsigned int* err) {
-  const uint32_t at = smem_u32(bar);
-  for (uint32_t i = 0; i < (1u << 21); ++i) {
-    const bool done = !need || mbar_try_wait_s(at, parity);
-    if (__all_sync(0xFFFFFFFFu, done)) return true;
-  }
-  if (need) set_device_error(err, MIXATTN_DEVERR_TIMEOUT);
-  return false;
-}
-
 // The same layout the other way.
 __device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -185,7 +173,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const uint32_t r_dst = smem_u32(smem + L::kRope) + sw128_off(r_key, lane & 7);
     // The queries go first: behind the keys of 2.5 steps, asked for by every SM at once, they would take
     // 5 us, and nothing starts without them.
-    if (it0 < it1) ok = warp_wait_one(q_asked, 0u, err);
+    if (it0 < it1) ok = warp_wait_fast(q_asked, 0u, err);
     for (int i = it0; ok && i < it1; ++i) {
       const LatentItem it = p.items[i];
       const LatentRowInfo ri = p.rows[it.row];
@@ -203,11 +191,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
         }
         const int ia = __shfl_sync(0xFFFFFFFFu, pid, (2 * s) & 31), ib = __shfl_sync(0xFFFFFFFFu, pid, (2 * s + 1) & 31);
-        {  // lane 0: the unit's slot, lane 1: the position keys'
-          const bool unit = lane == 0 && round > 0, rope = lane == 1 && g >= 2;
-          ok = warp_wait_each(unit || rope, lane == 0 ? &unit_empty[slot] : &rope_empty[g & 1],
-                              (uint32_t)((lane == 0 ? round - 1 : (g >> 1) - 1) & 1), err);
-        }
+        if (round > 0) ok = warp_wait_fast(&unit_empty[slot], (uint32_t)((round - 1) & 1), err);
+        if (ok && g >= 2) ok = warp_wait_fast(&rope_empty[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);
         if (!ok) break;
         // Keys past the row's end, and those of a page that is not there, are zeros: what the cache
         // holds there may be anything, and 0 x NaN is not 0.
@@ -261,14 +246,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           slot -= NU;
           ++round;
         }
-        if (__any_sync(0xFFFFFFFFu, *abort_flag)) ok = false;
-        if (!ok) break;
       }
+      if (__any_sync(0xFFFFFFFFu, *abort_flag)) ok = false;
     }
     if (!ok && lane == 0) *abort_flag = 1;
     // nothing asked for may still be on its way when the CTA ends
     cp_async_wait_all();
-    for (int k = max(0, g - 4); k < g; ++k) warp_wait_one(&full[k & 3], (uint32_t)((k >> 2) & 1), err);
+    for (int k = max(0, g - 4); k < g; ++k) warp_wait_fast(&full[k & 3], (uint32_t)((k >> 2) & 1), err);
   } else if (warp >= kMmaWarp) {
     // ======================= MMA: S (the first warp's elected lane), PV (the second's) =======================
     // (Two warps: one that did both would hold a PV that could run behind an S whose keys are still on
@@ -293,10 +277,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       const int n_steps = __shfl_sync(0xFFFFFFFFu, t.there ? (t.n_pages + 1) / 2 : 0, 0);
       if (n_steps == 0) continue;
       if (is_s) {
-        ok = warp_wait_one(q_full, (uint32_t)(n_item & 1), err);
+        ok = warp_wait_fast(q_full, (uint32_t)(n_item & 1), err);
         for (int s = 0; ok && s < n_steps; ++s, ++g) {
-          ok = warp_wait_one(&full[g & 3], (uint32_t)((g >> 2) & 1), err);
-          if (ok && g >= 2) ok = warp_wait_one(&p_full[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);  // S(g - 2) read
+          ok = warp_wait_fast(&full[g & 3], (uint32_t)((g >> 2) & 1), err);
+          if (ok && g >= 2) ok = warp_wait_fast(&p_full[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);  // S(g - 2) read
           if (!ok) break;
           fence_proxy_async_smem();  // (the copies are the generic proxy's)
           tc_fence_after();
@@ -338,8 +322,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         }
       } else {
         for (int s = 0; ok && s < n_steps; ++s, ++g) {
-          ok = warp_wait_one(&p_full[g & 1], (uint32_t)((g >> 1) & 1), err);
-          if (ok && s == 0 && n_item > 0) ok = warp_wait_one(o_free, (uint32_t)((n_item - 1) & 1), err);
+          ok = warp_wait_fast(&p_full[g & 1], (uint32_t)((g >> 1) & 1), err);
+          if (ok && s == 0 && n_item > 0) ok = warp_wait_fast(o_free, (uint32_t)((n_item - 1) & 1), err);
           if (!ok) break;
           // (the keys landed before S(g), and were fenced there: by another thread, so once more here)
           fence_proxy_async_smem();
@@ -476,7 +460,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         float al0 = 1.f, al1 = 1.f;
         bool need = false;
         if (rows_here) {
-          ok = warp_wait_one(&s_full[g & 1], (uint32_t)((g >> 1) & 1), err) && ok;
+          ok = warp_wait_fast(&s_full[g & 1], (uint32_t)((g >> 1) & 1), err) && ok;
           tc_fence_after();
           uint32_t v[32];
           tmem_ld_16x64(tmem + lane_base + kSCol + kSBuf * (g & 1), v);
@@ -545,7 +529,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             alpha_s[rr0 + 8] = al1;
           }
           bar_any(kBarGroup, kGroup, false);
-          ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err) && ok;
+          ok = warp_wait_fast(pv_done, (uint32_t)((g - 1) & 1), err) && ok;
           tc_fence_after();
 #pragma unroll 1
           for (int b = 0; b < 4 * N / 16; ++b) {
@@ -559,7 +543,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
           tmem_wait_st();
         } else if (g > 0) {
-          ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err) && ok;  // P(g - 1) has been read
+          ok = warp_wait_fast(pv_done, (uint32_t)((g - 1) & 1), err) && ok;  // P(g - 1) has been read
         }
         if (rows_here) {
           uint8_t* p0 = smem + L::kP + rr0 * 128 + 4 * c;
@@ -584,7 +568,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       // the next item's queries: the last S of this one is done
       write_q(i + 1, false);
       // ---- the item's output ----
-      ok = warp_wait_one(pv_done, (uint32_t)((g - 1) & 1), err);
+      ok = warp_wait_fast(pv_done, (uint32_t)((g - 1) & 1), err);
       tc_fence_after();
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
