@@ -234,14 +234,6 @@ __device__ __forceinline__ uint4 ldg_u128(const void* p) {
   return v;
 }
 
-// 32 bytes, 32-byte aligned.
-__device__ __forceinline__ void stg256(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
-                                       uint32_t g, uint32_t h) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
-               "r"(f), "r"(g), "r"(h)
-               : "memory");
-}
-
 // ---------------------------------------------------------------------------
 // Per-thread asynchronous copies global -> shared (decode staging rings)
 // ---------------------------------------------------------------------------

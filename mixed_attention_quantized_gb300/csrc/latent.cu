@@ -213,7 +213,7 @@ struct LatentTiling {
 };
 
 // Pages that an item costs beside its own: its queries' load, first step and output.
-constexpr int kItemPages = 3;
+constexpr int kItemPages = 5;
 // Pages of an item, at least, where a row is cut.
 constexpr int kMinItemPages = 6;
 constexpr int kMaxTeam = 16;

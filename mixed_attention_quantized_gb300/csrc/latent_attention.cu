@@ -5,7 +5,7 @@
 // A CTA takes a tile of N (16, 32 or 64) rows and walks a range of the row's pages, 64 keys (two
 // pages) a step, each loaded once into shared memory and used from there by both products:
 //   S   [64 rows][64 keys]   = Q (A, rows of 576) x K^T (B): M = 64, rows past N unused; Q in TMEM as far
-//                              as there is room (N = 64: 256 elements of 576), or its reads and those of K
+//                              as there is room (N = 64: 384 elements of 576, with one buffer of S), or its reads and those of K
 //                              fill shared memory's bandwidth, and copies and barriers wait behind them
 //   O^T [512 elements][N]   += c^T (A, the same bytes read MN-major) x P^T (B): four blocks of 128
 // O^T rather than O because 64 rows of 512 fp32 would fill TMEM alone, and because N then follows
@@ -37,13 +37,14 @@ constexpr int kStepKeys = 64;  // keys of a step: two pages
 
 template <int N>
 struct LatentSmem {
-  static constexpr int kTmemSlabs = N == 64 ? 4 : (N == 32 ? 8 : 9);  // of a row's nine 64-element slabs, those held in TMEM
+  static constexpr int kSBuffers = N == 64 ? 1 : 2;
+  static constexpr int kTmemSlabs = N == 64 ? 6 : (N == 32 ? 8 : 9);  // of a row's nine 64-element slabs, those held in TMEM
   static constexpr int kQSlab = N * 128;                 // 64 elements of N rows, swizzled
   static constexpr int kQ = 0;                           // the other slabs
   static constexpr int kP = kQ + (9 - kTmemSlabs) * kQSlab;          // [N][64 keys]
   static constexpr int kRope = (kP + N * 128 + 1023) / 1024 * 1024;  // 2 slots of [64 keys][64]
   static constexpr int kUnit0 = kRope + 2 * 8192;        // slots of [2][64 keys][64]
-  static constexpr int kUnits = N == 64 ? 10 : 12;
+  static constexpr int kUnits = N == 64 ? 11 : 12;
   static constexpr int kStat = kUnit0 + kUnits * 16384;  // alpha[64], l[64]
   static constexpr int kBar = kStat + 512;
   static constexpr int kTotal = kBar + 512 + 1024;       // + slack for 1024-byte alignment
@@ -112,10 +113,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ LatentParams p, unsigned int* err) {
   using L = LatentSmem<N>;
   constexpr int NU = L::kUnits;
-  // O^T blocks; two buffers of S, 64 rows in the lower 16 lanes of each warp's 32; the slabs of Q held
-  // here, two elements a column, in the same lanes
-  constexpr int QT = L::kTmemSlabs;
-  constexpr uint32_t kOCol = 0, kSCol = 4 * N, kSBuf = 64, kQCol = kSCol + 2 * kSBuf;
+  // O^T blocks; one or two buffers of S, 64 rows in the lower 16 lanes of each warp's 32; the slabs of Q
+  // held here, two elements a column, in the same lanes
+  constexpr int QT = L::kTmemSlabs, SB = L::kSBuffers;
+  constexpr uint32_t kOCol = 0, kSCol = 4 * N, kSBuf = 64, kQCol = kSCol + SB * kSBuf;
   constexpr uint32_t kTmemCols = 512;
   static_assert(kQCol + 32 * QT <= kTmemCols, "TMEM");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -125,13 +126,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   uint64_t* unit_empty = full + 4;         // [NU] by a commit: the unit's block of O^T done
   uint64_t* rope_empty = unit_empty + NU;  // [2] by a commit
   uint64_t* q_full = rope_empty + 2;       // by the softmax warps: the item's queries written
-  uint64_t* s_full = q_full + 1;           // [2] S(g) in buffer g % 2
-  uint64_t* p_full = s_full + 2;           // [2] by the softmax warps: S(g) read, P(g) written, O^T rescaled
-  uint64_t* pv_done = p_full + 2;          // PV(g) done
+  uint64_t* s_full = q_full + 1;           // [SB] S(g) in buffer g % SB
+  uint64_t* s_read = s_full + SB;          // [SB] by the softmax warps: S(g) read
+  uint64_t* p_full = s_read + SB;          // by the softmax warps: P(g) written, O^T rescaled
+  uint64_t* pv_done = p_full + 1;          // PV(g) done
   uint64_t* o_free = pv_done + 1;          // by the softmax warps: the item's O^T read
   uint64_t* q_asked = o_free + 1;          // by the softmax warps: the first item's queries are on their way
   uint64_t* fin = q_asked + 1;             // [2]
-  constexpr int kNumBars = NU + 16;
+  constexpr int kNumBars = NU + 13 + 2 * SB;
   static_assert(8 * kNumBars + 8 <= 512, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -140,7 +142,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
     for (int i = 0; i < 4; ++i) mbar_init(full + i, 32 * kLoadWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(p_full + i, kSoftmaxWarps);
+    for (int i = 0; i < SB; ++i) mbar_init(s_read + i, N / 16);  // (the warps with rows)
+    mbar_init(p_full, kSoftmaxWarps);
     mbar_init(o_free, kSoftmaxWarps);
     mbar_init(q_full, kSoftmaxWarps);
     mbar_init(q_asked, kSoftmaxWarps);
@@ -280,11 +283,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         ok = warp_wait_fast(q_full, (uint32_t)(n_item & 1), err);
         for (int s = 0; ok && s < n_steps; ++s, ++g) {
           ok = warp_wait_fast(&full[g & 3], (uint32_t)((g >> 2) & 1), err);
-          if (ok && g >= 2) ok = warp_wait_fast(&p_full[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);  // S(g - 2) read
+          if (ok && g >= SB) ok = warp_wait_fast(&s_read[g % SB], (uint32_t)((g / SB - 1) & 1), err);
           if (!ok) break;
           fence_proxy_async_smem();  // (the copies are the generic proxy's)
           tc_fence_after();
-          const uint32_t s_tm = tmem + kSCol + kSBuf * (g & 1);
+          const uint32_t s_tm = tmem + kSCol + kSBuf * (g % SB);
           // 128 elements of Q against a unit of the keys, those of Q in TMEM first
 #pragma unroll 1
           for (int b = 0; b < 4; ++b) {
@@ -315,14 +318,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
               if (QT == 9) tc_mma_ts_w(s_tm, tmem + kQCol + 256 + 8 * k, rd + ((32 * k) >> 4), kHi, kIdescS, 1u);
               else tc_mma_ss_w(s_tm, dQ + (((8 - QT) * L::kQSlab + 32 * k) >> 4), kHi, rd + ((32 * k) >> 4), kHi, kIdescS, 1u);
             }
-            tc_commit(&s_full[g & 1]);
+            tc_commit(&s_full[g % SB]);
             tc_commit(&rope_empty[g & 1]);
           }
           __syncwarp();
         }
       } else {
         for (int s = 0; ok && s < n_steps; ++s, ++g) {
-          ok = warp_wait_fast(&p_full[g & 1], (uint32_t)((g >> 1) & 1), err);
+          ok = warp_wait_fast(p_full, (uint32_t)(g & 1), err);
           if (ok && s == 0 && n_item > 0) ok = warp_wait_fast(o_free, (uint32_t)((n_item - 1) & 1), err);
           if (!ok) break;
           // (the keys landed before S(g), and were fenced there: by another thread, so once more here)
@@ -460,12 +463,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         float al0 = 1.f, al1 = 1.f;
         bool need = false;
         if (rows_here) {
-          ok = warp_wait_fast(&s_full[g & 1], (uint32_t)((g >> 1) & 1), err) && ok;
+          ok = warp_wait_fast(&s_full[g % SB], (uint32_t)((g / SB) & 1), err) && ok;
           tc_fence_after();
           uint32_t v[32];
-          tmem_ld_16x64(tmem + lane_base + kSCol + kSBuf * (g & 1), v);
+          tmem_ld_16x64(tmem + lane_base + kSCol + kSBuf * (g % SB), v);
           tmem_wait_ld();
           tc_fence_before();
+          if (lane == 0) mbar_arrive(&s_read[g % SB]);
           const int key0 = kPage * (it.page0 + 2 * s);
           if (!ok_a || !ok_b || key0 + kStepKeys > mask_hi) {
             uint32_t vis[2][2];  // [row][page]
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           stop = true;
           break;
         }
-        if (lane == 0) mbar_arrive(&p_full[g & 1]);
+        if (lane == 0) mbar_arrive(p_full);
       }
       if (stop) {
         *abort_flag = 1;
@@ -595,10 +599,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         uint32_t o[16];
         tmem_ld16(tmem + lane_base + kOCol + 16 * b, o);
         tmem_wait_ld();
-        if (it.n_parts > 1) {  // [16 rows of a block][element][row]: 64 bytes a lane
-          float* dst = p.part_o + ((part * (4 * N / 16) + b) * 128 + 32 * warp + lane) * 16;
-          stg256(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
-          stg256(dst + 8, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
+        if (it.n_parts > 1) {  // four rows at a time, [element][row]: 512 bytes a warp and store
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (part * (4 * N / 16) + b) * 512 + 32 * warp + lane;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[128 * e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           continue;
         }
         // lanes 2 k, 2 k + 1 hold two neighbouring elements of every row: the even lane takes both of
@@ -662,17 +666,17 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, 
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* src = p.part_o + (((int64_t)cut.slot * n + b) * 128 + 32 * (u & 3) + lane) * 16;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((int64_t)cut.slot * n + b) * 512 + 32 * (u & 3) + lane;
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int q = warp; q < cut.n_parts; q += 4) {
-    const float4* x = reinterpret_cast<const float4*>(src + (int64_t)q * n * 128 * 16);
+    const float4* x = src + (int64_t)q * n * 512;
     const float4* w = reinterpret_cast<const float4*>(weights + 16 * q);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float4 y = __ldcs(x + e), f = w[e];
+      const float4 y = __ldcs(x + 128 * e), f = w[e];
       // (where a part has no key of the row any value may stand)
       acc[4 * e] = fmaf(f.x, f.x != 0.f ? y.x : 0.f, acc[4 * e]);
       acc[4 * e + 1] = fmaf(f.y, f.y != 0.f ? y.y : 0.f, acc[4 * e + 1]);
