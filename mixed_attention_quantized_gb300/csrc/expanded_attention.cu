@@ -2,12 +2,13 @@
 // [128 | 64], keys of [128 | 64] whose last 64 all heads share, values of 128; causal.
 //
 // A tile is up to 256 queries of one head, in two groups of 128 rows that share each KV tile of 128
-// keys. One MMA thread issues PV_0(j-1) QK_0(j) PV_1(j-1) QK_1(j), and while one group's MMAs run
-// the other's softmax does: as the page-scaled chunk tiles (page_attention.cuh), whose softmax
-// against a reference that seldom moves this shares, with TMA in place of the conversion warps.
-// TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each, P of 32 keys over the first half of their scores.
+// keys; a group has an MMA warp and four softmax warps (a row a thread) of its own:
+//   MMA      PV(j-1), then S(j), each as soon as P(j-1) and the KV tile are there
+//   softmax  S(j) -> P(j) as the page-scaled chunk tiles do it (page_attention.cuh): one pass against a
+//            reference that seldom moves, 32 keys at a time, P over the first half of its own scores
+// While one group's softmax runs the other's MMAs do.  TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each.
 // Shared memory: Q of both groups (96 KB) and a ring of eight 16 KB slots of 128 keys x 64 elements,
-// three to a K tile (the third the shared position keys) and two to a V tile.
+// three to a K tile (the third the shared position keys) and two to a V tile, loaded by TMA.
 //
 // Values past a row's last key belong to the next row and may be anything: a warp of its own zeroes
 // them in the slots of the row's last KV tile before their MMAs.
@@ -19,7 +20,7 @@ namespace mixattn {
 
 namespace {
 
-constexpr int kExpandedThreads = 32 * 11;  // softmax 0-7, TMA 8, MMA 9, zeroing 10
+constexpr int kExpandedThreads = 32 * 12;  // softmax 0-7, MMA 8 and 9, TMA 10, zeroing 11
 constexpr int kSlots = 8;
 
 struct ExpandedSmem {
@@ -30,6 +31,11 @@ struct ExpandedSmem {
   static constexpr int kTotal = kBar + 256 + 1024;    // + slack for 1024-byte alignment
   static_assert(kTotal <= 227 * 1024, "the tile does not fit in shared memory");
 };
+
+// The ring's slots in order: K(0) K(0) K(0) V(0) V(0) K(1) ...; t counts the CTA's KV tiles.
+// K(t) takes the slots of K(t - 2)'s last and of V(t - 2), V(t) those of K(t - 1)'s first two.
+__device__ __forceinline__ int k_slot(int t, int s) { return (5 * t + s) % kSlots; }
+__device__ __forceinline__ int v_slot(int t, int s) { return (5 * t + 3 + s) % kSlots; }
 
 // KV tiles of an item that a group takes part in: those with a key that its last query sees.
 __device__ __forceinline__ int group_steps(const ExpandedItem& it, int group) {
@@ -49,17 +55,19 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* full = bars;                 // [8] slot loaded (a row's last V tile: and zeroed)
-  uint64_t* empty = full + kSlots;       // [8] slot read, by a commit
-  uint64_t* tail = empty + kSlots;       // [2] slots of a row's last V tile loaded
-  uint64_t* q_full = tail + 2;
-  uint64_t* q_empty = q_full + 1;        // the item's last S done
-  uint64_t* s_full = q_empty + 1;        // [2] a group's S done (and its PV before)
-  uint64_t* p_full = s_full + 2;         // [2] by 4 warps: P written, O rescaled
-  uint64_t* o_full = p_full + 2;         // [2] a group's last PV of the item done
-  uint64_t* o_free = o_full + 2;         // [2] by 4 warps: O read
-  uint64_t* fin = o_free + 2;
-  constexpr int kNumBars = 2 * kSlots + 2 + 2 + 8 + 1;
+  uint64_t* k_full = bars;               // [2] K(t) in t % 2, by TMA
+  uint64_t* v_full = bars + 2;           // [2] V(t), by TMA or (a row's last) by the zeroing warp
+  uint64_t* k_empty = bars + 4;          // [2] by both MMA warps: K(t) read
+  uint64_t* v_empty = bars + 6;          // [2] by both MMA warps: V(t) read
+  uint64_t* tail = bars + 8;             // a row's last V tile loaded
+  uint64_t* q_full = bars + 9;
+  uint64_t* q_empty = bars + 10;         // by both MMA warps: the item's last S done
+  uint64_t* s_full = bars + 11;          // [2] a group's S done (and its PV before)
+  uint64_t* p_full = bars + 13;          // [2] by 4 warps: P written, O rescaled
+  uint64_t* o_full = bars + 15;          // [2] a group's last PV of the item done
+  uint64_t* o_free = bars + 17;          // [2] by 4 warps: O read
+  uint64_t* fin = bars + 19;             // [2]
+  constexpr int kNumBars = 21;
   static_assert(8 * kNumBars + 8 <= 256, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
 
@@ -67,9 +75,12 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(k_empty + i, 2);
+      mbar_init(v_empty + i, 2);
       mbar_init(p_full + i, 4);
       mbar_init(o_free + i, 4);
     }
+    mbar_init(q_empty, 2);
     fence_mbar_init();
     tma_prefetch_map(&q_map);
     tma_prefetch_map(&k_map);
@@ -110,7 +121,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       const int pos = it.pos + min(prow, it.count - 1);
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
-        ok = warp_wait(&s_full[gq], n_s & 1, err);
+        ok = warp_wait_fast(&s_full[gq], n_s & 1, err);
         if (!ok) break;
         ++n_s;
         tc_fence_after();
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[gq]);
       }
       if (!ok) break;
-      ok = warp_wait(&o_full[gq], n_o & 1, err);
+      ok = warp_wait_fast(&o_full[gq], n_o & 1, err);
       ++n_o;
       if (!ok) break;
       tc_fence_after();
@@ -193,168 +204,174 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[gq]);
     }
-  } else if (warp == 8) {
-    // ======================= TMA (one thread) =======================
-    if (lane == 0) {
-      int slot = 0, round = 0, n_item = 0;
-      int tail_slot = -1, tail_round = 0;  // the last tail's second slot
-      bool ok = true;
-      auto take = [&] {  // the next slot, free
-        if (round > 0) ok = mbar_wait(&empty[slot], (uint32_t)((round - 1) & 1), err);
-        return ok;
-      };
-      auto next = [&] {
-        if (++slot == kSlots) {
-          slot = 0;
-          ++round;
-        }
-      };
-      for (int i = it0; ok && i < it1; ++i) {
-        const ExpandedItem it = p.items[i];
-        const int n = max(group_steps(it, 0), group_steps(it, 1));
-        if (n == 0) continue;
-        if (n_item > 0) ok = mbar_wait(q_empty, (uint32_t)((n_item - 1) & 1), err);
-        if (!ok) break;
-        ++n_item;
-        const int groups = it.count > 128 ? 2 : 1;
+  } else if (warp == 10) {
+    // ======================= TMA (its elected lane) =======================
+    int t = 0, n_item = 0, last_tail = -2;  // KV tiles and items so far; the last tail's KV tile
+    bool ok = true;
+    const uint32_t ring = smem_u32(smem + L::kRing);
+    for (int i = it0; ok && i < it1; ++i) {
+      const ExpandedItem it = p.items[i];
+      const int n = max(group_steps(it, 0), group_steps(it, 1));
+      if (n == 0) continue;
+      if (n_item > 0) ok = warp_wait_fast(q_empty, (uint32_t)((n_item - 1) & 1), err);
+      if (!ok) break;
+      ++n_item;
+      const int groups = it.count > 128 ? 2 : 1;
+      if (elect_one()) {
         mbar_arrive_expect_tx(q_full, groups * L::kGroupQ);
         for (int g = 0; g < groups; ++g)
           for (int s = 0; s < 3; ++s)
-            tma_load_3d(smem_u32(smem + L::kQ + g * L::kGroupQ + s * 16384), &q_map, 64 * s, it.head,
-                        it.q_start + 128 * g, smem_u32(q_full));
-        for (int j = 0; ok && j < n; ++j) {
-          const int key = (it.kv0 + j) * kChunkN, y = it.k_start + key;
-          for (int s = 0; s < 3; ++s) {
-            if (!take()) break;
-            const uint32_t dst = smem_u32(smem + L::kRing + slot * 16384), bar = smem_u32(&full[slot]);
-            mbar_arrive_expect_tx(&full[slot], 16384);
-            if (s < 2) tma_load_3d(dst, &k_map, 64 * s, it.head, y, bar);
-            else tma_load_2d(dst, &kr_map, 0, y, bar);
-            next();
-          }
-          const bool is_tail = key + kChunkN > it.seq_len;
-          // (one tail at a time on its barriers)
-          if (is_tail && tail_slot >= 0) ok = ok && mbar_wait(&full[tail_slot], (uint32_t)(tail_round & 1), err);
-          for (int s = 0; ok && s < 2; ++s) {
-            if (!take()) break;
-            if (is_tail) {
-              tail_slot = slot;
-              tail_round = round;
-            }
-            uint64_t* b = is_tail ? &tail[s] : &full[slot];
-            mbar_arrive_expect_tx(b, 16384);
-            tma_load_3d(smem_u32(smem + L::kRing + slot * 16384), &v_map, 64 * s, it.head, y, smem_u32(b));
-            next();
-          }
+            tma_load_3d(smem_u32(smem + L::kQ) + g * L::kGroupQ + s * 16384, &q_map, 64 * s, it.head, it.q_start + 128 * g,
+                        smem_u32(q_full));
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j, ++t) {
+        const int key = (it.kv0 + j) * kChunkN, y = it.k_start + key;
+        if (t >= 2) ok = warp_wait_fast(&v_empty[t & 1], (uint32_t)(((t >> 1) - 1) & 1), err);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&k_full[t & 1]);
+          mbar_arrive_expect_tx(&k_full[t & 1], 3 * 16384);
+          tma_load_3d(ring + k_slot(t, 0) * 16384, &k_map, 0, it.head, y, bar);
+          tma_load_3d(ring + k_slot(t, 1) * 16384, &k_map, 64, it.head, y, bar);
+          tma_load_2d(ring + k_slot(t, 2) * 16384, &kr_map, 0, y, bar);
         }
+        __syncwarp();
+        const bool is_tail = key + kChunkN > it.seq_len;
+        if (t >= 1) ok = warp_wait_fast(&k_empty[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1), err);
+        // (one tail at a time on its barrier; an earlier one than the last V tile has been read)
+        if (ok && is_tail && last_tail == t - 1 && t > 0)
+          ok = warp_wait_fast(&v_full[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1), err);
+        if (!ok) {
+          ++t;
+          break;
+        }
+        if (elect_one()) {
+          uint64_t* b = is_tail ? tail : &v_full[t & 1];
+          mbar_arrive_expect_tx(b, 2 * 16384);
+          tma_load_3d(ring + v_slot(t, 0) * 16384, &v_map, 0, it.head, y, smem_u32(b));
+          tma_load_3d(ring + v_slot(t, 1) * 16384, &v_map, 64, it.head, y, smem_u32(b));
+        }
+        __syncwarp();
+        if (is_tail) last_tail = t;
       }
-      // nothing asked for may still be on its way when the CTA ends (which, but for an error, it is not)
-      for (int k = 0; k < kSlots; ++k) {
-        const int rd = k < slot ? round : round - 1;
-        if (rd >= 0) mbar_wait(&full[k], (uint32_t)(rd & 1), err);
-      }
-      if (n_item > 0) mbar_wait(q_full, (uint32_t)((n_item - 1) & 1), err);
     }
-    __syncwarp();
-  } else if (warp == 10) {
+    // nothing asked for may still be on its way when the CTA ends (which, but for an error, it is not)
+    for (int k = max(0, t - 2); k < t; ++k) {
+      warp_wait_fast(&k_full[k & 1], (uint32_t)((k >> 1) & 1), err);
+      if (ok || k < t - 1) warp_wait_fast(&v_full[k & 1], (uint32_t)((k >> 1) & 1), err);
+    }
+    if (n_item > 0) warp_wait_fast(q_full, (uint32_t)((n_item - 1) & 1), err);
+  } else if (warp == 11) {
     // ======================= zeroing of a row's last V tile =======================
     bool ok = true;
-    int slot = 0;  // slots before the item
+    int t = 0;  // KV tiles before the item
     uint32_t n_tail = 0;
     for (int i = it0; ok && i < it1; ++i) {
       const ExpandedItem it = p.items[i];
       const int n = max(group_steps(it, 0), group_steps(it, 1));
+      t += n;
       if (n > 0 && (it.kv0 + n) * kChunkN > it.seq_len) {
         const int valid = it.seq_len - (it.kv0 + n - 1) * kChunkN;  // keys of the tile that are the row's
-        for (int s = 0; ok && s < 2; ++s) {
-          ok = warp_wait(&tail[s], n_tail & 1, err);
-          if (!ok) break;
-          const int at = (slot + 5 * (n - 1) + 3 + s) % kSlots;
-          uint4* rows = reinterpret_cast<uint4*>(smem + L::kRing + at * 16384);
-          for (int k = 8 * valid + lane; k < 8 * kChunkN; k += 32) rows[k] = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[at]);
-        }
+        ok = warp_wait_fast(tail, n_tail & 1, err);
+        if (!ok) break;
         ++n_tail;
+        for (int s = 0; s < 2; ++s) {
+          uint4* rows = reinterpret_cast<uint4*>(smem + L::kRing + v_slot(t - 1, s) * 16384);
+          for (int k = 8 * valid + lane; k < 8 * kChunkN; k += 32) rows[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[(t - 1) & 1]);
       }
-      slot = (slot + 5 * n) % kSlots;
     }
-  } else if (lane == 0) {
-    // ======================= MMA (one thread) =======================
+  } else {
+    // ======================= MMA (the elected lane of each group's warp) =======================
     constexpr uint32_t kIdescS = idesc_f16_f32(128, kChunkN, false, false);
     constexpr uint32_t kIdescO = idesc_f16_f32(128, 64, false, true);
-    const uint64_t dQ = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
-    const uint64_t dK = sw128_desc(smem_u32(smem + L::kRing), 16, 1024);
-    const uint64_t dV = sw128_desc(smem_u32(smem + L::kRing), 16384, 1024);  // (N = 64: one slab)
+    const int g = warp - 8;
+    auto lo = [](uint64_t d) { return (uint32_t)d; };
+    const uint32_t dQ = lo(sw128_desc(smem_u32(smem + L::kQ), 16, 1024)) + g * (L::kGroupQ >> 4);
+    const uint32_t dK = lo(sw128_desc(smem_u32(smem + L::kRing), 16, 1024));
+    const uint32_t dV = lo(sw128_desc(smem_u32(smem + L::kRing), 16384, 1024));  // (N = 64: one slab)
+    constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);              // the upper word of them all
+    const uint32_t s_tm = tmem + 128 * g, o_tm = s_tm + kOCol;
     bool ok = true;
-    int base = 0;             // slots before the item, over all the CTA's
-    uint32_t n_item = 0, n_p[2] = {0, 0}, n_out[2] = {0, 0};
-    auto wait_slot = [&](int k) { return mbar_wait(&full[k % kSlots], (uint32_t)((k / kSlots) & 1), err); };
-    for (int i = it0; ok && i < it1; ++i) {
+    int t = 0;
+    uint32_t n_item = 0, n_p = 0, n_out = 0;
+    const int first = __shfl_sync(0xFFFFFFFFu, it0, 0), end = __shfl_sync(0xFFFFFFFFu, it1, 0);
+    for (int i = first; ok && i < end; ++i) {
       const ExpandedItem it = p.items[i];
-      const int ng[2] = {group_steps(it, 0), group_steps(it, 1)};
-      const int n = max(ng[0], ng[1]);
+      // (control flow and operands the same in all lanes, and known to be)
+      const int mine = __shfl_sync(0xFFFFFFFFu, group_steps(it, g), 0);
+      const int n = max(mine, __shfl_sync(0xFFFFFFFFu, group_steps(it, g ^ 1), 0));
       if (n == 0) continue;
-      ok = mbar_wait(q_full, n_item & 1, err);
+      ok = warp_wait_fast(q_full, n_item & 1, err);
       for (int j = 0; ok && j <= n; ++j) {
-        const int kb = base + 5 * j, vb = base + 5 * (j - 1) + 3;  // first slots of K(j), V(j - 1)
-        bool k_here = false, v_here = false;
-        for (int g = 0; ok && g < 2; ++g) {
-          const uint32_t s_tm = tmem + 128 * g, o_tm = s_tm + kOCol;
-          if (j > 0 && j <= ng[g]) {
-            ok = mbar_wait(&p_full[g], n_p[g] & 1, err);
-            ++n_p[g];
-            if (ok && j == 1 && n_out[g] > 0) ok = mbar_wait(&o_free[g], (n_out[g] - 1) & 1, err);
-            for (int s = 0; ok && !v_here && s < 2; ++s) ok = wait_slot(vb + s);
-            v_here = true;
+        const int tv = t + j - 1, tk = t + j;
+        if (j > 0) {
+          ok = warp_wait_fast(&v_full[tv & 1], (uint32_t)((tv >> 1) & 1), err);
+          if (ok && j <= mine) {
+            ok = warp_wait_fast(&p_full[g], n_p & 1, err);
+            ++n_p;
+            if (ok && j == 1 && n_out > 0) ok = warp_wait_fast(&o_free[g], (n_out - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
-            // (the two slabs are separate MMAs of N = 64: they need not be neighbours in the ring)
+            // (a V tile's two slabs need not be neighbours in the ring: MMAs of N = 64)
+            if (elect_one()) {
+              const uint32_t acc = j > 1 ? 1u : 0u;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint64_t vd = dV + (uint64_t)((((vb + s) % kSlots) * 16384) >> 4);
+              for (int s = 0; s < 2; ++s) {
+                const uint32_t vd = dV + v_slot(tv, s) * (16384 >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {  // keys 16 kk ..: columns 32 (kk / 2) + 8 (kk % 2) of S
-                const uint64_t b = vd + (uint64_t)((kk * 16 * 128) >> 4);
-                tc_mma_ts(o_tm + 64 * s, s_tm + 32 * (kk >> 1) + 8 * (kk & 1), b, kIdescO, j > 1 || kk > 0 ? 1u : 0u);
+                for (int k = 0; k < 8; ++k)  // keys 16 k ..: columns 32 (k / 2) + 8 (k % 2) of S
+                  tc_mma_ts_w(o_tm + 64 * s, s_tm + 32 * (k >> 1) + 8 * (k & 1), vd + ((k * 16 * 128) >> 4), kHi, kIdescO,
+                              k > 0 ? 1u : acc);
               }
+              tc_commit(&v_empty[tv & 1]);
+              if (j == mine) tc_commit(&o_full[g]);
             }
-            if (j == ng[g]) {
-              tc_commit(&o_full[g]);
-              ++n_out[g];
-            }
+            __syncwarp();
+            n_out += j == mine;
+          } else if (ok && elect_one()) {
+            mbar_arrive(&v_empty[tv & 1]);
           }
-          // (V(j - 1) is read when the last group that takes it is done)
-          if (j > 0 && (g == 1 || j > ng[1]) && !(g == 1 && j > ng[1])) {
-            for (int s = 0; s < 2; ++s) tc_commit(&empty[(vb + s) % kSlots]);
-          }
-          if (j < ng[g]) {
-            for (int s = 0; ok && !k_here && s < 3; ++s) ok = wait_slot(kb + s);
-            k_here = true;
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < 3; ++s)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc_mma_ss(s_tm, dQ + (uint64_t)((g * L::kGroupQ + s * 16384 + 32 * k) >> 4),
-                          dK + (uint64_t)((((kb + s) % kSlots) * 16384 + 32 * k) >> 4), kIdescS, s + k > 0 ? 1u : 0u);
-            tc_commit(&s_full[g]);
-          }
+          __syncwarp();
+          if (!ok) break;
         }
-        if (!ok) break;
         if (j < n) {
-          for (int s = 0; s < 3; ++s) tc_commit(&empty[(kb + s) % kSlots]);
+          ok = warp_wait_fast(&k_full[tk & 1], (uint32_t)((tk >> 1) & 1), err);
+          if (!ok) break;
+          if (elect_one()) {
+            if (j < mine) {
+              tc_fence_after();
+#pragma unroll
+              for (int s = 0; s < 3; ++s) {
+                const uint32_t kd = dK + k_slot(tk, s) * (16384 >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  tc_mma_ss_w(s_tm, dQ + ((s * 16384 + 32 * k) >> 4), kHi, kd + ((32 * k) >> 4), kHi, kIdescS,
+                              s + k > 0 ? 1u : 0u);
+              }
+              tc_commit(&s_full[g]);
+              tc_commit(&k_empty[tk & 1]);
+              if (j == n - 1) tc_commit(q_empty);
+            } else {
+              mbar_arrive(&k_empty[tk & 1]);
+              if (j == n - 1) tc_commit(q_empty);  // (behind the group's last S)
+            }
+          }
+          __syncwarp();
         }
-        if (j == n - 1) tc_commit(q_empty);
       }
-      base += 5 * n;
+      t += n;
       ++n_item;
     }
-    // nothing this thread started may still run when TMEM is released
-    tc_commit(fin);
-    mbar_wait(fin, 0u, err);
+    // nothing the lane started may still run when TMEM is released
+    if (elect_one()) {
+      tc_commit(fin + g);
+      mbar_wait(fin + g, 0u, err);
+    }
   }
   __syncwarp();
   tc_fence_before();
