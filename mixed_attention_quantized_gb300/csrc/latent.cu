@@ -214,8 +214,10 @@ struct LatentTiling {
 
 // Pages that an item costs beside its own: its queries' load, first step and output.
 constexpr int kItemPages = 5;
-// Pages of an item, at least, where a row is cut.
-constexpr int kMinItemPages = 6;
+// Pages of an item, at least, where a row is cut: a step's chain of latencies is about as long as a part's
+// way through the join (one row of 300 tokens, 16 heads, with 2 / 4 / 6: 14.5 / 16.4 / 16.5 us, of 1000 14.6 /
+// 14.5 / 16.5, of 8000 26.7 / 20.8 / 20.6; 64 rows of 500 to 2000, 128 heads 80 / 73 / 80).
+int64_t min_item_pages(int64_t row_pages) { return row_pages <= 16 ? 2 : 4; }
 constexpr int kMaxTeam = 16;
 
 int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, const int32_t* kinds, const int32_t* seq,
@@ -275,7 +277,7 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
   T.n_teams = std::max(1, n_sm / T.team);
 
   // The passes' pages in a line, cut into one run for each team: every team the same number of pages
-  // (an item counts kItemPages more), no item shorter than kMinItemPages unless its row is.
+  // (an item counts kItemPages more), no item shorter than min_item_pages unless its row is.
   std::vector<LatentItem> items;
   std::vector<int32_t> team_first(1, 0);
   std::vector<LatentCut> cuts;
@@ -294,7 +296,7 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
   for (int r = 0; r < n_rows; ++r) {
     const int64_t n_tiles = tiles_of(r);
     for (int64_t mt0 = 0; mt0 < n_tiles; mt0 += T.team) {
-      const int64_t n_pages = pages_of(r, mt0 + T.team);
+      const int64_t n_pages = pages_of(r, mt0 + T.team), least = min_item_pages(n_pages);
       const size_t first = items.size();
       int64_t at = 0;
       while (at < n_pages) {
@@ -303,12 +305,12 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
         int64_t take = left;
         if (!last_team) {
           const int64_t room = (int64_t)(share * (team + 1) - used - kItemPages + 0.5);
-          if (room < kMinItemPages && !empty()) {
+          if (room < least && !empty()) {
             next_team();
             continue;
           }
-          take = std::max<int64_t>(kMinItemPages, room) & ~(int64_t)1;  // whole steps
-          if (left - take < kMinItemPages) take = left;
+          take = std::max<int64_t>(least, room) & ~(int64_t)1;  // whole steps
+          if (left - take < least) take = left;
         }
         if (items.size() > (size_t)INT32_MAX / 2) return MIXATTN_ERR_INVALID_ARG;
         items.push_back(LatentItem{r, (int32_t)mt0, (int32_t)at, (int32_t)take, 0, 1, 0, 0});
@@ -466,7 +468,6 @@ struct mixattn_latent_plan {
   mixattn_latent_cache cache;
   int32_t heads = 0, max_pages = 0;
   double scale = 0.0;
-  CUtensorMap kv_map;
   LatentTiling tiling;
   PlanList list;
 };
@@ -554,12 +555,6 @@ int mixattn_latent_plan_create(mixattn_latent_plan** plan_out, const mixattn_lat
   p->heads = num_heads;
   p->scale = softmax_scale;
   st = mixattn_latent_plan_update(p, n_rows, row_kinds, seq_lens, q_offsets, max_pages, workspace_bytes);
-  if (st == MIXATTN_OK) {
-    const uint64_t dims[3] = {kLatentRow, kPage, (uint64_t)cache->num_pages};
-    const int64_t strides[2] = {kLatentRow, kLatentRow * kPage};
-    const uint32_t box[3] = {64, kPage, 1};
-    if (!make_map(&p->kv_map, cache->data, 3, dims, strides, box)) st = MIXATTN_ERR_CUDA;
-  }
   if (st != MIXATTN_OK) {
     delete p;
     return st;
@@ -625,7 +620,7 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.n_cuts = T.n_cuts;
   p.max_parts = T.max_parts;
   p.scale_log2 = (float)(plan->scale * kLog2e);
-  return launch_latent_attention(T.tile_rows, plan->kv_map, p, err, s) == cudaSuccess ? MIXATTN_OK
+  return launch_latent_attention(T.tile_rows, p, err, s) == cudaSuccess ? MIXATTN_OK
                                                                                             : MIXATTN_ERR_CUDA;
 }
 

@@ -51,8 +51,7 @@ struct LatentParams {
 };
 
 // tile_rows: 16, 32 or 64 (query, head) rows a CTA
-cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& kv, const LatentParams& p, unsigned int* err,
-                                    cudaStream_t s);
+cudaError_t launch_latent_attention(int tile_rows, const LatentParams& p, unsigned int* err, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Expanded form

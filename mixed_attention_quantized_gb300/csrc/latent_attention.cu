@@ -22,7 +22,6 @@
 
 #include "latent.h"
 #include "page_attention.cuh"
-#include "tma.cuh"
 
 namespace mixattn {
 
@@ -30,7 +29,6 @@ namespace {
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kLoadWarps = 4;
-constexpr int kTmaWarps = 2;  // of these, whose units TMA loads
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kLatentThreads = 32 * (kMmaWarp + 2);
 constexpr int kStepKeys = 64;  // keys of a step: two pages
@@ -110,7 +108,7 @@ __device__ __forceinline__ LatentTile tile_of(const LatentParams& p, const Laten
 
 template <int N>
 __global__ void __launch_bounds__(kLatentThreads, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ LatentParams p, unsigned int* err) {
+    latent_kernel(const __grid_constant__ LatentParams p, unsigned int* err) {
   using L = LatentSmem<N>;
   constexpr int NU = L::kUnits;
   // O^T blocks; one or two buffers of S, 64 rows in the lower 16 lanes of each warp's 32; the slabs of Q
@@ -122,8 +120,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* full = bars;                   // [4] step g's keys, in g % 4, by the copies of all load warps' lanes
-  uint64_t* unit_empty = full + 4;         // [NU] by a commit: the unit's block of O^T done
+  // step g's keys in g % 4, by the copies of the load warps' lanes: units 0-2 and the position keys; unit 3,
+  // whose slot is the last to be free
+  uint64_t* full = bars;                   // [4]
+  uint64_t* full3 = full + 4;              // [4]
+  uint64_t* unit_empty = full3 + 4;        // [NU] by a commit: the unit's block of O^T done
   uint64_t* rope_empty = unit_empty + NU;  // [2] by a commit
   uint64_t* q_full = rope_empty + 2;       // by the softmax warps: the item's queries written
   uint64_t* s_full = q_full + 1;           // [SB] S(g) in buffer g % SB
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   uint64_t* o_free = pv_done + 1;          // by the softmax warps: the item's O^T read
   uint64_t* q_asked = o_free + 1;          // by the softmax warps: the first item's queries are on their way
   uint64_t* fin = q_asked + 1;             // [2]
-  constexpr int kNumBars = NU + 13 + 2 * SB;
+  constexpr int kNumBars = NU + 17 + 2 * SB;
   static_assert(8 * kNumBars + 8 <= 512, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -141,7 +142,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(full + i, 32 * kLoadWarps);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(full + i, 32 * (kLoadWarps - 1));
+      mbar_init(full3 + i, 32);
+    }
     for (int i = 0; i < SB; ++i) mbar_init(s_read + i, N / 16);  // (the warps with rows)
     mbar_init(p_full, kSoftmaxWarps);
     mbar_init(o_free, kSoftmaxWarps);
@@ -169,10 +173,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const int w = warp - kSoftmaxWarps;
     int slot = w, round = 0, g = 0;
     bool ok = true;
+    uint64_t* filled = w < 3 ? full : full3;
     const int ch = lane & 15, kk = lane >> 4;  // the lane's 16-byte chunk of a key's 256 bytes, and its key of two
     const uint32_t dst_lane = smem_u32(smem + L::kUnit0) + (ch >> 3) * 8192 + kk * 128;
-    // position keys: the warp's 16 of a step, chunk lane % 8 of keys lane / 8 + 4 q
-    const int r_key = 16 * w + (lane >> 3);
+    // position keys: warps 0 and 1 load a page's, chunk lane % 8 of keys lane / 8 + 4 q
+    const int r_key = 32 * (w & 1) + (lane >> 3);
     const uint32_t r_dst = smem_u32(smem + L::kRope) + sw128_off(r_key, lane & 7);
     // The queries go first: behind the keys of 2.5 steps, asked for by every SM at once, they would take
     // 5 us, and nothing starts without them.
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         }
         const int ia = __shfl_sync(0xFFFFFFFFu, pid, (2 * s) & 31), ib = __shfl_sync(0xFFFFFFFFu, pid, (2 * s + 1) & 31);
         if (round > 0) ok = warp_wait_fast(&unit_empty[slot], (uint32_t)((round - 1) & 1), err);
-        if (ok && g >= 2) ok = warp_wait_fast(&rope_empty[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);
+        if (ok && w < 2 && g >= 2) ok = warp_wait_fast(&rope_empty[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);
         if (!ok) break;
         // Keys past the row's end, and those of a page that is not there, are zeros: what the cache
         // holds there may be anything, and 0 x NaN is not 0.
@@ -207,35 +212,24 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         const uint16_t* sa = pa + kk * kLatentRow + 128 * w + 8 * ch;
         const uint16_t* sb = pb + kk * kLatentRow + 128 * w + 8 * ch;
         const uint32_t dst = dst_lane + slot * 16384;
-        const uint16_t* rs = (w < 2 ? pa : pb) + (r_key & 31) * kLatentRow + kLatent + 8 * (lane & 7);
+        const uint16_t* rs = (w == 0 ? pa : pb) + (r_key & 31) * kLatentRow + kLatent + 8 * (lane & 7);
         const uint32_t rd = r_dst + (g & 1) * 8192;
         if (whole) {
+          if (w < 2) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)  // (keys 4 apart: chunk bit 2 flips)
-            cp_async16_s((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow));
-          if (w < kTmaWarps) {
-            if (elect_one()) {
-              const uint32_t bar = smem_u32(&full[g & 3]), at = smem_u32(smem + L::kUnit0) + slot * 16384;
-              mbar_expect_tx(&full[g & 3], 16384);
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                tma_load_3d(at + c * 8192, &kv_map, 128 * w + 64 * c, 0, ia, bar);
-                tma_load_3d(at + c * 8192 + 4096, &kv_map, 128 * w + 64 * c, 0, ib, bar);
-              }
-            }
-            __syncwarp();
-          } else {
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              cp_async16_s(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
-                           (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow));
+            for (int q = 0; q < 8; ++q)  // (keys 4 apart: chunk bit 2 flips)
+              cp_async16_s((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow));
           }
-        } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int key = r_key + 4 * q;
-            cp_async16_or_zero((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow),
-                               (w < 2 ? ia : ib) >= 0 && key < valid);
+          for (int q = 0; q < 32; ++q)
+            cp_async16_s(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
+                         (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow));
+        } else {
+          if (w < 2) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              cp_async16_or_zero((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow),
+                                 (w == 0 ? ia : ib) >= 0 && r_key + 4 * q < valid);
           }
 #pragma unroll 4
           for (int q = 0; q < 32; ++q)
@@ -243,7 +237,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                                (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow),
                                (q < 16 ? ia : ib) >= 0 && 2 * q + kk < valid);
         }
-        cp_async_arrive(&full[g & 3]);  // (a slot is taken again four steps on, long after its MMAs)
+        cp_async_arrive(&filled[g & 3]);  // (taken again four steps on, long after its MMAs)
         slot += 4;
         if (slot >= NU) {
           slot -= NU;
@@ -255,7 +249,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (!ok && lane == 0) *abort_flag = 1;
     // nothing asked for may still be on its way when the CTA ends
     cp_async_wait_all();
-    for (int k = max(0, g - 4); k < g; ++k) warp_wait_fast(&full[k & 3], (uint32_t)((k >> 2) & 1), err);
   } else if (warp >= kMmaWarp) {
     // ======================= MMA: S (the first warp's elected lane), PV (the second's) =======================
     // (Two warps: one that did both would hold a PV that could run behind an S whose keys are still on
@@ -288,16 +281,32 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           fence_proxy_async_smem();  // (the copies are the generic proxy's)
           tc_fence_after();
           const uint32_t s_tm = tmem + kSCol + kSBuf * (g % SB);
+          if (elect_one()) {
+            const uint32_t rd = dR + (g & 1) * (8192 >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (QT == 9) tc_mma_ts_w(s_tm, tmem + kQCol + 256 + 8 * k, rd + ((32 * k) >> 4), kHi, kIdescS, k > 0 ? 1u : 0u);
+              else tc_mma_ss_w(s_tm, dQ + (((8 - QT) * L::kQSlab + 32 * k) >> 4), kHi, rd + ((32 * k) >> 4), kHi, kIdescS, k > 0 ? 1u : 0u);
+            }
+            tc_commit(&rope_empty[g & 1]);
+          }
+          __syncwarp();
           // 128 elements of Q against a unit of the keys, those of Q in TMEM first
 #pragma unroll 1
           for (int b = 0; b < 4; ++b) {
-            const uint32_t kd = dK + slot * (16384 >> 4), acc = b > 0 ? 1u : 0u;
+            if (b == 3) {
+              ok = warp_wait_fast(&full3[g & 3], (uint32_t)((g >> 2) & 1), err);
+              if (!ok) break;
+              fence_proxy_async_smem();
+              tc_fence_after();
+            }
+            const uint32_t kd = dK + slot * (16384 >> 4);
             if (2 * b < QT) {
               if (elect_one()) {
                 const uint32_t qt = tmem + kQCol + 64 * b;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                  tc_mma_ts_w(s_tm, qt + 8 * k, kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, k > 0 ? 1u : acc);
+                  tc_mma_ts_w(s_tm, qt + 8 * k, kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, 1u);
               }
             } else {
               if (elect_one()) {
@@ -305,22 +314,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                   tc_mma_ss_w(s_tm, qd + (((k >> 2) * L::kQSlab + 32 * (k & 3)) >> 4), kHi,
-                              kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, k > 0 ? 1u : acc);
+                              kd + (((k >> 2) * 8192 + 32 * (k & 3)) >> 4), kHi, kIdescS, 1u);
               }
             }
             __syncwarp();
             if (++slot == NU) slot = 0;
           }
-          if (elect_one()) {
-            const uint32_t rd = dR + (g & 1) * (8192 >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (QT == 9) tc_mma_ts_w(s_tm, tmem + kQCol + 256 + 8 * k, rd + ((32 * k) >> 4), kHi, kIdescS, 1u);
-              else tc_mma_ss_w(s_tm, dQ + (((8 - QT) * L::kQSlab + 32 * k) >> 4), kHi, rd + ((32 * k) >> 4), kHi, kIdescS, 1u);
-            }
-            tc_commit(&s_full[g % SB]);
-            tc_commit(&rope_empty[g & 1]);
-          }
+          if (!ok) break;
+          if (elect_one()) tc_commit(&s_full[g % SB]);
           __syncwarp();
         }
       } else {
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, 
 }
 
 template <int N>
-cudaError_t launch_n(const CUtensorMap& kv, const LatentParams& p, unsigned int* err, cudaStream_t s) {
+cudaError_t launch_n(const LatentParams& p, unsigned int* err, cudaStream_t s) {
   {
     static std::mutex mu;
     static bool configured[kMaxDevices] = {};
@@ -731,7 +732,7 @@ cudaError_t launch_n(const CUtensorMap& kv, const LatentParams& p, unsigned int*
   cfg.gridDim = dim3(p.n_teams * p.team);
   cfg.blockDim = dim3(kLatentThreads);
   cfg.dynamicSmemBytes = LatentSmem<N>::kTotal;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, kv, p, err);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, p, err);
   if (e != cudaSuccess || p.n_cuts == 0) return e;
   cfg.gridDim = dim3(p.n_cuts * N);
   cfg.blockDim = dim3(128);
@@ -741,11 +742,10 @@ cudaError_t launch_n(const CUtensorMap& kv, const LatentParams& p, unsigned int*
 
 }  // namespace
 
-cudaError_t launch_latent_attention(int tile_rows, const CUtensorMap& kv, const LatentParams& p, unsigned int* err,
-                                    cudaStream_t s) {
-  if (tile_rows == 16) return launch_n<16>(kv, p, err, s);
-  if (tile_rows == 32) return launch_n<32>(kv, p, err, s);
-  return launch_n<64>(kv, p, err, s);
+cudaError_t launch_latent_attention(int tile_rows, const LatentParams& p, unsigned int* err, cudaStream_t s) {
+  if (tile_rows == 16) return launch_n<16>(p, err, s);
+  if (tile_rows == 32) return launch_n<32>(p, err, s);
+  return launch_n<64>(p, err, s);
 }
 
 }  // namespace mixattn
