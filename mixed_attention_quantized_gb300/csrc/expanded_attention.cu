@@ -382,33 +382,54 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
   }
 }
 
-// Joins the parts of cut tiles: a warp a query, four elements a lane.
+// Joins the parts of cut tiles: a warp takes four queries, four elements a lane; the loads of a part
+// wait for nothing but the cut.
+constexpr int kJoinRows = 16;  // queries of a CTA
+
 __global__ void __launch_bounds__(128) expanded_join_kernel(const ExpandedParams p) {
   wait_for_upload();
-  constexpr int kPer = kExpandedRows / 4;
+  constexpr int kPer = kExpandedRows / kJoinRows;
   const ExpandedCut cut = p.cuts[blockIdx.x / kPer];
-  const int row = 4 * (blockIdx.x % kPer) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int row = kJoinRows * (blockIdx.x % kPer) + 4 * (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= cut.count) return;
   const float2* ml = p.part_ml + (int64_t)cut.slot * kExpandedRows + row;
   const float* src = p.part_o + ((int64_t)cut.slot * kExpandedRows + row) * kExpandedV + 4 * lane;
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int q = 0; q < cut.n_parts; ++q) m = fmaxf(m, ml[(int64_t)q * kExpandedRows].x);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int q = 0; q < cut.n_parts; ++q) {
-    const float2 x = ml[(int64_t)q * kExpandedRows];
-    if (x.x == -CUDART_INF_F) continue;  // (no key of the row in this part: any value may stand there)
-    const float w = ex2(x.x - m);
-    const float4 y = *reinterpret_cast<const float4*>(src + (int64_t)q * kExpandedRows * kExpandedV);
-    l += w * x.y;
-    o.x += w * y.x;
-    o.y += w * y.y;
-    o.z += w * y.z;
-    o.w += w * y.w;
+  float m[4], l[4];
+  float4 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -CUDART_INF_F;
+    l[i] = 0.f;
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(p.o + ((int64_t)(cut.q_start + row) * p.heads + cut.head) * kExpandedV + 4 * lane) =
-      make_uint2(pack_f16x2_out(o.x * inv, o.y * inv), pack_f16x2_out(o.z * inv, o.w * inv));
+#pragma unroll 2
+  for (int q = 0; q < cut.n_parts; ++q) {
+    float2 x[4];
+    float4 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (rows past the tile's are within the slot: any value may stand there)
+      x[i] = ml[(int64_t)q * kExpandedRows + i];
+      y[i] = __ldcs(reinterpret_cast<const float4*>(src + ((int64_t)q * kExpandedRows + i) * kExpandedV));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (x[i].x == -CUDART_INF_F) continue;  // (no key of the row in this part: the same)
+      const float top = fmaxf(m[i], x[i].x), a = ex2(m[i] - top), w = ex2(x[i].x - top);  // (2^-inf: 0)
+      m[i] = top;
+      l[i] = l[i] * a + w * x[i].y;
+      o[i].x = o[i].x * a + w * y[i].x;
+      o[i].y = o[i].y * a + w * y[i].y;
+      o[i].z = o[i].z * a + w * y[i].z;
+      o[i].w = o[i].w * a + w * y[i].w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (row + i >= cut.count) break;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    *reinterpret_cast<uint2*>(p.o + ((int64_t)(cut.q_start + row + i) * p.heads + cut.head) * kExpandedV + 4 * lane) =
+        make_uint2(pack_f16x2_out(o[i].x * inv, o[i].y * inv), pack_f16x2_out(o[i].z * inv, o[i].w * inv));
+  }
 }
 
 }  // namespace
@@ -441,7 +462,7 @@ cudaError_t launch_expanded_attention(const CUtensorMap& q, const CUtensorMap& k
   cfg.dynamicSmemBytes = ExpandedSmem::kTotal;
   cudaError_t e = cudaLaunchKernelEx(&cfg, expanded_kernel, q, k, kr, v, p, err);
   if (e != cudaSuccess || p.n_cuts == 0) return e;
-  cfg.gridDim = dim3(p.n_cuts * (kExpandedRows / 4));
+  cfg.gridDim = dim3(p.n_cuts * (kExpandedRows / kJoinRows));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, expanded_join_kernel, p);

@@ -219,6 +219,8 @@ constexpr int kItemPages = 5;
 // 14.5 / 16.5, of 8000 26.7 / 20.8 / 20.6; 64 rows of 500 to 2000, 128 heads 80 / 73 / 80).
 int64_t min_item_pages(int64_t row_pages) { return row_pages <= 16 ? 2 : 4; }
 constexpr int kMaxTeam = 16;
+// A tile of more parts is joined by four times as many CTAs.
+constexpr int kManyParts = 8;
 
 int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, const int32_t* kinds, const int32_t* seq,
                         const int32_t* off, int max_pages, int n_sm, LatentTiling* out) {
@@ -326,7 +328,11 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
           items[first + q].slot = (int32_t)slots;
         }
         for (int64_t m = 0; m < T.team && mt0 + m < n_tiles; ++m)
-          cuts.push_back(LatentCut{r, (int32_t)(mt0 + m), (int32_t)(slots + m * parts), parts});
+          for (int32_t quarter = parts > kManyParts ? 0 : -1; quarter < (parts > kManyParts ? 4 : 0); ++quarter)
+            cuts.push_back(LatentCut{(int64_t)rows[r].q_start * heads + (mt0 + m) * T.tile_rows,
+                                   (int32_t)std::min<int64_t>(T.tile_rows, (int64_t)(seq[r] - off[r]) * heads -
+                                                                               (mt0 + m) * T.tile_rows),
+                                   (int32_t)(slots + m * parts), parts, quarter});
         slots += (int64_t)parts * T.team;
         T.max_parts = std::max<int>(T.max_parts, parts);
         if (slots > INT32_MAX) return MIXATTN_ERR_INVALID_ARG;

@@ -31,7 +31,9 @@ struct LatentItem {
 
 // A tile whose parts are to be joined.
 struct LatentCut {
-  int32_t row, mt, slot, n_parts;
+  int64_t row0;  // first (query, head) row of the output
+  int32_t rows, slot, n_parts;
+  int32_t quarter;  // -1: all of each 128 elements; 0 .. 3: 32 of them (tiles of many parts, four entries each)
 };
 
 struct LatentParams {

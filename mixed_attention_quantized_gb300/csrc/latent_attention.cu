@@ -634,67 +634,86 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   }
 }
 
-// Joins the parts of cut tiles: a CTA takes 32 elements of 16 rows, warp w every fourth part.
-__global__ void __launch_bounds__(128) latent_join_kernel(const LatentParams p, int tile_rows) {
+// Joins the parts of cut tiles.  Most tiles have two to four: a CTA takes 128 elements of 16 rows, each half
+// of its threads every second part, and all loads go out together, behind that of the cut.  Of a long row's
+// many parts a CTA takes 32 elements, its eight warps every eighth part.
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, int tile_rows) {
   extern __shared__ float weights[];  // [parts][16]
   __shared__ float inv_l[16];
-  __shared__ float sums[3][16][33];
+  __shared__ float sums[7 * 16 * 32];  // [groups - 1][16][elements]
   wait_for_upload();
-  const LatentCut cut = p.cuts[blockIdx.x / tile_rows];
-  const int u = blockIdx.x % tile_rows, n = tile_rows / 4;       // n units of 16 rows by 128 elements
-  const int b = u >> 2, d0 = 128 * (16 * b / tile_rows) + 32 * (u & 3), col0 = 16 * b % tile_rows;
-  const LatentRowInfo ri = p.rows[cut.row];
-  const int rows = min(tile_rows, (ri.seq_len - ri.q_offset) * p.heads - cut.mt * tile_rows) - col0;  // here
+  const int n = tile_rows / 4;  // units of 16 rows by 128 elements
+  const LatentCut cut = p.cuts[blockIdx.x / n];
+  const int b = blockIdx.x % n, col0 = 16 * b % tile_rows, rows = cut.rows - col0;  // rows here
   if (rows <= 0) return;
-  {
-    // eight threads a row form its parts' weights; a part without a key of the row weighs nothing
-    const int row = threadIdx.x >> 3, k = threadIdx.x & 7;
-    const float2* ml = p.part_ml + (int64_t)cut.slot * tile_rows + col0 + row;
-    float m = -CUDART_INF_F, l = 0.f;
-    if (row < rows)
-      for (int q = k; q < cut.n_parts; q += 8) m = fmaxf(m, ml[(int64_t)q * tile_rows].x);
+  const int width = cut.quarter < 0 ? 128 : 32, groups = 256 / width;
+  const int e0 = threadIdx.x % width, group = threadIdx.x / width, d = max(cut.quarter, 0) * 32 + e0;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((int64_t)cut.slot * n + b) * 512 + d;
+  float4 y[2][4];
+  auto load = [&](int q, float4(&x)[4]) {
+    const float4* at = src + (int64_t)min(q, cut.n_parts - 1) * n * 512;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    for (int q = k; q < cut.n_parts; q += 8) {
-      const float2 x = row < rows ? ml[(int64_t)q * tile_rows] : make_float2(-CUDART_INF_F, 0.f);
+    for (int e = 0; e < 4; ++e) x[e] = __ldcs(at + 128 * e);
+  };
+  load(group, y[0]);
+  load(group + groups, y[1]);
+  {
+    // sixteen threads a row form its parts' weights; a part without a key of the row weighs nothing
+    const int row = threadIdx.x >> 4, k = threadIdx.x & 15;
+    const float2* ml = p.part_ml + (int64_t)cut.slot * tile_rows + col0 + row;
+    auto part = [&](int q) {
+      return row < rows && q < cut.n_parts ? ml[(int64_t)q * tile_rows] : make_float2(-CUDART_INF_F, 0.f);
+    };
+    const float2 first = part(k);
+    float m = first.x, l = 0.f;
+    for (int q = k + 16; q < cut.n_parts; q += 16) m = fmaxf(m, part(q).x);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int q = k; q < cut.n_parts; q += 16) {
+      const float2 x = q == k ? first : part(q);
       const float w = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - m);
       weights[16 * q + row] = w;
       if (w != 0.f) l += w * x.y;
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    for (int o = 1; o < 16; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     if (k == 0) inv_l[row] = l > 0.f ? 1.f / l : 0.f;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((int64_t)cut.slot * n + b) * 512 + 32 * (u & 3) + lane;
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int q = warp; q < cut.n_parts; q += 4) {
-    const float4* x = src + (int64_t)q * n * 512;
+  auto add = [&](int q, const float4(&x)[4]) {
     const float4* w = reinterpret_cast<const float4*>(weights + 16 * q);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float4 y = __ldcs(x + 128 * e), f = w[e];
+      const float4 f = w[e];
       // (where a part has no key of the row any value may stand)
-      acc[4 * e] = fmaf(f.x, f.x != 0.f ? y.x : 0.f, acc[4 * e]);
-      acc[4 * e + 1] = fmaf(f.y, f.y != 0.f ? y.y : 0.f, acc[4 * e + 1]);
-      acc[4 * e + 2] = fmaf(f.z, f.z != 0.f ? y.z : 0.f, acc[4 * e + 2]);
-      acc[4 * e + 3] = fmaf(f.w, f.w != 0.f ? y.w : 0.f, acc[4 * e + 3]);
+      acc[4 * e] = fmaf(f.x, f.x != 0.f ? x[e].x : 0.f, acc[4 * e]);
+      acc[4 * e + 1] = fmaf(f.y, f.y != 0.f ? x[e].y : 0.f, acc[4 * e + 1]);
+      acc[4 * e + 2] = fmaf(f.z, f.z != 0.f ? x[e].z : 0.f, acc[4 * e + 2]);
+      acc[4 * e + 3] = fmaf(f.w, f.w != 0.f ? x[e].w : 0.f, acc[4 * e + 3]);
     }
+  };
+#pragma unroll 1
+  for (int q = group; q < cut.n_parts; q += 2 * groups) {
+    add(q, y[0]);
+    if (q + 2 * groups < cut.n_parts) load(q + 2 * groups, y[0]);
+    if (q + groups < cut.n_parts) add(q + groups, y[1]);
+    if (q + 3 * groups < cut.n_parts) load(q + 3 * groups, y[1]);
   }
-  if (warp > 0) {
+  if (group > 0) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sums[warp - 1][e][lane] = acc[e];
+    for (int e = 0; e < 16; ++e) sums[((group - 1) * 16 + e) * width + e0] = acc[e];
   }
   __syncthreads();
-  if (warp > 0) return;
+  if (group > 0) return;
+  for (int g = 0; g < groups - 1; ++g) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = ((acc[e] + sums[0][e][lane]) + sums[1][e][lane]) + sums[2][e][lane];
-  const int odd = lane & 1;
-  uint16_t* dst = p.o + ((int64_t)ri.q_start * p.heads + cut.mt * tile_rows + col0) * kLatent + d0 + lane - odd;
+    for (int e = 0; e < 16; ++e) acc[e] += sums[(g * 16 + e) * width + e0];
+  }
+  const int odd = d & 1;
+  uint16_t* dst = p.o + (cut.row0 + col0) * kLatent + 128 * (16 * b / tile_rows) + d - odd;
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {  // (as the attention kernel writes its output)
     const float mine = odd ? acc[e + 1] : acc[e];
@@ -734,8 +753,8 @@ cudaError_t launch_n(const LatentParams& p, unsigned int* err, cudaStream_t s) {
   cfg.dynamicSmemBytes = LatentSmem<N>::kTotal;
   cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<N>, p, err);
   if (e != cudaSuccess || p.n_cuts == 0) return e;
-  cfg.gridDim = dim3(p.n_cuts * N);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(p.n_cuts * (N / 4));
+  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = p.max_parts * 16 * sizeof(float);  // (at most one part a team: 10 KB)
   return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, N);
 }
