@@ -54,7 +54,7 @@ typedef struct {
  * A step's new tokens into the cache, in one launch: the latent vectors as they are, the position
  * keys rotated by their positions, and the position parts of the queries rotated into q_out.
  *   rope         a table with rot_dim 64
- *   num_heads    query heads; 0 (q and q_out then ignored) appends only
+ *   num_heads    query heads, <= 65536; 0 (q and q_out then ignored) appends only
  *   q, q_out     64 elements a head, for instance the ends of the heads of a query projection and
  *                of the absorbed queries [n][heads][576]; q_out may be q itself (same strides) and
  *                must not overlap it otherwise, nor k_rope
@@ -83,7 +83,7 @@ int mixattn_latent_export(const mixattn_latent_cache* cache, const int32_t* slot
  * pairs of a row.  Work is cut over the SMs for the whole batch (a row's cuts, and so the last
  * bits of its output, depend on the batch it runs in; the same plan gives the same bits every time).
  *   num_heads      1 .. 128
- *   softmax_scale  > 0, finite (usually 1 / sqrt(128 + 64), times the squared rotary multiplier)
+ *   softmax_scale  1e-20 .. 1e6 (usually 1 / sqrt(128 + 64), times the squared rotary multiplier)
  */
 typedef struct mixattn_latent_plan mixattn_latent_plan;
 

@@ -732,8 +732,9 @@ class LatentPlan:
         if page_table.dtype is not rt.int32 or page_table.shape != self._table or not page_table.is_contiguous():
             raise ValueError(f"page_table: contiguous int32 {list(self._table)} expected, got {page_table.dtype} "
                              f"{tuple(page_table.shape)}")
-        if page_table.get_device() != here:
-            _wrong_device(page_table, "page_table")
+        for x, name in ((page_table, "page_table"), (workspace, "workspace"), (c.data, "cache")):
+            if x.get_device() != here:
+                _wrong_device(x, name)
         if tree_mask is not None:
             _check_mask(tree_mask, self._tree_tokens)
         st = self._lib.mixattn_latent_run(
@@ -792,6 +793,8 @@ class ExpandedPlan:
         vd = _strided_heads(rt, here, v, nk, "v", h, 128)
         ks = _strided_rows(rt, here, k_rope, nk, "k_rope", 64)
         op = _dense(rt, here, o, (nq, h, 128), "o")
+        if workspace.get_device() != here:
+            _wrong_device(workspace, "workspace")
         st = self._lib.mixattn_expanded_run(
             self._handle, ctypes.byref(qd), ctypes.byref(kd), k_rope.data_ptr(), ks, ctypes.byref(vd), op,
             workspace.data_ptr(), workspace.nbytes, stream.cuda_stream if stream is not None else rt.raw_stream(here))

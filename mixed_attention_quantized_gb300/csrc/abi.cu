@@ -452,6 +452,13 @@ int PlanList::upload(uint8_t* dst, size_t bytes, cudaStream_t s) {
   return MIXATTN_OK;
 }
 
+int PlanList::note_capture(cudaStream_t s) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MIXATTN_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) captured_ = true;
+  return MIXATTN_OK;
+}
+
 PlanList::~PlanList() {
   if (copy_recorded_ && copied_) cudaEventSynchronize(copied_);
   if (copied_) cudaEventDestroy(copied_);

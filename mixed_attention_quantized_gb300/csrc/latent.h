@@ -37,10 +37,8 @@ struct LatentCut {
 };
 
 struct LatentParams {
-  const LatentRowInfo* rows;
-  const LatentItem* items;
-  const int32_t* team_first;  // [n_teams + 1]
-  const LatentCut* cuts;
+  const uint8_t* image;  // the plan's list in the workspace
+  int32_t rows, items, team_first, cuts;  // offsets in the list: LatentRowInfo, LatentItem, int32 [n_teams + 1], LatentCut
   const uint16_t* q;          // [total_q][heads][576]
   const uint16_t* data;       // the cache
   const int32_t* page_table;
@@ -50,6 +48,15 @@ struct LatentParams {
   float2* part_ml;  // [slots][tile rows]: reference (log2 units) and sum
   int32_t tree_words, max_pages, num_pages, heads, team, n_teams, n_cuts, max_parts;
   float scale_log2;
+  int32_t inline_list;  // the list is here, and not in the workspace
+  uint4 list[96];
+
+#ifdef __CUDACC__
+  template <class T>
+  __device__ __forceinline__ const T* at(int32_t offset) const {
+    return reinterpret_cast<const T*>((inline_list ? reinterpret_cast<const uint8_t*>(list) : image) + offset);
+  }
+#endif
 };
 
 // tile_rows: 16, 32 or 64 (query, head) rows a CTA

@@ -166,7 +166,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int team = blockIdx.x / p.team, member = blockIdx.x - team * p.team;
-  const int it0 = p.team_first[team], it1 = p.team_first[team + 1];
+  const LatentItem* items = p.at<LatentItem>(p.items);
+  const LatentRowInfo* row_list = p.at<LatentRowInfo>(p.rows);
+  const int it0 = p.at<int32_t>(p.team_first)[team], it1 = p.at<int32_t>(p.team_first)[team + 1];
 
   if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
     // ======================= load (warp w: unit w of every step) =======================
@@ -183,8 +185,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // 5 us, and nothing starts without them.
     if (it0 < it1) ok = warp_wait_fast(q_asked, 0u, err);
     for (int i = it0; ok && i < it1; ++i) {
-      const LatentItem it = p.items[i];
-      const LatentRowInfo ri = p.rows[it.row];
+      const LatentItem it = items[i];
+      const LatentRowInfo ri = row_list[it.row];
       const LatentTile t = tile_of(p, it, ri, member, N);
       if (!t.there || t.n_pages == 0) continue;
       const int32_t* pt_row = p.page_table + (int64_t)it.row * p.max_pages + it.page0;
@@ -267,8 +269,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     int g = 0, n_item = 0, slot = 0;
     const int first = __shfl_sync(0xFFFFFFFFu, it0, 0), end = __shfl_sync(0xFFFFFFFFu, it1, 0);
     for (int i = first; ok && i < end; ++i) {
-      const LatentItem it = p.items[i];
-      const LatentTile t = tile_of(p, it, p.rows[it.row], member, N);
+      const LatentItem it = items[i];
+      const LatentTile t = tile_of(p, it, row_list[it.row], member, N);
       // (control flow and operands the same in all lanes, and known to be)
       const int n_steps = __shfl_sync(0xFFFFFFFFu, t.there ? (t.n_pages + 1) / 2 : 0, 0);
       if (n_steps == 0) continue;
@@ -374,8 +376,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // elements of a row: 32 bytes.
     auto write_q = [&](int i, bool first) {
       for (; i < it1; ++i) {
-        const LatentItem it = p.items[i];
-        const LatentRowInfo ri = p.rows[it.row];
+        const LatentItem it = items[i];
+        const LatentRowInfo ri = row_list[it.row];
         const LatentTile t = tile_of(p, it, ri, member, N);
         if (!t.there || t.n_pages == 0) continue;
         if (rows_here) {
@@ -433,8 +435,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     };
     write_q(it0, true);
     for (int i = it0; i < it1; ++i) {
-      const LatentItem it = p.items[i];
-      const LatentRowInfo ri = p.rows[it.row];
+      const LatentItem it = items[i];
+      const LatentRowInfo ri = row_list[it.row];
       const LatentTile t = tile_of(p, it, ri, member, N);
       if (!t.there) continue;
       const int64_t part = (int64_t)it.slot + (int64_t)member * it.n_parts + it.part;
@@ -637,13 +639,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 // Joins the parts of cut tiles.  Most tiles have two to four: a CTA takes 128 elements of 16 rows, each half
 // of its threads every second part, and all loads go out together, behind that of the cut.  Of a long row's
 // many parts a CTA takes 32 elements, its eight warps every eighth part.
-__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, int tile_rows) {
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LatentParams p, int tile_rows) {
   extern __shared__ float weights[];  // [parts][16]
   __shared__ float inv_l[16];
   __shared__ float sums[7 * 16 * 32];  // [groups - 1][16][elements]
   wait_for_upload();
   const int n = tile_rows / 4;  // units of 16 rows by 128 elements
-  const LatentCut cut = p.cuts[blockIdx.x / n];
+  const LatentCut cut = p.at<LatentCut>(p.cuts)[blockIdx.x / n];
   const int b = blockIdx.x % n, col0 = 16 * b % tile_rows, rows = cut.rows - col0;  // rows here
   if (rows <= 0) return;
   const int width = cut.quarter < 0 ? 128 : 32, groups = 256 / width;

@@ -28,6 +28,8 @@ class PlanList {
   int fill(const std::vector<uint8_t>& image);
   // Enqueues the copy of the list's first `bytes` (a multiple of 16) to `dst`.
   int upload(uint8_t* dst, size_t bytes, cudaStream_t s);
+  // For a run that takes the list otherwise: only notes that it is captured, if it is.
+  int note_capture(cudaStream_t s);
   // Some run was captured: replays read the pinned buffer at any time, so it keeps its list.
   bool captured() const { return captured_; }
 

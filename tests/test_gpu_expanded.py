@@ -59,6 +59,13 @@ def test_many_tiles_a_cta():
     _compare(rows, _run(rows, 32, *x), *x)
 
 
+def test_rows_of_many_kv_tiles_after_one_another():
+    """Several tiles a CTA, the ends of their rows more than two KV tiles apart."""
+    rows = [(700, 0), (1000, 0), (900, 500), (450, 0), (1100, 1000)]
+    x = _inputs(rows, 32, 15)
+    _compare(rows, _run(rows, 32, *x), *x)
+
+
 def test_long_rows_are_cut_and_joined():
     rows = [(6000, 5700)]
     x = _inputs(rows, 2, 6)

@@ -30,7 +30,8 @@ def _close(got, want, bound):
 
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("scaling", [0, 2])
-@pytest.mark.parametrize("n,heads", [(1, 1), (1, 128), (7, 3), (70, 16), (33, 128), (300, 0)])
+@pytest.mark.parametrize("n,heads", [(1, 1), (1, 128), (7, 3), (70, 16), (33, 128), (300, 0), (2501, 8), (2503, 0),
+                                     (1300, 33)])
 def test_append(interleaved, scaling, n, heads):
     import torch
     import mixed_attention_quantized_gb300 as mq
