@@ -57,7 +57,7 @@ typedef struct {
  *   num_heads    query heads, <= 65536; 0 (q and q_out then ignored) appends only
  *   q, q_out     64 elements a head, for instance the ends of the heads of a query projection and
  *                of the absorbed queries [n][heads][576]; q_out may be q itself (same strides) and
- *                must not overlap it otherwise, nor k_rope
+ *                must not overlap it otherwise (from its first element to its last), nor c_new or k_rope
  *   c_new        fp16 [n_new], 512 elements every c_stride;  k_rope  64 elements every k_stride
  *                (16-byte aligned, strides multiples of 8 and >= 512 and 64)
  *   positions, slot_mapping   device int32 [n_new]; slots as for mixattn_kv_append_quant (a skipped
@@ -103,7 +103,9 @@ int mixattn_latent_plan_update(mixattn_latent_plan* plan, int32_t n_rows, const 
  *   o           device fp16 [total_q][num_heads][512], 16-byte aligned
  *   workspace   device, >= workspace_bytes, 256-byte aligned, contents of no account
  * A page id outside the cache sets MIXATTN_DEVERR_PAGE_ID and its keys are left out; a query that
- * sees no key gets zeros.  May be captured into a graph, with mixattn_run's conditions.
+ * sees no key gets zeros.  Keys that no query of a row sees (unused nodes of a tree) need not have
+ * been appended; one that some see and that is not finite may reach the row's other outputs.  May be
+ * captured into a graph, with mixattn_run's conditions.
  */
 int mixattn_latent_run(const mixattn_latent_plan* plan, const void* q, const int32_t* page_table,
                        const uint32_t* tree_mask, int32_t mask_words, void* o, void* workspace,

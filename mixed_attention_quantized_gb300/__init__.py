@@ -699,6 +699,7 @@ class LatentPlan:
                  softmax_scale: float):
         self._lib = load()
         self.cache, self.num_heads = cache, int(num_heads)
+        self._data = cache.data  # the plan reads this memory, whatever the cache holds later
         self._handle = ctypes.c_void_p(0)
         ws = ctypes.c_size_t(0)
         st = self._lib.mixattn_latent_plan_create(
@@ -732,7 +733,7 @@ class LatentPlan:
         if page_table.dtype is not rt.int32 or page_table.shape != self._table or not page_table.is_contiguous():
             raise ValueError(f"page_table: contiguous int32 {list(self._table)} expected, got {page_table.dtype} "
                              f"{tuple(page_table.shape)}")
-        for x, name in ((page_table, "page_table"), (workspace, "workspace"), (c.data, "cache")):
+        for x, name in ((page_table, "page_table"), (workspace, "workspace"), (self._data, "cache")):
             if x.get_device() != here:
                 _wrong_device(x, name)
         if tree_mask is not None:

@@ -90,7 +90,8 @@ __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r
 // What one tile of an item covers.
 struct LatentTile {
   int f0, rows;           // first (query, head) row of the row's, rows here
-  int n_pages;            // pages with a key that some query of the tile sees
+  int n_keys;             // keys of the row up to the last that some query of the tile may see
+  int n_pages;            // the item's pages with such keys
   bool there;
 };
 
@@ -102,6 +103,7 @@ __device__ __forceinline__ LatentTile tile_of(const LatentParams& p, const Laten
   t.rows = min(N, total - t.f0);
   t.there = t.rows > 0;
   const int last = ri.tree_start >= 0 ? ri.seq_len - 1 : ri.q_offset + (t.f0 + max(t.rows, 1) - 1) / p.heads;
+  t.n_keys = last + 1;
   t.n_pages = max(0, min(it.n_pages, last / kPage + 1 - it.page0));
   return t;
 }
@@ -204,11 +206,24 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         if (round > 0) ok = warp_wait_fast(&unit_empty[slot], (uint32_t)((round - 1) & 1), err);
         if (ok && w < 2 && g >= 2) ok = warp_wait_fast(&rope_empty[g & 1], (uint32_t)(((g >> 1) - 1) & 1), err);
         if (!ok) break;
-        // Keys past the row's end, and those of a page that is not there, are zeros: what the cache
-        // holds there may be anything, and 0 x NaN is not 0.
+        // Keys that no query of the tile sees, and those of a page that is not there, are zeros: what the
+        // cache holds there may be anything, and 0 x NaN is not 0.
         const int key0 = kPage * (it.page0 + 2 * s);
-        const int valid = ri.seq_len - key0;  // keys of the step that exist
-        const bool whole = ia >= 0 && ib >= 0 && valid >= kStepKeys;
+        uint32_t seen_a = low_bits(t.n_keys - key0), seen_b = low_bits(t.n_keys - key0 - kPage);
+        if (ri.tree_start >= 0 && key0 + kStepKeys > ri.q_offset) {
+          seen_a = seen_b = 0;
+          const int q1 = (t.f0 + t.rows - 1) / p.heads;
+          for (int q = t.f0 / p.heads + lane; q <= q1; q += 32) {
+            const uint32_t* tm = p.tree_mask + (int64_t)(ri.tree_start + q) * p.tree_words;
+            seen_a |= tree_bits(tm, p.tree_words, ri.seq_len - ri.q_offset, key0 - ri.q_offset);
+            seen_b |= tree_bits(tm, p.tree_words, ri.seq_len - ri.q_offset, key0 + kPage - ri.q_offset);
+          }
+          seen_a = __reduce_or_sync(0xFFFFFFFFu, seen_a);
+          seen_b = __reduce_or_sync(0xFFFFFFFFu, seen_b);
+        }
+        if (ia < 0) seen_a = 0;
+        if (ib < 0) seen_b = 0;
+        const bool whole = (seen_a & seen_b) == 0xFFFFFFFFu;
         const uint16_t* pa = p.data + (int64_t)max(ia, 0) * (kPage * kLatentRow);
         const uint16_t* pb = p.data + (int64_t)max(ib, 0) * (kPage * kLatentRow);
         const uint16_t* sa = pa + kk * kLatentRow + 128 * w + 8 * ch;
@@ -231,13 +246,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               cp_async16_or_zero((rd ^ ((q & 1) << 6)) + q * 512, rs + q * (4 * kLatentRow),
-                                 (w == 0 ? ia : ib) >= 0 && r_key + 4 * q < valid);
+                                 (((w == 0 ? seen_a : seen_b) >> ((lane >> 3) + 4 * q)) & 1u) != 0u);
           }
 #pragma unroll 4
           for (int q = 0; q < 32; ++q)
             cp_async16_or_zero(dst + q * 256 + (((ch & 7) ^ ((2 * q + kk) & 7)) << 4),
                                (q < 16 ? sa : sb) + (q & 15) * (2 * kLatentRow),
-                               (q < 16 ? ia : ib) >= 0 && 2 * q + kk < valid);
+                               (((q < 16 ? seen_a : seen_b) >> (2 * (q & 15) + kk)) & 1u) != 0u);
         }
         cp_async_arrive(&filled[g & 3]);  // (taken again four steps on, long after its MMAs)
         slot += 4;

@@ -70,6 +70,38 @@ def test_trees(heads):
     assert bool((got[2] == 0).all())
 
 
+@pytest.mark.parametrize("heads", [1, 16, 128])
+def test_nodes_that_nobody_sees_may_hold_anything(heads):
+    """A padded tree: the masks of its last nodes are empty, no other names them, and their rows of the cache
+    are NaN; no output of the batch notices."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    rng = np.random.default_rng(71)
+    rows = [(TREE, 70, 30), (DECODE, 40, 39), (TREE, 203, 131), (TREE, 64, 0)]
+    used = [25, 7, 1]
+    masks = []
+    for (s, o), u in zip([r[1:] for r in rows if r[0] == TREE], used):
+        m = np.zeros((s - o, s - o), dtype=bool)
+        m[:u, :u] = tr.random_tree(u, rng)
+        masks.append(m)
+    cache, pt, slots = la.paged([r[1] for r in rows], 72)
+    q = la.queries(sum(s - o for _, s, o in rows), heads, 576, 73)
+    want = _run(cache, pt, rows, heads, q, masks)
+    flat = cache.data.view(-1, 576)
+    for r, u in zip((0, 2, 3), used):
+        flat[slots[r][rows[r][2] + u:]] = float("nan")
+    got = _run(cache, pt, rows, heads, q, masks)
+    assert mq.device_error(clear=True) == 0
+    assert torch.equal(got, want) and bool(got.isfinite().all())
+    assert bool((got[-63:] == 0).all())  # (no context: they see nothing)
+
+
+def test_a_tree_of_1024_nodes_and_one_of_a_single_node():
+    rng = np.random.default_rng(75)
+    masks = [tr.random_tree(1024, rng, 3), tr.random_tree(1, rng)]
+    _check([(TREE, 1124, 100), (TREE, 1, 0)], 8, masks, seed=76)
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_long_rows_are_cut_and_joined(heads):
     _check([(DECODE, 9000, 8999), (DECODE, 20, 19), (DECODE, 4001, 4000), (CHUNK, 3000, 2997)], heads, seed=41)
