@@ -2,7 +2,7 @@
  * mixattn.h -- C ABI of the mixed-batch attention library for GB300 (sm_103a).
  *
  * One launch serves chunked-prefill rows (a causal query slice at a position
- * offset) and decode rows (one query each) of the same batch, reading a paged
+ * offset), rows of drafted trees and decode rows (one query each) of the same batch, reading a paged
  * KV cache stored as 32-element blocks (fp16, Q8_0 or Q4_0) or as 8-bit codes
  * with one scale per page and kv head, and dequantising inside the attention.
  * A second entry point quantises new K/V into the cache; a third rotates
@@ -29,11 +29,13 @@
  *   - Kernels check page ids and slots on the device.  A bad one sets a bit in
  *     a device error word and the offending page or token is skipped (no trap);
  *     read and clear it with mixattn_device_error().  A decode split or chunk
- *     piece whose every page was skipped has no keys: its outputs are NaN.
+ *     piece whose every page was skipped has no keys: its outputs are NaN (those of
+ *     tree rows zeros).
  *   - Device checks surface at the next call: once a kernel has set an error
  *     bit on a device (a bad page id or slot, or a bounded wait that gave up),
  *     every later call of mixattn_kv_append_quant, mixattn_rope_append,
- *     mixattn_kv_export_blocks, mixattn_run and mixattn_mixed_attention on that device returns
+ *     mixattn_kv_export_blocks, mixattn_run, mixattn_run_tree and mixattn_mixed_attention (and
+ *     of those of mixattn_latent.h that launch) on that device returns
  *     MIXATTN_ERR_DEVICE_CHECK and launches nothing, until
  *     mixattn_device_error(1) clears the word.  The host learns of it through
  *     a pinned, host-mapped flag that the kernels set beside the word, so the

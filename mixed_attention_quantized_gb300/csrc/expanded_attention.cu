@@ -12,6 +12,10 @@
 //
 // Values past a row's last key belong to the next row and may be anything: a warp of its own zeroes
 // them in the slots of the row's last KV tile before their MMAs.
+//
+// 2048 tokens behind 8192, 32 heads: 303 us (1.31 PFLOP/s), 341 in a long run under the power cap. A step of both
+// groups takes 3540 cycles for 2768 of MMAs: what they wait is the softmax's chain. One MMA warp for both groups,
+// issuing from lane 0, took 569 us.
 #include "latent.h"
 #include "page_attention.cuh"
 #include "tma.cuh"

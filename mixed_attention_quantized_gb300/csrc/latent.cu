@@ -256,7 +256,10 @@ constexpr int kItemPages = 5;
 // way through the join (one row of 300 tokens, 16 heads, with 2 / 4 / 6: 14.5 / 16.4 / 16.5 us, of 1000 14.6 /
 // 14.5 / 16.5, of 8000 26.7 / 20.8 / 20.6; 64 rows of 500 to 2000, 128 heads 80 / 73 / 80).
 int64_t min_item_pages(int64_t row_pages) { return row_pages <= 16 ? 2 : 4; }
+
+// CTAs of a team, at most (128 heads: two tiles a token; trees of six, twelve).
 constexpr int kMaxTeam = 16;
+
 // A tile of more parts is joined by four times as many CTAs.
 constexpr int kManyParts = 8;
 
@@ -368,9 +371,9 @@ int build_latent_tiling(const mixattn_latent_cache& c, int heads, int n_rows, co
         for (int64_t m = 0; m < T.team && mt0 + m < n_tiles; ++m)
           for (int32_t quarter = parts > kManyParts ? 0 : -1; quarter < (parts > kManyParts ? 4 : 0); ++quarter)
             cuts.push_back(LatentCut{(int64_t)rows[r].q_start * heads + (mt0 + m) * T.tile_rows,
-                                   (int32_t)std::min<int64_t>(T.tile_rows, (int64_t)(seq[r] - off[r]) * heads -
-                                                                               (mt0 + m) * T.tile_rows),
-                                   (int32_t)(slots + m * parts), parts, quarter});
+                                     (int32_t)std::min<int64_t>(T.tile_rows, (int64_t)(seq[r] - off[r]) * heads -
+                                                                                 (mt0 + m) * T.tile_rows),
+                                     (int32_t)(slots + m * parts), parts, quarter});
         slots += (int64_t)parts * T.team;
         T.max_parts = std::max<int>(T.max_parts, parts);
         if (slots > INT32_MAX) return MIXATTN_ERR_INVALID_ARG;
@@ -682,8 +685,7 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   p.n_cuts = T.n_cuts;
   p.max_parts = T.max_parts;
   p.scale_log2 = (float)(plan->scale * kLog2e);
-  return launch_latent_attention(T.tile_rows, p, err, s) == cudaSuccess ? MIXATTN_OK
-                                                                                            : MIXATTN_ERR_CUDA;
+  return launch_latent_attention(T.tile_rows, p, err, s) == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
 }
 
 void mixattn_latent_plan_destroy(mixattn_latent_plan* plan) { delete plan; }
