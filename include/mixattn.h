@@ -374,8 +374,8 @@ int mixattn_run(const mixattn_plan* plan, const void* q, const int32_t* page_tab
  *   tree_mask   device uint32 [sum of n over the plan's tree rows, in row order][mask_words];
  *               read at run time, so one plan (and one captured graph) serves changing trees.
  *               Bits from n on are ignored.  May be NULL for a plan without tree rows.
- *               A node that no mask names is attended by nobody, but its K/V must have been appended
- *               all the same (a row of zeros will do): what is not finite there may reach the others.
+ *               A node that no mask names (of a padded tree) need not have been appended.  One that
+ *               some see and that is not finite may reach the row's other outputs.
  *   mask_words  >= ceil(n / 32) of the largest tree row
  * n <= 1024, else MIXATTN_ERR_UNSUPPORTED from the plan.  In a plan with a window W a drafted token
  * stands at position q_offset + max(1, bits set in its mask) - 1 (its depth) and sees the context

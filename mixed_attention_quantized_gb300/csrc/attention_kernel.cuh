@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -239,6 +240,42 @@ __device__ __forceinline__ TreeView tree_view(const AttnParams& p, const RowInfo
     int depth = 0;
     for (int b = 0; b < v.n; b += 32) depth += __popc(tree_bits(v.mask, p.tree_words, v.n, b));
     lo = window_first_key(v.ctx + max(depth, 1) - 1, p.window);
+  }
+  return v;
+}
+
+// The drafted tokens of a chunk tile, of which a key is seen by some or by none: what the cache holds
+// for the latter may be anything (unused nodes of a padded tree), and 0 x NaN is not 0.
+struct TreeTile {
+  const uint32_t* mask = nullptr;  // the tile's first token's words
+  int words = 0, count = 0;
+  int n = 0, ctx = 0;  // drafted tokens of the row, keys before them
+  bool tree = false;
+};
+struct NoTreeTile {};  // of kernels built without TREE
+template <bool TREE>
+using TreeTileOf = std::conditional_t<TREE, TreeTile, NoTreeTile>;
+
+// Those of 32 keys from `key` on that some token of the tile sees; a warp together.
+__device__ __forceinline__ uint32_t tree_union(const TreeTile& t, int key, int lane) {
+  const int rel = key - t.ctx;
+  if (rel <= -32) return 0xFFFFFFFFu;
+  uint32_t any = 0;
+  for (int i = lane; i < t.count; i += 32) any |= tree_bits(t.mask + (int64_t)i * t.words, t.words, t.n, rel);
+  return __reduce_or_sync(0xFFFFFFFFu, any);
+}
+
+template <bool TREE>
+__device__ __forceinline__ TreeTileOf<TREE> tree_tile(const AttnParams& p, const RowInfo& ri, const TileDesc& t) {
+  TreeTileOf<TREE> v;
+  if constexpr (TREE) {
+    const int start = p.tree_starts[t.row];
+    v.tree = start >= 0;
+    v.words = p.tree_words;
+    v.mask = p.tree_mask + (int64_t)(start + t.begin) * p.tree_words;
+    v.count = t.count;
+    v.n = ri.seq_len - ri.q_offset;
+    v.ctx = ri.q_offset - t.kv0 * kChunkN;  // (keys from the tile's first on)
   }
   return v;
 }
@@ -665,7 +702,10 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const TileDesc&
           uint32_t mk0 = 0xFFFFFFFFu, mk1 = 0xFFFFFFFFu;
           if (partial) {  // zero the keys no row sees, so stale data never reaches the MMA
             const int lo_first = window_first_key(tree ? ri.q_offset : ri.q_offset + qg0, p.window);
-            auto any_row = [&](int k) { return k < ri.seq_len && k >= lo_first; };
+            const uint32_t some = tree ? __reduce_or_sync(0xFFFFFFFFu, tv.bits(key0, p.tree_words)) : 0u;
+            auto any_row = [&](int k) {
+              return (tree ? ((some >> (k - key0)) & 1u) != 0u : k < ri.seq_len) && k >= lo_first;
+            };
             mk0 = (any_row(key0 + kv0) ? 0x0000FFFFu : 0u) | (any_row(key0 + kv0 + 1) ? 0xFFFF0000u : 0u);
             mk1 = (any_row(key0 + kv0 + 8) ? 0x0000FFFFu : 0u) | (any_row(key0 + kv0 + 9) ? 0xFFFF0000u : 0u);
           }
@@ -943,13 +983,14 @@ __device__ __forceinline__ void convert_half(const HalfRaw<F, D>& r, uint8_t* __
 //     jg-1 that read that half are done (pvh_done[h]); it arrives on ready[h]
 //     after each half.
 // Returns false when the group left early (a timeout here or elsewhere).
-template <int F, int D, bool LO>
+template <int F, int D, bool LO, bool TREE>
 __device__ __noinline__ bool dequant_loop(const uint8_t* __restrict__ q_plane, const uint16_t* __restrict__ s_plane,
                                           const int32_t* __restrict__ pt_row, int n_pages_row, int num_pages,
                                           int hkv, int g, int key_end, int n_kv, int jg0, int t0, bool is_k,
                                           uint8_t* dst_hi0, uint8_t* dst_lo0, uint8_t* dst_hi1, uint8_t* dst_lo1,
                                           uint64_t* free_bars, uint64_t* ready, int bar_id,
-                                          volatile int* abort_flag, unsigned int* err) {
+                                          volatile int* abort_flag, unsigned int* err,
+                                          const TreeTileOf<TREE> tt) {
   bool ok = true;
   // page ids of key half (j, h); the bounds check happens at load time
   auto pid_of = [&](int pg) { return ldg_s32_or(pt_row + pg, pg < n_pages_row && pg * kPage < key_end, kNoPage); };
@@ -966,6 +1007,24 @@ __device__ __noinline__ bool dequant_loop(const uint8_t* __restrict__ q_plane, c
     tc_fence_after();
     const bool b1 = is_k && (jg & 1);
     convert_half<F, D, LO>(r, b1 ? dst_hi1 : dst_hi0, b1 ? dst_lo1 : dst_lo0, h, t0);
+    if constexpr (TREE) {
+      // values that no token of the tile sees: zeros over what this thread wrote.  16 trees of 25 tokens, E4M3, 185
+      // -> 189 us, 8 of 64, Q8_0, 263 -> 269; with the union in every load's predicate 195 and 283, with the masks
+      // read at the tile's start 198 and 277.
+      const int key = j * kChunkN + h * (kChunkN / 2);
+      if (!is_k && tt.tree && key + kChunkN / 2 > tt.ctx) {
+        using Gm = DequantGeom<F, D>;
+        const int dc = t0 % Gm::CPR, key0 = t0 / Gm::CPR;
+        const uint32_t at = (uint32_t)((dc >> 3) * (kChunkN * 128) + (key0 + kChunkN / 2 * h) * 128 + (((dc & 7) ^ (key0 & 7)) << 4));
+        const uint32_t some_a = tree_union(tt, key, t0 & 31), some_b = tree_union(tt, key + kPage, t0 & 31);
+#pragma unroll 1
+        for (int i = 0; i < Gm::NH; ++i) {
+          if (((i < Gm::NH / 2 ? some_a : some_b) >> ((key0 + i * Gm::KPI) & (kPage - 1))) & 1u) continue;
+          *reinterpret_cast<uint4*>(dst_hi0 + at + i * Gm::KPI * 128) = make_uint4(0u, 0u, 0u, 0u);
+          if (LO) *reinterpret_cast<uint4*>(dst_lo0 + at + i * Gm::KPI * 128) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    }
     fence_proxy_async_smem();
     if (bar_any(bar_id, 128, !ok || *abort_flag)) {  // one decision for the group
       *abort_flag = 1;
@@ -1101,16 +1160,17 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
       const int key_end = tree ? ri.seq_len : min(ri.seq_len, ri.q_offset + t.begin + t.count);
       const int kv0 = t.kv0, n_kv = t.kv1 - t.kv0;
       const int32_t* pt_row = p.page_table + (int64_t)t.row * p.max_pages + kv0 * kPagesPerKvTile;
-      alive = is_k ? dequant_loop<FK, D, L::kKLo>(p.k_quant, p.k_scale, pt_row, n_pages_row - kv0 * kPagesPerKvTile,
+      const TreeTileOf<TREE> tt = tree_tile<TREE>(p, ri, t);
+      alive = is_k ? dequant_loop<FK, D, L::kKLo, TREE>(p.k_quant, p.k_scale, pt_row, n_pages_row - kv0 * kPagesPerKvTile,
                                                   p.num_pages, p.hkv, t.kvh, key_end - kv0 * kChunkN, n_kv, jg0,
                                                   tid - kGroup, true, smem + L::kK0, smem + L::kK0 + L::kTile,
                                                   smem + L::kK1, smem + L::kK1 + L::kTile, qk_done, kdeq, kBarK,
-                                                  abort_flag, err)
-                   : dequant_loop<FV, D, L::kVLo>(p.v_quant, p.v_scale, pt_row, n_pages_row - kv0 * kPagesPerKvTile,
+                                                  abort_flag, err, tt)
+                   : dequant_loop<FV, D, L::kVLo, TREE>(p.v_quant, p.v_scale, pt_row, n_pages_row - kv0 * kPagesPerKvTile,
                                                   p.num_pages, p.hkv, t.kvh, key_end - kv0 * kChunkN, n_kv, jg0,
                                                   tid - 2 * kGroup, false, smem + L::kVh, smem + L::kVl,
                                                   smem + L::kVh, smem + L::kVl, pvh_done, vdeq, kBarV, abort_flag,
-                                                  err);
+                                                  err, tt);
       jg0 += n_kv;
     }
     if (!alive) *abort_flag = 1;

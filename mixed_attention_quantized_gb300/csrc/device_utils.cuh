@@ -14,6 +14,9 @@
 
 namespace mixattn {
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
+
 // The device error block lives in abi.cu; kernels receive its address.  Word 0
 // collects the MIXATTN_DEVERR_* bits; words 2-3 hold the device address of a
 // host-mapped flag (0 until a plan has armed it on this device), which is set

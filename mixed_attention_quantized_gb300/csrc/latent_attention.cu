@@ -54,8 +54,6 @@ struct LatentSmem {
   static_assert(kTotal <= 227 * 1024, "the tile does not fit in shared memory");
 };
 
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
-
 // 16 lanes x 64 columns of 32-bit TMEM: register 4 j + 2 h + e holds row lane / 4 + 8 h, column
 // 8 j + 2 (lane % 4) + e.
 __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {

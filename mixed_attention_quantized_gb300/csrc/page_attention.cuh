@@ -269,10 +269,14 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
       const float mr0 = m0 == -CUDART_INF_F ? 0.f : m0, mr1 = m1 == -CUDART_INF_F ? 0.f : m1;
       float x[4] = {fmaf(u[0] + u2[0], a_pg, b_pg - mr0), fmaf(u[1] + u2[1], a_pg, b_pg - mr1),
                     fmaf(u[2] + u2[2], a_pg, b_pg - mr0), fmaf(u[3] + u2[3], a_pg, b_pg - mr1)};
+      uint32_t some = 0xFFFFFFFFu;  // keys that some row of a tree's tile sees; the others' page may have no scale
       if (partial) {
         const int k0 = key0 + r, k1 = k0 + 8;
         if (tree) {
-          const uint32_t v0 = tv0.bits(key0, p.tree_words) >> r, v1 = tv1.bits(key0, p.tree_words) >> r;
+          uint32_t v0 = tv0.bits(key0, p.tree_words), v1 = tv1.bits(key0, p.tree_words);
+          some = __reduce_or_sync(0xFFFFFFFFu, v0 | v1);
+          v0 >>= r;
+          v1 >>= r;
           if (!(v0 & 1u) || k0 < lo0) x[0] = -CUDART_INF_F;
           if (!(v1 & 1u) || k0 < lo1) x[1] = -CUDART_INF_F;
           if (!(v0 & 256u) || k1 < lo0) x[2] = -CUDART_INF_F;
@@ -323,8 +327,9 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-      l0 = fmaf(x[0] + x[2], inv_pg, l0);
-      l1 = fmaf(x[1] + x[3], inv_pg, l1);
+      const float inv = (some & 0xFFFFu) != 0u ? inv_pg : 0.f;
+      l0 = fmaf(x[0] + x[2], inv, l0);
+      l1 = fmaf(x[1] + x[3], inv, l1);
 
       // ---------------- O^T += c_v^T P' ----------------
       const uint32_t bq[2] = {transpose8x8(pack_f16x2(x[0], x[1])), transpose8x8(pack_f16x2(x[2], x[3]))};
@@ -336,7 +341,9 @@ __device__ __forceinline__ void page_decode_tile(const AttnParams& p, const Tile
       uint32_t mk0 = 0xFFFFFFFFu, mk1 = 0xFFFFFFFFu;
       if (!kOff && partial) {  // codes of keys that no row sees may be NaN
         const int lo_first = window_first_key(tree ? ri.q_offset : ri.q_offset + qg0, p.window);
-        auto any_row = [&](int k) { return k <= last_key && k >= lo_first; };
+        auto any_row = [&](int k) {
+          return (tree ? ((some >> (k - key0)) & 1u) != 0u : k <= last_key) && k >= lo_first;
+        };
         const int k0 = key0 + 2 * c;
         mk0 = (any_row(k0) ? 0x0000FFFFu : 0u) | (any_row(k0 + 1) ? 0xFFFF0000u : 0u);
         mk1 = (any_row(k0 + 8) ? 0x0000FFFFu : 0u) | (any_row(k0 + 9) ? 0xFFFF0000u : 0u);
@@ -1052,6 +1059,7 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
         return make_int2(ldg_s32_or(pt_row + pg, j < n_kv && pg * kPage < key_end, kNoPage),
                          ldg_s32_or(pt_row + pg + 1, j < n_kv && turn < n_load && (pg + 1) * kPage < key_end, kNoPage));
       };
+      const TreeTileOf<TREE> tt = tree_tile<TREE>(p, ri, t);
       uint4 raw[NL];
       float dk = 0.f, dv = 1.f;
       bool there = false;
@@ -1114,6 +1122,25 @@ __device__ __forceinline__ void page_chunk_cta(const AttnParams& p, int cta, int
             const uint32_t flip = (KPL == 4 && (i & 1)) ? 64u : 0u;
             *reinterpret_cast<uint4*>(dst + (off0 ^ flip) + i * (KPL * 128)) = x;
             *reinterpret_cast<uint4*>(dst + (off1 ^ flip) + i * (KPL * 128)) = y;
+          }
+        }
+        if constexpr (TREE) {
+          // values that no token of a tree's tile sees: zeros over what was written; pages of such keys alone count
+          // as missing (they may have no scale)
+          const int page0 = j * kChunkN + (r0 & ~(kPage - 1));
+          if (tt.tree && page0 + 2 * kPage > tt.ctx) {
+            const uint32_t some_a = tree_union(tt, page0, lane), some_b = tree_union(tt, page0 + kPage, lane);
+            if (!is_v && some_a == 0u) {
+              there = false;
+              dv = 1.f;
+            }
+#pragma unroll 1
+            for (int i = 0; is_v && i < n_load; ++i) {
+              if (((i < turn ? some_a : some_b) >> ((key0 + i * KPL) & (kPage - 1))) & 1u) continue;
+              const uint32_t flip = (KPL == 4 && (i & 1)) ? 64u : 0u;
+              *reinterpret_cast<uint4*>(dst + (off0 ^ flip) + i * (KPL * 128)) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(dst + (off1 ^ flip) + i * (KPL * 128)) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
         }
         if (!is_v && lane == 0)

@@ -182,3 +182,47 @@ def test_refusals():
         with pytest.raises(mq.MixattnError) as e:
             call(cache, q, pt, [110], [70], [TREE])
         assert e.value.status in (mq.ERR_INVALID_ARG, mq.ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("kf,vf", FORMATS)
+@pytest.mark.parametrize("d,window", [(128, 0), (64, 0), (64, 300)])
+def test_nodes_that_nobody_sees_need_not_be_in_the_cache(kf, vf, d, window):
+    """Padded trees: the last nodes' masks are empty, no other names them, and they were never appended, so that
+    their places in the cache, and the scales of whole pages, are NaN patterns."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    rng = np.random.default_rng(91)
+    rows = [(TREE, 70, 30), (DECODE, 40, 39), (TREE, 36, 31), (TREE, 38, 32), (TREE, 360, 131), (TREE, 164, 0), (CHUNK, 90, 60)]
+    used = [25, 1, 2, 1, 9, 1, 30]
+    masks = []
+    for (kind, s, o), u in zip(rows, used):
+        if kind == TREE:
+            m = np.zeros((s - o, s - o), dtype=bool)
+            m[:u, :u] = tr.random_tree(u, rng)
+            masks.append(m)
+    seqs = [r[1] for r in rows]
+    need = [-(-s // 32) for s in seqs]
+    cache = mq.KVCache.allocate(sum(need) + 3, 2, d, kf, vf, fill=0xFF)
+    perm = rng.permutation(sum(need) + 3).astype(np.int32)
+    pt = np.full((len(seqs), max(need)), -1, dtype=np.int32)
+    slots, at = [], 0
+    for r, n in enumerate(need):
+        pt[r, :n] = perm[at:at + n]
+        at += n
+        t = np.arange(seqs[r])
+        slots.append(torch.from_numpy((pt[r, t // 32] * 32 + t % 32).astype(np.int32)).cuda())
+        here = rows[r][2] + used[r]
+        k, v = (torch.from_numpy(rng.standard_normal((here, 2, d)).astype(np.float16)).cuda() for _ in range(2))
+        mq.kv_append_quant(cache, k, v, slots[r][:here])
+    pt = torch.from_numpy(pt).cuda()
+    total = sum(s - o for _, s, o in rows)
+    q = torch.from_numpy(rng.standard_normal((total, 8, d)).astype(np.float16)).cuda()
+    got = _run(cache, pt, rows, 8, q, masks, window)
+    at, left = 0, list(masks)
+    for r, (kind, s, o) in enumerate(rows):
+        k, v = (tr.cache_values(cache, i, slots[r]) for i in (0, 1))
+        vis = tr.seen(kind, s, o, left.pop(0) if kind == TREE else None, window)
+        want = tr.attention64(q[at:at + s - o], k, v, vis, d ** -0.5)
+        err = (got[at:at + s - o].double() - want).abs()
+        assert bool((err <= 2e-3 + 2.0 ** -11 * want.abs()).all()), (r, float(err.max()))
+        at += s - o
