@@ -52,7 +52,7 @@ __device__ __forceinline__ int group_steps(const ExpandedItem& it, int group) {
 __global__ void __launch_bounds__(kExpandedThreads, 1)
     expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map,
-                    const ExpandedParams p, unsigned int* err) {
+                    const __grid_constant__ ExpandedParams p, unsigned int* err) {
   using L = ExpandedSmem;
   constexpr uint32_t kTmemCols = 512, kOCol = 256;
   constexpr int kD = kExpandedV;
@@ -101,7 +101,9 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
   const uint32_t tmem = *tmem_slot;
   wait_for_upload();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int it0 = p.cta_first[blockIdx.x], it1 = p.cta_first[blockIdx.x + 1];
+  const ExpandedItem* items = p.list.at<ExpandedItem>(p.items);
+  const int32_t* cta_first = p.list.at<int32_t>(p.cta_first);
+  const int it0 = cta_first[blockIdx.x], it1 = cta_first[blockIdx.x + 1];
 
   if (warp < 8) {
     // ======================= softmax groups =======================
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     bool ok = true;
     uint32_t n_s = 0, n_o = 0;  // S tiles, outputs so far (barrier phases)
     for (int i = it0; ok && i < it1; ++i) {
-      const ExpandedItem it = p.items[i];
+      const ExpandedItem it = items[i];
       const int n = group_steps(it, gq);
       const int prow = 128 * gq + row;
       const bool valid = prow < it.count;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     bool ok = true;
     const uint32_t ring = smem_u32(smem + L::kRing);
     for (int i = it0; ok && i < it1; ++i) {
-      const ExpandedItem it = p.items[i];
+      const ExpandedItem it = items[i];
       const int n = max(group_steps(it, 0), group_steps(it, 1));
       if (n == 0) continue;
       if (n_item > 0) ok = warp_wait_fast(q_empty, (uint32_t)((n_item - 1) & 1), err);
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     int t = 0;  // KV tiles before the item
     uint32_t n_tail = 0;
     for (int i = it0; ok && i < it1; ++i) {
-      const ExpandedItem it = p.items[i];
+      const ExpandedItem it = items[i];
       const int n = max(group_steps(it, 0), group_steps(it, 1));
       t += n;
       if (n > 0 && (it.kv0 + n) * kChunkN > it.seq_len) {
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     uint32_t n_item = 0, n_p = 0, n_out = 0;
     const int first = __shfl_sync(0xFFFFFFFFu, it0, 0), end = __shfl_sync(0xFFFFFFFFu, it1, 0);
     for (int i = first; ok && i < end; ++i) {
-      const ExpandedItem it = p.items[i];
+      const ExpandedItem it = items[i];
       // (control flow and operands the same in all lanes, and known to be)
       const int mine = __shfl_sync(0xFFFFFFFFu, group_steps(it, g), 0);
       const int n = max(mine, __shfl_sync(0xFFFFFFFFu, group_steps(it, g ^ 1), 0));
@@ -390,10 +392,10 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
 // wait for nothing but the cut.
 constexpr int kJoinRows = 16;  // queries of a CTA
 
-__global__ void __launch_bounds__(128) expanded_join_kernel(const ExpandedParams p) {
+__global__ void __launch_bounds__(128) expanded_join_kernel(const __grid_constant__ ExpandedParams p) {
   wait_for_upload();
   constexpr int kPer = kExpandedRows / kJoinRows;
-  const ExpandedCut cut = p.cuts[blockIdx.x / kPer];
+  const ExpandedCut cut = p.list.at<ExpandedCut>(p.cuts)[blockIdx.x / kPer];
   const int row = kJoinRows * (blockIdx.x % kPer) + 4 * (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= cut.count) return;
   const float2* ml = p.part_ml + (int64_t)cut.slot * kExpandedRows + row;

@@ -501,6 +501,15 @@ int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32
   return MIXATTN_OK;
 }
 
+// The list into a run's parameters, or (a longer one) on its way into the workspace.
+int take_image(PlanList& list, const Image& image, uint8_t* ws, cudaStream_t s, PlanImage* out) {
+  out->image = ws + 256;
+  out->here = image.bytes.size() <= sizeof(out->list);
+  if (!out->here) return list.upload(ws + 256, image.bytes.size(), s);
+  memcpy(out->list, image.bytes.data(), image.bytes.size());
+  return list.note_capture(s);
+}
+
 bool valid_scale(double s) { return std::isfinite(s) && s > 1e-20 && s < 1e6; }
 
 constexpr double kLog2e = 1.4426950408889634;
@@ -654,17 +663,8 @@ int mixattn_latent_run(const mixattn_latent_plan* plan_c, const void* q, const i
   if (!err) return MIXATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  LatentParams p = {};
-  // a short list goes with the launch itself: no upload in front of it (two rows of up to 300 tokens, 16
-  // heads, called in a row: 10.6 us and not 14.4)
-  p.inline_list = T.image.bytes.size() <= sizeof(p.list);
-  if (p.inline_list) {
-    memcpy(p.list, T.image.bytes.data(), T.image.bytes.size());
-    if (int st = plan->list.note_capture(s)) return st;
-  } else if (int st = plan->list.upload(ws + 256, T.image.bytes.size(), s)) {
-    return st;
-  }
-  p.image = ws + 256;
+  LatentParams p;
+  if (int st = take_image(plan->list, T.image, ws, s, &p.list)) return st;
   p.rows = (int32_t)(T.rows - 256);
   p.items = (int32_t)(T.items - 256);
   p.team_first = (int32_t)(T.team_first - 256);
@@ -757,11 +757,11 @@ int mixattn_expanded_run(const mixattn_expanded_plan* plan_c, const mixattn_head
     return MIXATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (int st = plan->list.upload(ws + 256, T.image.bytes.size(), s)) return st;
-  ExpandedParams p = {};
-  p.items = reinterpret_cast<const ExpandedItem*>(ws + T.items);
-  p.cta_first = reinterpret_cast<const int32_t*>(ws + T.cta_first);
-  p.cuts = reinterpret_cast<const ExpandedCut*>(ws + T.cuts);
+  ExpandedParams p;
+  if (int st = take_image(plan->list, T.image, ws, s, &p.list)) return st;
+  p.items = (int32_t)(T.items - 256);
+  p.cta_first = (int32_t)(T.cta_first - 256);
+  p.cuts = (int32_t)(T.cuts - 256);
   p.o = static_cast<uint16_t*>(o);
   p.part_o = reinterpret_cast<float*>(ws + T.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + T.part_ml);

@@ -13,6 +13,24 @@ namespace mixattn {
 constexpr int kLatent = 512, kLatentRope = 64, kLatentRow = kLatent + kLatentRope;
 constexpr int kNopeDim = 128, kExpandedV = 128, kExpandedQ = kNopeDim + kLatentRope;
 
+// A plan's list as its kernels take it: all but the largest go with the launch itself, with no upload in front
+// (32 rows of 500 to 2000 tokens, 16 heads, a call among others 23.5 -> 20.1 us; five prompts of up to 900, 8 heads,
+// 18.8 -> 15.3; two of up to 2000, 32 heads, 72.4 -> 68.9; no call slower for the longer parameters).
+constexpr int kInlineBytes = 24576;  // (parameters may have 32764)
+
+struct PlanImage {
+  const uint8_t* image;  // the list in the workspace
+  int32_t here;          // it is below, and not there
+  uint4 list[kInlineBytes / 16];
+
+#ifdef __CUDACC__
+  template <class T>
+  __device__ __forceinline__ const T* at(int32_t offset) const {
+    return reinterpret_cast<const T*>((here ? reinterpret_cast<const uint8_t*>(list) : image) + offset);
+  }
+#endif
+};
+
 // ---------------------------------------------------------------------------
 // Absorbed form
 // ---------------------------------------------------------------------------
@@ -37,7 +55,6 @@ struct LatentCut {
 };
 
 struct LatentParams {
-  const uint8_t* image;  // the plan's list in the workspace
   int32_t rows, items, team_first, cuts;  // offsets in the list: LatentRowInfo, LatentItem, int32 [n_teams + 1], LatentCut
   const uint16_t* q;          // [total_q][heads][576]
   const uint16_t* data;       // the cache
@@ -48,15 +65,7 @@ struct LatentParams {
   float2* part_ml;  // [slots][tile rows]: reference (log2 units) and sum
   int32_t tree_words, max_pages, num_pages, heads, team, n_teams, n_cuts, max_parts;
   float scale_log2;
-  int32_t inline_list;  // the list is here, and not in the workspace
-  uint4 list[96];
-
-#ifdef __CUDACC__
-  template <class T>
-  __device__ __forceinline__ const T* at(int32_t offset) const {
-    return reinterpret_cast<const T*>((inline_list ? reinterpret_cast<const uint8_t*>(list) : image) + offset);
-  }
-#endif
+  PlanImage list;
 };
 
 // tile_rows: 16, 32 or 64 (query, head) rows a CTA
@@ -82,14 +91,13 @@ struct ExpandedCut {
 };
 
 struct ExpandedParams {
-  const ExpandedItem* items;
-  const int32_t* cta_first;  // [n_ctas + 1]
-  const ExpandedCut* cuts;
+  int32_t items, cta_first, cuts;  // offsets in the list: ExpandedItem, int32 [n_ctas + 1], ExpandedCut
   uint16_t* o;
   float* part_o;    // [slots][256][128], unnormalised
   float2* part_ml;  // [slots][256]
   int32_t heads, n_ctas, n_cuts;
   float scale_log2;
+  PlanImage list;
 };
 
 cudaError_t launch_expanded_attention(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& kr,

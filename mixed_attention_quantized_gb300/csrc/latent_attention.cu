@@ -19,10 +19,10 @@
 // rows moves 49 bytes a ns and SM at most (7.4 TB/s over all, measured with 192 KB in flight an SM, from
 // HBM and from L2 alike), these 130 from L2.
 //
-// Bound by HBM with 16 heads: 64 rows of 1024 to 16384 tokens 117 us (638 MB, 5.4 TB/s over all; a steady step
+// Bound by HBM with 16 heads: 64 rows of 1024 to 16384 tokens 115 us (638 MB, 5.6 TB/s over all; a steady step
 // 6.5 to 7.2, the rest is items' starts and the join).  By the chain of a step's latencies over a ring of 2.75 steps
-// with 64-row tiles, tensor pipe 59 % active: 128 heads, a session of 131072 tokens and 31 short rows 130 us, 16
-// trees of 6 302 us (0.81 PFLOP/s).  32-key steps: 127, 152 us (the third not measured) where these took 118, 146.
+// with 64-row tiles, tensor pipe 59 % active: 128 heads, a session of 131072 tokens and 31 short rows 125 us, 16
+// trees of 6 298 us (0.82 PFLOP/s).  32-key steps: 127, 152 us (the third not measured) where these took 118, 146.
 #include <mutex>
 
 #include "latent.h"
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int team = blockIdx.x / p.team, member = blockIdx.x - team * p.team;
-  const LatentItem* items = p.at<LatentItem>(p.items);
-  const LatentRowInfo* row_list = p.at<LatentRowInfo>(p.rows);
-  const int it0 = p.at<int32_t>(p.team_first)[team], it1 = p.at<int32_t>(p.team_first)[team + 1];
+  const LatentItem* items = p.list.at<LatentItem>(p.items);
+  const LatentRowInfo* row_list = p.list.at<LatentRowInfo>(p.rows);
+  const int it0 = p.list.at<int32_t>(p.team_first)[team], it1 = p.list.at<int32_t>(p.team_first)[team + 1];
 
   if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
     // ======================= load (warp w: unit w of every step) =======================
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
   __shared__ float sums[7 * 16 * 32];  // [groups - 1][16][elements]
   wait_for_upload();
   const int n = tile_rows / 4;  // units of 16 rows by 128 elements
-  const LatentCut cut = p.at<LatentCut>(p.cuts)[blockIdx.x / n];
+  const LatentCut cut = p.list.at<LatentCut>(p.cuts)[blockIdx.x / n];
   const int b = blockIdx.x % n, col0 = 16 * b % tile_rows, rows = cut.rows - col0;  // rows here
   if (rows <= 0) return;
   const int width = cut.quarter < 0 ? 128 : 32, groups = 256 / width;
