@@ -13,9 +13,8 @@
 // Values past a row's last key belong to the next row and may be anything: a warp of its own zeroes
 // them in the slots of the row's last KV tile before their MMAs.
 //
-// 2048 tokens behind 8192, 32 heads: 303 us (1.31 PFLOP/s), 341 in a long run under the power cap. A step of both
-// groups takes 3540 cycles for 2768 of MMAs: what they wait is the softmax's chain. One MMA warp for both groups,
-// issuing from lane 0, took 569 us.
+// 2048 tokens behind 8192, 32 heads: 295 us (1.35 PFLOP/s). A step of both groups takes 3540 cycles for 2768 of
+// MMAs: what they wait is the softmax's chain. One MMA warp for both groups, issuing from lane 0, took 569 us.
 #include "latent.h"
 #include "page_attention.cuh"
 #include "tma.cuh"
@@ -47,6 +46,61 @@ __device__ __forceinline__ int group_steps(const ExpandedItem& it, int group) {
   if (rows <= 0) return 0;
   const int last = it.pos + 128 * group + rows - 1;
   return max(0, min(it.kv1, last / kChunkN + 1) - it.kv0);
+}
+
+// Four 16-byte pieces a lane: piece e of lane q and piece q of lane e of each four lanes change places.
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16], int lane) {
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &a = w[4 * i + e], &b = w[4 * (i ^ s) + e];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, s);
+        if (up) a = got;
+        else b = got;
+      }
+    }
+  }
+}
+
+// A warp's 32 rows of O from TMEM.  Four lanes write 64 bytes of a row together, of four rows (`rows` of which
+// exist) in turn: a row a lane is 32 lines an instruction.  Out of line, or the softmax loop's code suffers: 2048
+// queries behind 8192, 32 heads, 322 us with a row a lane, 330 with this in line, 311 as it is.
+__device__ __noinline__ void write_out(uint32_t o_col, uint16_t* dst, int stride, float inv_l, int rows, int lane) {
+  dst += 8 * (lane & 3);
+#pragma unroll 1
+  for (int ch = 0; ch < kExpandedV / 32; ++ch) {
+    uint32_t v[32], w[16];
+    tmem_ld32(o_col + 32 * ch, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      w[e] = pack_f16x2_out(__uint_as_float(v[2 * e]) * inv_l, __uint_as_float(v[2 * e + 1]) * inv_l);
+    transpose_pieces(w, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < rows)
+        *reinterpret_cast<uint4*>(dst + (int64_t)e * stride + 32 * ch) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+  }
+}
+
+__device__ __noinline__ void write_part(uint32_t o_col, float* dst, int rows, int lane) {
+  dst += 4 * (lane & 3);
+#pragma unroll 1
+  for (int ch = 0; ch < kExpandedV / 16; ++ch) {
+    uint32_t v[16];
+    tmem_ld16(o_col + 16 * ch, v);
+    tmem_wait_ld();
+    transpose_pieces(v, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < rows)
+        *reinterpret_cast<uint4*>(dst + e * kExpandedV + 16 * ch) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+  }
 }
 
 __global__ void __launch_bounds__(kExpandedThreads, 1)
@@ -118,7 +172,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       const ExpandedItem it = items[i];
       const int n = group_steps(it, gq);
       const int prow = 128 * gq + row;
-      const bool valid = prow < it.count;
       const int64_t part = (int64_t)it.slot + it.part;
       if (n == 0) {  // (a part past the group's last key, or a tile without the group)
         if (it.n_parts > 1) p.part_ml[part * kExpandedRows + prow] = make_float2(-CUDART_INF_F, 0.f);
@@ -184,27 +237,11 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       tc_fence_after();
       const bool whole = it.n_parts == 1;
       const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
-      uint16_t* dst = p.o + ((int64_t)(it.q_start + prow) * p.heads + it.head) * kD;
-      float* o_part = p.part_o + (part * kExpandedRows + prow) * kD;
-#pragma unroll 1
-      for (int ch = 0; ch < kD / 16; ++ch) {
-        uint32_t v[16];
-        tmem_ld16(o_col + 16 * ch, v);
-        tmem_wait_ld();
-        if (!valid) continue;
-        if (whole) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = pack_f16x2_out(__uint_as_float(v[2 * e]) * inv_l, __uint_as_float(v[2 * e + 1]) * inv_l);
-          reinterpret_cast<uint4*>(dst + 16 * ch)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(dst + 16 * ch)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4*>(o_part + 16 * ch)[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        }
-      }
+      const int row0 = prow & ~3;
+      if (whole)
+        write_out(o_col, p.o + ((int64_t)(it.q_start + row0) * p.heads + it.head) * kD, p.heads * kD, inv_l, it.count - row0, lane);
+      else
+        write_part(o_col, p.part_o + (part * kExpandedRows + row0) * kD, it.count - row0, lane);
       if (!whole) p.part_ml[part * kExpandedRows + prow] = make_float2(m_run, l_run);
       tc_fence_before();
       __syncwarp();
