@@ -598,8 +598,8 @@ class LatentCache:
     def _ref(self):
         """byref(desc()), the structure kept while nothing in it has changed."""
         x = self.data
-        key = (self.num_pages, self.latent_dim, self.rope_dim, x.data_ptr() if x is not None else 0,
-               x.shape if x is not None else None)
+        key = (self.num_pages, self.latent_dim, self.rope_dim,
+               (x.data_ptr(), x.shape, x.stride(), x.dtype) if x is not None else None)
         kept = self.__dict__.get("_kept")
         if kept is None or kept[0] != key:
             desc = self.desc()

@@ -77,3 +77,19 @@ def test_runs_refuse_a_missing_plan():
     assert lib.mixattn_expanded_run(None, ctypes.byref(q), ctypes.byref(q), FAKE, 64, ctypes.byref(q), FAKE, FAKE, 1 << 20,
                                     None) == mq.ERR_INVALID_ARG
     assert lib.mixattn_latent_plan_update(None, 1, None, None, None, 1, None) == mq.ERR_INVALID_ARG
+
+
+def test_a_cache_whose_data_changes_is_looked_at_again():
+    import copy
+    import torch
+    c = mq.LatentCache(2)
+    x = torch.zeros(2 * 32 * 576, dtype=torch.float16)
+    c.data = x.view(2, 32, 576)
+    assert c._ref()._obj.data == x.data_ptr()
+    for bad in (c.data.view(torch.bfloat16), x.view(32, 576, 2).permute(2, 0, 1), x.view(2, 576, 32), x.view(1, 64, 576)):
+        c.data = bad  # the same memory
+        with pytest.raises(ValueError):
+            c._ref()
+    c.data = torch.ones(2, 32, 576, dtype=torch.float16)
+    assert c._ref()._obj.data == c.data.data_ptr()
+    assert bool((copy.deepcopy(c).data == 1).all())
