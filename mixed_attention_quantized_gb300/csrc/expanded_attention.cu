@@ -13,8 +13,8 @@
 // Values past a row's last key belong to the next row and may be anything: a warp of its own zeroes
 // them in the slots of the row's last KV tile before their MMAs.
 //
-// 2048 tokens behind 8192, 32 heads: 295 us (1.35 PFLOP/s). A step of both groups takes 3540 cycles for 2768 of
-// MMAs: what they wait is the softmax's chain. One MMA warp for both groups, issuing from lane 0, took 569 us.
+// 2048 tokens behind 8192, 32 heads: 283 us (1.40 PFLOP/s). A step of both groups has 2768 cycles of
+// MMAs, which keep the tensor pipe 67 % active: the rest is the softmax's chain, the items' starts and ends. One MMA warp for both groups, issuing from lane 0, took 569 us.
 #include "latent.h"
 #include "page_attention.cuh"
 #include "tma.cuh"
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
         tc_fence_after();
         const int last = pos - (it.kv0 + j) * kChunkN;  // the last visible key of the row in this tile
         const bool diag = __any_sync(0xFFFFFFFFu, last < kChunkN - 1);
-#pragma unroll 1
+#pragma unroll 2  // (not unrolled 295 us for the case above, wholly 291, two of 32 scores loaded as halves 331)
         for (int c = 0; c < 4; ++c) {
           const int c_last = last - 32 * c;
           const uint32_t sc = s_col + 32 * c;
