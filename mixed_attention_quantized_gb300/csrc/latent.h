@@ -62,7 +62,7 @@ struct LatentParams {
   const uint32_t* tree_mask;
   uint16_t* o;
   float* part_o;    // [slots][tile rows / 4 units of 128 elements by 16 rows][4][128][4 rows], unnormalised
-  float2* part_ml;  // [slots][tile rows]: reference (log2 units) and sum
+  float2* part_ml;  // [slots][tile rows]: reference (a score before the scale) and sum
   int32_t tree_words, max_pages, num_pages, heads, team, n_teams, n_cuts, max_parts;
   float scale_log2;
   PlanImage list;

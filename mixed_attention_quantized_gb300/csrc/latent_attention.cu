@@ -1,6 +1,10 @@
 // latent_attention.cu -- absorbed latent attention: every (query, head) row of a token meets the
 // cached rows [c | r] of 512 + 64 fp16 elements, whose first 512 are the values too:
-//     S = q [c | r]^T,   P = 2^(scale S - m),   O = sum P c,   o = O / sum P.
+//     S = q [c | r]^T,   P = 2^(scale (S - m) + 7),   O = sum P c,   o = O / sum P.
+//
+// The reference m is a score and not one times the scale: the differences that weigh something are then exact to
+// fp32 however large the scores are.  (Of scale S near 2^28 no fp32 number is closer than 16: weights 2^(scale S - m')
+// about such an m' overflow fp16 or vanish.)  An addition more a score, of two scores together: no slower.
 //
 // A CTA takes a tile of N (16, 32 or 64) rows and walks a range of the row's pages, 64 keys (two
 // pages) a step, each loaded once into shared memory and used from there by both products:
@@ -381,6 +385,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // ======================= softmax =======================
     constexpr int kGroup = 32 * kSoftmaxWarps;
     constexpr float kTop = 15.f, kSet = 7.f;  // as page_decode_tile: P up to 2^15, set at 2^7
+    const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), set2 = f2_pack(kSet, kSet);
     constexpr int kBarGroup = 1;
     const int r = lane >> 2, c = lane & 3;
     const bool rows_here = 16 * warp < N;  // the warp's 16 rows of S; every warp has 32 elements of each O^T block
@@ -520,25 +525,30 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
           t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 1));
           t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 1));
-          t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 2)) * p.scale_log2;
-          t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 2)) * p.scale_log2;
-          const bool g0 = m0 == -CUDART_INF_F ? t0 > m0 : t0 > m0 + kTop;
-          const bool g1 = m1 == -CUDART_INF_F ? t1 > m1 : t1 > m1 + kTop;
+          t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 2));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 2));
+          const bool g0 = m0 == -CUDART_INF_F ? t0 > m0 : (t0 - m0) * p.scale_log2 > kTop - kSet;
+          const bool g1 = m1 == -CUDART_INF_F ? t1 > m1 : (t1 - m1) * p.scale_log2 > kTop - kSet;
           if (g0) {
-            al0 = ex2(m0 - (t0 - kSet));
-            m0 = t0 - kSet;
+            al0 = ex2((m0 - t0) * p.scale_log2);
+            m0 = t0;
             l0 *= al0;
           }
           if (g1) {
-            al1 = ex2(m1 - (t1 - kSet));
-            m1 = t1 - kSet;
+            al1 = ex2((m1 - t1) * p.scale_log2);
+            m1 = t1;
             l1 *= al1;
           }
           need = g0 || g1;
           const float n0 = m0 == -CUDART_INF_F ? 0.f : -m0, n1 = m1 == -CUDART_INF_F ? 0.f : -m1;
+          const uint64_t n0_2 = f2_pack(n0, n0), n1_2 = f2_pack(n1, n1);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = ex2(fmaf(__uint_as_float(v[e]), p.scale_log2, (e & 2) ? n1 : n0));
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t d = fadd2(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), (e & 2) ? n1_2 : n0_2);
+            f2_unpack(ffma2(d, scale2, set2), x[e], x[e + 1]);
+            x[e] = ex2(x[e]);
+            x[e + 1] = ex2(x[e + 1]);
+          }
           float a0 = 0.f, a1 = 0.f;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -692,7 +702,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     for (int q = k; q < cut.n_parts; q += 16) {
       const float2 x = q == k ? first : part(q);
-      const float w = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - m);
+      const float w = x.x == -CUDART_INF_F ? 0.f : ex2((x.x - m) * p.scale_log2);
       weights[16 * q + row] = w;
       if (w != 0.f) l += w * x.y;
     }
