@@ -49,6 +49,75 @@ __device__ __forceinline__ int group_steps(const ExpandedItem& it, int group) {
   return max(0, min(it.kv1, last / kChunkN + 1) - it.kv0);
 }
 
+// A row's weights are P = 2^(scale (S - r) - m); its reference (m = -inf: none yet) and their sum.  Up to kLargeScore
+// r is 0.  Beyond, m alone would not do: of scale S near 2^28 no fp32 number is closer than 16, and the weights about
+// such an m overflow fp16 or vanish.  Those rows take a score as r, so that S - r is exact to fp32 where a weight counts, and
+// all their blocks the rare step: subtracting r from every row's scores, 283 -> 321 us for the case above; as it is 281 -> 283.
+struct ExpandedRef {
+  float r, m, l;
+  // what the common path adds to scale S: NaN, and with it the sum of the block, where a block needs the rare step
+  __device__ __forceinline__ float shift() const {
+    return m == -CUDART_INF_F || r != 0.f ? CUDART_NAN_F : -m;
+  }
+};
+constexpr float kLargeScore = 4194304.f;
+
+// page_move_reference for these rows, which see the scores up to c_last of block c's 32.  A change of more bits than
+// P' have starts again.
+__device__ __noinline__ ExpandedRef move_reference(uint32_t s_col, uint32_t o_col, int c, float scale, int c_last,
+                                                   ExpandedRef ref, bool scale_o) {
+  const uint32_t sc = s_col + 32 * c;
+  float mx = -CUDART_INF_F;
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    uint32_t o[16];
+    tmem_ld16(sc + 16 * b, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (16 * b + e <= c_last) mx = fmaxf(mx, __uint_as_float(o[e]));
+  }
+  const bool first = ref.m == -CUDART_INF_F;
+  const float top = fmaf(mx - ref.r, scale, -ref.m);  // exponent of the largest weight
+  const bool grow = mx > -CUDART_INF_F && (first || top >= kChunkMoved);
+  float up = 0.f, alpha = 1.f;
+  if (grow && (first || top - kChunkSet > 40.f)) {
+    up = first ? 0.f : top - kChunkSet;
+    alpha = first ? 0.f : ex2(-up);
+    const bool large = fabsf(mx * scale) >= kLargeScore;
+    ref.r = large ? mx : 0.f;
+    ref.m = large ? -kChunkSet : fmaf(mx, scale, -kChunkSet);
+  } else if (grow) {
+    up = floorf(top - kChunkSet);
+    alpha = ex2(-up);  // a power of two
+    ref.m += up;
+    if (ref.r == 0.f && fabsf(ref.m) >= kLargeScore) {
+      ref.m = fmaf(-mx, scale, ref.m);  // (the same reference: rounded once, at its small difference)
+      ref.r = mx;
+    }
+  }
+  ref.l *= alpha;
+  if (scale_o) scale_output<kExpandedV>(o_col, alpha);
+  scale_weights(s_col, c, up);
+  // the block's P', 16 scores at a time: their 8 words stay before the scores not yet read
+  const float cb = ref.m == -CUDART_INF_F ? 0.f : -ref.m;
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    uint32_t o[16], w[8];
+    tmem_ld16(sc + 16 * b, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float p0 = 16 * b + e <= c_last ? ex2(fmaf(__uint_as_float(o[e]) - ref.r, scale, cb)) : 0.f;
+      const float p1 = 16 * b + e + 1 <= c_last ? ex2(fmaf(__uint_as_float(o[e + 1]) - ref.r, scale, cb)) : 0.f;
+      ref.l += p0 + p1;
+      w[e >> 1] = pack_f16x2(p0, p1);
+    }
+    tmem_st8(sc + 8 * b, w);
+  }
+  return ref;
+}
+
 // Four 16-byte pieces a lane: piece e of lane q and piece q of lane e of each four lanes change places.
 __device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16], int lane) {
 #pragma unroll
@@ -165,8 +234,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     const int gq = warp >> 2, row = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + 128 * gq, o_col = tmem + lane_base + kOCol + 128 * gq;
-    const float4 tm = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
-    const uint64_t ca2 = f2_pack(tm.x, tm.x);
+    const uint64_t ca2 = f2_pack(p.scale_log2, p.scale_log2);
     bool ok = true;
     uint32_t n_s = 0, n_o = 0;  // S tiles, outputs so far (barrier phases)
     for (int i = it0; ok && i < it1; ++i) {
@@ -175,11 +243,12 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       const int prow = 128 * gq + row;
       const int64_t part = (int64_t)it.slot + it.part;
       if (n == 0) {  // (a part past the group's last key, or a tile without the group)
-        if (it.n_parts > 1) p.part_ml[part * kExpandedRows + prow] = make_float2(-CUDART_INF_F, 0.f);
+        if (it.n_parts > 1) p.part_ml[part * kExpandedRows + prow] = make_float4(0.f, -CUDART_INF_F, 0.f, 0.f);
         continue;
       }
       const int pos = it.pos + min(prow, it.count - 1);
-      float m_run = -CUDART_INF_F, l_run = 0.f;
+      ExpandedRef ref{0.f, -CUDART_INF_F, 0.f};
+      float cb = ref.shift();
       for (int j = 0; j < n; ++j) {
         ok = warp_wait_fast(&s_full[gq], n_s & 1, err);
         if (!ok) break;
@@ -193,7 +262,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
           const uint32_t sc = s_col + 32 * c;
           uint32_t x[32], pk[16];
           tmem_ld32(sc, x);
-          const float cb = m_run == -CUDART_INF_F ? 0.f : -m_run;
           const uint64_t cb2 = f2_pack(cb, cb);
           tmem_wait_ld();
           if (diag) {
@@ -216,15 +284,13 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
           float s0, s1;
           f2_unpack(fadd2(sum_a, sum_b), s0, s1);
           const float l_new = s0 + s1;
-          const bool over = !(l_new < kChunkTop) || m_run == -CUDART_INF_F;
-          if (!__any_sync(0xFFFFFFFFu, over)) {
+          if (!__any_sync(0xFFFFFFFFu, !(l_new < kChunkTop))) {
             tmem_st16(sc, pk);
-            l_run += l_new;
+            ref.l += l_new;
             continue;
           }
-          const float2 ml = page_move_reference<kD, false>(s_col, o_col, c, tm, 0, c_last, m_run, l_run, j > 0);
-          m_run = ml.x;
-          l_run = ml.y;
+          ref = move_reference(s_col, o_col, c, p.scale_log2, c_last, ref, j > 0);
+          cb = ref.shift();
         }
         tmem_wait_st();
         tc_fence_before();
@@ -237,13 +303,13 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const bool whole = it.n_parts == 1;
-      const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv_l = ref.l > 0.f ? 1.f / ref.l : 0.f;
       const int row0 = prow & ~3;
       if (whole)
         write_out(o_col, p.o + ((int64_t)(it.q_start + row0) * p.heads + it.head) * kD, p.heads * kD, inv_l, it.count - row0, lane);
       else
         write_part(o_col, p.part_o + (part * kExpandedRows + row0) * kD, it.count - row0, lane);
-      if (!whole) p.part_ml[part * kExpandedRows + prow] = make_float2(m_run, l_run);
+      if (!whole) p.part_ml[part * kExpandedRows + prow] = make_float4(ref.r, ref.m, ref.l, 0.f);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[gq]);
@@ -436,20 +502,20 @@ __global__ void __launch_bounds__(128) expanded_join_kernel(const __grid_constan
   const ExpandedCut cut = p.list.at<ExpandedCut>(p.cuts)[blockIdx.x / kPer];
   const int row = kJoinRows * (blockIdx.x % kPer) + 4 * (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= cut.count) return;
-  const float2* ml = p.part_ml + (int64_t)cut.slot * kExpandedRows + row;
+  const float4* ml = p.part_ml + (int64_t)cut.slot * kExpandedRows + row;
   const float* src = p.part_o + ((int64_t)cut.slot * kExpandedRows + row) * kExpandedV + 4 * lane;
-  float m[4], l[4];
+  float r[4], m[4], l[4];
   float4 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    r[i] = 0.f;
     m[i] = -CUDART_INF_F;
     l[i] = 0.f;
     o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 #pragma unroll 2
   for (int q = 0; q < cut.n_parts; ++q) {
-    float2 x[4];
-    float4 y[4];
+    float4 x[4], y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // (rows past the tile's are within the slot: any value may stand there)
       x[i] = ml[(int64_t)q * kExpandedRows + i];
@@ -457,10 +523,19 @@ __global__ void __launch_bounds__(128) expanded_join_kernel(const __grid_constan
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (x[i].x == -CUDART_INF_F) continue;  // (no key of the row in this part: the same)
-      const float top = fmaxf(m[i], x[i].x), a = ex2(m[i] - top), w = ex2(x[i].x - top);  // (2^-inf: 0)
-      m[i] = top;
-      l[i] = l[i] * a + w * x[i].y;
+      if (x[i].y == -CUDART_INF_F) continue;  // (no key of the row in this part: the same)
+      // the part's reference above the one so far, in bits: the larger is kept (2^-inf: 0).  (An m beside an r of 0
+      // may be large: it belongs into the product's rounding.)
+      const float dr = x[i].x - r[i];
+      const float d = m[i] == -CUDART_INF_F ? CUDART_INF_F
+                      : r[i] == 0.f         ? fmaf(dr, p.scale_log2, -m[i]) + x[i].y
+                                            : fmaf(dr, p.scale_log2, x[i].y) - m[i];
+      const float a = ex2(fminf(-d, 0.f)), w = ex2(fminf(d, 0.f));
+      if (d > 0.f) {
+        r[i] = x[i].x;
+        m[i] = x[i].y;
+      }
+      l[i] = l[i] * a + w * x[i].z;
       o[i].x = o[i].x * a + w * y[i].x;
       o[i].y = o[i].y * a + w * y[i].y;
       o[i].z = o[i].z * a + w * y[i].z;

@@ -503,7 +503,7 @@ int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32
   T.cuts = T.image.add(cuts);
   T.part_o = align_up(256 + T.image.bytes.size(), 256);
   T.part_ml = align_up(T.part_o + (size_t)slots * kExpandedRows * kExpandedV * sizeof(float), 256);
-  T.total = align_up(T.part_ml + (size_t)slots * kExpandedRows * sizeof(float2), 256);
+  T.total = align_up(T.part_ml + (size_t)slots * kExpandedRows * sizeof(float4), 256);
   return MIXATTN_OK;
 }
 
@@ -770,7 +770,7 @@ int mixattn_expanded_run(const mixattn_expanded_plan* plan_c, const mixattn_head
   p.cuts = (int32_t)(T.cuts - 256);
   p.o = static_cast<uint16_t*>(o);
   p.part_o = reinterpret_cast<float*>(ws + T.part_o);
-  p.part_ml = reinterpret_cast<float2*>(ws + T.part_ml);
+  p.part_ml = reinterpret_cast<float4*>(ws + T.part_ml);
   p.heads = h;
   p.n_ctas = T.n_ctas;
   p.n_cuts = T.n_cuts;

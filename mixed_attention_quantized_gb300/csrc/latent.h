@@ -94,7 +94,7 @@ struct ExpandedParams {
   int32_t items, cta_first, cuts;  // offsets in the list: ExpandedItem, int32 [n_ctas + 1], ExpandedCut
   uint16_t* o;
   float* part_o;    // [slots][256][128], unnormalised
-  float2* part_ml;  // [slots][256]
+  float4* part_ml;  // [slots][256]: reference (a score or 0, and bits above it) and sum
   int32_t heads, n_ctas, n_cuts;
   float scale_log2;
   PlanImage list;

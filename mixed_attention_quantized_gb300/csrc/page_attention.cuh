@@ -561,6 +561,44 @@ __device__ __forceinline__ float4 page_terms(float dk, float dv, bool there, flo
 // chunk of 2048 tokens at 32768 keys 1160 -> 1200 us.
 constexpr float kChunkSet = 6.f, kChunkTop = 65000.f, kChunkMoved = 10.9f;
 
+// A row's D columns of O times alpha.
+template <int D>
+__device__ __forceinline__ void scale_output(uint32_t o_col, float alpha) {
+  const uint64_t al2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+  for (int ch = 0; ch < D / 16; ++ch) {
+    uint32_t o[16];
+    tmem_ld16(o_col + 16 * ch, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float y0, y1;
+      f2_unpack(fmul2(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), y0, y1);
+      o[e] = __float_as_uint(y0);
+      o[e + 1] = __float_as_uint(y1);
+    }
+    tmem_st16(o_col + 16 * ch, o);
+  }
+}
+
+// The P' of a KV tile's pages before c times 2^-up (whole bits), as two fp16 powers of two down to
+// 2^-48: below 2^-40 no P' is left of it.
+__device__ __forceinline__ void scale_weights(uint32_t s_col, int c, float up) {
+  const float e_all = fmaxf(-up, -48.f), e_half = ceilf(0.5f * e_all);
+  const float al_1 = ex2(e_half), al_2 = ex2(e_all - e_half);
+  const uint32_t al_h = pack_f16x2(al_1, al_1), al_l = pack_f16x2(al_2, al_2);
+  tmem_wait_st();  // the P' of the pages before are in place
+#pragma unroll 1
+  for (int b = 0; b < c; ++b) {
+    uint32_t o[16];
+    tmem_ld16(s_col + 32 * b, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(hmul2_u32(o[e], al_h), al_l);
+    tmem_st16(s_col + 32 * b, o);
+  }
+}
+
 // The softmax's rare step, for page c (32 scores at s_col + 32 c) of a warp in which some row's
 // P' sum to kChunkTop, or which has rows without a reference: moves the references of the rows
 // that need it, multiplies O (if there is one yet: `scale_o`), l and the P' of the KV tile's
@@ -592,37 +630,8 @@ __device__ __noinline__ float2 page_move_reference(uint32_t s_col, uint32_t o_co
   const float m_new = grow ? (first ? mx - kChunkSet : m_run + up) : m_run;
   const float alpha = grow && first ? 0.f : ex2(-up);  // a power of two, or 0
   l_run *= alpha;
-  if (scale_o) {
-    const uint64_t al2 = f2_pack(alpha, alpha);
-#pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
-      uint32_t o[16];
-      tmem_ld16(o_col + 16 * ch, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        float y0, y1;
-        f2_unpack(fmul2(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), y0, y1);
-        o[e] = __float_as_uint(y0);
-        o[e + 1] = __float_as_uint(y1);
-      }
-      tmem_st16(o_col + 16 * ch, o);
-    }
-  }
-  // alpha as two fp16 powers of two, down to 2^-48: below 2^-40 no P' is left of it
-  const float e_all = fmaxf(-up, -48.f), e_half = ceilf(0.5f * e_all);
-  const float al_1 = ex2(e_half), al_2 = ex2(e_all - e_half);
-  const uint32_t al_h = pack_f16x2(al_1, al_1), al_l = pack_f16x2(al_2, al_2);
-  tmem_wait_st();  // the P' of the pages before are in place
-#pragma unroll 1
-  for (int b = 0; b < c; ++b) {
-    uint32_t o[16];
-    tmem_ld16(s_col + 32 * b, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(hmul2_u32(o[e], al_h), al_l);
-    tmem_st16(s_col + 32 * b, o);
-  }
+  if (scale_o) scale_output<D>(o_col, alpha);
+  scale_weights(s_col, c, up);
   // the page's P', 16 scores at a time: their 8 words stay before the scores not yet read
   const float cb = tm.y - (m_new == -CUDART_INF_F ? 0.f : m_new);
   float l_page = 0.f;

@@ -52,3 +52,58 @@ def test_absorbed(heads, scale):
         la.check(out[at:at + s - o], want, bound, (r, kind, s, o))
         at += s - o
     plan.close()
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("heads,rows", [(3, [(1, 0), (300, 0), (700, 650)]), (1, [(6000, 5700)]), (2, [(130, 0), (1000, 200)])])
+def test_expanded(heads, rows, scale):
+    """S up to 192 x 100^2 = 2^21."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    nk, nq = sum(s for s, _ in rows), sum(s - o for s, o in rows)
+    q, k, kr = _whole((nq, heads, 192), 100, 131), _whole((nk, heads, 128), 100, 132), _whole((nk, 64), 100, 133)
+    k[1::2], kr[1::2] = k[:nk - nk % 2:2].clone(), kr[:nk - nk % 2:2].clone()  # neighbours alike: weights of a half
+    v = la.queries(nk, heads, 128, 134, 1.0)
+    plan = mq.ExpandedPlan(heads, [r[0] for r in rows], [r[1] for r in rows], scale)
+    ws = mq.alloc_workspace(plan.workspace_bytes)
+    ws.fill_(0xFF)
+    out = torch.full((nq, heads, 128), float("nan"), dtype=torch.float16, device="cuda")
+    plan.run(q, k, kr, v, out, ws)
+    assert mq.device_error(clear=True) == 0
+    at = first = 0
+    for r, (s, o) in enumerate(rows):
+        key = torch.cat([k[first:first + s], kr[first:first + s, None].expand(-1, heads, -1)], -1)
+        want, bound = la.attention64(q[at:at + s - o], key, v[first:first + s], la.seen(CHUNK, s, o), scale)
+        la.check(out[at:at + s - o], want, bound, (r, s, o))
+        at += s - o
+        first += s
+    plan.close()
+
+
+@pytest.mark.parametrize("rows", [[(3000, 2900)], [(2600, 2590), (3000, 0)]])
+def test_expanded_scores_that_rise_slowly_past_2_to_the_22(rows):
+    """Key j's score is 2906000 + j / 2, 2^22 / log2(e) at j = 2540: about 23 bits a block of 32 keys, before and
+    after the reference takes a score."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    nk, nq, heads = sum(s for s, _ in rows), sum(s - o for s, o in rows), 2
+    j = torch.cat([torch.arange(s) for s, _ in rows]).cuda()
+    q, k = torch.zeros(nq, heads, 192, device="cuda").half(), torch.zeros(nk, heads, 128, device="cuda").half()
+    q[..., 0], q[..., 130], k[..., 0] = 2000, 1, 1453
+    kr = torch.zeros(nk, 64, device="cuda").half()
+    kr[:, 2] = j // 2
+    v = la.queries(nk, heads, 128, 141, 1.0)
+    plan = mq.ExpandedPlan(heads, [r[0] for r in rows], [r[1] for r in rows], 1.0)
+    out = torch.full((nq, heads, 128), float("nan"), dtype=torch.float16, device="cuda")
+    plan.run(q, k, kr, v, out, mq.alloc_workspace(plan.workspace_bytes))
+    assert mq.device_error(clear=True) == 0
+    at = first = 0
+    for s, o in rows:
+        key = torch.cat([k[first:first + s], kr[first:first + s, None].expand(-1, heads, -1)], -1)
+        for a in range(0, s - o, 256):
+            b = min(s - o, a + 256)
+            want, bound = la.attention64(q[at + a:at + b], key, v[first:first + s], la.seen(CHUNK, s, o)[a:b], 1.0)
+            la.check(out[at + a:at + b], want, bound, (s, o, a))
+        at += s - o
+        first += s
+    plan.close()
