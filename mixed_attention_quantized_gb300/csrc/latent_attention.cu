@@ -704,11 +704,11 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
       const float2 x = q == k ? first : part(q);
       const float w = x.x == -CUDART_INF_F ? 0.f : ex2((x.x - m) * p.scale_log2);
       weights[16 * q + row] = w;
-      if (w != 0.f) l += w * x.y;
+      l += w * x.y;  // (0 of a part without a key of the row; NaN where its scores are NaN, whatever the part weighs)
     }
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    if (k == 0) inv_l[row] = l > 0.f ? 1.f / l : 0.f;
+    if (k == 0) inv_l[row] = l > 0.f ? 1.f / l : l;  // (0, or the NaN of a query that is one)
   }
   __syncthreads();
   float acc[16];

@@ -1,0 +1,42 @@
+"""A query that is not a number answers NaN, whether its row is cut over the SMs or not, and no other query notices."""
+import numpy as np
+import pytest
+
+import _latent as la
+import _trees as tr
+
+pytestmark = pytest.mark.gpu
+
+DECODE, CHUNK, TREE = 0, 1, 3
+NAN = float("nan")
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_absorbed(heads):
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    rows = [(DECODE, 5000, 4999), (DECODE, 40, 39), (CHUNK, 900, 896), (TREE, 705, 700)]
+    cache, pt, slots = la.paged([r[1] for r in rows], 201)
+    q = la.queries(11, heads, 576, 202)
+    bad = [(0, 3), (1, 0), (3, 5), (9, heads - 1)]
+    for t, h in bad:
+        q[t, h] = NAN
+    mask = tr.random_tree(5, np.random.default_rng(203))
+    plan = mq.LatentPlan(cache, heads, [r[0] for r in rows], [r[1] for r in rows], [r[2] for r in rows], pt.shape[1], 0.07)
+    out = torch.zeros(11, heads, 512, dtype=torch.float16, device="cuda")
+    plan.run(q, pt, out, mq.alloc_workspace(plan.workspace_bytes), tree_mask=torch.from_numpy(tr.pack([mask])).cuda())
+    assert mq.device_error(clear=True) == 0
+    at = 0
+    for t, h in bad:
+        assert bool(out[t, h].isnan().all()), (t, h)
+        q[t, h] = 0
+        out[t, h] = 0
+    for r, (kind, s, o) in enumerate(rows):
+        k = cache.data.view(-1, 576)[slots[r]][:, None]
+        want, bound = la.attention64(q[at:at + s - o], k, k[..., :512], la.seen(kind, s, o, mask if kind == TREE else None), 0.07)
+        for t, h in bad:
+            if at <= t < at + s - o:
+                want[t - at, h] = 0
+        la.check(out[at:at + s - o], want, bound, (r, kind, s, o))
+        at += s - o
+    plan.close()
