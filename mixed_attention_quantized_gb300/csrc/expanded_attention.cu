@@ -523,7 +523,10 @@ __global__ void __launch_bounds__(128) expanded_join_kernel(const __grid_constan
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (x[i].y == -CUDART_INF_F) continue;  // (no key of the row in this part: the same)
+      if (x[i].y == -CUDART_INF_F) {  // no key of the row in this part, a sum of 0: the same; or scores that are all NaN
+        l[i] += x[i].z;
+        continue;
+      }
       // the part's reference above the one so far, in bits: the larger is kept (2^-inf: 0).  (An m beside an r of 0
       // may be large: it belongs into the product's rounding.)
       const float dr = x[i].x - r[i];
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(128) expanded_join_kernel(const __grid_constan
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (row + i >= cut.count) break;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];
     *reinterpret_cast<uint2*>(p.o + ((int64_t)(cut.q_start + row + i) * p.heads + cut.head) * kExpandedV + 4 * lane) =
         make_uint2(pack_f16x2_out(o[i].x * inv, o[i].y * inv), pack_f16x2_out(o[i].z * inv, o[i].w * inv));
   }

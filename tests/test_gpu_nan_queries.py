@@ -40,3 +40,33 @@ def test_absorbed(heads):
         la.check(out[at:at + s - o], want, bound, (r, kind, s, o))
         at += s - o
     plan.close()
+
+
+def test_expanded():
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    rows, heads = [(6000, 5700), (200, 0)], 2
+    nk, nq = 6200, 500
+    q, kv, kr = la.queries(nq, heads, 192, 211, 1.0), la.queries(nk, heads, 256, 212, 1.0), la.queries(nk, 1, 64, 213, 1.0)[:, 0]
+    bad = [(0, 0), (170, 1), (299, 0), (303, 1), (450, 0)]
+    for t, h in bad:
+        q[t, h] = NAN
+    plan = mq.ExpandedPlan(heads, [r[0] for r in rows], [r[1] for r in rows], 0.07)
+    out = torch.zeros(nq, heads, 128, dtype=torch.float16, device="cuda")
+    plan.run(q, kv[..., :128], kr, kv[..., 128:], out, mq.alloc_workspace(plan.workspace_bytes))
+    assert mq.device_error(clear=True) == 0
+    for t, h in bad:
+        assert bool(out[t, h].isnan().all()), (t, h)
+        q[t, h] = 0
+        out[t, h] = 0
+    at = first = 0
+    for r, (s, o) in enumerate(rows):
+        key = torch.cat([kv[first:first + s, :, :128], kr[first:first + s, None].expand(-1, heads, -1)], -1)
+        want, bound = la.attention64(q[at:at + s - o], key, kv[first:first + s, :, 128:], la.seen(CHUNK, s, o), 0.07)
+        for t, h in bad:
+            if at <= t < at + s - o:
+                want[t - at, h] = 0
+        la.check(out[at:at + s - o], want, bound, (r, s, o))
+        at += s - o
+        first += s
+    plan.close()
