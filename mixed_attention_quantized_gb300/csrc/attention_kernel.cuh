@@ -1402,9 +1402,9 @@ __device__ __forceinline__ void chunk_cta(const AttnParams& p, int cta, int n_ct
           for (int q = 0; q < t.nsplit; ++q) {
             const float* ml = p.chunk_partials + n_o + ((int64_t)(first + q) * kChunkM + row) * 2;
             const float mq = __ldcg(ml);
-            l_all += mq == -CUDART_INF_F ? 0.f : __ldcg(ml + 1) * ex2(mq - m_all);
+            l_all += __ldcg(ml + 1) * (mq == -CUDART_INF_F ? 0.f : ex2(mq - m_all));  // (NaN where its scores are all NaN)
           }
-          const float inv_l = (l_all > 0.f) ? 1.f / l_all : 0.f;
+          const float inv_l = (l_all > 0.f) ? 1.f / l_all : l_all;
 #pragma unroll 1
           for (int d0 = 0; d0 < D; d0 += 8) {
             float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

@@ -705,7 +705,7 @@ __device__ __noinline__ void page_merge_pieces(PageRowsOut out, const float* o, 
 #pragma unroll
     for (int q = 0; q < kPageMaxPieces; ++q) {
       s[q].x = s[q].x == -CUDART_INF_F ? 0.f : ex2(s[q].x - m_all);
-      if (s[q].x != 0.f) l_all += s[q].x * s[q].y;
+      if (q < nsplit) l_all += s[q].x * s[q].y;  // (NaN where a piece's scores are all NaN)
     }
     const float inv_l = TREE && tree && l_all == 0.f ? 0.f : 1.f / l_all;
     uint32_t x[16];

@@ -70,3 +70,38 @@ def test_expanded():
         at += s - o
         first += s
     plan.close()
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("kind", [CHUNK, TREE])
+@pytest.mark.parametrize("n,ctx", [(5, 300), (5, 20000), (40, 300), (40, 20000)])
+def test_paged_formats(fmt, kind, n, ctx):
+    """Short and long rows on decode and on chunk tiles, in one piece and in several."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    pages = -(-(ctx + n) // 32)
+    cache = mq.KVCache.allocate(pages, 1, 128, fmt, fmt)
+    g = torch.Generator("cuda").manual_seed(221)
+    k, v = (torch.randn(ctx + n, 1, 128, device="cuda", generator=g).half() for _ in range(2))
+    mq.kv_append_quant(cache, k, v, torch.arange(ctx + n, dtype=torch.int32, device="cuda"))
+    pt = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    q = torch.randn(n, 4, 128, device="cuda", generator=g).half()
+    plan = mq.Plan(cache, 4, [kind], [ctx + n], [ctx], pages)
+    ws = mq.alloc_workspace(plan.workspace_bytes)
+    mask = torch.from_numpy(tr.pack([tr.random_tree(n, np.random.default_rng(222))])).cuda() if kind == TREE else None
+
+    def run(x):
+        out = torch.zeros_like(x)
+        plan.run(x, pt, out, ws, tree_mask=mask)
+        assert mq.device_error(clear=True) == 0
+        return out
+
+    want, bad = run(q), q.clone()
+    bad[1, 2] = bad[n - 1, 0] = NAN
+    got = run(bad)
+    for t, h in ((1, 2), (n - 1, 0)):
+        assert bool(got[t, h].isnan().all()), (t, h)
+        got[t, h] = want[t, h]
+    # (a NaN row may move its neighbours to the softmax's exact step, which sums in another order: fp32)
+    assert float((got.float() - want.float()).abs().max()) <= 2.0 ** -10
+    plan.close()
