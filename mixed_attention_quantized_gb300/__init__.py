@@ -221,6 +221,13 @@ def _i32_array(values: Sequence[int]):
     return arr
 
 
+def _row_arrays(n, *lists):
+    """A batch's n rows as the library takes them: it reads n entries of every list."""
+    if any(len(x) < n for x in lists):
+        raise ValueError(f"lists of {[len(x) for x in lists]} entries for {n} rows")
+    return (n, *(_i32_array(x) for x in lists))
+
+
 class _Runtime:
     """What every call needs of torch, looked up once (a call's own time is a few microseconds)."""
 
@@ -511,10 +518,9 @@ class Plan:
         self._handle = ctypes.c_void_p(0)
         ws = ctypes.c_size_t(0)
         self._desc = cache.desc()
-        n = len(seq_lens)
         st = self._lib.mixattn_plan_create_window(ctypes.byref(self._handle), ctypes.byref(self._desc),
-                                                  self.num_q_heads, self.window, n, _i32_array(row_kinds),
-                                                  _i32_array(seq_lens), _i32_array(q_offsets),
+                                                  self.num_q_heads, self.window,
+                                                  *_row_arrays(len(seq_lens), row_kinds, seq_lens, q_offsets),
                                                   int(max_pages), ctypes.byref(ws))
         _check(st, "mixattn_plan_create")
         self.workspace_bytes = int(ws.value)
@@ -522,8 +528,7 @@ class Plan:
 
     def update(self, row_kinds, seq_lens, q_offsets, max_pages: int) -> None:
         ws = ctypes.c_size_t(0)
-        st = self._lib.mixattn_plan_update(self._handle, len(seq_lens), _i32_array(row_kinds),
-                                           _i32_array(seq_lens), _i32_array(q_offsets),
+        st = self._lib.mixattn_plan_update(self._handle, *_row_arrays(len(seq_lens), row_kinds, seq_lens, q_offsets),
                                            int(max_pages), ctypes.byref(ws))
         _check(st, "mixattn_plan_update")
         self.workspace_bytes = int(ws.value)
@@ -703,8 +708,8 @@ class LatentPlan:
         self._handle = ctypes.c_void_p(0)
         ws = ctypes.c_size_t(0)
         st = self._lib.mixattn_latent_plan_create(
-            ctypes.byref(self._handle), cache._ref(), self.num_heads, float(softmax_scale), len(seq_lens),
-            _i32_array(row_kinds), _i32_array(seq_lens), _i32_array(q_offsets), int(max_pages), ctypes.byref(ws))
+            ctypes.byref(self._handle), cache._ref(), self.num_heads, float(softmax_scale),
+            *_row_arrays(len(seq_lens), row_kinds, seq_lens, q_offsets), int(max_pages), ctypes.byref(ws))
         _check(st, "mixattn_latent_plan_create")
         self._keep(ws, row_kinds, seq_lens, q_offsets, max_pages)
 
@@ -716,9 +721,8 @@ class LatentPlan:
 
     def update(self, row_kinds, seq_lens, q_offsets, max_pages: int) -> None:
         ws = ctypes.c_size_t(0)
-        st = self._lib.mixattn_latent_plan_update(self._handle, len(seq_lens), _i32_array(row_kinds),
-                                                  _i32_array(seq_lens), _i32_array(q_offsets), int(max_pages),
-                                                  ctypes.byref(ws))
+        st = self._lib.mixattn_latent_plan_update(self._handle, *_row_arrays(len(seq_lens), row_kinds, seq_lens, q_offsets),
+                                                  int(max_pages), ctypes.byref(ws))
         _check(st, "mixattn_latent_plan_update")
         self._keep(ws, row_kinds, seq_lens, q_offsets, max_pages)
 
@@ -766,20 +770,18 @@ class ExpandedPlan:
         self._handle = ctypes.c_void_p(0)
         ws = ctypes.c_size_t(0)
         st = self._lib.mixattn_expanded_plan_create(ctypes.byref(self._handle), self.num_heads, float(softmax_scale),
-                                                    len(seq_lens), _i32_array(seq_lens), _i32_array(q_offsets),
-                                                    ctypes.byref(ws))
+                                                    *_row_arrays(len(seq_lens), seq_lens, q_offsets), ctypes.byref(ws))
         _check(st, "mixattn_expanded_plan_create")
         self._keep(ws, seq_lens, q_offsets)
 
     def _keep(self, ws, seq_lens, q_offsets) -> None:
         self.workspace_bytes = int(ws.value)
         self._total_k = sum(int(s) for s in seq_lens)
-        self._total_q = self._total_k - sum(int(o) for o in q_offsets)
+        self._total_q = sum(int(s) - int(o) for s, o in zip(seq_lens, q_offsets))
 
     def update(self, seq_lens, q_offsets) -> None:
         ws = ctypes.c_size_t(0)
-        st = self._lib.mixattn_expanded_plan_update(self._handle, len(seq_lens), _i32_array(seq_lens),
-                                                    _i32_array(q_offsets), ctypes.byref(ws))
+        st = self._lib.mixattn_expanded_plan_update(self._handle, *_row_arrays(len(seq_lens), seq_lens, q_offsets), ctypes.byref(ws))
         _check(st, "mixattn_expanded_plan_update")
         self._keep(ws, seq_lens, q_offsets)
 
@@ -818,8 +820,8 @@ def workspace_bytes(cache: KVCache, num_q_heads: int, row_kinds, seq_lens, q_off
                     max_pages: int) -> int:
     ws = ctypes.c_size_t(0)
     st = load().mixattn_workspace_bytes(ctypes.byref(cache.desc(raw=True)), int(num_q_heads),
-                                        len(seq_lens), _i32_array(row_kinds), _i32_array(seq_lens),
-                                        _i32_array(q_offsets), int(max_pages), ctypes.byref(ws))
+                                        *_row_arrays(len(seq_lens), row_kinds, seq_lens, q_offsets), int(max_pages),
+                                        ctypes.byref(ws))
     _check(st, "mixattn_workspace_bytes")
     return int(ws.value)
 
@@ -844,8 +846,8 @@ def mixed_attention(cache: KVCache, q, page_table, seq_lens, q_offsets, row_kind
     if o is None:
         o = _empty(q, stream)
     st = load().mixattn_mixed_attention(
-        ctypes.byref(cache.desc()), hq, _ptr(q), _ptr(page_table), max_pages, len(seq_lens),
-        _i32_array(seq_lens), _i32_array(q_offsets), _i32_array(row_kinds), _ptr(o), _ptr(workspace),
+        ctypes.byref(cache.desc()), hq, _ptr(q), _ptr(page_table), max_pages,
+        *_row_arrays(len(seq_lens), seq_lens, q_offsets, row_kinds), _ptr(o), _ptr(workspace),
         int(workspace.numel()), _stream_handle(stream))
     _check(st, "mixattn_mixed_attention")
     return o
@@ -861,7 +863,7 @@ def mixed_attention_noalloc(cache: KVCache, q, page_table, seq_lens, q_offsets, 
         o = _empty(q, stream)
     st = load().mixattn_mixed_attention_noalloc(
         ctypes.byref(cache.desc()), int(q.shape[1]), _ptr(q), _ptr(page_table), int(page_table.shape[1]),
-        len(seq_lens), _i32_array(seq_lens), _i32_array(q_offsets), _i32_array(row_kinds), _ptr(o),
+        *_row_arrays(len(seq_lens), seq_lens, q_offsets, row_kinds), _ptr(o),
         _stream_handle(stream))
     _check(st, "mixattn_mixed_attention_noalloc")
     return o
