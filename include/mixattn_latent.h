@@ -118,7 +118,7 @@ void mixattn_latent_plan_destroy(mixattn_latent_plan* plan);
  * sequence, packed in row order (those of row r start at the sum of the seq_lens before it); its
  * queries are the last seq_len - q_offset of them, packed likewise, and see keys up to their own.
  *   o[t][h] = sum_j softmax_j(softmax_scale (q[t][h][:128] . k[j][h] + q[t][h][128:] . r[j])) v[j][h]
- *   num_heads      >= 1
+ *   num_heads      1 .. 65536
  * Work is cut over the SMs for the whole batch, as that of an absorbed plan.
  */
 typedef struct mixattn_expanded_plan mixattn_expanded_plan;

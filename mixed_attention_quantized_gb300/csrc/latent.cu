@@ -414,6 +414,8 @@ struct ExpandedTiling {
 // 900, 16 heads 34.3 / 34.3 / 42.
 constexpr int kExpandedItemCost = 2, kMinItemTiles = 4;
 
+constexpr int kMaxExpandedHeads = 1 << 16;  // an output token's elements (128 a head) then count in 32 bits
+
 // The tiles' KV tiles in a line -- neighbouring blocks of queries of one head read the same keys --
 // cut into one run of equal cost for each SM.
 int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32_t* off, int n_sm,
@@ -438,6 +440,7 @@ int build_expanded_tiling(int heads, int n_rows, const int32_t* seq, const int32
     T.total_k += s;
     if (T.total_q > INT32_MAX / heads || T.total_k > INT32_MAX / 2) return MIXATTN_ERR_INVALID_ARG;
   }
+  if (heads > kMaxExpandedHeads) return MIXATTN_ERR_UNSUPPORTED;
   if (n_tiles > 1 << 28) return MIXATTN_ERR_INVALID_ARG;
   const double share = total / n_sm + kExpandedItemCost;
   double used = 0.0;  // of all so far: what one took too much or too little, the next ones even out
