@@ -62,7 +62,8 @@ typedef struct {
  *                (16-byte aligned, strides multiples of 8 and >= 512 and 64)
  *   positions, slot_mapping   device int32 [n_new]; slots as for mixattn_kv_append_quant (a skipped
  *                token's queries are still rotated).  Two tokens of one slot race.
- * Elements that are not finite stay what they are (of rotated ones infinities saturate).
+ * Latent elements that are not finite stay what they are.  Both elements of a rotated pair are sums of products of
+ * both: one that is not finite makes them NaN or (an infinity) +-65504, and touches no other pair.
  */
 int mixattn_latent_append(const mixattn_latent_cache* cache, const mixattn_rope* rope, int32_t num_heads,
                           const mixattn_heads* q, const mixattn_heads* q_out, const void* c_new, int64_t c_stride,
