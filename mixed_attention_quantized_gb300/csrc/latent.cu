@@ -39,10 +39,12 @@ struct LatentAppendArgs {
 
 // Bound by bytes, so every load of a CTA is under way before its tokens' cosines are formed: a thread
 // takes kAppendJobs jobs -- 16 bytes of a latent vector to copy, or 16 elements (both halves of 8
-// pairs) of a position key or of a query head to rotate -- of the CTA's one to four tokens.
+// pairs) of a position key or of a query head to rotate -- of the CTA's one to three tokens.
 // 8201 tokens of 32 heads 20.5 us (86 MB, 4.2 TB/s), 16 of 128 4.3 us; with 256 threads 22.7 and 4.3, with
 // four jobs a thread 20.5 and 6.2, with one 24.7 and 4.3.
-constexpr int kAppendJobs = 2, kAppendTokens = 4, kAppendThreads = 128;
+constexpr int kAppendJobs = 2, kAppendTokens = 3, kAppendThreads = 128;
+static_assert((kAppendTokens + 1) * (kLatent / 8 + kLatentRope / 16) > kAppendJobs * kAppendThreads,
+              "a CTA's jobs are those of more tokens");
 
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __grid_constant__ RopeTable t,
                                                                        const __grid_constant__ LatentAppendArgs a) {
