@@ -52,7 +52,7 @@ __device__ __forceinline__ int group_steps(const ExpandedItem& it, int group) {
 // A row's weights are P = 2^(scale (S - r) - m); its reference (m = -inf: none yet) and their sum.  Up to kLargeScore
 // r is 0.  Beyond, m alone would not do: of scale S near 2^28 no fp32 number is closer than 16, and the weights about
 // such an m overflow fp16 or vanish.  Those rows take a score as r, so that S - r is exact to fp32 where a weight counts, and
-// all their blocks the rare step: subtracting r from every row's scores, 283 -> 321 us for the case above; as it is 281 -> 283.
+// all their blocks the rare step: subtracting r from every row's scores, 283 -> 321 us for the case above.
 struct ExpandedRef {
   float r, m, l;
   // what the common path adds to scale S: NaN, and with it the sum of the block, where a block needs the rare step
@@ -101,6 +101,7 @@ __device__ __noinline__ ExpandedRef move_reference(uint32_t s_col, uint32_t o_co
   scale_weights(s_col, c, up);
   // the block's P', 16 scores at a time: their 8 words stay before the scores not yet read
   const float cb = ref.m == -CUDART_INF_F ? 0.f : -ref.m;
+  const uint64_t nr2 = f2_pack(-ref.r, -ref.r), scale2 = f2_pack(scale, scale), cb2 = f2_pack(cb, cb);
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {
     uint32_t o[16], w[8];
@@ -108,8 +109,10 @@ __device__ __noinline__ ExpandedRef move_reference(uint32_t s_col, uint32_t o_co
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      const float p0 = 16 * b + e <= c_last ? ex2(fmaf(__uint_as_float(o[e]) - ref.r, scale, cb)) : 0.f;
-      const float p1 = 16 * b + e + 1 <= c_last ? ex2(fmaf(__uint_as_float(o[e + 1]) - ref.r, scale, cb)) : 0.f;
+      float p0, p1;
+      f2_unpack(ffma2(fadd2(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), nr2), scale2, cb2), p0, p1);
+      p0 = 16 * b + e <= c_last ? ex2(p0) : 0.f;
+      p1 = 16 * b + e + 1 <= c_last ? ex2(p1) : 0.f;
       ref.l += p0 + p1;
       w[e >> 1] = pack_f16x2(p0, p1);
     }
@@ -248,7 +251,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
       }
       const int pos = it.pos + min(prow, it.count - 1);
       ExpandedRef ref{0.f, -CUDART_INF_F, 0.f};
-      float cb = ref.shift();
       for (int j = 0; j < n; ++j) {
         ok = warp_wait_fast(&s_full[gq], n_s & 1, err);
         if (!ok) break;
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
           const uint32_t sc = s_col + 32 * c;
           uint32_t x[32], pk[16];
           tmem_ld32(sc, x);
+          const float cb = ref.shift();  // (kept from block to block 305 us for 301, in a long run of the case above)
           const uint64_t cb2 = f2_pack(cb, cb);
           tmem_wait_ld();
           if (diag) {
@@ -290,7 +293,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             continue;
           }
           ref = move_reference(s_col, o_col, c, p.scale_log2, c_last, ref, j > 0);
-          cb = ref.shift();
         }
         tmem_wait_st();
         tc_fence_before();
