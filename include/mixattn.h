@@ -48,6 +48,9 @@
  *   - Outputs are rounded to the nearest fp16, saturating at +-65504: a Q8_0
  *     block whose largest element is 65504 dequantises it to 127 * 516 = 65532,
  *     and a mean dominated by such values stays finite.
+ *   - Scores and softmax sums are fp32, the softmax weights that meet the values
+ *     fp16.  Scores q . k / sqrt(head_dim) of up to 2^20 in magnitude are served;
+ *     far beyond, weights may overflow and outputs be infinite or NaN.
  */
 #ifndef MIXATTN_H
 #define MIXATTN_H
@@ -272,8 +275,8 @@ int mixattn_rope_apply(const mixattn_rope* rope, const void* x, int64_t x_stride
  * Elements that are not finite: the page-scaled formats take K and V as described above.
  * In Q8_0 and Q4_0 a key's infinities and rotated values beyond +-65504 saturate there and
  * its NaN count as 0; values (V) are encoded as mixattn_kv_append_quant does, which does not
- * look for them (an infinity or NaN spoils its block).  F16 keeps NaN; of rotated elements
- * infinities saturate.
+ * look for them (an infinity or NaN spoils its block).  F16 keeps NaN; a rotated pair with an
+ * infinity becomes NaN or +-65504 (its elements are sums of products of both).
  */
 int mixattn_rope_append(const mixattn_kv_cache* cache, const mixattn_rope* rope, int32_t num_q_heads, const void* q,
                         int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k_new, int64_t k_stride,

@@ -14,7 +14,9 @@
  *
  * Conventions (streams, ownership, status codes, device checks, captured graphs) are those of
  * mixattn.h, whose device error word these calls share.  Outputs are rounded to the nearest fp16,
- * saturating at +-65504; sums and softmax statistics are fp32.
+ * saturating at +-65504.  Scores, sums and softmax statistics are fp32, whatever the scores' size; the
+ * softmax weights that meet the values are rounded to fp16, 2^-11 of each (those below 2^-20 of their
+ * row's largest, 2^-31 of that).  A query with a NaN answers NaN.
  */
 #ifndef MIXATTN_LATENT_H
 #define MIXATTN_LATENT_H
@@ -119,6 +121,8 @@ void mixattn_latent_plan_destroy(mixattn_latent_plan* plan);
  * sequence, packed in row order (those of row r start at the sum of the seq_lens before it); its
  * queries are the last seq_len - q_offset of them, packed likewise, and see keys up to their own.
  *   o[t][h] = sum_j softmax_j(softmax_scale (q[t][h][:128] . k[j][h] + q[t][h][128:] . r[j])) v[j][h]
+ * A value that is not finite may reach the outputs of its row's earlier queries too, which do not see it
+ * (a weight of 0 times it); those of other rows it does not reach.
  *   num_heads      1 .. 65536
  * Work is cut over the SMs for the whole batch, as that of an absorbed plan.
  */

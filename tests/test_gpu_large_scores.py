@@ -107,3 +107,36 @@ def test_expanded_scores_that_rise_slowly_past_2_to_the_22(rows):
         at += s - o
         first += s
     plan.close()
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("kind,n", [(DECODE, 1), (CHUNK, 5), (CHUNK, 40), (TREE, 5), (TREE, 40)])
+@pytest.mark.parametrize("ctx", [200, 9000])
+def test_paged_formats_up_to_2_to_the_20(fmt, kind, n, ctx):
+    """Every kind of row, short and cut, with scores of up to 2^20 (and beside 64 bits over what the cache holds): keys
+    and queries of +-1 times one size each, so that scores are whole multiples of one step, far enough apart for a
+    key, or several alike, to weigh all; the weights' and the output's rounding is what is left."""
+    import torch
+    import mixed_attention_quantized_gb300 as mq
+    g = torch.Generator("cuda").manual_seed(151)
+    keys, pages = ctx + n, -(-(ctx + n) // 32)
+    sign = lambda *s: (torch.randint(0, 2, s, device="cuda", generator=g) * 2 - 1).float()
+    # 128 equal signs: a score of 128 a b / sqrt(128) = 2^20 x 0.72
+    a, b = 256.0, 254.0
+    cache = mq.KVCache.allocate(pages, 1, 128, fmt, fmt)
+    k, v = (sign(keys, 1, 128) * b).half(), la.queries(keys, 1, 128, 152, 1.0)
+    mq.kv_append_quant(cache, k, v, torch.arange(keys, dtype=torch.int32, device="cuda"))
+    slots = torch.arange(keys, dtype=torch.int32, device="cuda")
+    k, v = tr.cache_values(cache, 0, slots), tr.cache_values(cache, 1, slots)
+    assert float((k.abs() - b).abs().max()) <= 0.13 * b  # (a code's step)
+    q = torch.empty(n, 4, 128, device="cuda", dtype=torch.float16)
+    q[:] = k[ctx // 2 + torch.arange(4, device="cuda"), 0].sign().half() * a  # a key of the context each
+    mask = tr.random_tree(n, np.random.default_rng(153))
+    pt = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    plan, out = mq.Plan(cache, 4, [kind], [keys], [ctx], pages), torch.zeros_like(q)
+    plan.run(q, pt, out, mq.alloc_workspace(plan.workspace_bytes),
+             tree_mask=torch.from_numpy(tr.pack([mask])).cuda() if kind == TREE else None)
+    assert mq.device_error(clear=True) == 0
+    want = tr.attention64(q, k, v, tr.seen(kind, keys, ctx, mask if kind == TREE else None), 128 ** -0.5)
+    assert float((out.double() - want).abs().max()) <= 2e-3 + 2.0 ** -11 * float(want.abs().max())
+    plan.close()
