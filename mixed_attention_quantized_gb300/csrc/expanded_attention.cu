@@ -13,7 +13,7 @@
 // Values past a row's last key belong to the next row and may be anything: a warp of its own zeroes
 // them in the slots of the row's last KV tile before their MMAs.
 //
-// 2048 tokens behind 8192, 32 heads: 283 us (1.40 PFLOP/s). A step of both groups has 2768 cycles of MMAs, and
+// 2048 tokens behind 8192, 32 heads: 283 us (1.40 PFLOP/s), 302 in a long run, at the power limit. A step of both groups has 2768 cycles of MMAs, and
 // the tensor pipe is 67 % active: the rest is the softmax's chain, the items' starts and ends. One MMA warp for
 // both groups, issuing from lane 0, took 569 us.
 #include "latent.h"

@@ -14,8 +14,9 @@ constexpr int kLatent = 512, kLatentRope = 64, kLatentRow = kLatent + kLatentRop
 constexpr int kNopeDim = 128, kExpandedV = 128, kExpandedQ = kNopeDim + kLatentRope;
 
 // A plan's list as its kernels take it: all but the largest go with the launch itself, with no upload in front
-// (32 rows of 500 to 2000 tokens, 16 heads, a call among others 23.5 -> 20.1 us; five prompts of up to 900, 8 heads,
-// 18.8 -> 15.3; two of up to 2000, 32 heads, 72.4 -> 68.9; no call slower for the longer parameters).
+// (a call among others: 32 rows of 500 to 2000 tokens, 16 heads, 24.4 -> 19.5 us, two rows of up to 300 14.4 -> 10.6; five
+// prompts of up to 900, 8 heads, 26.9 -> 22.5, two of up to 2000, 32 heads, 83.1 -> 78.4; a session of 131072 tokens and
+// 31 short rows, 128 heads, 123.1 -> 118.2: no call slower for the longer parameters).  500 decode rows pass it.
 constexpr int kInlineBytes = 24576;  // (parameters may have 32764)
 
 struct PlanImage {
