@@ -223,9 +223,9 @@ def _i32_array(values: Sequence[int]):
 
 def _row_arrays(n, *lists):
     """A batch's n rows as the library takes them: it reads n entries of every list."""
-    if any(len(x) < n for x in lists):
+    if min(map(len, lists)) < n:
         raise ValueError(f"lists of {[len(x) for x in lists]} entries for {n} rows")
-    return (n, *(_i32_array(x) for x in lists))
+    return (n, *map(_i32_array, lists))
 
 
 class _Runtime:
