@@ -330,8 +330,8 @@ int mixattn_plan_create_window(mixattn_plan** plan_out, const mixattn_kv_cache* 
                                const int32_t* q_offsets, int32_t max_pages, size_t* workspace_bytes);
 
 /* Re-tile an existing plan for a new batch (same cache and heads), reusing its
- * pinned buffer when it is large enough.  Waits for the plan's previous
- * mixattn_run to have copied the old tile list before overwriting it. */
+ * pinned buffer when it is large enough.  Waits for the runs before it, on whatever
+ * streams, to have copied the old tile list before overwriting it. */
 int mixattn_plan_update(mixattn_plan* plan, int32_t n_rows, const int32_t* row_kinds,
                         const int32_t* seq_lens, const int32_t* q_offsets, int32_t max_pages,
                         size_t* workspace_bytes);

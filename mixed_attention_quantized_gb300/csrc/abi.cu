@@ -395,15 +395,8 @@ static __global__ void upload_kernel(const uint4* __restrict__ src, uint4* __res
 }
 
 int PlanList::fill(const std::vector<uint8_t>& image) {
-  if (!copied_ && cudaEventCreateWithFlags(&copied_, cudaEventDisableTiming) != cudaSuccess) {
-    copied_ = nullptr;
-    return MIXATTN_ERR_CUDA;
-  }
-  // the previous run may still be copying from the pinned buffer
-  if (copy_recorded_) {
-    if (cudaEventSynchronize(copied_) != cudaSuccess) return MIXATTN_ERR_CUDA;
-    copy_recorded_ = false;
-  }
+  // runs before this may still be copying from the pinned buffer
+  if (!wait_for_copies()) return MIXATTN_ERR_CUDA;
   if (image.size() > cap_) {
     if (buf_) cudaFreeHost(buf_);
     buf_ = nullptr;
@@ -445,11 +438,51 @@ int PlanList::upload(uint8_t* dst, size_t bytes, cudaStream_t s) {
   if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MIXATTN_ERR_CUDA;
   if (capture != cudaStreamCaptureStatusNone) {
     captured_ = true;
-  } else {
-    if (cudaEventRecord(copied_, s) != cudaSuccess) return MIXATTN_ERR_CUDA;
-    copy_recorded_ = true;
+    return MIXATTN_OK;
   }
+  return note_copy(s);
+}
+
+int PlanList::note_copy(cudaStream_t s) {
+  int dev = 0;
+  unsigned long long id = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaStreamGetId(s, &id) != cudaSuccess) return MIXATTN_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu_);
+  Copy* c = nullptr;
+  for (Copy& x : copies_)
+    if (x.event && x.device == dev && x.stream == id) c = &x;
+  for (Copy& x : copies_) {  // (an event belongs to the device it was made on)
+    if (c) break;
+    if (!x.event) {
+      if (cudaEventCreateWithFlags(&x.event, cudaEventDisableTiming) != cudaSuccess) {
+        x.event = nullptr;
+        return MIXATTN_ERR_CUDA;
+      }
+      x.device = dev;
+    }
+    if (!x.recorded && x.device == dev) c = &x;
+  }
+  for (Copy& x : copies_) {
+    if (c) break;
+    if (x.device != dev) continue;
+    if (cudaStreamWaitEvent(s, x.event, 0) != cudaSuccess) return MIXATTN_ERR_CUDA;
+    c = &x;
+  }
+  if (!c)  // every place is another device's: nothing to note once it is done
+    return cudaStreamSynchronize(s) == cudaSuccess ? MIXATTN_OK : MIXATTN_ERR_CUDA;
+  if (cudaEventRecord(c->event, s) != cudaSuccess) return MIXATTN_ERR_CUDA;
+  c->stream = id;
+  c->recorded = true;
   return MIXATTN_OK;
+}
+
+bool PlanList::wait_for_copies() {
+  std::lock_guard<std::mutex> lock(mu_);
+  for (Copy& x : copies_) {
+    if (x.recorded && cudaEventSynchronize(x.event) != cudaSuccess) return false;
+    x.recorded = false;
+  }
+  return true;
 }
 
 int PlanList::note_capture(cudaStream_t s) {
@@ -460,8 +493,9 @@ int PlanList::note_capture(cudaStream_t s) {
 }
 
 PlanList::~PlanList() {
-  if (copy_recorded_ && copied_) cudaEventSynchronize(copied_);
-  if (copied_) cudaEventDestroy(copied_);
+  wait_for_copies();
+  for (Copy& x : copies_)
+    if (x.event) cudaEventDestroy(x.event);
   if (buf_) cudaFreeHost(buf_);
 }
 

@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <mutex>
 #include <vector>
 
 #include "internal.h"
@@ -24,7 +25,7 @@ class PlanList {
   PlanList& operator=(const PlanList&) = delete;
   ~PlanList();
 
-  // Replaces the list; waits until the previous run has copied the old one.
+  // Replaces the list; waits until every run so far, on whatever stream, has copied the old one.
   int fill(const std::vector<uint8_t>& image);
   // Enqueues the copy of the list's first `bytes` (a multiple of 16) to `dst`.
   int upload(uint8_t* dst, size_t bytes, cudaStream_t s);
@@ -37,8 +38,19 @@ class PlanList {
   uint8_t* buf_ = nullptr;
   const uint8_t* dev_ = nullptr;  // the same buffer as the device sees it
   size_t cap_ = 0, size_ = 0;
-  cudaEvent_t copied_ = nullptr;
-  bool copy_recorded_ = false;
+  // The last copy on each stream that has made one since the list was filled; of more streams than
+  // there are places, one waits for another's copy and stands for both.
+  struct Copy {
+    cudaEvent_t event = nullptr;
+    int device = 0;
+    unsigned long long stream = 0;
+    bool recorded = false;
+  };
+  int note_copy(cudaStream_t s);
+  bool wait_for_copies();
+  static constexpr int kStreams = 8;
+  Copy copies_[kStreams];
+  std::mutex mu_;  // (host threads may run one plan at once)
   bool captured_ = false;
 };
 
